@@ -1,4 +1,4 @@
-"""ctypes declarations of libconvtp.so (include/convtp.h), nothing else.
+"""ctypes declarations of libconvtp.so (include/convtp.h, include/convtp_train.h), nothing else.
 
 Loading fails loudly if the HIP library has not been built: there is no
 fallback implementation of any entry point.
@@ -26,6 +26,12 @@ EXPORTS = ("conv_tp_num_paths", "conv_tp_paths", "conv_tp_layout", "conv_tp_coup
            "conv_tp_version")
 
 
+# Every symbol include/convtp_train.h declares.
+TRAIN_EXPORTS = ("conv_tp_embed_fwd", "conv_tp_embed_bwd", "conv_tp_embed_bwd_workspace", "conv_tp_norm_fwd",
+                 "conv_tp_norm_bwd", "conv_tp_norm_bwd_workspace", "conv_tp_clip", "conv_tp_clip_workspace",
+                 "conv_tp_train_last_error")
+
+
 class Problem(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("n_edges", ctypes.c_int32),
                 ("channels", ctypes.c_int32), ("l_in", ctypes.c_int32),
@@ -36,6 +42,20 @@ class Problem(ctypes.Structure):
 class NodeProblem(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("channels", ctypes.c_int32), ("l_x", ctypes.c_int32),
                 ("l_y", ctypes.c_int32), ("l_out", ctypes.c_int32)]
+
+
+class EmbedProblem(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_rows", ctypes.c_int64), ("src_stride", ctypes.c_int64),
+                ("dst_stride", ctypes.c_int64), ("channels", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("index_bits", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("h_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("grad_r_stride", ctypes.c_int64), ("grad_u_stride", ctypes.c_int64),
+                ("lmax", ctypes.c_int32), ("channels", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class ConvTPError(RuntimeError):
@@ -96,3 +116,39 @@ def lib() -> ctypes.CDLL:
 def check(status: int) -> None:
     if status != CTP_OK:
         raise ConvTPError(status, lib().conv_tp_last_error().decode())
+
+
+_train = None
+
+
+def train_lib() -> ctypes.CDLL:
+    """The library with the entry points of include/convtp_train.h declared."""
+    global _train
+    if _train is not None:
+        return _train
+    L = lib()
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    i64p = ctypes.POINTER(i64)
+    ep, np_ = ctypes.POINTER(EmbedProblem), ctypes.POINTER(NormProblem)
+    sig = {
+        "conv_tp_embed_fwd": ([ep, vp, vp, vp, vp], i32),
+        "conv_tp_embed_bwd": ([ep, vp, vp, vp, vp, i64, vp], i32),
+        "conv_tp_embed_bwd_workspace": ([ep, i64p], i32),
+        "conv_tp_norm_fwd": ([np_] + [vp] * 8, i32),
+        "conv_tp_norm_bwd": ([np_] + [vp] * 13 + [i64, vp], i32),
+        "conv_tp_norm_bwd_workspace": ([np_, i64p], i32),
+        "conv_tp_clip": ([i32, vp, vp, vp, vp, f32, f32, vp, vp, i64, vp], i32),
+        "conv_tp_clip_workspace": ([i32], i64),
+        "conv_tp_train_last_error": ([], ctypes.c_char_p),
+    }
+    for name, (args, res) in sig.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = res
+    _train = L
+    return L
+
+
+def train_check(status: int) -> None:
+    if status != CTP_OK:
+        raise ConvTPError(status, train_lib().conv_tp_train_last_error().decode())

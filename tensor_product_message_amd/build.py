@@ -23,6 +23,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvtp.so")
 SOURCES = ["convtp_common.hip", "nodetp_kernels.hip", "graph_kernels.hip", "stream_probe.hip", "convtp_api.hip"]
+# the operators of a training step (include/convtp_train.h), apart from the convolution's sources and headers
+TRAIN_SOURCES = ["embed_kernels.hip", "norm_kernels.hip", "clip_kernels.hip", "train_api.hip"]
+TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "../include/convtp_train.h", "../include/convtp.h"]
 TRIPLE_SOURCE = "convtp_triple.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -59,7 +62,7 @@ def _compile(job) -> None:
 def _jobs(objdir: str):
     jobs = [(TRIPLE_SOURCE, os.path.join(objdir, f"triple_{a}{b}{c}.o"),
              [f"-DCTP_L1={a}", f"-DCTP_L2={b}", f"-DCTP_L3={c}"]) for a, b, c in TRIPLES]
-    jobs += [(s, os.path.join(objdir, s.replace(".hip", ".o")), []) for s in SOURCES]
+    jobs += [(s, os.path.join(objdir, s.replace(".hip", ".o")), []) for s in TRAIN_SOURCES + SOURCES]
     return jobs
 
 
@@ -70,12 +73,15 @@ def build(verbose: bool = True, incremental: bool = False, workers: int = None) 
     jobs = _jobs(objdir)
     todo = jobs
     if incremental:
-        headers = glob.glob(os.path.join(CSRC, "*.hpp")) + glob.glob(os.path.join(HERE, "..", "include", "*.h"))
-        newest_header = max(os.path.getmtime(p) for p in headers)
+        train = [os.path.normpath(os.path.join(HERE, p)) for p in TRAIN_HEADERS]
+        conv = [p for p in glob.glob(os.path.join(CSRC, "*.hpp")) if p not in train]
+        conv.append(os.path.normpath(os.path.join(HERE, "..", "include", "convtp.h")))
+        newest_train, newest_conv = (max(os.path.getmtime(p) for p in ps) for ps in (train, conv))
 
         def stale(job):
             src, obj, _ = job
-            newest = max(newest_header, os.path.getmtime(os.path.join(CSRC, src)))
+            newest = max(newest_train if src in TRAIN_SOURCES else newest_conv,
+                         os.path.getmtime(os.path.join(CSRC, src)))
             return not os.path.exists(obj) or os.path.getmtime(obj) < newest
         todo = [j for j in jobs if stale(j)]
     n = workers or min(16, os.cpu_count() or 8)
