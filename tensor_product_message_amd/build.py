@@ -24,8 +24,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvtp.so")
 SOURCES = ["convtp_common.hip", "nodetp_kernels.hip", "graph_kernels.hip", "stream_probe.hip", "convtp_api.hip"]
 # the operators of a training step (include/convtp_train.h), apart from the convolution's sources and headers
-TRAIN_SOURCES = ["embed_kernels.hip", "norm_kernels.hip", "clip_kernels.hip", "train_api.hip"]
-TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "../include/convtp_train.h", "../include/convtp.h"]
+TRAIN_SOURCES = ["embed_kernels.hip", "norm_fwd.hip", "norm_bwd.hip", "clip_kernels.hip", "train_api.hip"]
+TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "csrc/norm_common.hpp",
+                 "../include/convtp_train.h", "../include/convtp.h"]
 TRIPLE_SOURCE = "convtp_triple.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -50,16 +50,18 @@ k_embed_fwd(const T* __restrict__ table, const void* __restrict__ tokens, T* __r
         row[u] = t < n ? token_at(tokens, wide, t, rows) : -1;
     }
     for (int v = lane; v < nvec; v += 1 << lg) {
+        const Span span = span_of<T>(v, channels);
         vec_t<T> x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             x[u] = vec_t<T>{};
-            if (row[u] >= 0) x[u] = load_vec<T>(table + row[u] * table_stride, v, channels);
+            if (row[u] >= 0) x[u] = read_span<T>(table + row[u] * table_stride, span, channels);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long t = t0 + u * groups;
             if (t >= n) break;
+            settle<T>(x[u], span);
             Floats<T> f = widen<T>(x[u]);
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) f.v[k] *= scale;
@@ -293,6 +295,7 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
     int cur = s.keys[begin];
     bool head = begin > 0 && s.keys[begin - 1] == cur;      // the run began in an earlier chunk
     const int next = end < s.n ? s.keys[end] : s.rows;
+    const Span span = span_of<T>(tl.v, channels);
     Floats<T> acc = {};
     for (long i0 = begin; i0 < end && cur != s.rows; i0 += kBatch) {
         int key[kBatch];
@@ -302,7 +305,7 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             x[q] = vec_t<T>{};
-            if (key[q] != s.rows) x[q] = load_vec<T>(grad + s.pos[i0 + q] * grad_stride, tl.v, channels);
+            if (key[q] != s.rows) x[q] = read_span<T>(grad + s.pos[i0 + q] * grad_stride, span, channels);
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
@@ -315,6 +318,7 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
                 acc = Floats<T>{};
                 if (cur == s.rows) break;
             }
+            settle<T>(x[q], span);
             const Floats<T> f = widen<T>(x[q]);
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) acc.v[k] += f.v[k];

@@ -1,0 +1,312 @@
+// Gradients of the norms after and before a block (formulas in norm_common.hpp).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "norm_common.hpp"
+
+namespace ctp {
+
+namespace {
+
+// Gradients of shared parameters: every workgroup goes through rows
+// blockIdx.x, + gridDim.x, .. and keeps the sums of its columns in registers;
+// k_norm_join adds the workgroups' sums.  More workgroups hide more of a row's
+// two reductions, but each leaves a row of partial sums.
+constexpr int kSums = 3;        // dw_post, dw_pre, dg
+
+// Threads of all workgroups together.
+constexpr int kTotalThreads = 1024 * 256;
+
+// Full: everything is there (h, both norms, both gradients) and a row is no
+// shorter than a vector, so that a row's reads are issued in one straight line.
+template <class T, int Lanes, int NV, int G, bool Full>
+__global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
+    constexpr int kRowsAtOnce = rows_at_once(Lanes);
+    __shared__ float part[2][3][kSumWaves<Lanes>];
+    __shared__ float part1[2][1][kSumWaves<Lanes>];
+    extern __shared__ __align__(16) float row_buf[];    // the rows in work, in fp32, where lanes share sums
+    RowSum<Lanes, 3> sum3{part};
+    RowSum<Lanes, 1> sum1{part1};
+    const int lane = threadIdx.x % Lanes, sub = row_in_group<Lanes>();
+    const int C = a.channels, nvec = (C + kVec<T> - 1) / kVec<T>, nl = a.lmax + 1, comps = nl * nl;
+    const long W = (long)comps * C;
+    const bool has_h = Full || a.h, has_post = Full || a.w_post, has_pre = Full || a.w_pre;
+    const bool has_gr = Full || a.grad_r, has_gu = Full || a.grad_u;
+    const float inv = 1.0f / ((float)nl * (float)C);
+    const Params<T> post{a.w_post, a.param_dtype != a.dtype, C}, pre{a.w_pre, post.wide, C}, shared{a.gate_p, post.wide, C};
+    Place p[NV];
+    float b[NV];
+    // w_post, w_pre and the shared gate stay in registers where a lane has one vector, else they are read again
+    constexpr bool kKeep = NV == 1;
+    Floats<T> wq0{}, wp0{}, wg0{};
+    Floats<T> acc_post[NV] = {}, acc_pre[NV] = {}, acc_gate[G == kGateChannel ? NV : 1] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        p[i] = place_of<T>(lane + i * Lanes, nvec, comps, C);
+        b[i] = inv / (float)(2 * p[i].l + 1);
+    }
+    if (kKeep && p[0].on) {
+        if (has_post) wq0 = post.load(p[0]);
+        if (has_pre) wp0 = pre.load(p[0]);
+        if constexpr (G == kGateChannel) wg0 = shared.load(p[0]);
+    }
+    auto w_post = [&](int i) {
+        if (kKeep) return wq0;
+        return p[i].on ? post.load(p[i]) : Floats<T>{};
+    };
+    auto w_pre = [&](int i) {
+        if (kKeep) return wp0;
+        return p[i].on ? pre.load(p[i]) : Floats<T>{};
+    };
+    for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
+        const long row = row0 + sub;
+        const bool live = row < a.n_rows;
+        vec_t<T> hx[NV], rx[NV], grx[NV], gux[NV], gx[G == kGateRow ? NV : 1];
+        auto read_row = [&](auto stream) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                hx[i] = rx[i] = grx[i] = gux[i] = vec_t<T>{};
+                if constexpr (G == kGateRow) gx[i] = vec_t<T>{};
+                if (!p[i].on || !live) continue;
+                auto read = [&](const void* x, long stride, unsigned from) {
+                    return read_at<T, Full, stream>(row_of<const T>(x, row, stride) + from, p[i].span, C);
+                };
+                if (has_pre) rx[i] = read(a.r, a.r_stride, p[i].from);
+                if (has_gu) gux[i] = read(a.grad_u, a.grad_u_stride, p[i].from);
+                if (has_h) hx[i] = read(a.h, a.h_stride, p[i].from);
+                if (has_gr) grx[i] = read(a.grad_r, a.grad_r_stride, p[i].from);
+                if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p[i].par_from);
+            }
+        };
+        if (a.stream) {
+            read_row(std::true_type{});
+            keep_apart();
+        } else {
+            read_row(std::false_type{});
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (p[i].span.shift <= 0) continue;
+            settle<T>(rx[i], p[i].span), settle<T>(gux[i], p[i].span);
+            settle<T>(hx[i], p[i].span), settle<T>(grx[i], p[i].span);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p[i].span);
+        }
+        // the squares of h and r' and <A, r'>
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Floats<T> h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
+            const Floats<T> w = has_pre ? w_pre(i) : Floats<T>{};
+            float qh = 0.0f, qr = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                qh = __builtin_fmaf(h.v[k], h.v[k], qh);
+                qr = __builtin_fmaf(r.v[k], r.v[k], qr);
+                s[2] = __builtin_fmaf(w.v[k] * gu.v[k], r.v[k], s[2]);
+            }
+            s[0] = __builtin_fmaf(qh, b[i], s[0]);
+            s[1] = __builtin_fmaf(qr, b[i], s[1]);
+        }
+        sum3(s);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) forget(hx[i]), forget(rx[i]), forget(gux[i]);
+        const float s1 = has_post ? inv_root(s[0], a.eps) : 1.0f;
+        const float s2 = has_pre ? inv_root(s[1], a.eps) : 0.0f;
+        const float pull = s2 * s[2];
+        float t[1] = {0.0f};
+        Floats<T> B[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool on = p[i].on && live;    // the others work on zeros
+            B[i] = Floats<T>{};
+            Floats<T> d = widen<T>(grx[i]);
+            if (has_pre) {
+                const Floats<T> r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
+                const Floats<T> w = w_pre(i);
+                const float c = pull * b[i];
+#pragma unroll
+                for (int k = 0; k < kVec<T>; ++k) {
+                    const float rs = r.v[k] * s2;
+                    d.v[k] = __builtin_fmaf(s2, __builtin_fmaf(-c, rs, w.v[k] * gu.v[k]), d.v[k]);
+                    acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], rs, acc_pre[i].v[k]);
+                }
+            }
+            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p[i].to, p[i].left, narrow<T>(d));
+            if (!has_h) continue;
+            const Floats<T> h = widen<T>(hx[i]);
+            Floats<T> w, g, dg;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) w.v[k] = g.v[k] = 1.0f;
+            if (has_post) w = w_post(i);
+            if constexpr (G == kGateRow) g = widen<T>(gx[i]);
+            if constexpr (G == kGateChannel) g = kKeep ? wg0 : p[i].on ? shared.load(p[i]) : Floats<T>{};
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                const float ad = a.alpha * d.v[k], hs = h.v[k] * s1, dy = ad * g.v[k];
+                dg.v[k] = ad * hs * w.v[k];
+                acc_post[i].v[k] = __builtin_fmaf(dy, hs, acc_post[i].v[k]);
+                B[i].v[k] = dy * w.v[k];
+                t[0] = __builtin_fmaf(B[i].v[k], h.v[k], t[0]);
+            }
+            if constexpr (G == kGateChannel) {
+#pragma unroll
+                for (int k = 0; k < kVec<T>; ++k) acc_gate[i].v[k] += dg.v[k];
+            }
+            if constexpr (G == kGateRow) {
+                if (comps == 1) {
+                    if (on) store_left<T>(row_of<T>(a.d_gate, row, C) + p[i].to, p[i].left, narrow<T>(dg));
+                } else if (p[i].on) {
+                    float* at = row_buf + (sub * comps * nvec + lane + i * Lanes) * kVec<T>;
+#pragma unroll
+                    for (int k = 0; k < kVec<T>; ++k) at[k] = dg.v[k];
+                }
+            }
+        }
+        if (!has_h) continue;
+        float pull1 = 0.0f;
+        if (has_post) {
+            sum1(t);
+            pull1 = s1 * t[0];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) forget(hx[i]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Floats<T> h = widen<T>(hx[i]);
+            const float c = pull1 * b[i];
+            Floats<T> dh;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) dh.v[k] = s1 * __builtin_fmaf(-c, h.v[k] * s1, B[i].v[k]);
+            if (p[i].on && live) store_left<T>(row_of<T>(a.d_h, row, W) + p[i].to, p[i].left, narrow<T>(dh));
+        }
+        if constexpr (G == kGateRow) {
+            if (comps > 1) {
+                // the components of a degree share the row's gate
+                lds_barrier();
+                for (int i = lane; live && i < nl * nvec; i += Lanes) {
+                    const int l = i / nvec, v = i - l * nvec;
+                    Floats<T> g = {};
+                    for (int d = l * l; d < (l + 1) * (l + 1); ++d) {
+                        const float* at = row_buf + ((sub * comps + d) * nvec + v) * kVec<T>;
+#pragma unroll
+                        for (int k = 0; k < kVec<T>; ++k) g.v[k] += at[k];
+                    }
+                    store_vec<T>(static_cast<T*>(a.d_gate) + (row * nl + l) * C, v, C, narrow<T>(g));
+                }
+                lds_barrier();
+            }
+        }
+    }
+    // the workgroup's sums: over its rows at once and over the components of a degree, [sum][l][padded channels]
+    const int width = nl * nvec * kVec<T>;
+    float* ws = static_cast<float*>(a.workspace) + (long)blockIdx.x * kSums * width;
+    const bool fold = kRowsAtOnce > 1 || comps > 1;
+    auto leave = [&](int which, const Floats<T>* acc) {
+        float* to = fold ? row_buf + sub * comps * nvec * kVec<T> : ws + which * width;
+        if (fold) lds_barrier();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!p[i].on) continue;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; k += 4)
+                *reinterpret_cast<float4*>(to + (lane + i * Lanes) * kVec<T> + k) =
+                    make_float4(acc[i].v[k], acc[i].v[k + 1], acc[i].v[k + 2], acc[i].v[k + 3]);
+        }
+        if (!fold) return;
+        lds_barrier();
+        for (int c = threadIdx.x; c < width; c += kNormThreads<Lanes>) {
+            const int l = c / (nvec * kVec<T>), at = c - l * (nvec * kVec<T>);
+            float x = 0.0f;
+            for (int q = 0; q < kRowsAtOnce; ++q)
+                for (int d = l * l; d < (l + 1) * (l + 1); ++d) x += row_buf[(q * comps + d) * (nvec * kVec<T>) + at];
+            ws[which * width + c] = x;
+        }
+    };
+    if (a.d_w_post) leave(0, acc_post);
+    if (a.d_w_pre) leave(1, acc_pre);
+    if constexpr (G == kGateChannel) leave(2, acc_gate);
+}
+
+// Adds the workgroups' sums: 64 columns a workgroup, whose 16 waves share the
+// groups and meet in LDS.
+constexpr int kJoinWaves = 16;
+
+__global__ void __launch_bounds__(64 * kJoinWaves)
+k_norm_join(const float* __restrict__ ws, int groups, int nl, int channels, int padded, int out_dtype, void* d_post,
+            void* d_pre, void* d_gate) {
+    __shared__ float part[kJoinWaves][64];
+    const int which = blockIdx.y, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    void* out = which == 0 ? d_post : which == 1 ? d_pre : d_gate;
+    if (!out) return;
+    const int width = nl * padded, col = blockIdx.x * 64 + lane;
+    const int l = col / padded, c = col - l * padded;
+    const bool on = col < width && c < channels;
+    float x = 0.0f;
+    if (on) {
+        const float* at = ws + which * width + col;
+#pragma unroll 8
+        for (int g = wave; g < groups; g += kJoinWaves) x += at[(long)g * (kSums * width)];
+    }
+    part[wave][lane] = x;
+    lds_barrier();
+    if (wave != 0 || !on) return;
+    for (int w = 1; w < kJoinWaves; ++w) x += part[w][lane];
+    const long to = (long)l * channels + c;
+    if (out_dtype == kBF16) static_cast<__bf16*>(out)[to] = (__bf16)x;
+    else if (out_dtype == kF16) static_cast<_Float16*>(out)[to] = (_Float16)x;
+    else static_cast<float*>(out)[to] = x;
+}
+
+int bwd_grid(long n_rows, int lanes) {
+    const int at_once = rows_at_once(lanes), threads = std::max(256, lanes);
+    return (int)std::min<long>((n_rows + at_once - 1) / at_once, kTotalThreads / threads);
+}
+
+}  // namespace
+
+long norm_bwd_workspace(long n_rows, int lmax, int channels) {
+    // over both vector widths
+    long most = 0;
+    for (int kvec : {4, 8}) {
+        const int n = row_vectors(lmax, channels, kvec);
+        const long groups = with_shape(n, [&](auto lanes, auto) { return (long)bwd_grid(n_rows, lanes); });
+        most = std::max(most, groups * kSums * (n / (lmax + 1)) * kvec * (long)sizeof(float));
+    }
+    return most;
+}
+
+hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
+    NormArgs a = args;
+    const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
+    a.stream = streams(a.n_rows * row * (2 * !!a.h + !!a.grad_r + !!a.grad_u + !!a.w_pre + 1));
+    return with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        const int n = row_vectors(a.lmax, a.channels, kVec<T>);
+        return with_shape(n, [&](auto lanes, auto nv) {
+            const int grid = bwd_grid(a.n_rows, lanes);
+            if (grid > 0) {
+                constexpr int kAtOnce = rows_at_once(lanes);
+                const size_t lds = kAtOnce > 1 || a.lmax > 0 ? (size_t)kAtOnce * n * kVec<T> * sizeof(float) : 0;
+                auto go = [&](auto kernel) { kernel<<<grid, kNormThreads<lanes>, lds, st>>>(a); };
+                const bool full = a.h && a.w_post && a.w_pre && a.grad_r && a.grad_u && a.channels >= kVec<T>;
+                auto gated = [&](auto g) {
+                    if (full) go(k_norm_bwd<T, lanes, nv, g, true>);
+                    else go(k_norm_bwd<T, lanes, nv, g, false>);
+                };
+                if (a.gate == kGateRow) gated(std::integral_constant<int, kGateRow>{});
+                else if (a.gate == kGateChannel) gated(std::integral_constant<int, kGateChannel>{});
+                else gated(std::integral_constant<int, kGateNone>{});
+            }
+            const int padded = (a.channels + kVec<T> - 1) / kVec<T> * kVec<T>, cols = (a.lmax + 1) * padded;
+            void* d_gate = a.gate == kGateChannel ? a.d_gate : nullptr;
+            if (a.d_w_post || a.d_w_pre || d_gate)
+                k_norm_join<<<dim3((cols + 63) / 64, kSums), 64 * kJoinWaves, 0, st>>>(
+                    static_cast<const float*>(a.workspace), grid, a.lmax + 1, a.channels, padded, a.param_dtype,
+                    a.d_w_post, a.d_w_pre, d_gate);
+            return hipGetLastError();
+        });
+    });
+}
+
+}  // namespace ctp

@@ -50,28 +50,94 @@ struct Vec {
 template <class T>
 using vec_t = typename Vec<T>::type;
 
-// Vector v of a row of n values (n > v * kVec); what lies past the row's end reads as 0.
+// Vector v of a row of n values.  A last vector that the row does not fill is
+// read from kVec values before the row's end, one access like the others, and
+// shifted down afterwards (settle): the shift waits for the access, so it comes
+// after all of a lane's accesses are on their way.  Rows shorter than a vector
+// are read value by value.
+struct Span {
+    int at;         // first value read
+    int shift;      // bits to shift out
+    int few;        // values of a row that is shorter than a vector, else 0
+};
+
 template <class T>
-__device__ __forceinline__ vec_t<T> load_vec(const T* row, int v, int n) {
-    const int at = v * kVec<T>;
-    if (at + kVec<T> <= n) return *reinterpret_cast<const typename Vec<T>::unaligned*>(row + at);
+__device__ __forceinline__ Span span_of(int v, int n) {
+    const int at = v * kVec<T>, over = at + kVec<T> - n;
+    if (n < kVec<T>) return Span{at, 0, v == 0 ? n : 0};
+    return over > 0 ? Span{at - over, over * 8 * (int)sizeof(T), 0} : Span{at, 0, 0};
+}
+
+template <class T, bool Whole = false, bool Stream = false>
+__device__ __forceinline__ vec_t<T> read_at(const T* at, const Span& s, int n) {
+    if (Whole || n >= kVec<T>) {
+        auto* x = reinterpret_cast<const typename Vec<T>::unaligned*>(at);
+        return Stream ? __builtin_nontemporal_load(x) : *x;
+    }
     vec_t<T> x = {};
 #pragma unroll
     for (int k = 0; k < kVec<T> - 1; ++k)
-        if (at + k < n) x[k] = row[at + k];
+        if (k < s.few) x[k] = at[k];
     return x;
+}
+template <class T>
+__device__ __forceinline__ vec_t<T> read_span(const T* row, const Span& s, int n) {
+    return read_at<T>(row + s.at, s, n);
+}
+
+// (Whole: the caller knows that rows are no shorter; Stream: see streams.)  What lies past the row's end becomes 0.
+template <class T>
+__device__ __forceinline__ void settle(vec_t<T>& x, const Span& s) {
+    if (s.shift > 0) x = __builtin_bit_cast(vec_t<T>, __builtin_bit_cast(unsigned __int128, x) >> s.shift);
+}
+
+template <class T>
+__device__ __forceinline__ vec_t<T> load_vec(const T* row, int v, int n) {
+    const Span s = span_of<T>(v, n);
+    vec_t<T> x = read_span<T>(row, s, n);
+    settle<T>(x, s);
+    return x;
+}
+
+// Values [k, k + N) of x to where the row has room for them.
+template <class T, int N>
+__device__ __forceinline__ void store_part(T* row, vec_t<T> x, int k) {
+    typedef T part_t __attribute__((ext_vector_type(N), aligned(alignof(T))));
+    part_t y;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        T z = x[q];
+#pragma unroll
+        for (int m = N; m + q < kVec<T>; m += N) z = k == m ? x[m + q] : z;
+        y[q] = z;
+    }
+    *reinterpret_cast<part_t*>(row + k) = y;
+}
+
+// x to `to`, where `left` > 0 values have room.
+template <class T>
+__device__ __forceinline__ void store_left(T* to, int left, vec_t<T> x) {
+    if (left >= kVec<T>) {
+        *reinterpret_cast<typename Vec<T>::unaligned*>(to) = x;
+        return;
+    }
+    // the row's last values, in halves of halves of a vector
+    int k = 0;
+    if constexpr (kVec<T> == 8)
+        if (left & 4) {
+            store_part<T, 4>(to, x, k);
+            k += 4;
+        }
+    if (left & 2) {
+        store_part<T, 2>(to, x, k);
+        k += 2;
+    }
+    if (left & 1) store_part<T, 1>(to, x, k);
 }
 
 template <class T>
 __device__ __forceinline__ void store_vec(T* row, int v, int n, vec_t<T> x) {
-    const int at = v * kVec<T>;
-    if (at + kVec<T> <= n) {
-        *reinterpret_cast<typename Vec<T>::unaligned*>(row + at) = x;
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < kVec<T> - 1; ++k)
-        if (at + k < n) row[at + k] = x[k];
+    store_left<T>(row + v * kVec<T>, n - v * kVec<T>, x);
 }
 
 // kVec<T> values in fp32, and back with one rounding to nearest even.
@@ -96,6 +162,14 @@ __device__ __forceinline__ vec_t<T> narrow(const Floats<T>& f) {
     return x;
 }
 
+// A vector that the compiler takes for a new one: what it has derived from the
+// old (the fp32 values, four times the registers of bf16 pairs) is not kept
+// alive for later uses but derived again.
+template <class V>
+__device__ __forceinline__ void forget(V& x) {
+    asm volatile("" : "+v"(x));
+}
+
 // Vector v of a row of parameters, which are held in T or in fp32 (`wide`): kVec<T> values either way.
 template <class T>
 __device__ __forceinline__ Floats<T> load_param(const void* row, bool wide, int v, int n) {
@@ -112,11 +186,48 @@ __device__ __forceinline__ Floats<T> load_param(const void* row, bool wide, int 
     return f;
 }
 
-// Sum over aligned groups of `Width` lanes (a power of two up to 64), the same in every lane, in a fixed order.
+// Whether a call's reads are marked non-temporal: where it moves more than the
+// 256 MB last-level cache holds, what it reads would only push out what it
+// writes.  Norm gradients over 805 MB take 129 us with the mark and 147 without
+// it; over 60 MB, which an earlier kernel leaves in that cache, 21 and 19 us.
+constexpr long kStreamBytes = 256L << 20;
+inline bool streams(long bytes) { return bytes > kStreamBytes; }
+
+// Barrier of the workgroup for what it shares in LDS.  __syncthreads also waits
+// until the waves' stores to memory have arrived, which costs a row of a norm
+// another trip to memory at each of its reductions.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Ends one of two branches that differ in their reads' cache policy alone: the
+// compiler would make one of them, and drop the policy.
+__device__ __forceinline__ void keep_apart() { asm volatile("; reads with a policy of their own" ::: "memory"); }
+
+// The value of another lane by a DPP control, 0 in rows of 16 lanes outside Rows.
+template <int Ctrl, int Rows = 0xf>
+__device__ __forceinline__ float dpp(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), Ctrl, Rows, 0xf, false));
+}
+
+// Sum over aligned groups of 16 or 64 lanes, the same bits in every lane.  All
+// lanes of the wave take part.  The lanes trade in registers (DPP); through
+// LDS each of the six steps would wait some 100 clocks.
 template <int Width>
 __device__ __forceinline__ float lane_sum(float x) {
-#pragma unroll
-    for (int d = Width / 2; d >= 1; d /= 2) x += __shfl_xor(x, d, 64);
+    static_assert(Width == 16 || Width == 64);
+    // both lanes of a pair add the same two values
+    x += dpp<0xB1>(x);      // quad_perm 1 0 3 2
+    x += dpp<0x4E>(x);      // quad_perm 2 3 0 1
+    x += dpp<0x141>(x);     // row_half_mirror
+    x += dpp<0x140>(x);     // row_mirror
+    if constexpr (Width == 64) {
+        x += dpp<0x142, 0xa>(x);    // lane 15 of rows 0 and 2 to rows 1 and 3
+        x += dpp<0x143, 0xc>(x);    // lane 31 to rows 2 and 3: lane 63 has all
+        x = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+    }
     return x;
 }
 __device__ __forceinline__ double wave_sum(double x) {

@@ -44,6 +44,7 @@ struct NormArgs {
     const void *grad_r, *grad_u;                // backward (null: zero)
     void *d_h, *d_r, *d_w_post, *d_w_pre, *d_gate;
     void* workspace;
+    bool stream;            // set by the launch: reads are non-temporal
 };
 
 // Largest row: D * channels values.
