@@ -13,6 +13,7 @@
 // in order, and a run of equal tokens that spans several chunks is joined from
 // the chunks' partial sums by a second kernel.  Cutting the sorted list and
 // not the table's rows keeps the work even when a few tokens take most of it.
+// A few tokens under a small table need no sort: one kernel (k_embed_few).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -71,19 +72,180 @@ k_embed_fwd(const T* __restrict__ table, const void* __restrict__ tokens, T* __r
     }
 }
 
-// ------------------------------------------------------------ sort
+// ------------------------------------------------------------ gradient: places of a row
+
+// The vector of a row that a lane works on: 2^lg lanes a row, a workgroup of
+// `Threads` has Threads >> lg groups of them, blockIdx.y counts the tiles of
+// 2^lg vectors.
+template <int Threads>
+struct Tile {
+    int lane, group, groups, v, nvec;
+    __device__ Tile(int lg, int channels, int kvec) {
+        lane = threadIdx.x & ((1 << lg) - 1);
+        group = threadIdx.x >> lg;
+        groups = Threads >> lg;
+        nvec = (channels + kvec - 1) / kvec;
+        v = (blockIdx.y << lg) + lane;
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void add_vec(Floats<T>& acc, const vec_t<T>& x) {
+    const Floats<T> f = widen<T>(x);
+#pragma unroll
+    for (int k = 0; k < kVec<T>; ++k) acc.v[k] += f.v[k];
+}
+
+template <class T>
+__device__ __forceinline__ void store_floats(float* p, const Floats<T>& f) {
+#pragma unroll
+    for (int k = 0; k < kVec<T>; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f.v[k], f.v[k + 1], f.v[k + 2], f.v[k + 3]);
+}
+
+template <class T>
+__device__ __forceinline__ void add_floats(const float* p, Floats<T>& f) {
+#pragma unroll
+    for (int k = 0; k < kVec<T>; k += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p + k);
+        f.v[k] += q.x;
+        f.v[k + 1] += q.y;
+        f.v[k + 2] += q.z;
+        f.v[k + 3] += q.w;
+    }
+}
+
+// Writes kVec<T> finished sums of vector v of a row of O.
+template <class T, class O>
+__device__ __forceinline__ void store_sum(O* row, int v, int n, const Floats<T>& f, float scale) {
+#pragma unroll
+    for (int p = 0; p < kVec<T> / kVec<O>; ++p) {
+        Floats<O> g;
+#pragma unroll
+        for (int k = 0; k < kVec<O>; ++k) g.v[k] = f.v[p * kVec<O> + k] * scale;
+        const int w = v * (kVec<T> / kVec<O>) + p;
+        if (w * kVec<O> < n) store_vec<O>(row, w, n, narrow<O>(g));
+    }
+}
+
+// ------------------------------------------------------------ gradient: few tokens, small table
+
+// One workgroup a table row and tile of channels goes through all tokens,
+// keeps the places of its own in order and sums their rows.  Every workgroup
+// reads all tokens, so this is for a few thousand of them and workgroups; it
+// saves the sort's launches (the water box's 1503 tokens: one launch instead
+// of three).
+constexpr int kFewThreads = 512;
+constexpr int kFewTokens = 4096;
+constexpr int kFewGroups = 2048;    // workgroups
+constexpr int kFewLanes = 3;        // log2 of the lanes of a row
+
+template <class T, class O>
+__global__ void __launch_bounds__(kFewThreads)
+k_embed_few(const T* __restrict__ grad, const void* __restrict__ tokens, O* __restrict__ d_table, int n, int rows,
+            int channels, int wide, float scale, long grad_stride, long table_stride) {
+    __shared__ uint16_t place[kFewTokens];
+    __shared__ int wave_count[kFewThreads / 64];
+    __shared__ __align__(16) float part[kFewThreads / 64][(1 << kFewLanes) * kVec<T>];
+    const int row = blockIdx.x, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    // a thread's tokens are consecutive, so that the places come out in order
+    constexpr int kPer = kFewTokens / kFewThreads;
+    const int per = (n + kFewThreads - 1) / kFewThreads;
+    unsigned mine = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int t = threadIdx.x * per + k;
+        if (k < per && t < n && token_at(tokens, wide, t, rows) == row) mine |= 1u << k;
+    }
+    const int count = __popc(mine);
+    int incl = count;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += up;
+    }
+    if (lane == 63) wave_count[wave] = incl;
+    __syncthreads();
+    int at = incl - count, total = 0;
+    for (int w = 0; w < kFewThreads / 64; ++w) {
+        if (w < wave) at += wave_count[w];
+        total += wave_count[w];
+    }
+    for (unsigned m = mine; m; m &= m - 1) place[at++] = (uint16_t)(threadIdx.x * per + __builtin_ctz(m));
+    __syncthreads();
+    const Tile<kFewThreads> tl(kFewLanes, channels, kVec<T>);
+    const bool on = tl.v < tl.nvec;
+    const Span span = span_of<T>(tl.v, channels);
+    Floats<T> acc = {};
+    constexpr int kAtOnce = 4;
+    for (int i0 = tl.group; i0 < total; i0 += tl.groups * kAtOnce) {
+        vec_t<T> x[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int i = i0 + q * tl.groups;
+            x[q] = vec_t<T>{};
+            if (on && i < total) x[q] = read_span<T>(grad + place[i] * grad_stride, span, channels);
+        }
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            settle<T>(x[q], span);
+            add_vec<T>(acc, x[q]);
+        }
+    }
+    // the wave's groups, then the waves
+#pragma unroll
+    for (int k = 0; k < kVec<T>; ++k)
+        for (int d = 1 << kFewLanes; d < 64; d <<= 1) acc.v[k] += __shfl_xor(acc.v[k], d, 64);
+    if (lane < 1 << kFewLanes) store_floats<T>(&part[wave][lane * kVec<T>], acc);
+    __syncthreads();
+    if (tl.group != 0 || !on) return;
+    for (int w = 1; w < kFewThreads / 64; ++w) add_floats<T>(&part[w][lane * kVec<T>], acc);
+    store_sum<T, O>(d_table + row * table_stride, tl.v, channels, acc, scale);
+}
+
+// ------------------------------------------------------------ gradient: sort
 
 // Least-significant-digit radix sort of the tokens, padding as id `rows` at
 // the end.  Each pass is two kernels: digit counts of every tile, then every
 // tile finds where its digits begin from all tiles' counts and places its
 // tokens stably.  Up to 10 bits a pass: 2 passes sort a million-row table, 1 a
-// table of elements.
+// table of elements.  With one tile its own counts are all there are, and the
+// first kernel is left out.  At most 64 tiles: every tile reads the counts of
+// all of them, one digit a thread.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 10;
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kMaxTiles = 128;
-constexpr int kTile = 1024;     // tokens of a tile, or a multiple
-constexpr int kWaves = kThreads / 64;
-constexpr int kRounds = kTile / kThreads;    // rounds of 64 tokens a wave has of each 1024
+constexpr int kMaxTiles = 64;
+constexpr int kTile = 2048;     // tokens of a tile, or a multiple
+static_assert(kDigits <= kSortThreads);
+
+// The sort's kernels are short and few workgroups wide, so a share of the
+// table's zeros can be written beside them: workgroups from `first` on fill
+// rows [begin, end) of `row_bytes` each.
+struct Zeros {
+    char* base;
+    long begin, end, row_bytes, stride_bytes;
+    int first, groups;
+};
+
+__device__ __forceinline__ void fill_zeros(const Zeros& z) {
+    typedef uint32_t quad __attribute__((ext_vector_type(4), aligned(2)));
+    const long units = z.row_bytes / 16, rest = z.row_bytes - units * 16;
+    const long rows = z.end - z.begin, per = (rows + z.groups - 1) / z.groups;
+    const long r0 = z.begin + (blockIdx.x - z.first) * per, r1 = min(z.end, r0 + per);
+    if (r0 >= r1) return;
+    if (rest == 0 && z.stride_bytes == z.row_bytes) {
+        char* to = z.base + r0 * z.stride_bytes;
+        const long n = (r1 - r0) * units;
+        for (long u = threadIdx.x; u < n; u += kSortThreads) *reinterpret_cast<quad*>(to + u * 16) = quad{};
+        return;
+    }
+    // a wave a row
+    for (long r = r0 + threadIdx.x / 64; r < r1; r += kSortWaves) {
+        char* to = z.base + r * z.stride_bytes;
+        for (long u = threadIdx.x % 64; u < units; u += 64) *reinterpret_cast<quad*>(to + u * 16) = quad{};
+        for (long u = threadIdx.x % 64; u < rest / 2; u += 64) reinterpret_cast<uint16_t*>(to + units * 16)[u] = 0;
+    }
+}
 
 struct SortSrc {
     const void* tokens;     // first pass: the tokens themselves
@@ -98,17 +260,18 @@ __device__ __forceinline__ int sort_key(const SortSrc& s, int i) {
     return v < 0 ? s.rows : v;
 }
 
-__global__ void __launch_bounds__(kThreads)
-k_sort_count(SortSrc src, int tile, int shift, int bits, int32_t* __restrict__ counts) {
+__global__ void __launch_bounds__(kSortThreads)
+k_sort_count(SortSrc src, int tile, int n_tiles, int shift, int bits, int32_t* __restrict__ counts, Zeros zeros) {
     __shared__ int32_t cnt[kDigits];
+    if (blockIdx.x >= n_tiles) return fill_zeros(zeros);
     const int digits = 1 << bits;
-    for (int d = threadIdx.x; d < digits; d += kThreads) cnt[d] = 0;
+    if (threadIdx.x < digits) cnt[threadIdx.x] = 0;
     __syncthreads();
     const long end = min((long)src.n, (long)(blockIdx.x + 1) * tile);
-    for (long i = (long)blockIdx.x * tile + threadIdx.x; i < end; i += kThreads)
+    for (long i = (long)blockIdx.x * tile + threadIdx.x; i < end; i += kSortThreads)
         atomicAdd(&cnt[(sort_key(src, (int)i) >> shift) & (digits - 1)], 1);
     __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kThreads) counts[(long)blockIdx.x * digits + d] = cnt[d];
+    if (threadIdx.x < digits) counts[(long)blockIdx.x * digits + threadIdx.x] = cnt[threadIdx.x];
 }
 
 // Lanes of the wave that hold the same digit (of `bits` bits) among those of `active`.
@@ -122,60 +285,52 @@ __device__ __forceinline__ uint64_t same_digit(int digit, int bits, uint64_t act
     return m;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSortThreads)
 k_sort_place(SortSrc src, int tile, int n_tiles, int shift, int bits, const int32_t* __restrict__ counts,
-             int32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out) {
-    __shared__ int32_t at[kWaves][kDigits];     // first counts, then the next free place of every wave and digit
-    __shared__ int32_t wave_total[kWaves];
+             int32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out, Zeros zeros) {
+    __shared__ int32_t at[kSortWaves][kDigits];     // first counts, then the next free place of every wave and digit
+    __shared__ int32_t wave_total[kSortWaves];
+    if (blockIdx.x >= n_tiles) return fill_zeros(zeros);
     const int digits = 1 << bits, mine = blockIdx.x;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    constexpr int kPer = kDigits / kThreads;    // digits tid * kPer .. of this thread
-    int before[kPer] = {}, total[kPer] = {};
-    for (int t = 0; t < n_tiles; ++t) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int d = tid * kPer + j;
-            const int c = d < digits ? counts[(long)t * digits + d] : 0;
-            total[j] += c;
-            if (t < mine) before[j] += c;
+    int before = 0, total = 0;
+    if (n_tiles > 1 && tid < digits) {
+#pragma unroll 16
+        for (int t = 0; t < n_tiles; ++t) {
+            const int c = counts[(long)t * digits + tid];
+            total += c;
+            before += t < mine ? c : 0;
         }
     }
-    for (int d = tid; d < kWaves * kDigits; d += kThreads) (&at[0][0])[d] = 0;
+    for (int d = lane; d < digits; d += 64) at[wave][d] = 0;
+    // every wave counts its own part of the tile
+    const int part = tile / kSortWaves;
+    const long begin = (long)mine * tile + (long)wave * part;
+    const long end = min((long)src.n, begin + part);
+    for (long i = begin + lane; i < end; i += 64)
+        atomicAdd(&at[wave][(sort_key(src, (int)i) >> shift) & (digits - 1)], 1);
+    __syncthreads();
+    if (n_tiles == 1 && tid < digits)
+        for (int w = 0; w < kSortWaves; ++w) total += at[w][tid];
     // exclusive sum of the totals over all digits
-    int sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += total[j];
-    int incl = sum;
+    int incl = total;
     for (int d = 1; d < 64; d <<= 1) {
         const int up = __shfl_up(incl, d, 64);
         if (lane >= d) incl += up;
     }
     if (lane == 63) wave_total[wave] = incl;
     __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < wave; ++w) base += wave_total[w];
-    // every wave counts its own part of the tile
-    const long tile_begin = (long)mine * tile;
-    const int part = tile / kWaves;
-    const long begin = tile_begin + (long)wave * part;
-    const long end = min((long)src.n, begin + part);
-    for (long i = begin + lane; i < end; i += 64)
-        atomicAdd(&at[wave][(sort_key(src, (int)i) >> shift) & (digits - 1)], 1);
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int d = tid * kPer + j;
-        if (d < digits) {
-            int next = base + before[j];
-            for (int w = 0; w < kWaves; ++w) {
-                const int c = at[w][d];
-                at[w][d] = next;
-                next += c;
-            }
+    if (tid < digits) {
+        int next = incl - total + before;
+        for (int w = 0; w < wave; ++w) next += wave_total[w];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = at[w][tid];
+            at[w][tid] = next;
+            next += c;
         }
-        base += total[j];
     }
     __syncthreads();
+    constexpr int kRounds = 2;
     for (long i0 = begin; i0 < end; i0 += 64 * kRounds) {
         int key[kRounds], pos[kRounds];
 #pragma unroll
@@ -205,7 +360,7 @@ k_sort_place(SortSrc src, int tile, int n_tiles, int shift, int bits, const int3
     }
 }
 
-// ------------------------------------------------------------ sums of the sorted rows
+// ------------------------------------------------------------ gradient: sums of the sorted rows
 
 struct Sorted {
     const int32_t* keys;    // ascending, padding (id `rows`) last
@@ -216,62 +371,24 @@ struct Sorted {
 
 constexpr int kBatch = 8;       // rows of a chunk read at once
 constexpr int kZeroRows = 64;   // table rows of a workgroup that writes the zero rows
+constexpr int kShortChunk = 16;
+constexpr int kEntries = 4096;  // most sorted tokens of a workgroup
+static_assert(kEntries >= kShortChunk * kThreads);  // a chunk is never shorter than the workspace allows for
 
-// Places of the channel tile a lane works on.
-struct Tile {
-    int lane, group, groups, v, nvec;
-    __device__ Tile(int lg, int channels, int kvec) {
-        lane = threadIdx.x & ((1 << lg) - 1);
-        group = threadIdx.x >> lg;
-        groups = kThreads >> lg;
-        nvec = (channels + kvec - 1) / kvec;
-        v = (blockIdx.y << lg) + lane;
-    }
-};
-
-// Row of a partial sum: `nvec` whole vectors of fp32.
+// Row j of partial sums, `nvec` whole vectors of fp32.
 template <class T, class F>
-__device__ __forceinline__ F* partial_row(F* base, long j, const Tile& t) {
+__device__ __forceinline__ F* partial_row(F* base, long j, const Tile<kThreads>& t) {
     return base + (j * t.nvec + t.v) * kVec<T>;
 }
 
-template <class T>
-__device__ __forceinline__ void store_partial(float* p, const Floats<T>& f) {
-#pragma unroll
-    for (int k = 0; k < kVec<T>; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f.v[k], f.v[k + 1], f.v[k + 2], f.v[k + 3]);
-}
-
-template <class T>
-__device__ __forceinline__ void add_partial(const float* p, Floats<T>& f) {
-#pragma unroll
-    for (int k = 0; k < kVec<T>; k += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(p + k);
-        f.v[k] += q.x;
-        f.v[k + 1] += q.y;
-        f.v[k + 2] += q.z;
-        f.v[k + 3] += q.w;
-    }
-}
-
-// Writes kVec<T> finished sums of vector v of a row of O.
-template <class T, class O>
-__device__ __forceinline__ void store_sum(O* row, int v, int n, const Floats<T>& f, float scale) {
-#pragma unroll
-    for (int p = 0; p < kVec<T> / kVec<O>; ++p) {
-        Floats<O> g;
-#pragma unroll
-        for (int k = 0; k < kVec<O>; ++k) g.v[k] = f.v[p * kVec<O> + k] * scale;
-        const int w = v * (kVec<T> / kVec<O>) + p;
-        if (w * kVec<O> < n) store_vec<O>(row, w, n, narrow<O>(g));
-    }
-}
-
-// Workgroups below `chunk_wgs` sum chunks, one a group of lanes; the others write the zero rows of the table.
+// Workgroups below `chunk_wgs` sum chunks, one a group of lanes; the others, if
+// any, write the zero rows of the table.
 template <class T, class O>
 __global__ void __launch_bounds__(kThreads)
 k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int channels, float scale, long grad_stride,
             long table_stride, int lg, long chunk_wgs, float* __restrict__ heads, float* __restrict__ tails) {
-    const Tile tl(lg, channels, kVec<T>);
+    extern __shared__ int32_t sorted_lds[];     // a workgroup's ids with one neighbour on each side, then its places
+    const Tile<kThreads> tl(lg, channels, kVec<T>);
     if (blockIdx.x >= chunk_wgs) {
         // which of 64 table rows have a token: a binary search in the sorted ids, one row a lane
         const long v0 = (blockIdx.x - chunk_wgs) * kZeroRows;
@@ -288,79 +405,92 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
             if (!(present >> k & 1)) store_sum<T, O>(d_table + (v0 + k) * table_stride, tl.v, channels, Floats<T>{}, 0.0f);
         return;
     }
-    const long j = (long)blockIdx.x * tl.groups + tl.group;
-    const long begin = j * s.chunk;
-    if (begin >= s.n || tl.v >= tl.nvec) return;
-    const long end = min((long)s.n, begin + s.chunk);
-    int cur = s.keys[begin];
-    bool head = begin > 0 && s.keys[begin - 1] == cur;      // the run began in an earlier chunk
-    const int next = end < s.n ? s.keys[end] : s.rows;
+    const long wg_begin = (long)blockIdx.x * tl.groups * s.chunk;
+    const int entries = tl.groups * s.chunk;
+    int32_t *skey = sorted_lds, *spos = sorted_lds + entries + 2;
+    for (int k = threadIdx.x; k < entries + 2; k += kThreads) {
+        const long i = wg_begin + k - 1;
+        skey[k] = i < 0 ? -1 : i < s.n ? s.keys[i] : s.rows;
+        if (k < entries && i + 1 < s.n) spos[k] = s.pos[i + 1];
+    }
+    __syncthreads();
+    const long j = (long)blockIdx.x * tl.groups + tl.group;     // the chunk
+    const int at = tl.group * s.chunk;                          // its first entry
+    const int32_t* key = skey + 1 + at;
+    const int32_t* pos = spos + at;
+    int cur = key[0];
+    if (cur == s.rows || tl.v >= tl.nvec) return;
+    bool head = key[-1] == cur;                 // the run began in an earlier chunk
     const Span span = span_of<T>(tl.v, channels);
     Floats<T> acc = {};
-    for (long i0 = begin; i0 < end && cur != s.rows; i0 += kBatch) {
-        int key[kBatch];
-        vec_t<T> x[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) key[q] = i0 + q < end ? s.keys[i0 + q] : s.rows;
+    auto read = [&](vec_t<T> (&x)[kBatch], int k0) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             x[q] = vec_t<T>{};
-            if (key[q] != s.rows) x[q] = read_span<T>(grad + s.pos[i0 + q] * grad_stride, span, channels);
+            if (k0 < s.chunk && key[k0 + q] != s.rows)
+                x[q] = read_span<T>(grad + pos[k0 + q] * grad_stride, span, channels);
         }
+    };
+    vec_t<T> x[kBatch], y[kBatch];
+    read(x, 0);
+    for (int k0 = 0; k0 < s.chunk; k0 += kBatch) {
+        read(y, k0 + kBatch);       // on their way while the rows before them are added
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            if (i0 + q >= end) break;
-            if (key[q] != cur) {
-                if (head) store_partial<T>(partial_row<T>(heads, j, tl), acc);
-                else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
-                cur = key[q];
+            const int now = key[k0 + q];
+            if (now != cur) {
+                if (cur != s.rows) {
+                    if (head) store_floats<T>(partial_row<T>(heads, j, tl), acc);
+                    else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+                }
+                cur = now;
                 head = false;
                 acc = Floats<T>{};
-                if (cur == s.rows) break;
             }
             settle<T>(x[q], span);
-            const Floats<T> f = widen<T>(x[q]);
-#pragma unroll
-            for (int k = 0; k < kVec<T>; ++k) acc.v[k] += f.v[k];
+            add_vec<T>(acc, x[q]);
         }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) x[q] = y[q];
     }
     if (cur == s.rows) return;
-    if (head) store_partial<T>(partial_row<T>(heads, j, tl), acc);
-    else if (next == cur) store_partial<T>(partial_row<T>(tails, j, tl), acc);
+    if (head) store_floats<T>(partial_row<T>(heads, j, tl), acc);
+    else if (key[s.chunk] == cur) store_floats<T>(partial_row<T>(tails, j, tl), acc);
     else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
 }
 
 // One workgroup a chunk: where a run begins in the chunk and leaves it, its
-// sum is the chunk's tail plus the heads of the chunks that the run reaches.
+// sum is the chunk's tail plus the heads of the chunks that the run reaches,
+// which are those that begin with its id.
 template <class T, class O>
 __global__ void __launch_bounds__(kThreads)
-k_embed_join(Sorted s, O* __restrict__ d_table, int channels, float scale, long table_stride, int lg,
-             const float* heads, const float* tails) {
-    __shared__ float part[kThreads * kVec<T>];
-    const Tile tl(lg, channels, kVec<T>);
+k_embed_join(Sorted s, O* __restrict__ d_table, int channels, float scale, long table_stride, int lg, long chunks,
+             const float* __restrict__ heads, const float* __restrict__ tails) {
+    __shared__ __align__(16) float part[kThreads * kVec<T>];
+    const Tile<kThreads> tl(lg, channels, kVec<T>);
     const long j = blockIdx.x, begin = j * s.chunk, end = begin + s.chunk;
     if (end >= s.n) return;
-    const int cur = s.keys[end];
-    if (cur == s.rows || s.keys[end - 1] != cur) return;
-    if (begin > 0 && s.keys[begin - 1] == cur) return;      // it began in an earlier chunk
-    int lo = (int)end, hi = s.n;                            // one past the run's last token
-    while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (s.keys[mid] <= cur) lo = mid + 1;
-        else hi = mid;
+    const int cur = s.keys[end], last_key = s.keys[end - 1], before = begin > 0 ? s.keys[begin - 1] : -1;
+    // no run leaves, or it began in an earlier chunk
+    if (cur == s.rows || last_key != cur || before == cur) return;
+    long last = j;      // the last chunk that the run reaches
+    for (;;) {
+        const long k = last + 1 + (threadIdx.x & 63);
+        const uint64_t reaches = __ballot(k < chunks && s.keys[k * s.chunk] == cur);
+        last += __popcll(reaches);
+        if (reaches != ~0ull) break;
     }
-    const long last = (lo - 1) / s.chunk;
     Floats<T> acc = {};
     if (tl.v < tl.nvec) {
-        if (tl.group == 0) add_partial<T>(partial_row<T>(tails, j, tl), acc);
+        if (tl.group == 0) add_floats<T>(partial_row<T>(tails, j, tl), acc);
 #pragma unroll 4
-        for (long k = j + 1 + tl.group; k <= last; k += tl.groups)
-            add_partial<T>(partial_row<T>(heads, k, tl), acc);
+        for (long k = j + 1 + tl.group; k <= last; k += tl.groups) add_floats<T>(partial_row<T>(heads, k, tl), acc);
     }
-    store_partial<T>(part + threadIdx.x * kVec<T>, acc);
+    store_floats<T>(part + threadIdx.x * kVec<T>, acc);
     __syncthreads();
     if (tl.group != 0 || tl.v >= tl.nvec) return;
-    for (int g = 1; g < tl.groups; ++g) add_partial<T>(part + ((g << lg) + tl.lane) * kVec<T>, acc);
+    const int used = (int)min((long)tl.groups, last - j);
+    for (int g = 1; g < used; ++g) add_floats<T>(part + ((g << lg) + tl.lane) * kVec<T>, acc);
     store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
 }
 
@@ -375,9 +505,14 @@ int log2_up(long x) {
 // Lanes of a row: enough for all of its vectors, up to a workgroup.
 int lanes_log2(int channels, int kvec) { return std::min(8, log2_up((channels + kvec - 1) / kvec)); }
 
+int few_tiles(int channels, int kvec) { return ((channels + kvec - 1) / kvec + (1 << kFewLanes) - 1) >> kFewLanes; }
+
+bool few(long n, long rows, int channels, int kvec) {
+    return n <= kFewTokens && rows * few_tiles(channels, kvec) <= kFewGroups;
+}
+
 struct Plan {
-    int passes, bits, tile, tiles, chunk;
-    long chunks;
+    int passes, bits, tile, tiles;
     long keys, counts, partials, total;    // byte sizes: of one id array, the digit counts, one partial array; all
 };
 
@@ -390,31 +525,83 @@ Plan plan_of(long n, long rows, int channels) {
     p.bits = (bits + p.passes - 1) / p.passes;
     p.tile = kTile * (int)std::max(1L, (n + (long)kTile * kMaxTiles - 1) / ((long)kTile * kMaxTiles));
     p.tiles = (int)((n + p.tile - 1) / p.tile);
-    // chunks of 16 rows keep a few thousand groups busy; longer ones, as n grows, leave fewer partial sums
-    p.chunk = n <= 65536 ? 16 : n <= 262144 ? 32 : 64;
-    p.chunks = (n + p.chunk - 1) / p.chunk;
     p.keys = up256(4 * n);
     p.counts = up256(4L * p.tiles << p.bits);
-    p.partials = up256(p.chunks * ((channels + 7L) / 8 * 8) * 4);
+    p.partials = up256((n + kShortChunk - 1) / kShortChunk * ((channels + 7L) / 8 * 8) * 4);
     p.total = 4 * p.keys + p.counts + 2 * p.partials;
     return p;
 }
 
 template <class T, class O>
-hipError_t sum_and_join(const EmbedArgs& a, const Plan& p, const int32_t* keys, const int32_t* pos, float* heads,
-                        float* tails, hipStream_t st) {
-    const Sorted s{keys, pos, (int)a.n_tokens, (int)a.n_rows, p.chunk};
+hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* pos, float* heads, float* tails,
+                        bool zeroed, hipStream_t st) {
     const int lg = lanes_log2(a.channels, kVec<T>), groups = kThreads >> lg;
+    // chunks of 16 rows keep thousands of groups busy; longer ones, as n grows, leave fewer partial sums
+    int chunk = a.n_tokens <= 65536 ? kShortChunk : a.n_tokens <= 262144 ? 2 * kShortChunk : 4 * kShortChunk;
+    chunk = std::min(chunk, kEntries / groups);
+    const Sorted s{keys, pos, (int)a.n_tokens, (int)a.n_rows, chunk};
     const int nvec = (a.channels + kVec<T> - 1) / kVec<T>;
     const unsigned tiles = (unsigned)((nvec + (1 << lg) - 1) >> lg);
-    const long chunk_wgs = (p.chunks + groups - 1) / groups, zero_wgs = (a.n_rows + kZeroRows - 1) / kZeroRows;
-    k_embed_sum<T, O><<<dim3((unsigned)(chunk_wgs + zero_wgs), tiles), kThreads, 0, st>>>(
-        s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride, lg,
-        chunk_wgs, heads, tails);
-    if (p.chunks > 1)
-        k_embed_join<T, O><<<dim3((unsigned)p.chunks, tiles), kThreads, 0, st>>>(
-            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, heads, tails);
+    const long chunks = (a.n_tokens + chunk - 1) / chunk;
+    const long chunk_wgs = (chunks + groups - 1) / groups, zero_wgs = zeroed ? 0 : (a.n_rows + kZeroRows - 1) / kZeroRows;
+    if (chunk_wgs + zero_wgs > 0)
+        k_embed_sum<T, O><<<dim3((unsigned)(chunk_wgs + zero_wgs), tiles), kThreads, (2 * groups * chunk + 2) * sizeof(int32_t), st>>>(
+            s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride,
+            lg, chunk_wgs, heads, tails);
+    if (chunks > 1)
+        k_embed_join<T, O><<<dim3((unsigned)chunks, tiles), kThreads, 0, st>>>(
+            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, heads, tails);
     return hipGetLastError();
+}
+
+template <class T, class O>
+hipError_t embed_bwd(const EmbedArgs& a, hipStream_t st) {
+    if (few(a.n_tokens, a.n_rows, a.channels, kVec<T>)) {
+        k_embed_few<T, O><<<dim3((unsigned)a.n_rows, few_tiles(a.channels, kVec<T>)), kFewThreads, 0, st>>>(
+            static_cast<const T*>(a.src), a.tokens, static_cast<O*>(a.dst), (int)a.n_tokens, (int)a.n_rows, a.channels,
+            a.wide_index, a.scale, a.src_stride, a.dst_stride);
+        return hipGetLastError();
+    }
+    const Plan p = plan_of(a.n_tokens, a.n_rows, a.channels);
+    char* ws = static_cast<char*>(a.workspace);
+    int32_t* ids[2] = {reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + p.keys)};
+    int32_t* pos[2] = {reinterpret_cast<int32_t*>(ws + 2 * p.keys), reinterpret_cast<int32_t*>(ws + 3 * p.keys)};
+    int32_t* counts = reinterpret_cast<int32_t*>(ws + 4 * p.keys);
+    float* heads = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts);
+    float* tails = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts + p.partials);
+    // Where tokens reach a quarter of the table at most, all of it is set to
+    // zero beside the sort, which hides the sort; else the rows without a
+    // token are looked up and written beside the sums.
+    const bool zeroed = a.n_tokens > 0 && a.n_rows >= 4 * a.n_tokens;
+    const int launches = p.passes * (p.tiles > 1 ? 2 : 1);
+    int launch = 0;
+    auto zeros = [&]() {
+        Zeros z{};
+        z.first = p.tiles;
+        if (!zeroed) return z;
+        z.base = static_cast<char*>(a.dst);
+        z.row_bytes = (long)a.channels * sizeof(O);
+        z.stride_bytes = a.dst_stride * (long)sizeof(O);
+        z.begin = a.n_rows * launch / launches;
+        z.end = a.n_rows * (launch + 1) / launches;
+        // some 64 KB a workgroup
+        z.groups = (int)std::max(1L, std::min(16384L, (z.end - z.begin) * z.row_bytes / 65536));
+        ++launch;
+        return z;
+    };
+    int to = 0;
+    for (int k = 0; k < p.passes && a.n_tokens > 0; ++k, to ^= 1) {
+        SortSrc src{a.tokens, k ? ids[to ^ 1] : nullptr, k ? pos[to ^ 1] : nullptr, a.wide_index, (int)a.n_tokens,
+                    (int)a.n_rows};
+        if (p.tiles > 1) {
+            const Zeros z = zeros();
+            k_sort_count<<<p.tiles + z.groups, kSortThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts, z);
+        }
+        const Zeros z = zeros();
+        k_sort_place<<<p.tiles + z.groups, kSortThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts,
+                                                                 ids[to], pos[to], z);
+    }
+    return sum_and_join<T, O>(a, ids[to ^ 1], pos[to ^ 1], heads, tails, zeroed, st);
 }
 
 }  // namespace
@@ -444,26 +631,9 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, hipStream_t st) {
 
 hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
     if (a.n_rows == 0) return hipSuccess;
-    const Plan p = plan_of(a.n_tokens, a.n_rows, a.channels);
-    char* ws = static_cast<char*>(a.workspace);
-    int32_t* ids[2] = {reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + p.keys)};
-    int32_t* pos[2] = {reinterpret_cast<int32_t*>(ws + 2 * p.keys), reinterpret_cast<int32_t*>(ws + 3 * p.keys)};
-    int32_t* counts = reinterpret_cast<int32_t*>(ws + 4 * p.keys);
-    float* heads = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts);
-    float* tails = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts + p.partials);
-    int to = 0;
-    for (int k = 0; k < p.passes && a.n_tokens > 0; ++k, to ^= 1) {
-        SortSrc src{a.tokens, k ? ids[to ^ 1] : nullptr, k ? pos[to ^ 1] : nullptr, a.wide_index, (int)a.n_tokens,
-                    (int)a.n_rows};
-        k_sort_count<<<p.tiles, kThreads, 0, st>>>(src, p.tile, k * p.bits, p.bits, counts);
-        k_sort_place<<<p.tiles, kThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts, ids[to], pos[to]);
-    }
-    const int32_t* keys_sorted = ids[to ^ 1];
-    const int32_t* pos_sorted = pos[to ^ 1];
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
-        if (a.out_dtype == a.dtype) return sum_and_join<T, T>(a, p, keys_sorted, pos_sorted, heads, tails, st);
-        return sum_and_join<T, float>(a, p, keys_sorted, pos_sorted, heads, tails, st);
+        return a.out_dtype == a.dtype ? embed_bwd<T, T>(a, st) : embed_bwd<T, float>(a, st);
     });
 }
 
