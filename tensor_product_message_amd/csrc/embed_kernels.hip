@@ -127,6 +127,21 @@ __device__ __forceinline__ void store_sum(O* row, int v, int n, const Floats<T>&
     }
 }
 
+// Zeros in the same places, non-temporal: a large table's zero rows would push
+// the gradients out of the last-level cache (a bf16 table of 131072 x 2048
+// with 16384 tokens: sums, zeros and joins in 118 us, 124 without the mark).
+template <class T, class O>
+__device__ __forceinline__ void store_zeros(O* row, int v, int n) {
+#pragma unroll
+    for (int p = 0; p < kVec<T> / kVec<O>; ++p) {
+        const int w = v * (kVec<T> / kVec<O>) + p, left = n - w * kVec<O>;
+        if (left >= kVec<O>)
+            __builtin_nontemporal_store(vec_t<O>{}, reinterpret_cast<typename Vec<O>::unaligned*>(row + w * kVec<O>));
+        else if (left > 0)
+            store_left<O>(row + w * kVec<O>, left, vec_t<O>{});
+    }
+}
+
 // ------------------------------------------------------------ gradient: few tokens, small table
 
 // One workgroup a table row and tile of channels goes through all tokens,
@@ -218,35 +233,6 @@ constexpr int kMaxTiles = 64;
 constexpr int kTile = 2048;     // tokens of a tile, or a multiple
 static_assert(kDigits <= kSortThreads);
 
-// The sort's kernels are short and few workgroups wide, so a share of the
-// table's zeros can be written beside them: workgroups from `first` on fill
-// rows [begin, end) of `row_bytes` each.
-struct Zeros {
-    char* base;
-    long begin, end, row_bytes, stride_bytes;
-    int first, groups;
-};
-
-__device__ __forceinline__ void fill_zeros(const Zeros& z) {
-    typedef uint32_t quad __attribute__((ext_vector_type(4), aligned(2)));
-    const long units = z.row_bytes / 16, rest = z.row_bytes - units * 16;
-    const long rows = z.end - z.begin, per = (rows + z.groups - 1) / z.groups;
-    const long r0 = z.begin + (blockIdx.x - z.first) * per, r1 = min(z.end, r0 + per);
-    if (r0 >= r1) return;
-    if (rest == 0 && z.stride_bytes == z.row_bytes) {
-        char* to = z.base + r0 * z.stride_bytes;
-        const long n = (r1 - r0) * units;
-        for (long u = threadIdx.x; u < n; u += kSortThreads) *reinterpret_cast<quad*>(to + u * 16) = quad{};
-        return;
-    }
-    // a wave a row
-    for (long r = r0 + threadIdx.x / 64; r < r1; r += kSortWaves) {
-        char* to = z.base + r * z.stride_bytes;
-        for (long u = threadIdx.x % 64; u < units; u += 64) *reinterpret_cast<quad*>(to + u * 16) = quad{};
-        for (long u = threadIdx.x % 64; u < rest / 2; u += 64) reinterpret_cast<uint16_t*>(to + units * 16)[u] = 0;
-    }
-}
-
 struct SortSrc {
     const void* tokens;     // first pass: the tokens themselves
     const int32_t* keys;    // later passes: ids and positions as the pass before left them
@@ -261,9 +247,8 @@ __device__ __forceinline__ int sort_key(const SortSrc& s, int i) {
 }
 
 __global__ void __launch_bounds__(kSortThreads)
-k_sort_count(SortSrc src, int tile, int n_tiles, int shift, int bits, int32_t* __restrict__ counts, Zeros zeros) {
+k_sort_count(SortSrc src, int tile, int shift, int bits, int32_t* __restrict__ counts) {
     __shared__ int32_t cnt[kDigits];
-    if (blockIdx.x >= n_tiles) return fill_zeros(zeros);
     const int digits = 1 << bits;
     if (threadIdx.x < digits) cnt[threadIdx.x] = 0;
     __syncthreads();
@@ -287,31 +272,56 @@ __device__ __forceinline__ uint64_t same_digit(int digit, int bits, uint64_t act
 
 __global__ void __launch_bounds__(kSortThreads)
 k_sort_place(SortSrc src, int tile, int n_tiles, int shift, int bits, const int32_t* __restrict__ counts,
-             int32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out, Zeros zeros) {
+             int32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out) {
     __shared__ int32_t at[kSortWaves][kDigits];     // first counts, then the next free place of every wave and digit
     __shared__ int32_t wave_total[kSortWaves];
-    if (blockIdx.x >= n_tiles) return fill_zeros(zeros);
     const int digits = 1 << bits, mine = blockIdx.x;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    int before = 0, total = 0;
-    if (n_tiles > 1 && tid < digits) {
-#pragma unroll 16
-        for (int t = 0; t < n_tiles; ++t) {
-            const int c = counts[(long)t * digits + tid];
-            total += c;
-            before += t < mine ? c : 0;
-        }
-    }
-    for (int d = lane; d < digits; d += 64) at[wave][d] = 0;
-    // every wave counts its own part of the tile
+    // the first 128 tokens of every wave's part of the tile, all of them in a short tile, stay in registers
+    constexpr int kRounds = kTile / kSortThreads;
     const int part = tile / kSortWaves;
     const long begin = (long)mine * tile + (long)wave * part;
     const long end = min((long)src.n, begin + part);
-    for (long i = begin + lane; i < end; i += 64)
+    int key[kRounds], pos[kRounds];
+    auto read = [&](long i0) {
+#pragma unroll
+        for (int q = 0; q < kRounds; ++q) {
+            const long i = i0 + q * 64 + lane;
+            key[q] = i < end ? sort_key(src, (int)i) : 0;
+            pos[q] = i < end ? (src.pos ? src.pos[i] : (int)i) : 0;
+        }
+    };
+    read(begin);
+    int before = 0, total = 0;
+    if (n_tiles > 1 && tid < digits) {
+        constexpr int kAhead = 32;      // counts read at once
+        for (int t0 = 0; t0 < n_tiles; t0 += kAhead) {
+            int c[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) c[k] = t0 + k < n_tiles ? counts[(long)(t0 + k) * digits + tid] : 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                total += c[k];
+                before += t0 + k < mine ? c[k] : 0;
+            }
+        }
+    }
+    for (int d = lane; d < digits; d += 64) at[wave][d] = 0;
+    // every wave counts its own part
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q)
+        if (begin + q * 64 + lane < end) atomicAdd(&at[wave][(key[q] >> shift) & (digits - 1)], 1);
+    for (long i = begin + 64 * kRounds + lane; i < end; i += 64)
         atomicAdd(&at[wave][(sort_key(src, (int)i) >> shift) & (digits - 1)], 1);
     __syncthreads();
-    if (n_tiles == 1 && tid < digits)
-        for (int w = 0; w < kSortWaves; ++w) total += at[w][tid];
+    int of_wave[kSortWaves] = {};
+    if (tid < digits) {
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) of_wave[w] = at[w][tid];
+        if (n_tiles == 1)
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) total += of_wave[w];
+    }
     // exclusive sum of the totals over all digits
     int incl = total;
     for (int d = 1; d < 64; d <<= 1) {
@@ -322,23 +332,17 @@ k_sort_place(SortSrc src, int tile, int n_tiles, int shift, int bits, const int3
     __syncthreads();
     if (tid < digits) {
         int next = incl - total + before;
-        for (int w = 0; w < wave; ++w) next += wave_total[w];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) next += w < wave ? wave_total[w] : 0;
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = at[w][tid];
             at[w][tid] = next;
-            next += c;
+            next += of_wave[w];
         }
     }
     __syncthreads();
-    constexpr int kRounds = 2;
     for (long i0 = begin; i0 < end; i0 += 64 * kRounds) {
-        int key[kRounds], pos[kRounds];
-#pragma unroll
-        for (int q = 0; q < kRounds; ++q) {
-            const long i = i0 + q * 64 + lane;
-            key[q] = i < end ? sort_key(src, (int)i) : 0;
-            pos[q] = i < end ? (src.pos ? src.pos[i] : (int)i) : 0;
-        }
+        if (i0 != begin) read(i0);
 #pragma unroll
         for (int q = 0; q < kRounds; ++q) {
             const bool on = i0 + q * 64 + lane < end;
@@ -370,14 +374,14 @@ struct Sorted {
 };
 
 constexpr int kBatch = 8;       // rows of a chunk read at once
-constexpr int kZeroRows = 64;   // table rows of a workgroup that writes the zero rows
+constexpr int kZeroRows = 32;   // table rows of a workgroup that writes the zero rows
 constexpr int kShortChunk = 16;
 constexpr int kEntries = 4096;  // most sorted tokens of a workgroup
 static_assert(kEntries >= kShortChunk * kThreads);  // a chunk is never shorter than the workspace allows for
 
 // Row j of partial sums, `nvec` whole vectors of fp32.
-template <class T, class F>
-__device__ __forceinline__ F* partial_row(F* base, long j, const Tile<kThreads>& t) {
+template <class T, class F, int Threads>
+__device__ __forceinline__ F* partial_row(F* base, long j, const Tile<Threads>& t) {
     return base + (j * t.nvec + t.v) * kVec<T>;
 }
 
@@ -390,9 +394,9 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
     extern __shared__ int32_t sorted_lds[];     // a workgroup's ids with one neighbour on each side, then its places
     const Tile<kThreads> tl(lg, channels, kVec<T>);
     if (blockIdx.x >= chunk_wgs) {
-        // which of 64 table rows have a token: a binary search in the sorted ids, one row a lane
+        // which of 32 table rows have a token: a binary search in the sorted ids, one row a lane
         const long v0 = (blockIdx.x - chunk_wgs) * kZeroRows;
-        const int row = (int)min(v0 + (threadIdx.x & 63), (long)s.rows - 1);
+        const int row = (int)min(v0 + (threadIdx.x & (kZeroRows - 1)), (long)s.rows - 1);
         int lo = 0, hi = s.n;
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
@@ -402,7 +406,7 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
         const uint64_t present = __ballot(lo < s.n && s.keys[lo] == row);
         if (tl.v >= tl.nvec) return;
         for (int k = tl.group; k < kZeroRows && v0 + k < s.rows; k += tl.groups)
-            if (!(present >> k & 1)) store_sum<T, O>(d_table + (v0 + k) * table_stride, tl.v, channels, Floats<T>{}, 0.0f);
+            if (!(present >> k & 1)) store_zeros<T, O>(d_table + (v0 + k) * table_stride, tl.v, channels);
         return;
     }
     const long wg_begin = (long)blockIdx.x * tl.groups * s.chunk;
@@ -459,39 +463,55 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
     else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
 }
 
-// One workgroup a chunk: where a run begins in the chunk and leaves it, its
-// sum is the chunk's tail plus the heads of the chunks that the run reaches,
-// which are those that begin with its id.
+// Where a run begins in a chunk and leaves it, its sum is the chunk's tail plus
+// the heads of the chunks that the run reaches, which are those that begin with
+// its id.  A workgroup looks through as many chunks as it has groups of lanes
+// (most have no such run) and adds the partial rows of each run it finds with
+// all groups at once: the hottest run decides how long the kernel takes.
+constexpr int kJoinThreads = 1024;
+
 template <class T, class O>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 k_embed_join(Sorted s, O* __restrict__ d_table, int channels, float scale, long table_stride, int lg, long chunks,
-             const float* __restrict__ heads, const float* __restrict__ tails) {
-    __shared__ __align__(16) float part[kThreads * kVec<T>];
-    const Tile<kThreads> tl(lg, channels, kVec<T>);
-    const long j = blockIdx.x, begin = j * s.chunk, end = begin + s.chunk;
-    if (end >= s.n) return;
-    const int cur = s.keys[end], last_key = s.keys[end - 1], before = begin > 0 ? s.keys[begin - 1] : -1;
-    // no run leaves, or it began in an earlier chunk
-    if (cur == s.rows || last_key != cur || before == cur) return;
-    long last = j;      // the last chunk that the run reaches
-    for (;;) {
-        const long k = last + 1 + (threadIdx.x & 63);
-        const uint64_t reaches = __ballot(k < chunks && s.keys[k * s.chunk] == cur);
-        last += __popcll(reaches);
-        if (reaches != ~0ull) break;
+             int at_once, const float* __restrict__ heads, const float* __restrict__ tails) {
+    __shared__ __align__(16) float part[kJoinThreads * kVec<T>];
+    const Tile<kJoinThreads> tl(lg, channels, kVec<T>);
+    // every wave looks at all of the workgroup's chunks, one a lane
+    const int lane = threadIdx.x & 63;
+    const long mine = (long)blockIdx.x * at_once + lane, end = (mine + 1) * s.chunk;
+    int id = s.rows;
+    if (lane < at_once && end < s.n) {
+        const int first = mine > 0 ? s.keys[mine * s.chunk - 1] : -1, last = s.keys[end - 1];
+        id = s.keys[end];
+        if (last != id || first == id) id = s.rows;     // no run leaves, or it began in an earlier chunk
     }
-    Floats<T> acc = {};
-    if (tl.v < tl.nvec) {
-        if (tl.group == 0) add_floats<T>(partial_row<T>(tails, j, tl), acc);
+    for (uint64_t found = __ballot(id != s.rows); found; found &= found - 1) {
+        const int which = __builtin_ctzll(found);
+        const long j = (long)blockIdx.x * at_once + which;
+        const int cur = __builtin_amdgcn_readlane(id, which);
+        // the last chunk that the run reaches, before `beyond`: a search by 64 probes at a time
+        long last = j;
+        for (long beyond = chunks; beyond - last > 1;) {
+            const long step = (beyond - last + 63) / 64, k = last + (lane + 1) * step;
+            last += step * __popcll(__ballot(k < beyond && s.keys[k * s.chunk] == cur));
+            beyond = min(beyond, last + step);
+        }
+        Floats<T> acc = {};
+        if (tl.v < tl.nvec) {
+            if (tl.group == 0) add_floats<T>(partial_row<T>(tails, j, tl), acc);
 #pragma unroll 4
-        for (long k = j + 1 + tl.group; k <= last; k += tl.groups) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+            for (long k = j + 1 + tl.group; k <= last; k += tl.groups) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+        }
+        const int used = (int)min((long)tl.groups, last - j);
+        if (used > 1) {
+            if (tl.group < used) store_floats<T>(part + threadIdx.x * kVec<T>, acc);
+            __syncthreads();
+            if (tl.group == 0)
+                for (int g = 1; g < used; ++g) add_floats<T>(part + ((g << lg) + tl.lane) * kVec<T>, acc);
+            __syncthreads();
+        }
+        if (tl.group == 0 && tl.v < tl.nvec) store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
     }
-    store_floats<T>(part + threadIdx.x * kVec<T>, acc);
-    __syncthreads();
-    if (tl.group != 0 || tl.v >= tl.nvec) return;
-    const int used = (int)min((long)tl.groups, last - j);
-    for (int g = 1; g < used; ++g) add_floats<T>(part + ((g << lg) + tl.lane) * kVec<T>, acc);
-    store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
 }
 
 // ------------------------------------------------------------ plans
@@ -534,7 +554,7 @@ Plan plan_of(long n, long rows, int channels) {
 
 template <class T, class O>
 hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* pos, float* heads, float* tails,
-                        bool zeroed, hipStream_t st) {
+                        hipStream_t st) {
     const int lg = lanes_log2(a.channels, kVec<T>), groups = kThreads >> lg;
     // chunks of 16 rows keep thousands of groups busy; longer ones, as n grows, leave fewer partial sums
     int chunk = a.n_tokens <= 65536 ? kShortChunk : a.n_tokens <= 262144 ? 2 * kShortChunk : 4 * kShortChunk;
@@ -543,14 +563,16 @@ hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* 
     const int nvec = (a.channels + kVec<T> - 1) / kVec<T>;
     const unsigned tiles = (unsigned)((nvec + (1 << lg) - 1) >> lg);
     const long chunks = (a.n_tokens + chunk - 1) / chunk;
-    const long chunk_wgs = (chunks + groups - 1) / groups, zero_wgs = zeroed ? 0 : (a.n_rows + kZeroRows - 1) / kZeroRows;
+    const long chunk_wgs = (chunks + groups - 1) / groups, zero_wgs = (a.n_rows + kZeroRows - 1) / kZeroRows;
     if (chunk_wgs + zero_wgs > 0)
         k_embed_sum<T, O><<<dim3((unsigned)(chunk_wgs + zero_wgs), tiles), kThreads, (2 * groups * chunk + 2) * sizeof(int32_t), st>>>(
             s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride,
             lg, chunk_wgs, heads, tails);
-    if (chunks > 1)
-        k_embed_join<T, O><<<dim3((unsigned)chunks, tiles), kThreads, 0, st>>>(
-            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, heads, tails);
+    if (chunks > 1) {
+        const int at_once = std::min(64, kJoinThreads >> lg);
+        k_embed_join<T, O><<<dim3((unsigned)((chunks + at_once - 1) / at_once), tiles), kJoinThreads, 0, st>>>(
+            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, at_once, heads, tails);
+    }
     return hipGetLastError();
 }
 
@@ -569,39 +591,14 @@ hipError_t embed_bwd(const EmbedArgs& a, hipStream_t st) {
     int32_t* counts = reinterpret_cast<int32_t*>(ws + 4 * p.keys);
     float* heads = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts);
     float* tails = reinterpret_cast<float*>(ws + 4 * p.keys + p.counts + p.partials);
-    // Where tokens reach a quarter of the table at most, all of it is set to
-    // zero beside the sort, which hides the sort; else the rows without a
-    // token are looked up and written beside the sums.
-    const bool zeroed = a.n_tokens > 0 && a.n_rows >= 4 * a.n_tokens;
-    const int launches = p.passes * (p.tiles > 1 ? 2 : 1);
-    int launch = 0;
-    auto zeros = [&]() {
-        Zeros z{};
-        z.first = p.tiles;
-        if (!zeroed) return z;
-        z.base = static_cast<char*>(a.dst);
-        z.row_bytes = (long)a.channels * sizeof(O);
-        z.stride_bytes = a.dst_stride * (long)sizeof(O);
-        z.begin = a.n_rows * launch / launches;
-        z.end = a.n_rows * (launch + 1) / launches;
-        // some 64 KB a workgroup
-        z.groups = (int)std::max(1L, std::min(16384L, (z.end - z.begin) * z.row_bytes / 65536));
-        ++launch;
-        return z;
-    };
     int to = 0;
     for (int k = 0; k < p.passes && a.n_tokens > 0; ++k, to ^= 1) {
         SortSrc src{a.tokens, k ? ids[to ^ 1] : nullptr, k ? pos[to ^ 1] : nullptr, a.wide_index, (int)a.n_tokens,
                     (int)a.n_rows};
-        if (p.tiles > 1) {
-            const Zeros z = zeros();
-            k_sort_count<<<p.tiles + z.groups, kSortThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts, z);
-        }
-        const Zeros z = zeros();
-        k_sort_place<<<p.tiles + z.groups, kSortThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts,
-                                                                 ids[to], pos[to], z);
+        if (p.tiles > 1) k_sort_count<<<p.tiles, kSortThreads, 0, st>>>(src, p.tile, k * p.bits, p.bits, counts);
+        k_sort_place<<<p.tiles, kSortThreads, 0, st>>>(src, p.tile, p.tiles, k * p.bits, p.bits, counts, ids[to], pos[to]);
     }
-    return sum_and_join<T, O>(a, ids[to ^ 1], pos[to ^ 1], heads, tails, zeroed, st);
+    return sum_and_join<T, O>(a, ids[to ^ 1], pos[to ^ 1], heads, tails, st);
 }
 
 }  // namespace
