@@ -129,7 +129,7 @@ def train_lib() -> ctypes.CDLL:
     L = lib()
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     i64p = ctypes.POINTER(i64)
-    ep, np_ = ctypes.POINTER(EmbedProblem), ctypes.POINTER(NormProblem)
+    ep = np_ = vp       # problem structs by address: EmbedProblem, NormProblem or their packed bytes
     sig = {
         "conv_tp_embed_fwd": ([ep, vp, vp, vp, vp], i32),
         "conv_tp_embed_bwd": ([ep, vp, vp, vp, vp, i64, vp], i32),

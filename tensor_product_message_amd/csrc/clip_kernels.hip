@@ -26,62 +26,112 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerLaunch = 128;
-constexpr long kChunk = 16384;      // elements a workgroup takes at a time
-constexpr int kMaxGroups = 2048;    // workgroups, and partial sums, of a launch
+constexpr long kChunk = 2048;       // elements; a workgroup takes a run of chunks
+constexpr int kMaxGroups = 1024;    // workgroups, and partial sums, of a launch: four a CU (eight are no faster)
+constexpr int kAhead = 4;           // vectors that a lane has on their way
 
 struct Batch {
     const void* in[kPerLaunch];
     void* out[kPerLaunch];
     int64_t numel[kPerLaunch];
-    int32_t first[kPerLaunch + 1];  // first chunk of each tensor
+    int32_t first[kPerLaunch + 1];  // first chunk of each tensor, and the number of chunks
     uint8_t dtype[kPerLaunch];
     int n;
 };
 
-// Tensor of a chunk: the last one whose first chunk is not beyond it.
-__device__ __forceinline__ int tensor_of(const Batch& b, int chunk) {
-    int lo = 0, hi = b.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (b.first[mid] <= chunk) lo = mid;
+// Calls f(tensor, begin, end) for the elements that a workgroup has of each
+// tensor: the chunks of all tensors, in a row, are cut into equal runs.
+// Backwards: in the opposite order.
+template <bool Backwards, class F>
+__device__ __forceinline__ void each_span(const Batch& b, F&& f) {
+    const long chunks = b.first[b.n];
+    const int from = (int)(chunks * blockIdx.x / gridDim.x), to = (int)(chunks * (blockIdx.x + 1) / gridDim.x);
+    // the last tensor whose first chunk is not beyond the run's first (backwards: last) chunk
+    const int chunk = Backwards ? to - 1 : from;
+    int t = 0;
+    for (int hi = b.n - 1; t < hi;) {
+        const int mid = (t + hi + 1) / 2;
+        if (b.first[mid] <= chunk) t = mid;
         else hi = mid - 1;
     }
-    return lo;
+    while (t >= 0 && t < b.n && b.first[t] < to && b.first[t + 1] >= from) {
+        const long lo = max(from, b.first[t]) - b.first[t], hi = min(to, b.first[t + 1]) - b.first[t];
+        if (hi > lo) f(t, lo * kChunk, min(hi * kChunk, (long)b.numel[t]));
+        t += Backwards ? -1 : 1;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ double square(T x) {
+    const double d = (double)(float)x;
+    return d * d;
 }
 
 template <class T>
 __device__ __forceinline__ double squares(const T* x, long n) {
     double s = 0.0;
     const long whole = n / kVec<T>;
-#pragma unroll 4
-    for (long v = threadIdx.x; v < whole; v += kThreads) {
-        const vec_t<T> q = *reinterpret_cast<const typename Vec<T>::unaligned*>(x + v * kVec<T>);
+    auto* xv = reinterpret_cast<const typename Vec<T>::unaligned*>(x);
+    long v = threadIdx.x;
+    for (; v + (kAhead - 1) * kThreads < whole; v += kAhead * kThreads) {
+        vec_t<T> q[kAhead];
 #pragma unroll
-        for (int k = 0; k < kVec<T>; ++k) {
-            const double d = (double)(float)q[k];
-            s = __builtin_fma(d, d, s);
-        }
+        for (int u = 0; u < kAhead; ++u) q[u] = xv[v + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                const double d = (double)(float)q[u][k];
+                s = __builtin_fma(d, d, s);
+            }
+    }
+    for (; v < whole; v += kThreads) {
+        const vec_t<T> q = xv[v];
+#pragma unroll
+        for (int k = 0; k < kVec<T>; ++k) s += square(q[k]);
     }
     const long at = whole * kVec<T> + threadIdx.x;
-    if (at < n) {
-        const double d = (double)(float)x[at];
-        s = __builtin_fma(d, d, s);
-    }
+    if (at < n) s += square(x[at]);
     return s;
 }
 
-template <class T>
+// y = factor x, from the end to the beginning.
+template <class T, bool Stream>
 __device__ __forceinline__ void scaled(const T* x, T* y, long n, float factor) {
     const long whole = n / kVec<T>;
-#pragma unroll 4
-    for (long v = threadIdx.x; v < whole; v += kThreads) {
-        Floats<T> f = widen<T>(*reinterpret_cast<const typename Vec<T>::unaligned*>(x + v * kVec<T>));
-#pragma unroll
-        for (int k = 0; k < kVec<T>; ++k) f.v[k] *= factor;
-        *reinterpret_cast<typename Vec<T>::unaligned*>(y + v * kVec<T>) = narrow<T>(f);
-    }
     const long at = whole * kVec<T> + threadIdx.x;
     if (at < n) y[at] = (T)((float)x[at] * factor);
+    auto* xv = reinterpret_cast<const typename Vec<T>::unaligned*>(x);
+    auto* yv = reinterpret_cast<typename Vec<T>::unaligned*>(y);
+    auto put = [&](long v, const vec_t<T>& q) {
+        Floats<T> f = widen<T>(q);
+#pragma unroll
+        for (int k = 0; k < kVec<T>; ++k) f.v[k] *= factor;
+        if (Stream) __builtin_nontemporal_store(narrow<T>(f), yv + v);
+        else yv[v] = narrow<T>(f);
+    };
+    long v = whole - 1 - threadIdx.x;
+    for (; v - (kAhead - 1) * kThreads >= 0; v -= kAhead * kThreads) {
+        vec_t<T> q[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            q[u] = Stream ? __builtin_nontemporal_load(xv + (v - u * kThreads)) : xv[v - u * kThreads];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) put(v - u * kThreads, q[u]);
+    }
+    for (; v >= 0; v -= kThreads) {
+        const vec_t<T> q = xv[v];
+        put(v, q);
+    }
+}
+
+// Calls f with a value of the type of a code.
+template <class F>
+__device__ __forceinline__ void typed(int dtype, F&& f) {
+    if (dtype == kBF16) f(__bf16{});
+    else if (dtype == kF16) f(_Float16{});
+    else f(float{});
 }
 
 // Sum over the workgroup in a fixed order, in every thread.
@@ -94,16 +144,15 @@ __device__ __forceinline__ double group_sum(double x, double* part) {
     return s;
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_squares(Batch b, int chunks, double* __restrict__ partial) {
+__global__ void __launch_bounds__(kThreads) k_clip_squares(Batch b, double* __restrict__ partial) {
     __shared__ double part[kThreads / 64];
     double s = 0.0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int t = tensor_of(b, c);
-        const long at = (long)(c - b.first[t]) * kChunk, n = min(kChunk, (long)b.numel[t] - at);
-        if (b.dtype[t] == kBF16) s += squares(static_cast<const __bf16*>(b.in[t]) + at, n);
-        else if (b.dtype[t] == kF16) s += squares(static_cast<const _Float16*>(b.in[t]) + at, n);
-        else s += squares(static_cast<const float*>(b.in[t]) + at, n);
-    }
+    each_span<false>(b, [&](int t, long begin, long end) {
+        typed(b.dtype[t], [&](auto x) {
+            using T = decltype(x);
+            s += squares(static_cast<const T*>(b.in[t]) + begin, end - begin);
+        });
+    });
     s = group_sum(s, part);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
@@ -121,22 +170,25 @@ __global__ void __launch_bounds__(kThreads) k_clip_norm(const double* __restrict
     if (threadIdx.x == 0) *norm = x;
 }
 
+// Goes through its run backwards: what the last-level cache holds of the
+// gradients is what the first kernel read last.  Stream: where the gradients
+// do not fit there, what is written stays out of it.
+template <bool Stream>
 __global__ void __launch_bounds__(kThreads)
-k_clip_scale(Batch b, int chunks, const double* __restrict__ partial, int n_partial, float max_norm, float eps, float* norm) {
+k_clip_scale(Batch b, const double* __restrict__ partial, int n_partial, float max_norm, float eps, float* norm) {
     __shared__ double part[kThreads / 64];
     const float x = total_norm(partial, n_partial, part);
     if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = x;
     float factor = max_norm / (x + eps);
     if (factor > 1.0f) factor = 1.0f;       // a NaN norm stays NaN
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int t = tensor_of(b, c);
+    each_span<true>(b, [&](int t, long begin, long end) {
         // in place with nothing to clip: the values stay as they are
-        if (factor == 1.0f && b.in[t] == b.out[t]) continue;
-        const long at = (long)(c - b.first[t]) * kChunk, n = min(kChunk, (long)b.numel[t] - at);
-        if (b.dtype[t] == kBF16) scaled(static_cast<const __bf16*>(b.in[t]) + at, static_cast<__bf16*>(b.out[t]) + at, n, factor);
-        else if (b.dtype[t] == kF16) scaled(static_cast<const _Float16*>(b.in[t]) + at, static_cast<_Float16*>(b.out[t]) + at, n, factor);
-        else scaled(static_cast<const float*>(b.in[t]) + at, static_cast<float*>(b.out[t]) + at, n, factor);
-    }
+        if (factor == 1.0f && b.in[t] == b.out[t]) return;
+        typed(b.dtype[t], [&](auto q) {
+            using T = decltype(q);
+            scaled<T, Stream>(static_cast<const T*>(b.in[t]) + begin, static_cast<T*>(b.out[t]) + begin, end - begin, factor);
+        });
+    });
 }
 
 long chunks_of(long numel) { return (numel + kChunk - 1) / kChunk; }
@@ -151,8 +203,8 @@ long clip_workspace(int n_tensors) {
 hipError_t launch_clip(const ClipArgs& a, hipStream_t st) {
     Batch b;
     int n_partial = 0;
+    long bytes = 0;
     auto batches = [&](auto&& go) {
-        bool first = true;
         for (int t0 = 0; t0 < a.n_tensors; t0 += kPerLaunch) {
             b.n = std::min(kPerLaunch, a.n_tensors - t0);
             int32_t chunks = 0;
@@ -165,22 +217,23 @@ hipError_t launch_clip(const ClipArgs& a, hipStream_t st) {
                 chunks += (int32_t)chunks_of(b.numel[k]);
             }
             b.first[b.n] = chunks;
-            if (chunks == 0) continue;
-            go(chunks, std::min(chunks, (int32_t)kMaxGroups), first);
-            first = false;
+            if (chunks > 0) go(std::min(chunks, (int32_t)kMaxGroups));
         }
-        return first;
     };
-    batches([&](int chunks, int grid, bool) {
-        k_clip_squares<<<grid, kThreads, 0, st>>>(b, chunks, a.workspace + n_partial);
+    for (int k = 0; k < a.n_tensors; ++k) bytes += a.numel[k] * (a.dtype[k] == kF32 ? 4 : 2);
+    batches([&](int grid) {
+        k_clip_squares<<<grid, kThreads, 0, st>>>(b, a.workspace + n_partial);
         n_partial += grid;
     });
     if (!a.out || n_partial == 0) {
         k_clip_norm<<<1, kThreads, 0, st>>>(a.workspace, n_partial, a.norm);
         return hipGetLastError();
     }
-    batches([&](int chunks, int grid, bool first) {
-        k_clip_scale<<<grid, kThreads, 0, st>>>(b, chunks, a.workspace, n_partial, a.max_norm, a.eps, first ? a.norm : nullptr);
+    float* norm = a.norm;       // the first launch writes it
+    batches([&](int grid) {
+        auto* kernel = streams(bytes) ? k_clip_scale<true> : k_clip_scale<false>;
+        kernel<<<grid, kThreads, 0, st>>>(b, a.workspace, n_partial, a.max_norm, a.eps, norm);
+        norm = nullptr;
     });
     return hipGetLastError();
 }

@@ -15,9 +15,11 @@ Shapes (lmax = 0: plain rows; else D = (lmax + 1)^2 components a row):
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
+import struct
 
-import numpy as np
 import torch
 
 from ._capi import EmbedProblem, NormProblem, train_check, train_lib
@@ -25,97 +27,93 @@ from ._capi import EmbedProblem, NormProblem, train_check, train_lib
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _INDEX_BITS = {torch.int32: 32, torch.int64: 64}
 
+# The problem structs as packed bytes: a tenth of the time of filling a ctypes.Structure.
+_EMBED = struct.Struct("@qqqqiiiif4x")
+_NORM = struct.Struct("@qqqqqqiiiiiff4x")
+assert _EMBED.size == ctypes.sizeof(EmbedProblem) and _NORM.size == ctypes.sizeof(NormProblem)
 
-def _float_code(t, name):
+
+def _tensor(t, name):
+    """The device index of a float tensor on a HIP device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    code = _DTYPES.get(t.dtype)
-    if code is None:
+    if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return code
-
-
-def _on(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _hip_device(t, name):
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a HIP device, got {t.device}")
-    return t.device
+    return index
 
 
-def _rows(t, name, tail, dtype, device, rows=None):
-    """(rows, stride) of a tensor [..., *tail] as rows of dense tails."""
+def _row_stride(t, name, shape, tail, width, dtype, index):
+    """Elements from row to row of a tensor [..., *tail] of rows of `width` dense values."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    _on(t, name, device)
-    k = t.dim() - len(tail)
-    if k < 0 or tuple(t.shape[k:]) != tail:
-        raise ValueError(f"{name} must have shape [..., {', '.join(map(str, tail))}], got {tuple(t.shape)}")
-    width = 1
-    for v in tail:
-        width *= v
-    n = t.numel() // width if width else 0
-    if rows is not None and n != rows:
-        raise ValueError(f"{name} has {n} rows, expected {rows}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
     if t.is_contiguous():
-        return n, width
-    if k == 1 and n <= 1 or k == 0:
-        inner, stride = t, width
-    elif k == 1 and t.stride(0) >= width:
-        inner, stride = t[0], t.stride(0)
-    else:
-        raise ValueError(f"{name}: its rows must lie one stride apart (strides {t.stride()})")
-    if not inner.is_contiguous() and n > 0:
-        raise ValueError(f"{name}: a row must be contiguous (strides {t.stride()})")
-    return n, stride
+        return width
+    strides = t.stride()
+    inner, dense = strides[t.dim() - tail:], 1
+    for size, stride in zip(reversed(shape[t.dim() - tail:]), reversed(inner)):
+        if size > 1 and stride != dense:
+            raise ValueError(f"{name}: a row must be contiguous (strides {strides})")
+        dense *= size
+    rows = [(n, s) for n, s in zip(shape[:t.dim() - tail], strides) if n > 1]
+    if not rows:
+        return width
+    if len(rows) > 1 and any(a != n * b for (_, a), (n, b) in zip(rows, rows[1:])) or rows[-1][1] < width:
+        raise ValueError(f"{name}: its rows must lie one stride apart and not overlap (strides {strides})")
+    return rows[-1][1]
 
 
-class _OnDevice:
-    """Makes a tensor's device current around a launch where it is not."""
-    __slots__ = ("index", "before")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _run(index, call, *args):
+    """A library call on a device's current stream, with the device current."""
+    before = torch.cuda.current_device()
+    if before == index:
+        train_check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+        return
+    torch.cuda.set_device(index)
+    try:
+        train_check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+    finally:
+        torch.cuda.set_device(before)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(nbytes, device, given):
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(kind, problem):
+    """Bytes of workspace of a problem (sizes alone, so the answer never changes)."""
+    out = ctypes.c_int64()
+    train_check(getattr(train_lib(), f"conv_tp_{kind}_bwd_workspace")(problem, ctypes.byref(out)))
+    return out.value
+
+
+def _workspace(kind, problem, like, given):
+    """(tensor, bytes): the caller's workspace, or one from torch's allocator."""
     if given is None:
-        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
-    if given.device != device or not given.is_contiguous():
+        nbytes = max(16, _workspace_bytes(kind, problem))
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+    if given.get_device() != like.get_device() or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return given
+    return given, given.numel() * given.element_size()
 
 
-def _nbytes(t):
-    return t.numel() * t.element_size()
-
-
-def _tokens(tokens, device):
+def _tokens(tokens, index):
     if not isinstance(tokens, torch.Tensor):
         raise TypeError("tokens must be a tensor")
     bits = _INDEX_BITS.get(tokens.dtype)
     if bits is None:
         raise ValueError(f"tokens must be int32 or int64, got {tokens.dtype}")
-    _on(tokens, "tokens", device)
+    if tokens.get_device() != index:
+        raise ValueError(f"tokens is on {tokens.device}, expected device {index}")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
     return bits
@@ -126,52 +124,46 @@ def _tokens(tokens, device):
 
 def embed_fwd(table, tokens, scale: float = 1.0, out=None):
     """out[..., C] = scale * table[tokens]; a token outside the table is padding and gives a zero row."""
-    code = _float_code(table, "table")
+    index = _tensor(table, "table")
     if table.dim() != 2 or table.shape[1] < 1:
         raise ValueError(f"table must be [rows, C], got {tuple(table.shape)}")
-    device = _hip_device(table, "table")
-    bits = _tokens(tokens, device)
+    bits = _tokens(tokens, index)
     v, c = table.shape
-    _, src = _rows(table, "table", (c,), table.dtype, device)
-    n = tokens.numel()
+    dt = table.dtype
+    src = _row_stride(table, "table", table.shape, 1, c, dt, index)
     if out is None:
-        out = torch.empty((*tokens.shape, c), dtype=table.dtype, device=device)
+        out = torch.empty((*tokens.shape, c), dtype=dt, device=table.device)
         dst = c
     else:
-        if tuple(out.shape) != (*tokens.shape, c):
-            raise ValueError(f"out must have shape {(*tokens.shape, c)}, got {tuple(out.shape)}")
-        _, dst = _rows(out, "out", (c,), table.dtype, device)
-    prob = EmbedProblem(n, v, src, dst, c, code, code, bits, scale)
-    with _OnDevice(device) as st:
-        train_check(train_lib().conv_tp_embed_fwd(ctypes.byref(prob), table.data_ptr(), tokens.data_ptr(),
-                                                  out.data_ptr(), st))
+        dst = _row_stride(out, "out", torch.Size((*tokens.shape, c)), 1, c, dt, index)
+    code = _DTYPES[dt]
+    prob = _EMBED.pack(tokens.numel(), v, src, dst, c, code, code, bits, scale)
+    _run(index, train_lib().conv_tp_embed_fwd, prob, table.data_ptr(), tokens.data_ptr(), out.data_ptr())
     return out
 
 
 def embed_bwd(grad_out, tokens, n_rows: int, scale: float = 1.0, out=None, dtype=None, workspace=None):
     """d_table[n_rows, C]: row v is scale times the sum of grad_out's rows whose token is v, zeros where there is
     none.  dtype: grad_out's, or float32.  workspace: any device tensor of enough bytes, allocated here if None."""
-    code = _float_code(grad_out, "grad_out")
-    device = _hip_device(grad_out, "grad_out")
-    bits = _tokens(tokens, device)
-    c = grad_out.shape[-1] if grad_out.dim() else 0
-    if c < 1 or tuple(grad_out.shape[:-1]) != tuple(tokens.shape):
-        raise ValueError(f"grad_out must have shape {(*tokens.shape, 'C')}, got {tuple(grad_out.shape)}")
-    n, src = _rows(grad_out, "grad_out", (c,), grad_out.dtype, device, tokens.numel())
+    index = _tensor(grad_out, "grad_out")
+    bits = _tokens(tokens, index)
+    shape, dt = grad_out.shape, grad_out.dtype
+    c = shape[-1] if len(shape) else 0
+    if c < 1 or shape[:-1] != tokens.shape:
+        raise ValueError(f"grad_out must have shape {(*tokens.shape, 'C')}, got {tuple(shape)}")
+    src = _row_stride(grad_out, "grad_out", shape, 1, c, dt, index)
     n_rows = int(n_rows)
     if out is None:
-        out = torch.empty((n_rows, c), dtype=dtype or grad_out.dtype, device=device)
-    elif tuple(out.shape) != (n_rows, c) or dtype not in (None, out.dtype):
-        raise ValueError(f"out must be [{n_rows}, {c}] {dtype or ''}, got {tuple(out.shape)} {out.dtype}")
-    _, dst = _rows(out, "out", (c,), out.dtype, device)
-    prob = EmbedProblem(n, n_rows, src, dst, c, code, _float_code(out, "out"), bits, scale)
-    L = train_lib()
-    nbytes = ctypes.c_int64()
-    train_check(L.conv_tp_embed_bwd_workspace(ctypes.byref(prob), ctypes.byref(nbytes)))
-    workspace = _workspace(nbytes.value, device, workspace)
-    with _OnDevice(device) as st:
-        train_check(L.conv_tp_embed_bwd(ctypes.byref(prob), grad_out.data_ptr(), tokens.data_ptr(), out.data_ptr(),
-                                        workspace.data_ptr(), _nbytes(workspace), st))
+        out = torch.empty((n_rows, c), dtype=dtype or dt, device=grad_out.device)
+        dst = c
+    else:
+        dst = _row_stride(out, "out", torch.Size((n_rows, c)), 1, c, dtype or out.dtype, index)
+    if out.dtype not in _DTYPES:
+        raise ValueError(f"out must be {dt} or float32, got {out.dtype}")
+    prob = _EMBED.pack(tokens.numel(), n_rows, src, dst, c, _DTYPES[dt], _DTYPES[out.dtype], bits, scale)
+    ws, nbytes = _workspace("embed", prob, grad_out, workspace)
+    _run(index, train_lib().conv_tp_embed_bwd, prob, grad_out.data_ptr(), tokens.data_ptr(), out.data_ptr(),
+         ws.data_ptr(), nbytes)
     return out
 
 
@@ -214,82 +206,80 @@ _GATE_NONE, _GATE_CHANNEL, _GATE_ROW = 0, 1, 2
 
 
 def _norm_problem(h, r, w_post, w_pre, gate, alpha, eps, lmax, grad_r=None, grad_u=None):
-    """Checks a norm's arguments; (problem, device, row shape, parameter shape)."""
+    """Checks a norm's arguments: (packed problem, device index, a tensor of the features' shape)."""
     lmax = int(lmax)
     if not 0 <= lmax <= 3:
         raise ValueError(f"lmax must be 0..3, got {lmax}")
-    first = next((t for t in (h, r, grad_r) if t is not None), None)
-    code = _float_code(first, "h" if h is not None else "r")
-    device = _hip_device(first, "h" if h is not None else "r")
-    dt = first.dtype
-    if first.dim() < (1 if lmax == 0 else 2):
-        raise ValueError(f"features must be [..., C] or [..., D, C], got {tuple(first.shape)}")
-    c = first.shape[-1]
-    tail = (c,) if lmax == 0 else ((lmax + 1) ** 2, c)
-    per = (c,) if lmax == 0 else (lmax + 1, c)
-    n, hs = _rows(first, "h" if h is not None else "r", tail, dt, device)
-    strides = []
-    for t, name in ((r, "r"), (grad_r, "grad_r"), (grad_u, "grad_u")):
+    first, name = (h, "h") if h is not None else (r, "r") if r is not None else (grad_r, "grad_r")
+    index = _tensor(first, name)
+    dt, shape = first.dtype, first.shape
+    tail = 1 if lmax == 0 else 2
+    lead = len(shape) - tail
+    if lead < 0 or shape[-1] < 1 or (lmax and shape[-2] != (lmax + 1) ** 2):
+        raise ValueError(f"features must be [..., C], for lmax = {lmax} > 0 [..., {(lmax + 1) ** 2}, C], "
+                         f"got {tuple(shape)}")
+    c = shape[-1]
+    width, per = (c, shape[lead:]) if lmax == 0 else (c * (lmax + 1) ** 2, torch.Size((lmax + 1, c)))
+    stride = lambda t, name: 0 if t is None else _row_stride(t, name, shape, tail, width, dt, index)  # noqa: E731
+    hs, rs, grs, gus = stride(h, "h"), stride(r, "r"), stride(grad_r, "grad_r"), stride(grad_u, "grad_u")
+    kind, gs, pdt = _GATE_NONE, 0, None
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre"), (gate, "gate")):
         if t is None:
-            strides.append(0)
             continue
-        if t.shape != first.shape:
-            raise ValueError(f"{name} must have shape {tuple(first.shape)}, got {tuple(t.shape)}")
-        strides.append(_rows(t, name, tail, dt, device, n)[1])
-    kind, gs = _GATE_NONE, 0
-    params = [(t, name) for t, name in ((w_post, "w_post"), (w_pre, "w_pre")) if t is not None]
-    if gate is not None:
-        if not isinstance(gate, torch.Tensor):
-            raise TypeError("gate must be a tensor")
-        if tuple(gate.shape) == per and tuple(first.shape) != per:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if name == "gate":
+            if t.shape != per or lead == 0:
+                kind = _GATE_ROW
+                gs = _row_stride(t, "gate", shape[:lead] + per, tail, c * (lmax + 1), dt, index)
+                continue
             kind = _GATE_CHANNEL
-            params.append((gate, "gate"))
-        else:
-            kind = _GATE_ROW
-            if tuple(gate.shape) != (*first.shape[:first.dim() - len(tail)], *per):
-                raise ValueError(f"gate must have shape {per} or one such for every row, got {tuple(gate.shape)}")
-            gs = _rows(gate, "gate", per, dt, device, n)[1]
-    pdt = params[0][0].dtype if params else dt
-    if pdt != dt and pdt != torch.float32:
-        raise ValueError(f"parameters must be {dt} or float32, got {pdt}")
-    for t, name in params:
+        if pdt is None:
+            pdt = t.dtype
+            if pdt != dt and pdt != torch.float32:
+                raise ValueError(f"parameters must be {dt} or float32, got {pdt}")
         if t.dtype != pdt:
             raise ValueError(f"{name} must be {pdt} like the other parameters, got {t.dtype}")
-        if tuple(t.shape) != per:
-            raise ValueError(f"{name} must have shape {per}, got {tuple(t.shape)}")
+        if t.shape != per:
+            raise ValueError(f"{name} must have shape {tuple(per)}, got {tuple(t.shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected device {index}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        _on(t, name, device)
-    prob = NormProblem(n, hs, strides[0], gs, strides[1], strides[2], lmax, c, code, _DTYPES[pdt], kind, alpha, eps)
-    return prob, device, first
+    n = 1
+    for size in shape[:lead]:
+        n *= size
+    prob = _NORM.pack(n, hs, rs, gs, grs, gus, lmax, c, _DTYPES[dt], _DTYPES[pdt or dt], kind, alpha, eps)
+    return prob, index, first
+
+
+def _dense(t):
+    """A new dense tensor like t."""
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def norm_residual_fwd(h, r, w_post, w_pre, gate=None, alpha: float = 1.0, eps: float = 1e-6, lmax: int = 0, out=None):
     """(r', u) with r' = r + alpha * gate * N(h; w_post) and u = N(r'; w_pre), N the root-mean-square norm over a
     row (balanced over the degrees for lmax > 0; see include/convtp_train.h).  h None: u = N(r; w_pre) alone, r'
     is r itself.  w_post None: h is added without a norm.  w_pre None: u is None.  gate: one row, or one for every
-    row.  out: (r', u) to write into; r' may be r."""
+    row.  out: (r', u) to write into, None for a new one; r' may be r."""
     if r is None:
         raise TypeError("r must be a tensor")
-    prob, device, first = _norm_problem(h, r, w_post, w_pre, gate, alpha, eps, lmax)
+    prob, index, first = _norm_problem(h, r, w_post, w_pre, gate, alpha, eps, lmax)
     r_out, u = out if out is not None else (None, None)
-    if h is None:
-        r_out = r
-    elif r_out is None:
-        r_out = torch.empty(first.shape, dtype=first.dtype, device=device)
+    for t, name in ((r_out, "r'"), (u, "u")):
+        if t is not None and (t.shape != first.shape or t.dtype != first.dtype or t.get_device() != index
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {first.dtype} tensor of shape {tuple(first.shape)}")
+    if h is not None and r_out is None:
+        r_out = _dense(first)
     if w_pre is None:
         u = None
     elif u is None:
-        u = torch.empty(first.shape, dtype=first.dtype, device=device)
-    if out is not None:
-        for t, name in ((r_out if h is not None else None, "r'"), (u, "u")):
-            if t is not None and (t.shape != first.shape or t.dtype != first.dtype or t.device != device
-                                  or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {first.dtype} tensor of shape {tuple(first.shape)}")
-    with _OnDevice(device) as st:
-        train_check(train_lib().conv_tp_norm_fwd(ctypes.byref(prob), _ptr(h), r.data_ptr(), _ptr(w_post), _ptr(w_pre),
-                                                 _ptr(gate), _ptr(r_out if h is not None else None), _ptr(u), st))
-    return r_out, u
+        u = _dense(first)
+    _run(index, train_lib().conv_tp_norm_fwd, prob, _ptr(h), r.data_ptr(), _ptr(w_post), _ptr(w_pre), _ptr(gate),
+         None if h is None else r_out.data_ptr(), _ptr(u))
+    return r if h is None else r_out, u
 
 
 def norm_residual_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate=None, alpha: float = 1.0, eps: float = 1e-6,
@@ -302,19 +292,12 @@ def norm_residual_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate=None, alpha:
         raise ValueError("grad_u without w_pre")
     if w_pre is not None and r_out is None:
         raise TypeError("r_out must be a tensor where there is w_pre")
-    prob, device, first = _norm_problem(h, r_out, w_post, w_pre, gate, alpha, eps, lmax, grad_r, grad_u)
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)  # noqa: E731
-    d_h, d_w_post, d_w_pre, d_gate = new(h), new(w_post), new(w_pre), new(gate)
-    d_r = torch.empty(first.shape, dtype=first.dtype, device=device)
-    L = train_lib()
-    nbytes = ctypes.c_int64()
-    train_check(L.conv_tp_norm_bwd_workspace(ctypes.byref(prob), ctypes.byref(nbytes)))
-    workspace = _workspace(nbytes.value, device, workspace)
-    with _OnDevice(device) as st:
-        train_check(L.conv_tp_norm_bwd(ctypes.byref(prob), _ptr(grad_r), _ptr(grad_u), _ptr(h), _ptr(r_out),
-                                       _ptr(w_post), _ptr(w_pre), _ptr(gate), _ptr(d_h), d_r.data_ptr(),
-                                       _ptr(d_w_post), _ptr(d_w_pre), _ptr(d_gate), workspace.data_ptr(),
-                                       _nbytes(workspace), st))
+    prob, index, first = _norm_problem(h, r_out, w_post, w_pre, gate, alpha, eps, lmax, grad_r, grad_u)
+    d_r, d_h, d_w_post, d_w_pre, d_gate = _dense(first), _dense(h), _dense(w_post), _dense(w_pre), _dense(gate)
+    ws, nbytes = _workspace("norm", prob, first, workspace)
+    _run(index, train_lib().conv_tp_norm_bwd, prob, _ptr(grad_r), _ptr(grad_u), _ptr(h), _ptr(r_out), _ptr(w_post),
+         _ptr(w_pre), _ptr(gate), _ptr(d_h), d_r.data_ptr(), _ptr(d_w_post), _ptr(d_w_pre), _ptr(d_gate),
+         ws.data_ptr(), nbytes)
     return d_h, d_r, d_w_post, d_w_pre, d_gate
 
 
@@ -347,42 +330,40 @@ def norm_residual(h, r, w_post, w_pre, gate=None, alpha: float = 1.0, eps: float
 # ---------------------------------------------------------------- clipping
 
 
-def _address_list(tensors, name, device):
-    """(addresses, elements, dtype codes) of dense tensors as arrays."""
-    codes = [_DTYPES.get(t.dtype, -1) for t in tensors]
-    if -1 in codes:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {tensors[codes.index(-1)].dtype}")
-    for t in tensors:
-        if t.device != device:
-            raise ValueError(f"{name} must be on one device: {t.device} and {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous (strides {t.stride()})")
-    return (np.array([t.data_ptr() for t in tensors], dtype=np.int64),
-            np.array([t.numel() for t in tensors], dtype=np.int64), np.array(codes, dtype=np.int32))
+def _addresses(tensors, name, index):
+    """(addresses, elements, dtype codes) of dense tensors on one device."""
+    T = torch.Tensor
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    if set(map(T.get_device, tensors)) != {index}:
+        raise ValueError(f"{name} must be on one HIP device, {index}")
+    dtypes = [t.dtype for t in tensors]
+    kinds = set(dtypes)
+    if not kinds <= _DTYPES.keys():
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {kinds - _DTYPES.keys()}")
+    codes = [_DTYPES[dtypes[0]]] * len(dtypes) if len(kinds) == 1 else [_DTYPES[d] for d in dtypes]
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), codes
 
 
 def _clip(tensors, out, max_norm, eps, norm):
-    device = _hip_device(tensors[0], "tensors")
-    at, numel, codes = _address_list(tensors, "tensors", device)
-    to = None
+    index = _tensor(tensors[0], "tensors")
+    at, numel, codes = _addresses(tensors, "tensors", index)
+    to = 0
     if out is not None:
-        if out is tensors:
-            to = at
-        else:
-            to, out_numel, out_codes = _address_list(out, "out", device)
-            if not (np.array_equal(numel, out_numel) and np.array_equal(codes, out_codes)):
-                raise ValueError("out must have the tensors' sizes and types")
+        to, out_numel, out_codes = _addresses(out, "out", index)
+        if out_numel != numel or out_codes != codes:
+            raise ValueError("out must have the tensors' sizes and types")
+        to = array.array("q", to)
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != device:
+        norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
+    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != index:
         raise ValueError("norm must be one float32 value on the tensors' device")
     L = train_lib()
+    at, numel, codes = array.array("q", at), array.array("q", numel), array.array("i", codes)
     nbytes = L.conv_tp_clip_workspace(len(tensors))
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with _OnDevice(device) as st:
-        train_check(L.conv_tp_clip(len(tensors), at.ctypes.data, None if to is None else to.ctypes.data,
-                                   numel.ctypes.data, codes.ctypes.data, max_norm, eps, norm.data_ptr(),
-                                   workspace.data_ptr(), nbytes, st))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=norm.device)
+    _run(index, L.conv_tp_clip, len(tensors), at.buffer_info()[0], to.buffer_info()[0] if to else None,
+         numel.buffer_info()[0], codes.buffer_info()[0], max_norm, eps, norm.data_ptr(), ws.data_ptr(), nbytes)
     return norm
 
 
