@@ -37,7 +37,10 @@ __device__ __forceinline__ int token_at(const void* tokens, int wide, long t, in
 
 // A row is shared by 2^lg lanes, one 16-byte vector each at a time; every
 // group of lanes looks up U rows at once so that U reads are in flight.
-template <class T, int U>
+// Stream: an output that the last-level cache does not hold is written around
+// it, which leaves it to the table (262144 rows of 512 floats: 125 us, 162
+// without).
+template <class T, int U, bool Stream>
 __global__ void __launch_bounds__(kThreads)
 k_embed_fwd(const T* __restrict__ table, const void* __restrict__ tokens, T* __restrict__ out, int n, int rows,
             int channels, int wide, float scale, long table_stride, long out_stride, int lg) {
@@ -67,7 +70,10 @@ k_embed_fwd(const T* __restrict__ table, const void* __restrict__ tokens, T* __r
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) f.v[k] *= scale;
             if (row[u] < 0) f = Floats<T>{};
-            store_vec<T>(out + t * out_stride, v, channels, narrow<T>(f));
+            if (Stream && (v + 1) * kVec<T> <= channels)
+                __builtin_nontemporal_store(narrow<T>(f), reinterpret_cast<typename Vec<T>::unaligned*>(out + t * out_stride + v * kVec<T>));
+            else
+                store_vec<T>(out + t * out_stride, v, channels, narrow<T>(f));
         }
     }
 }
@@ -147,10 +153,9 @@ __device__ __forceinline__ void store_zeros(O* row, int v, int n) {
 // One workgroup a table row and tile of channels goes through all tokens,
 // keeps the places of its own in order and sums their rows.  Every workgroup
 // reads all tokens, so this is for a few thousand of them and workgroups; it
-// saves the sort's launches (the water box's 1503 tokens: one launch instead
-// of three).
-constexpr int kFewThreads = 512;
-constexpr int kFewTokens = 4096;
+// saves the sort's launches.
+constexpr int kFewThreads = 1024;
+constexpr int kFewTokens = 8192;
 constexpr int kFewGroups = 2048;    // workgroups
 constexpr int kFewLanes = 3;        // log2 of the lanes of a row
 
@@ -377,7 +382,7 @@ constexpr int kBatch = 8;       // rows of a chunk read at once
 constexpr int kZeroRows = 32;   // table rows of a workgroup that writes the zero rows
 constexpr int kShortChunk = 16;
 constexpr int kEntries = 4096;  // most sorted tokens of a workgroup
-static_assert(kEntries >= kShortChunk * kThreads);  // a chunk is never shorter than the workspace allows for
+static_assert(kEntries >= kShortChunk * kThreads / 2);  // a chunk is never shorter than the workspace allows for
 
 // Row j of partial sums, `nvec` whole vectors of fp32.
 template <class T, class F, int Threads>
@@ -465,52 +470,72 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
 
 // Where a run begins in a chunk and leaves it, its sum is the chunk's tail plus
 // the heads of the chunks that the run reaches, which are those that begin with
-// its id.  A workgroup looks through as many chunks as it has groups of lanes
-// (most have no such run) and adds the partial rows of each run it finds with
-// all groups at once: the hottest run decides how long the kernel takes.
+// its id.  Every group of lanes looks at one chunk and joins a run of a few
+// chunks by itself; longer runs (hot tokens) are then joined by the whole
+// workgroup one after the other, since the longest decides how long the kernel
+// takes.
 constexpr int kJoinThreads = 1024;
+constexpr int kShortRun = 8;        // chunks that a short run reaches beyond its own
 
 template <class T, class O>
 __global__ void __launch_bounds__(kJoinThreads)
 k_embed_join(Sorted s, O* __restrict__ d_table, int channels, float scale, long table_stride, int lg, long chunks,
-             int at_once, const float* __restrict__ heads, const float* __restrict__ tails) {
+             const float* __restrict__ heads, const float* __restrict__ tails) {
     __shared__ __align__(16) float part[kJoinThreads * kVec<T>];
+    __shared__ int32_t long_run[kJoinThreads / 2];      // id of the long run that begins in each group's chunk, else `rows`
     const Tile<kJoinThreads> tl(lg, channels, kVec<T>);
-    // every wave looks at all of the workgroup's chunks, one a lane
     const int lane = threadIdx.x & 63;
-    const long mine = (long)blockIdx.x * at_once + lane, end = (mine + 1) * s.chunk;
+    const long j = (long)blockIdx.x * tl.groups + tl.group, end = (j + 1) * s.chunk;
     int id = s.rows;
-    if (lane < at_once && end < s.n) {
-        const int first = mine > 0 ? s.keys[mine * s.chunk - 1] : -1, last = s.keys[end - 1];
-        id = s.keys[end];
-        if (last != id || first == id) id = s.rows;     // no run leaves, or it began in an earlier chunk
+    if (end < s.n) {
+        const int first = j > 0 ? s.keys[j * s.chunk - 1] : -1, last = s.keys[end - 1], next = s.keys[end];
+        // else no run leaves, or it began in an earlier chunk
+        if (last == next && first != next) id = next;
     }
-    for (uint64_t found = __ballot(id != s.rows); found; found &= found - 1) {
-        const int which = __builtin_ctzll(found);
-        const long j = (long)blockIdx.x * at_once + which;
-        const int cur = __builtin_amdgcn_readlane(id, which);
-        // the last chunk that the run reaches, before `beyond`: a search by 64 probes at a time
-        long last = j;
-        for (long beyond = chunks; beyond - last > 1;) {
-            const long step = (beyond - last + 63) / 64, k = last + (lane + 1) * step;
-            last += step * __popcll(__ballot(k < beyond && s.keys[k * s.chunk] == cur));
-            beyond = min(beyond, last + step);
+    bool is_long = false;
+    if (id != s.rows) {
+        const long far = j + 1 + kShortRun;
+        is_long = far < chunks && s.keys[far * s.chunk] == id;
+        if (!is_long && tl.v < tl.nvec) {
+            Floats<T> acc = {};
+            add_floats<T>(partial_row<T>(tails, j, tl), acc);
+            for (long k = j + 1; k < chunks && s.keys[k * s.chunk] == id; ++k) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+            store_sum<T, O>(d_table + id * table_stride, tl.v, channels, acc, scale);
         }
-        Floats<T> acc = {};
-        if (tl.v < tl.nvec) {
-            if (tl.group == 0) add_floats<T>(partial_row<T>(tails, j, tl), acc);
-#pragma unroll 4
-            for (long k = j + 1 + tl.group; k <= last; k += tl.groups) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+    }
+    if (tl.lane == 0) long_run[tl.group] = is_long ? id : s.rows;
+    __syncthreads();
+    for (int g0 = 0; g0 < tl.groups; g0 += 64) {
+        const int mine = g0 + lane < tl.groups ? long_run[g0 + lane] : s.rows;
+        for (uint64_t found = __ballot(mine != s.rows); found; found &= found - 1) {
+            const int which = __builtin_ctzll(found);
+            const long first = (long)blockIdx.x * tl.groups + g0 + which;
+            const int cur = __builtin_amdgcn_readlane(mine, which);
+            // the last chunk that the run reaches, before `beyond`: a search by 64 probes at a time
+            long last = first;
+            for (long beyond = chunks; beyond - last > 1;) {
+                const long step = (beyond - last + 63) / 64, k = last + (lane + 1) * step;
+                last += step * __popcll(__ballot(k < beyond && s.keys[k * s.chunk] == cur));
+                beyond = min(beyond, last + step);
+            }
+            Floats<T> acc = {};
+            if (tl.v < tl.nvec) {
+                if (tl.group == 0) add_floats<T>(partial_row<T>(tails, first, tl), acc);
+#pragma unroll 8
+                for (long k = first + 1 + tl.group; k <= last; k += tl.groups) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+            }
+            // groups' sums by halves: `used` of them have any
+            int used = (int)min((long)tl.groups, last - first);
+            while (used > 1) {
+                const int half = (used + 1) / 2;
+                if (tl.group >= half && tl.group < used) store_floats<T>(part + threadIdx.x * kVec<T>, acc);
+                __syncthreads();
+                if (tl.group + half < used) add_floats<T>(part + (threadIdx.x + (half << lg)) * kVec<T>, acc);
+                __syncthreads();
+                used = half;
+            }
+            if (tl.group == 0 && tl.v < tl.nvec) store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
         }
-        const int used = (int)min((long)tl.groups, last - j);
-        if (used > 1) {
-            if (tl.group < used) store_floats<T>(part + threadIdx.x * kVec<T>, acc);
-            __syncthreads();
-            if (tl.group == 0)
-                for (int g = 1; g < used; ++g) add_floats<T>(part + ((g << lg) + tl.lane) * kVec<T>, acc);
-            __syncthreads();
-        }
-        if (tl.group == 0 && tl.v < tl.nvec) store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
     }
 }
 
@@ -522,8 +547,8 @@ int log2_up(long x) {
     return b;
 }
 
-// Lanes of a row: enough for all of its vectors, up to a workgroup.
-int lanes_log2(int channels, int kvec) { return std::min(8, log2_up((channels + kvec - 1) / kvec)); }
+// Lanes of a row: enough for all of its vectors, from 2 up to a workgroup.
+int lanes_log2(int channels, int kvec) { return std::clamp(log2_up((channels + kvec - 1) / kvec), 1, 8); }
 
 int few_tiles(int channels, int kvec) { return ((channels + kvec - 1) / kvec + (1 << kFewLanes) - 1) >> kFewLanes; }
 
@@ -569,9 +594,9 @@ hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* 
             s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride,
             lg, chunk_wgs, heads, tails);
     if (chunks > 1) {
-        const int at_once = std::min(64, kJoinThreads >> lg);
+        const long at_once = kJoinThreads >> lg;
         k_embed_join<T, O><<<dim3((unsigned)((chunks + at_once - 1) / at_once), tiles), kJoinThreads, 0, st>>>(
-            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, at_once, heads, tails);
+            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, heads, tails);
     }
     return hipGetLastError();
 }
@@ -620,8 +645,9 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, hipStream_t st) {
                                               a.dst_stride, lg);
         };
         // one row a group until the GPU is full, then four
-        if (a.n_tokens <= 1024L * groups) go(k_embed_fwd<T, 1>, 1);
-        else go(k_embed_fwd<T, 4>, 4);
+        if (a.n_tokens <= 1024L * groups) go(k_embed_fwd<T, 1, false>, 1);
+        else if (streams(2 * a.n_tokens * a.channels * (long)sizeof(T))) go(k_embed_fwd<T, 4, true>, 4);
+        else go(k_embed_fwd<T, 4, false>, 4);
         return hipGetLastError();
     });
 }

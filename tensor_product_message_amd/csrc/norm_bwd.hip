@@ -18,10 +18,11 @@ constexpr int kSums = 3;        // dw_post, dw_pre, dg
 // Threads of all workgroups together.
 constexpr int kTotalThreads = 1024 * 256;
 
-// Full: everything is there (h, both norms, both gradients) and a row is no
+// Four waves a SIMD, 128 registers a lane, are what two workgroups of 512 a CU
+// need.  Full: everything is there (h, both norms, both gradients) and a row is no
 // shorter than a vector, so that a row's reads are issued in one straight line.
 template <class T, int Lanes, int NV, int G, bool Full>
-__global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a) {
     constexpr int kRowsAtOnce = rows_at_once(Lanes);
     __shared__ float part[2][3][kSumWaves<Lanes>];
     __shared__ float part1[2][1][kSumWaves<Lanes>];
@@ -35,29 +36,36 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
     const bool has_gr = Full || a.grad_r, has_gu = Full || a.grad_u;
     const float inv = 1.0f / ((float)nl * (float)C);
     const Params<T> post{a.w_post, a.param_dtype != a.dtype, C}, pre{a.w_pre, post.wide, C}, shared{a.gate_p, post.wide, C};
-    Place p[NV];
-    float b[NV];
+    const bool fold = kRowsAtOnce > 1 || comps > 1;     // lanes share columns, through row_buf
+    // With several vectors a lane their places are worked out again at each use
+    // (the compiler must not see that they are the same), and one vector is
+    // finished before the next: kept, they would take the registers of the rows.
+    const Place p0 = place_of<T>(lane, nvec, comps, C);
+    auto place = [&](int i) {
+        if (NV == 1) return p0;
+        __builtin_amdgcn_sched_barrier(0);
+        int at = lane + i * Lanes;
+        forget(at);
+        return place_of<T>(at, nvec, comps, C);
+    };
+    auto weight = [&](const Place& p) { return inv / (float)(2 * p.l + 1); };
+    const float b0 = weight(p0);
     // w_post, w_pre and the shared gate stay in registers where a lane has one vector, else they are read again
     constexpr bool kKeep = NV == 1;
     Floats<T> wq0{}, wp0{}, wg0{};
     Floats<T> acc_post[NV] = {}, acc_pre[NV] = {}, acc_gate[G == kGateChannel ? NV : 1] = {};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        p[i] = place_of<T>(lane + i * Lanes, nvec, comps, C);
-        b[i] = inv / (float)(2 * p[i].l + 1);
+    if (kKeep && p0.on) {
+        if (has_post) wq0 = post.load(p0);
+        if (has_pre) wp0 = pre.load(p0);
+        if constexpr (G == kGateChannel) wg0 = shared.load(p0);
     }
-    if (kKeep && p[0].on) {
-        if (has_post) wq0 = post.load(p[0]);
-        if (has_pre) wp0 = pre.load(p[0]);
-        if constexpr (G == kGateChannel) wg0 = shared.load(p[0]);
-    }
-    auto w_post = [&](int i) {
+    auto w_post = [&](const Place& p) {
         if (kKeep) return wq0;
-        return p[i].on ? post.load(p[i]) : Floats<T>{};
+        return p.on ? post.load(p) : Floats<T>{};
     };
-    auto w_pre = [&](int i) {
+    auto w_pre = [&](const Place& p) {
         if (kKeep) return wp0;
-        return p[i].on ? pre.load(p[i]) : Floats<T>{};
+        return p.on ? pre.load(p) : Floats<T>{};
     };
     for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
         const long row = row0 + sub;
@@ -66,17 +74,18 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
         auto read_row = [&](auto stream) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
+                const Place p = place(i);
                 hx[i] = rx[i] = grx[i] = gux[i] = vec_t<T>{};
                 if constexpr (G == kGateRow) gx[i] = vec_t<T>{};
-                if (!p[i].on || !live) continue;
+                if (!p.on || !live) continue;
                 auto read = [&](const void* x, long stride, unsigned from) {
-                    return read_at<T, Full, stream>(row_of<const T>(x, row, stride) + from, p[i].span, C);
+                    return read_at<T, Full, stream>(row_of<const T>(x, row, stride) + from, p.span, C);
                 };
-                if (has_pre) rx[i] = read(a.r, a.r_stride, p[i].from);
-                if (has_gu) gux[i] = read(a.grad_u, a.grad_u_stride, p[i].from);
-                if (has_h) hx[i] = read(a.h, a.h_stride, p[i].from);
-                if (has_gr) grx[i] = read(a.grad_r, a.grad_r_stride, p[i].from);
-                if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p[i].par_from);
+                if (has_pre) rx[i] = read(a.r, a.r_stride, p.from);
+                if (has_gu) gux[i] = read(a.grad_u, a.grad_u_stride, p.from);
+                if (has_h) hx[i] = read(a.h, a.h_stride, p.from);
+                if (has_gr) grx[i] = read(a.grad_r, a.grad_r_stride, p.from);
+                if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p.par_from);
             }
         };
         if (a.stream) {
@@ -87,17 +96,20 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (p[i].span.shift <= 0) continue;
-            settle<T>(rx[i], p[i].span), settle<T>(gux[i], p[i].span);
-            settle<T>(hx[i], p[i].span), settle<T>(grx[i], p[i].span);
-            if constexpr (G == kGateRow) settle<T>(gx[i], p[i].span);
+            const Place p = place(i);
+            if (p.span.shift <= 0) continue;
+            settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
+            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p.span);
         }
         // the squares of h and r' and <A, r'>
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Floats<T> h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
-            const Floats<T> w = has_pre ? w_pre(i) : Floats<T>{};
+            const Place p = place(i);
+            const float b = NV == 1 ? b0 : weight(p);
+            const Floats<T> w = has_pre ? w_pre(p) : Floats<T>{};
             float qh = 0.0f, qr = 0.0f;
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) {
@@ -105,8 +117,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
                 qr = __builtin_fmaf(r.v[k], r.v[k], qr);
                 s[2] = __builtin_fmaf(w.v[k] * gu.v[k], r.v[k], s[2]);
             }
-            s[0] = __builtin_fmaf(qh, b[i], s[0]);
-            s[1] = __builtin_fmaf(qr, b[i], s[1]);
+            s[0] = __builtin_fmaf(qh, b, s[0]);
+            s[1] = __builtin_fmaf(qr, b, s[1]);
         }
         sum3(s);
 #pragma unroll
@@ -115,16 +127,20 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
         const float s2 = has_pre ? inv_root(s[1], a.eps) : 0.0f;
         const float pull = s2 * s[2];
         float t[1] = {0.0f};
-        Floats<T> B[NV];
+        // with several vectors a lane, B waits in LDS for the second reduction, each lane's in its own places
+        Floats<T> B0{};
+        float* B_lds = row_buf + (G == kGateRow && comps > 1 ? comps * nvec * kVec<T> : 0) + lane * kVec<T>;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool on = p[i].on && live;    // the others work on zeros
-            B[i] = Floats<T>{};
+            const Place p = place(i);
+            const float b = NV == 1 ? b0 : weight(p);
+            Floats<T> B{};
+            const bool on = p.on && live;    // the others work on zeros
             Floats<T> d = widen<T>(grx[i]);
             if (has_pre) {
                 const Floats<T> r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
-                const Floats<T> w = w_pre(i);
-                const float c = pull * b[i];
+                const Floats<T> w = w_pre(p);
+                const float c = pull * b;
 #pragma unroll
                 for (int k = 0; k < kVec<T>; ++k) {
                     const float rs = r.v[k] * s2;
@@ -132,22 +148,29 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
                     acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], rs, acc_pre[i].v[k]);
                 }
             }
-            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p[i].to, p[i].left, narrow<T>(d));
+            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(d));
             if (!has_h) continue;
             const Floats<T> h = widen<T>(hx[i]);
             Floats<T> w, g, dg;
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) w.v[k] = g.v[k] = 1.0f;
-            if (has_post) w = w_post(i);
+            if (has_post) w = w_post(p);
             if constexpr (G == kGateRow) g = widen<T>(gx[i]);
-            if constexpr (G == kGateChannel) g = kKeep ? wg0 : p[i].on ? shared.load(p[i]) : Floats<T>{};
+            if constexpr (G == kGateChannel) g = kKeep ? wg0 : p.on ? shared.load(p) : Floats<T>{};
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) {
                 const float ad = a.alpha * d.v[k], hs = h.v[k] * s1, dy = ad * g.v[k];
                 dg.v[k] = ad * hs * w.v[k];
                 acc_post[i].v[k] = __builtin_fmaf(dy, hs, acc_post[i].v[k]);
-                B[i].v[k] = dy * w.v[k];
-                t[0] = __builtin_fmaf(B[i].v[k], h.v[k], t[0]);
+                B.v[k] = dy * w.v[k];
+                t[0] = __builtin_fmaf(B.v[k], h.v[k], t[0]);
+            }
+            if constexpr (kKeep) {
+                B0 = B;
+            } else if (p.on) {
+#pragma unroll
+                for (int k = 0; k < kVec<T>; k += 4)
+                    *reinterpret_cast<float4*>(B_lds + i * Lanes * kVec<T> + k) = make_float4(B.v[k], B.v[k + 1], B.v[k + 2], B.v[k + 3]);
             }
             if constexpr (G == kGateChannel) {
 #pragma unroll
@@ -155,8 +178,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
             }
             if constexpr (G == kGateRow) {
                 if (comps == 1) {
-                    if (on) store_left<T>(row_of<T>(a.d_gate, row, C) + p[i].to, p[i].left, narrow<T>(dg));
-                } else if (p[i].on) {
+                    if (on) store_left<T>(row_of<T>(a.d_gate, row, C) + p.to, p.left, narrow<T>(dg));
+                } else if (p.on) {
                     float* at = row_buf + (sub * comps * nvec + lane + i * Lanes) * kVec<T>;
 #pragma unroll
                     for (int k = 0; k < kVec<T>; ++k) at[k] = dg.v[k];
@@ -173,12 +196,21 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
         for (int i = 0; i < NV; ++i) forget(hx[i]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const Place p = place(i);
+            const float b = NV == 1 ? b0 : weight(p);
             const Floats<T> h = widen<T>(hx[i]);
-            const float c = pull1 * b[i];
-            Floats<T> dh;
+            const float c = pull1 * b;
+            Floats<T> dh = B0;
+            if (!kKeep && p.on) {
 #pragma unroll
-            for (int k = 0; k < kVec<T>; ++k) dh.v[k] = s1 * __builtin_fmaf(-c, h.v[k] * s1, B[i].v[k]);
-            if (p[i].on && live) store_left<T>(row_of<T>(a.d_h, row, W) + p[i].to, p[i].left, narrow<T>(dh));
+                for (int k = 0; k < kVec<T>; k += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(B_lds + i * Lanes * kVec<T> + k);
+                    dh.v[k] = q.x, dh.v[k + 1] = q.y, dh.v[k + 2] = q.z, dh.v[k + 3] = q.w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) dh.v[k] = s1 * __builtin_fmaf(-c, h.v[k] * s1, dh.v[k]);
+            if (p.on && live) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(dh));
         }
         if constexpr (G == kGateRow) {
             if (comps > 1) {
@@ -201,13 +233,12 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd(NormArgs a) {
     // the workgroup's sums: over its rows at once and over the components of a degree, [sum][l][padded channels]
     const int width = nl * nvec * kVec<T>;
     float* ws = static_cast<float*>(a.workspace) + (long)blockIdx.x * kSums * width;
-    const bool fold = kRowsAtOnce > 1 || comps > 1;
     auto leave = [&](int which, const Floats<T>* acc) {
         float* to = fold ? row_buf + sub * comps * nvec * kVec<T> : ws + which * width;
         if (fold) lds_barrier();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (!p[i].on) continue;
+            if (!place(i).on) continue;
 #pragma unroll
             for (int k = 0; k < kVec<T>; k += 4)
                 *reinterpret_cast<float4*>(to + (lane + i * Lanes) * kVec<T> + k) =
@@ -284,11 +315,23 @@ hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
         using T = decltype(t);
         const int n = row_vectors(a.lmax, a.channels, kVec<T>);
         return with_shape(n, [&](auto lanes, auto nv) {
+            hipError_t asked = hipSuccess;
             const int grid = bwd_grid(a.n_rows, lanes);
             if (grid > 0) {
                 constexpr int kAtOnce = rows_at_once(lanes);
-                const size_t lds = kAtOnce > 1 || a.lmax > 0 ? (size_t)kAtOnce * n * kVec<T> * sizeof(float) : 0;
-                auto go = [&](auto kernel) { kernel<<<grid, kNormThreads<lanes>, lds, st>>>(a); };
+                // one row in work in fp32, and a second one where both uses of row_buf meet
+                const size_t row_lds = (size_t)kAtOnce * n * kVec<T> * sizeof(float);
+                const bool two = nv > 1 && a.lmax > 0 && a.gate == kGateRow;
+                const size_t lds = two ? 2 * row_lds : kAtOnce > 1 || a.lmax > 0 || nv > 1 ? row_lds : 0;
+                auto go = [&](auto kernel) {
+                    // beyond 64 KB a kernel has to ask
+                    if (lds > 60000)
+                        if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                            e != hipSuccess)
+                            asked = e;
+                    if (asked == hipSuccess) kernel<<<grid, kNormThreads<lanes>, lds, st>>>(a);
+                };
                 const bool full = a.h && a.w_post && a.w_pre && a.grad_r && a.grad_u && a.channels >= kVec<T>;
                 auto gated = [&](auto g) {
                     if (full) go(k_norm_bwd<T, lanes, nv, g, true>);
@@ -298,6 +341,7 @@ hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
                 else if (a.gate == kGateChannel) gated(std::integral_constant<int, kGateChannel>{});
                 else gated(std::integral_constant<int, kGateNone>{});
             }
+            if (asked != hipSuccess) return asked;
             const int padded = (a.channels + kVec<T> - 1) / kVec<T> * kVec<T>, cols = (a.lmax + 1) * padded;
             void* d_gate = a.gate == kGateChannel ? a.d_gate : nullptr;
             if (a.d_w_post || a.d_w_pre || d_gate)
