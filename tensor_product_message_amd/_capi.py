@@ -1,4 +1,5 @@
-"""ctypes declarations of libconvtp.so (include/convtp.h, include/convtp_train.h), nothing else.
+"""ctypes declarations of libconvtp.so (include/convtp.h, include/convtp_train.h) and
+the loading of the training-step operators' binding module, nothing else.
 
 Loading fails loudly if the HIP library has not been built: there is no
 fallback implementation of any entry point.
@@ -129,7 +130,7 @@ def train_lib() -> ctypes.CDLL:
     L = lib()
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     i64p = ctypes.POINTER(i64)
-    ep = np_ = vp       # problem structs by address: EmbedProblem, NormProblem or their packed bytes
+    ep, np_ = ctypes.POINTER(EmbedProblem), ctypes.POINTER(NormProblem)
     sig = {
         "conv_tp_embed_fwd": ([ep, vp, vp, vp, vp], i32),
         "conv_tp_embed_bwd": ([ep, vp, vp, vp, vp, i64, vp], i32),
@@ -152,3 +153,21 @@ def train_lib() -> ctypes.CDLL:
 def train_check(status: int) -> None:
     if status != CTP_OK:
         raise ConvTPError(status, train_lib().conv_tp_train_last_error().decode())
+
+
+_native = None
+
+
+def native():
+    """The binding module of the training-step operators (csrc/train_binding.cpp), on the loaded library."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (the module links to its libraries)
+        try:
+            from . import _train
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(HERE, '_train.so')} is missing or does not load ({e}): build it with "
+                               "`python -m tensor_product_message_amd.build`") from e
+        _train.bind(train_lib()._handle, train_check)
+        _native = _train
+    return _native

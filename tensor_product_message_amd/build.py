@@ -1,4 +1,5 @@
-"""Build libconvtp.so (HIP, gfx950) in-tree with hipcc.
+"""Build libconvtp.so (HIP, gfx950) in-tree with hipcc, and the Python binding of
+the training-step operators (_train.so, host code) with g++.
 
     python -m tensor_product_message_amd.build [--incremental]
 
@@ -14,9 +15,11 @@ source (for development; the default rebuilds everything).
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +30,9 @@ SOURCES = ["convtp_common.hip", "nodetp_kernels.hip", "graph_kernels.hip", "stre
 TRAIN_SOURCES = ["embed_kernels.hip", "norm_fwd.hip", "norm_bwd.hip", "clip_kernels.hip", "train_api.hip"]
 TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "csrc/norm_common.hpp",
                  "../include/convtp_train.h", "../include/convtp.h"]
+# their Python binding, an extension module next to the package's other files
+BINDING_SOURCE = "train_binding.cpp"
+BINDING = os.path.join(HERE, "_train.so")
 TRIPLE_SOURCE = "convtp_triple.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -67,6 +73,26 @@ def _jobs(objdir: str):
     return jobs
 
 
+def _build_binding() -> None:
+    """Host code only (g++): torch's and Python's headers, the library's entry points are looked up at run time."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=1"]
+    for path in (include, os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(rocm, "include"),
+                 sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", path]
+    tmp = BINDING + ".tmp"
+    cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}{r.stderr}")
+    if r.stderr:
+        print(r.stderr, file=sys.stderr)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True, incremental: bool = False, workers: int = None) -> str:
     """Compile every HIP source and link libconvtp.so; returns its path."""
     objdir = os.path.join(HERE, "_build")
@@ -86,8 +112,13 @@ def build(verbose: bool = True, incremental: bool = False, workers: int = None) 
             return not os.path.exists(obj) or os.path.getmtime(obj) < newest
         todo = [j for j in jobs if stale(j)]
     n = workers or min(16, os.cpu_count() or 8)
+    binding = not incremental or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(
+        newest_train, os.path.getmtime(os.path.join(CSRC, BINDING_SOURCE)))
     with ThreadPoolExecutor(max_workers=n) as ex:
+        jobs_done = [ex.submit(_build_binding)] if binding else []
         list(ex.map(_compile, todo))
+        for f in jobs_done:
+            f.result()
     tmp = LIB + ".tmp"
     subprocess.run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *[j[1] for j in jobs]],
                    check=True)
