@@ -390,13 +390,14 @@ __device__ __forceinline__ F* partial_row(F* base, long j, const Tile<Threads>& 
     return base + (j * t.nvec + t.v) * kVec<T>;
 }
 
-// Workgroups below `chunk_wgs` sum chunks, one a group of lanes; the others, if
-// any, write the zero rows of the table.
+// Workgroups below `chunk_wgs` sum chunks, one a group of lanes; the others write
+// the zero rows of the table.
 template <class T, class O>
 __global__ void __launch_bounds__(kThreads)
 k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int channels, float scale, long grad_stride,
             long table_stride, int lg, long chunk_wgs, float* __restrict__ heads, float* __restrict__ tails) {
     extern __shared__ int32_t sorted_lds[];     // a workgroup's ids with one neighbour on each side, then its places
+    __shared__ __align__(16) float head_lds[kThreads * kVec<T>];    // each chunk's share of the run that it begins with
     const Tile<kThreads> tl(lg, channels, kVec<T>);
     if (blockIdx.x >= chunk_wgs) {
         // which of 32 table rows have a token: a binary search in the sorted ids, one row a lane
@@ -423,12 +424,11 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
         if (k < entries && i + 1 < s.n) spos[k] = s.pos[i + 1];
     }
     __syncthreads();
-    const long j = (long)blockIdx.x * tl.groups + tl.group;     // the chunk
-    const int at = tl.group * s.chunk;                          // its first entry
+    const int at = tl.group * s.chunk;      // the chunk's first entry
     const int32_t* key = skey + 1 + at;
     const int32_t* pos = spos + at;
     int cur = key[0];
-    if (cur == s.rows || tl.v >= tl.nvec) return;
+    const bool on = cur != s.rows && tl.v < tl.nvec;
     bool head = key[-1] == cur;                 // the run began in an earlier chunk
     const Span span = span_of<T>(tl.v, channels);
     Floats<T> acc = {};
@@ -436,44 +436,69 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             x[q] = vec_t<T>{};
-            if (k0 < s.chunk && key[k0 + q] != s.rows)
+            if (on && k0 < s.chunk && key[k0 + q] != s.rows)
                 x[q] = read_span<T>(grad + pos[k0 + q] * grad_stride, span, channels);
         }
     };
-    vec_t<T> x[kBatch], y[kBatch];
-    read(x, 0);
-    for (int k0 = 0; k0 < s.chunk; k0 += kBatch) {
-        read(y, k0 + kBatch);       // on their way while the rows before them are added
+    float* mine = head_lds + threadIdx.x * kVec<T>;
+    if (on) {
+        vec_t<T> x[kBatch], y[kBatch];
+        read(x, 0);
+        for (int k0 = 0; k0 < s.chunk; k0 += kBatch) {
+            read(y, k0 + kBatch);       // on their way while the rows before them are added
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int now = key[k0 + q];
-            if (now != cur) {
-                if (cur != s.rows) {
-                    if (head) store_floats<T>(partial_row<T>(heads, j, tl), acc);
-                    else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+            for (int q = 0; q < kBatch; ++q) {
+                const int now = key[k0 + q];
+                if (now != cur) {
+                    if (cur != s.rows) {
+                        if (head) store_floats<T>(mine, acc);
+                        else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+                    }
+                    cur = now;
+                    head = false;
+                    acc = Floats<T>{};
                 }
-                cur = now;
-                head = false;
-                acc = Floats<T>{};
+                settle<T>(x[q], span);
+                add_vec<T>(acc, x[q]);
             }
-            settle<T>(x[q], span);
-            add_vec<T>(acc, x[q]);
-        }
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) x[q] = y[q];
+            for (int q = 0; q < kBatch; ++q) x[q] = y[q];
+        }
+        if (cur != s.rows && head) store_floats<T>(mine, acc);
     }
-    if (cur == s.rows) return;
-    if (head) store_floats<T>(partial_row<T>(heads, j, tl), acc);
-    else if (key[s.chunk] == cur) store_floats<T>(partial_row<T>(tails, j, tl), acc);
-    else store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+    // what the run at the chunk's end goes on to; `tail`: it began in this chunk
+    const bool leaves = key[s.chunk] == cur, tail = on && cur != s.rows && !head;
+    if (tail && !leaves) store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+    __syncthreads();
+    // Runs inside the workgroup's chunks: the chunk where one begins adds the
+    // heads of the next ones.  A run that enters the workgroup's first chunk or
+    // leaves its last one is left to k_embed_join.
+    auto add_heads = [&](int id, int g) {       // from group g on; the first group that the run does not reach
+        for (; g < tl.groups && skey[1 + g * s.chunk] == id; ++g)
+            add_floats<T>(head_lds + ((g << lg) + tl.lane) * kVec<T>, acc);
+        return g;
+    };
+    if (tail && leaves) {
+        const int g = add_heads(cur, tl.group + 1);
+        if (g == tl.groups && key[(g - tl.group) * s.chunk] == cur)
+            store_floats<T>(partial_row<T>(tails, blockIdx.x, tl), acc);
+        else
+            store_sum<T, O>(d_table + cur * table_stride, tl.v, channels, acc, scale);
+    }
+    if (on && tl.group == 0 && key[-1] == key[0]) {
+        acc = Floats<T>{};
+        add_heads(key[0], 0);
+        store_floats<T>(partial_row<T>(heads, blockIdx.x, tl), acc);
+    }
 }
 
-// Where a run begins in a chunk and leaves it, its sum is the chunk's tail plus
-// the heads of the chunks that the run reaches, which are those that begin with
-// its id.  Every group of lanes looks at one chunk and joins a run of a few
-// chunks by itself; longer runs (hot tokens) are then joined by the whole
-// workgroup one after the other, since the longest decides how long the kernel
-// takes.
+// What is left are the spans of k_embed_sum's workgroups (`s.chunk` tokens here,
+// one row of heads and tails each).  Where a run begins in a span and leaves
+// it, its sum is the span's tail plus the heads of the spans that the run
+// reaches, which are those that begin with its id.  Every group of lanes looks
+// at one span and joins a run over a few of them by itself; longer runs (hot
+// tokens) are then joined by the whole workgroup one after the other, since
+// the longest decides how long the kernel takes.
 constexpr int kJoinThreads = 1024;
 constexpr int kShortRun = 8;        // chunks that a short run reaches beyond its own
 
@@ -486,20 +511,25 @@ k_embed_join(Sorted s, O* __restrict__ d_table, int channels, float scale, long 
     const Tile<kJoinThreads> tl(lg, channels, kVec<T>);
     const int lane = threadIdx.x & 63;
     const long j = (long)blockIdx.x * tl.groups + tl.group, end = (j + 1) * s.chunk;
+    // the ids around the span's end, and all first ones that a short run may reach, are read at once
     int id = s.rows;
+    int32_t next[kShortRun + 1];
     if (end < s.n) {
-        const int first = j > 0 ? s.keys[j * s.chunk - 1] : -1, last = s.keys[end - 1], next = s.keys[end];
-        // else no run leaves, or it began in an earlier chunk
-        if (last == next && first != next) id = next;
+        const int first = j > 0 ? s.keys[j * s.chunk - 1] : -1, last = s.keys[end - 1];
+#pragma unroll
+        for (int k = 0; k <= kShortRun; ++k) next[k] = j + 1 + k < chunks ? s.keys[(j + 1 + k) * s.chunk] : s.rows;
+        // else no run leaves, or it began in an earlier span
+        if (last == next[0] && first != last) id = last;
     }
     bool is_long = false;
     if (id != s.rows) {
-        const long far = j + 1 + kShortRun;
-        is_long = far < chunks && s.keys[far * s.chunk] == id;
+        is_long = next[kShortRun] == id;
         if (!is_long && tl.v < tl.nvec) {
             Floats<T> acc = {};
             add_floats<T>(partial_row<T>(tails, j, tl), acc);
-            for (long k = j + 1; k < chunks && s.keys[k * s.chunk] == id; ++k) add_floats<T>(partial_row<T>(heads, k, tl), acc);
+#pragma unroll
+            for (int k = 0; k < kShortRun; ++k)
+                if (next[k] == id) add_floats<T>(partial_row<T>(heads, j + 1 + k, tl), acc);
             store_sum<T, O>(d_table + id * table_stride, tl.v, channels, acc, scale);
         }
     }
@@ -572,7 +602,9 @@ Plan plan_of(long n, long rows, int channels) {
     p.tiles = (int)((n + p.tile - 1) / p.tile);
     p.keys = up256(4 * n);
     p.counts = up256(4L * p.tiles << p.bits);
-    p.partials = up256((n + kShortChunk - 1) / kShortChunk * ((channels + 7L) / 8 * 8) * 4);
+    // a row a span; spans are shortest where rows take the most lanes, in float32
+    const long span = (long)kShortChunk * (kThreads >> lanes_log2(channels, kVec<float>));
+    p.partials = up256((n + span - 1) / span * ((channels + 7L) / 8 * 8) * 4);
     p.total = 4 * p.keys + p.counts + 2 * p.partials;
     return p;
 }
@@ -588,15 +620,18 @@ hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* 
     const int nvec = (a.channels + kVec<T> - 1) / kVec<T>;
     const unsigned tiles = (unsigned)((nvec + (1 << lg) - 1) >> lg);
     const long chunks = (a.n_tokens + chunk - 1) / chunk;
-    const long chunk_wgs = (chunks + groups - 1) / groups, zero_wgs = (a.n_rows + kZeroRows - 1) / kZeroRows;
+    const long chunk_wgs = (chunks + groups - 1) / groups;     // spans too
+    const long zero_wgs = (a.n_rows + kZeroRows - 1) / kZeroRows;
     if (chunk_wgs + zero_wgs > 0)
         k_embed_sum<T, O><<<dim3((unsigned)(chunk_wgs + zero_wgs), tiles), kThreads, (2 * groups * chunk + 2) * sizeof(int32_t), st>>>(
             s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride,
             lg, chunk_wgs, heads, tails);
-    if (chunks > 1) {
+    if (chunk_wgs > 1) {
+        Sorted spans = s;
+        spans.chunk = chunk * groups;
         const long at_once = kJoinThreads >> lg;
-        k_embed_join<T, O><<<dim3((unsigned)((chunks + at_once - 1) / at_once), tiles), kJoinThreads, 0, st>>>(
-            s, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunks, heads, tails);
+        k_embed_join<T, O><<<dim3((unsigned)((chunk_wgs + at_once - 1) / at_once), tiles), kJoinThreads, 0, st>>>(
+            spans, static_cast<O*>(a.dst), a.channels, a.scale, a.dst_stride, lg, chunk_wgs, heads, tails);
     }
     return hipGetLastError();
 }
