@@ -46,14 +46,13 @@ template <bool Backwards, class F>
 __device__ __forceinline__ void each_span(const Batch& b, F&& f) {
     const long chunks = b.first[b.n];
     const int from = (int)(chunks * blockIdx.x / gridDim.x), to = (int)(chunks * (blockIdx.x + 1) / gridDim.x);
-    // the last tensor whose first chunk is not beyond the run's first (backwards: last) chunk
-    const int chunk = Backwards ? to - 1 : from;
-    int t = 0;
-    for (int hi = b.n - 1; t < hi;) {
-        const int mid = (t + hi + 1) / 2;
-        if (b.first[mid] <= chunk) t = mid;
-        else hi = mid - 1;
-    }
+    // The last tensor whose first chunk is not beyond the run's first (backwards:
+    // last) chunk.  All first chunks are read at once, one a lane: the arguments
+    // lie in host memory, and a search by halves would go there step by step.
+    const int chunk = Backwards ? to - 1 : from, lane = threadIdx.x % 64;
+    int t = -1;
+#pragma unroll
+    for (int k = 0; k < kPerLaunch; k += 64) t += __popcll(__ballot(k + lane < b.n && b.first[k + lane] <= chunk));
     while (t >= 0 && t < b.n && b.first[t] < to && b.first[t + 1] >= from) {
         const long lo = max(from, b.first[t]) - b.first[t], hi = min(to, b.first[t + 1]) - b.first[t];
         if (hi > lo) f(t, lo * kChunk, min(hi * kChunk, (long)b.numel[t]));

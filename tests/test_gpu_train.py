@@ -518,3 +518,83 @@ def test_refusals(ctp, dev):
             (lambda: ctp.clip_grad_norm([f(4)], float("nan")), ctp.ConvTPError)):
         with pytest.raises(err):
             call()
+
+
+# ---------------------------------------------------------------- long runs, long arrays, the example
+
+
+@pytest.mark.parametrize("n,v,c,dtype,same", [
+    (9000, 2, 2048, torch.bfloat16, 0.7),       # one row a workgroup, a run over hundreds of spans
+    (30000, 2000, 64, torch.float32, 1.0),      # one token in a large table
+    (40000, 3, 5, torch.float16, 0.5),          # many rows a workgroup
+    (20000, 900, 260, torch.float32, 0.02),     # runs that end and begin all over the spans
+])
+def test_embed_bwd_long_runs(ctp, dev, n, v, c, dtype, same):
+    g = gen(n)
+    tok = torch.randint(0, v, (n,), generator=g)
+    tok[torch.rand(n, generator=g) < same] = v - 1
+    grad = normal(g, (n, c), dtype)
+    tell("embed_bwd runs", n, v, c, dtype)
+    ref, S, K = embed_bwd_ref(grad, tok, v, 1.0)
+    got = ctp.embed_bwd(grad.to(dev), tok.to(dev), v)
+    close("d_table", got, ref, S, K)
+
+
+def test_embed_bwd_every_run_length(ctp, dev):
+    """Runs of 1, 2, 3 .. tokens: every place of a run's ends in chunks and spans."""
+    for c, dtype in ((24, torch.float32), (200, torch.float32), (1030, torch.bfloat16)):
+        lengths = torch.arange(1, 180)
+        tok = torch.repeat_interleave(torch.arange(len(lengths)), lengths)
+        g = gen(c)
+        tok = tok[torch.randperm(len(tok), generator=g)]
+        grad = normal(g, (len(tok), c), dtype)
+        ref, S, K = embed_bwd_ref(grad, tok, len(lengths) + 3, 1.0)
+        close("d_table", ctp.embed_bwd(grad.to(dev), tok.to(dev), len(lengths) + 3), ref, S, K)
+
+
+def test_offsets_beyond_32_bits(ctp, dev):
+    """Tables, features and gradients of more than 2^31 elements: sampled rows against the definition."""
+    v, c = 1_100_000, 2048
+    table = torch.empty((v, c), dtype=torch.bfloat16, device=dev)
+    for k in range(0, v, 100_000):
+        table[k:k + 100_000].normal_()
+    tok = torch.tensor([0, v - 1, v // 2, 1_048_577, -1], device=dev)
+    tell("large embed")
+    out = ctp.embed_fwd(table, tok, 1.0)
+    assert torch.equal(out[:4], table[tok[:4]]) and float(out[4].abs().sum()) == 0.0
+    grad = torch.randn((5, c), device=dev).to(torch.bfloat16)
+    ctp.embed_bwd(grad, tok, v, out=table)
+    assert torch.equal(table[tok[:4]], grad[:4])
+    assert int((table != 0).any(1).sum()) == 4
+    del out
+    rows = table.view(137_500, 16384)                 # the same memory as wide rows
+    rows.normal_()
+    h = rows.clone()
+    w = torch.ones(16384, dtype=torch.bfloat16, device=dev)
+    tell("large norm")
+    r_out, u = ctp.norm_residual_fwd(h, rows, w, w)
+    at = [0, 70_000, 131_073, 137_499]
+    one = ctp.norm_residual_fwd(h[at], rows[at], w, w)
+    assert torch.equal(r_out[at], one[0]) and torch.equal(u[at], one[1])
+    d_h, d_r, *_ = ctp.norm_residual_bwd(u, h, h, r_out, w, w)
+    one = ctp.norm_residual_bwd(u[at], h[at], h[at], r_out[at], w, w)
+    assert torch.equal(d_h[at], one[0]) and torch.equal(d_r[at], one[1])
+    del d_h, d_r, u, r_out
+    tell("large clip")
+    flat = h.view(-1)
+    (clipped,), norm = ctp.clip_grad_norm([flat], 1.0)
+    total = sum(float(flat[k:k + 2 ** 28].double().square().sum()) for k in range(0, flat.numel(), 2 ** 28)) ** 0.5
+    assert abs(float(norm) - total) <= 1e-6 * total
+    factor = np.float32(1.0) / (np.float32(float(norm)) + np.float32(1e-6))
+    for k in (0, 2 ** 31 - 5, 2 ** 31 + 3, flat.numel() - 9):
+        assert torch.equal(clipped[k:k + 9], (flat[k:k + 9].float() * float(factor)).to(torch.bfloat16))
+
+
+def test_example_trains(dev):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import train_energy
+    losses, norms = train_energy.train(steps=30, atoms=200, channels=16, lmax=2, log=None)
+    assert all(np.isfinite(losses)) and all(np.isfinite(norms))
+    assert losses[-1] < 0.5 * losses[0], (losses[0], losses[-1])
