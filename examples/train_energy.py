@@ -1,5 +1,5 @@
 #!/usr/bin/env python3
-"""A small message-passing potential, trained on the energies of synthetic structures.
+"""A small message-passing potential, trained on the energies and forces of synthetic structures.
 
     python examples/train_energy.py [--steps 40] [--atoms 400] [--channels 32] [--lmax 2]
 
@@ -10,11 +10,12 @@ One training step runs the package's operators as a model uses them:
     norm_residual                          r1 = r0 + alpha gate N(h1), u1 = N(r1)
     conv_tp  (degrees in, degrees out)     block 2
     norm_residual                          r2, u2; the scalars of u2 give the energies
-    backward, clip_grad_norm, one step of Adam
+    forces = -dE/d(edge vectors), summed onto atoms (first gradients, kept for the loss)
+    backward of the energy and force loss, clip_grad_norm, one step of Adam
 
 The radial weights of every edge come from a small torch network on Bessel
-functions of the distance.  The targets are a sum over atoms of a number per
-species, which a model can learn through the embedding.
+functions of the distance.  The targets are a number per species for every
+atom and a repulsion exp(-distance) between neighbours.
 """
 from __future__ import annotations
 
@@ -35,7 +36,7 @@ CUTOFF = 4.0
 
 
 def structures(n_atoms, n_structures, device, seed):
-    """Random atoms in boxes of 12 Angstrom, edges within the cutoff, receivers in order; energies per structure."""
+    """Random atoms in boxes of 12 Angstrom, edges within the cutoff, receivers in order; energies and forces."""
     gen = torch.Generator().manual_seed(seed)
     pos = torch.rand(n_atoms, 3, generator=gen) * 12.0
     batch = torch.arange(n_atoms) * n_structures // n_atoms
@@ -45,9 +46,14 @@ def structures(n_atoms, n_structures, device, seed):
     row_ptr = torch.zeros(n_atoms + 1, dtype=torch.int32)
     row_ptr[1:] = torch.cumsum(near.sum(1), 0)
     of_species = torch.randn(SPECIES, generator=gen)
+    vec = pos[recv] - pos[send]
+    pair = torch.exp(-vec.norm(dim=1))
     energy = torch.zeros(n_structures).index_add_(0, batch, of_species[species.long()])
+    energy.index_add_(0, batch[recv], 0.5 * pair)
+    forces = torch.zeros(n_atoms, 3).index_add_(0, recv, pair[:, None] * vec / vec.norm(dim=1, keepdim=True))
     graph = ctp.Graph(n_atoms, row_ptr.to(device), send.to(torch.int32).to(device))
-    return species.to(device), (pos[recv] - pos[send]).to(device), graph, batch.to(device), energy.to(device)
+    edges = (recv.to(device), send.to(device))
+    return species.to(device), vec.to(device), edges, graph, batch.to(device), energy.to(device), forces.to(device)
 
 
 class Potential(torch.nn.Module):
@@ -84,16 +90,20 @@ class Potential(torch.nn.Module):
 def train(steps=40, atoms=400, channels=32, lmax=2, n_structures=8, max_norm=10.0, seed=0, device="cuda:0", log=print):
     """(losses, gradient norms) of every step, as lists."""
     torch.manual_seed(seed)
-    species, vec, graph, batch, energy = structures(atoms, n_structures, torch.device(device), seed)
+    species, vec, (recv, send), graph, batch, energy, forces = structures(atoms, n_structures, torch.device(device), seed)
+    vec.requires_grad_()
     model = Potential(channels, lmax, device)
     params = list(model.parameters())
-    adam = torch.optim.Adam(params, lr=2e-2)
+    adam = torch.optim.Adam(params, lr=1e-2)
     losses, norms = [], []
     per_atom = atoms / n_structures
     for step in range(steps):
         adam.zero_grad()
-        loss = ((model(species, vec, graph, batch, n_structures) - energy) / per_atom).square().mean()
-        loss.backward()
+        e = model(species, vec, graph, batch, n_structures)
+        g, = torch.autograd.grad(e.sum(), vec, create_graph=True)
+        f = torch.zeros_like(forces).index_add(0, send, g).index_add(0, recv, -g)
+        loss = ((e - energy) / per_atom).square().mean() + (f - forces).square().mean()
+        loss.backward(inputs=params)
         grads = [p.grad for p in params]
         _, norm = ctp.clip_grad_norm(grads, max_norm, out=grads)
         adam.step()

@@ -107,6 +107,19 @@ int32_t conv_tp_norm_bwd(const conv_tp_norm_problem *prob, const void *grad_r, c
                          int64_t workspace_bytes, void *stream);
 int32_t conv_tp_norm_bwd_workspace(const conv_tp_norm_problem *prob, int64_t *bytes);
 
+/* The second backward pass, for losses on first gradients (training on
+ * forces): with cotangents a_d_h and a_d_r of conv_tp_norm_bwd's d_h and d_r
+ * (dense; one may be NULL: zero), the gradients of <a_d_h, d_h> + <a_d_r, d_r>
+ * in that call's inputs: g_grad_r, g_grad_u (NULL: not wanted), g_h (with h),
+ * g_r (in r_out, with w_pre) and g_w_post, g_w_pre, g_gate with their
+ * parameters.  All outputs are dense.  The parameters' first gradients have
+ * no cotangents here.  workspace as for conv_tp_norm_bwd. */
+int32_t conv_tp_norm_bwd_bwd(const conv_tp_norm_problem *prob, const void *a_d_h, const void *a_d_r, const void *grad_r,
+                             const void *grad_u, const void *h, const void *r_out, const void *w_post,
+                             const void *w_pre, const void *gate, void *g_grad_r, void *g_grad_u, void *g_h, void *g_r,
+                             void *g_w_post, void *g_w_pre, void *g_gate, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+
 /* ---------------------------------------------------------------------------
  * Clipping by the global norm of n_tensors dense tensors:
  *

@@ -13,4 +13,4 @@ from .ops import (SLOTS, SUMMED, layout, out_dim, degrees, ConvTPBackward, ConvT
                   spherical_harmonics,
                   spherical_harmonics_backward, stream_probe, valu_probe)
 from .train import (clip_grad_norm, embed, embed_bwd, embed_fwd, grad_norm, norm_residual, norm_residual_bwd,  # noqa: F401
-                    norm_residual_fwd)
+                    norm_residual_bwd_bwd, norm_residual_fwd)

@@ -29,7 +29,7 @@ EXPORTS = ("conv_tp_num_paths", "conv_tp_paths", "conv_tp_layout", "conv_tp_coup
 
 # Every symbol include/convtp_train.h declares.
 TRAIN_EXPORTS = ("conv_tp_embed_fwd", "conv_tp_embed_bwd", "conv_tp_embed_bwd_workspace", "conv_tp_norm_fwd",
-                 "conv_tp_norm_bwd", "conv_tp_norm_bwd_workspace", "conv_tp_clip", "conv_tp_clip_workspace",
+                 "conv_tp_norm_bwd", "conv_tp_norm_bwd_bwd", "conv_tp_norm_bwd_workspace", "conv_tp_clip", "conv_tp_clip_workspace",
                  "conv_tp_train_last_error")
 
 
@@ -137,6 +137,7 @@ def train_lib() -> ctypes.CDLL:
         "conv_tp_embed_bwd_workspace": ([ep, i64p], i32),
         "conv_tp_norm_fwd": ([np_] + [vp] * 8, i32),
         "conv_tp_norm_bwd": ([np_] + [vp] * 13 + [i64, vp], i32),
+        "conv_tp_norm_bwd_bwd": ([np_] + [vp] * 17 + [i64, vp], i32),
         "conv_tp_norm_bwd_workspace": ([np_, i64p], i32),
         "conv_tp_clip": ([i32, vp, vp, vp, vp, f32, f32, vp, vp, i64, vp], i32),
         "conv_tp_clip_workspace": ([i32], i64),

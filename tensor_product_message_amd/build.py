@@ -27,8 +27,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libconvtp.so")
 SOURCES = ["convtp_common.hip", "nodetp_kernels.hip", "graph_kernels.hip", "stream_probe.hip", "convtp_api.hip"]
 # the operators of a training step (include/convtp_train.h), apart from the convolution's sources and headers
-TRAIN_SOURCES = ["embed_kernels.hip", "norm_fwd.hip", "norm_bwd.hip", "clip_kernels.hip", "train_api.hip"]
-TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "csrc/norm_common.hpp",
+TRAIN_SOURCES = ["embed_kernels.hip", "norm_fwd.hip", "norm_bwd.hip", "norm_bwd_bwd.hip", "clip_kernels.hip", "train_api.hip"]
+TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "csrc/norm_common.hpp", "csrc/norm_sums.hpp",
                  "../include/convtp_train.h", "../include/convtp.h"]
 # their Python binding, an extension module next to the package's other files
 BINDING_SOURCE = "train_binding.cpp"
@@ -67,10 +67,10 @@ def _compile(job) -> None:
 
 
 def _jobs(objdir: str):
-    jobs = [(TRIPLE_SOURCE, os.path.join(objdir, f"triple_{a}{b}{c}.o"),
-             [f"-DCTP_L1={a}", f"-DCTP_L2={b}", f"-DCTP_L3={c}"]) for a, b, c in TRIPLES]
-    jobs += [(s, os.path.join(objdir, s.replace(".hip", ".o")), []) for s in TRAIN_SOURCES + SOURCES]
-    return jobs
+    single = lambda names: [(s, os.path.join(objdir, s.replace(".hip", ".o")), []) for s in names]  # noqa: E731
+    triples = [(TRIPLE_SOURCE, os.path.join(objdir, f"triple_{a}{b}{c}.o"),
+                [f"-DCTP_L1={a}", f"-DCTP_L2={b}", f"-DCTP_L3={c}"]) for a, b, c in TRIPLES]
+    return single(TRAIN_SOURCES) + triples + single(SOURCES)     # the longest first
 
 
 def _build_binding() -> None:

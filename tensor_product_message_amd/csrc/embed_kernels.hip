@@ -218,7 +218,8 @@ k_embed_few(const T* __restrict__ grad, const void* __restrict__ tokens, O* __re
     __syncthreads();
     if (tl.group != 0 || !on) return;
     for (int w = 1; w < kFewThreads / 64; ++w) add_floats<T>(&part[w][lane * kVec<T>], acc);
-    store_sum<T, O>(d_table + row * table_stride, tl.v, channels, acc, scale);
+    // a row without tokens is zero whatever the scale
+    store_sum<T, O>(d_table + row * table_stride, tl.v, channels, acc, total > 0 ? scale : 0.0f);
 }
 
 // ------------------------------------------------------------ gradient: sort

@@ -3,20 +3,11 @@
 
 #include <algorithm>
 
-#include "norm_common.hpp"
+#include "norm_sums.hpp"
 
 namespace ctp {
 
 namespace {
-
-// Gradients of shared parameters: every workgroup goes through rows
-// blockIdx.x, + gridDim.x, .. and keeps the sums of its columns in registers;
-// k_norm_join adds the workgroups' sums.  More workgroups hide more of a row's
-// two reductions, but each leaves a row of partial sums.
-constexpr int kSums = 3;        // dw_post, dw_pre, dg
-
-// Threads of all workgroups together.
-constexpr int kTotalThreads = 1024 * 256;
 
 // Four waves a SIMD, 128 registers a lane, are what two workgroups of 512 a CU
 // need.  Full: everything is there (h, both norms, both gradients) and a row is no
@@ -36,7 +27,6 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
     const bool has_gr = Full || a.grad_r, has_gu = Full || a.grad_u;
     const float inv = 1.0f / ((float)nl * (float)C);
     const Params<T> post{a.w_post, a.param_dtype != a.dtype, C}, pre{a.w_pre, post.wide, C}, shared{a.gate_p, post.wide, C};
-    const bool fold = kRowsAtOnce > 1 || comps > 1;     // lanes share columns, through row_buf
     // With several vectors a lane their places are worked out again at each use
     // (the compiler must not see that they are the same), and one vector is
     // finished before the next: kept, they would take the registers of the rows.
@@ -230,68 +220,10 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             }
         }
     }
-    // the workgroup's sums: over its rows at once and over the components of a degree, [sum][l][padded channels]
-    const int width = nl * nvec * kVec<T>;
-    float* ws = static_cast<float*>(a.workspace) + (long)blockIdx.x * kSums * width;
-    auto leave = [&](int which, const Floats<T>* acc) {
-        float* to = fold ? row_buf + sub * comps * nvec * kVec<T> : ws + which * width;
-        if (fold) lds_barrier();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!place(i).on) continue;
-#pragma unroll
-            for (int k = 0; k < kVec<T>; k += 4)
-                *reinterpret_cast<float4*>(to + (lane + i * Lanes) * kVec<T> + k) =
-                    make_float4(acc[i].v[k], acc[i].v[k + 1], acc[i].v[k + 2], acc[i].v[k + 3]);
-        }
-        if (!fold) return;
-        lds_barrier();
-        for (int c = threadIdx.x; c < width; c += kNormThreads<Lanes>) {
-            const int l = c / (nvec * kVec<T>), at = c - l * (nvec * kVec<T>);
-            float x = 0.0f;
-            for (int q = 0; q < kRowsAtOnce; ++q)
-                for (int d = l * l; d < (l + 1) * (l + 1); ++d) x += row_buf[(q * comps + d) * (nvec * kVec<T>) + at];
-            ws[which * width + c] = x;
-        }
-    };
+    const GroupSums<T, Lanes, NV> leave{a, row_buf, lane, sub, nvec, nl};
     if (a.d_w_post) leave(0, acc_post);
     if (a.d_w_pre) leave(1, acc_pre);
     if constexpr (G == kGateChannel) leave(2, acc_gate);
-}
-
-// Adds the workgroups' sums: 64 columns a workgroup, whose 16 waves share the
-// groups and meet in LDS.
-constexpr int kJoinWaves = 16;
-
-__global__ void __launch_bounds__(64 * kJoinWaves)
-k_norm_join(const float* __restrict__ ws, int groups, int nl, int channels, int padded, int out_dtype, void* d_post,
-            void* d_pre, void* d_gate) {
-    __shared__ float part[kJoinWaves][64];
-    const int which = blockIdx.y, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    void* out = which == 0 ? d_post : which == 1 ? d_pre : d_gate;
-    if (!out) return;
-    const int width = nl * padded, col = blockIdx.x * 64 + lane;
-    const int l = col / padded, c = col - l * padded;
-    const bool on = col < width && c < channels;
-    float x = 0.0f;
-    if (on) {
-        const float* at = ws + which * width + col;
-#pragma unroll 8
-        for (int g = wave; g < groups; g += kJoinWaves) x += at[(long)g * (kSums * width)];
-    }
-    part[wave][lane] = x;
-    lds_barrier();
-    if (wave != 0 || !on) return;
-    for (int w = 1; w < kJoinWaves; ++w) x += part[w][lane];
-    const long to = (long)l * channels + c;
-    if (out_dtype == kBF16) static_cast<__bf16*>(out)[to] = (__bf16)x;
-    else if (out_dtype == kF16) static_cast<_Float16*>(out)[to] = (_Float16)x;
-    else static_cast<float*>(out)[to] = x;
-}
-
-int bwd_grid(long n_rows, int lanes) {
-    const int at_once = rows_at_once(lanes), threads = std::max(256, lanes);
-    return (int)std::min<long>((n_rows + at_once - 1) / at_once, kTotalThreads / threads);
 }
 
 }  // namespace
@@ -301,7 +233,7 @@ long norm_bwd_workspace(long n_rows, int lmax, int channels) {
     long most = 0;
     for (int kvec : {4, 8}) {
         const int n = row_vectors(lmax, channels, kvec);
-        const long groups = with_shape(n, [&](auto lanes, auto) { return (long)bwd_grid(n_rows, lanes); });
+        const long groups = with_shape(n, [&](auto lanes, auto) { return (long)sums_grid(n_rows, lanes); });
         most = std::max(most, groups * kSums * (n / (lmax + 1)) * kvec * (long)sizeof(float));
     }
     return most;
@@ -316,22 +248,11 @@ hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
         const int n = row_vectors(a.lmax, a.channels, kVec<T>);
         return with_shape(n, [&](auto lanes, auto nv) {
             hipError_t asked = hipSuccess;
-            const int grid = bwd_grid(a.n_rows, lanes);
+            const int grid = sums_grid(a.n_rows, lanes);
             if (grid > 0) {
                 constexpr int kAtOnce = rows_at_once(lanes);
-                // one row in work in fp32, and a second one where both uses of row_buf meet
-                const size_t row_lds = (size_t)kAtOnce * n * kVec<T> * sizeof(float);
-                const bool two = nv > 1 && a.lmax > 0 && a.gate == kGateRow;
-                const size_t lds = two ? 2 * row_lds : kAtOnce > 1 || a.lmax > 0 || nv > 1 ? row_lds : 0;
-                auto go = [&](auto kernel) {
-                    // beyond 64 KB a kernel has to ask
-                    if (lds > 60000)
-                        if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-                            e != hipSuccess)
-                            asked = e;
-                    if (asked == hipSuccess) kernel<<<grid, kNormThreads<lanes>, lds, st>>>(a);
-                };
+                const size_t lds = sums_lds(a, n * kVec<T>, kAtOnce, nv > 1);
+                auto go = [&](auto kernel) { asked = launch_sums(kernel, grid, kNormThreads<lanes>, lds, st, a); };
                 const bool full = a.h && a.w_post && a.w_pre && a.grad_r && a.grad_u && a.channels >= kVec<T>;
                 auto gated = [&](auto g) {
                     if (full) go(k_norm_bwd<T, lanes, nv, g, true>);
@@ -342,13 +263,7 @@ hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
                 else gated(std::integral_constant<int, kGateNone>{});
             }
             if (asked != hipSuccess) return asked;
-            const int padded = (a.channels + kVec<T> - 1) / kVec<T> * kVec<T>, cols = (a.lmax + 1) * padded;
-            void* d_gate = a.gate == kGateChannel ? a.d_gate : nullptr;
-            if (a.d_w_post || a.d_w_pre || d_gate)
-                k_norm_join<<<dim3((cols + 63) / 64, kSums), 64 * kJoinWaves, 0, st>>>(
-                    static_cast<const float*>(a.workspace), grid, a.lmax + 1, a.channels, padded, a.param_dtype,
-                    a.d_w_post, a.d_w_pre, d_gate);
-            return hipGetLastError();
+            return launch_join(a, kVec<T>, grid, st);
         });
     });
 }

@@ -1,0 +1,217 @@
+// Second backward pass of the norms after and before a block: the gradients of
+// <P, d_r> + <Q, d_h>, the outputs of the first backward pass (norm_common.hpp)
+// with cotangents P and Q, in its inputs.  Training on forces needs it: they
+// are first gradients, which the loss differentiates again.  In the notation
+// there, with x^ = s x for h (s1) and r' (s2), per row
+//
+//   EB = s1 (Q - h^ <b Q, h^>)              (dL/dB; Q without w_post)
+//   Ed = P + alpha g w_post EB              (dL/dd: the gradient in grad_r)
+//   EA = s2 (Ed - r^ <b Ed, r^>)            (dL/dA; the gradient in grad_u is w_pre EA)
+//   g_h = -s1^2 (b h^ (<Q, B> - 3 <b Q, h^> <B, h^>) + b Q <B, h^> + B <b Q, h^>)
+//   g_r = -s2^2 (b r^ (<Ed, A> - 3 <b Ed, r^> <A, r^>) + b Ed <A, r^> + A <b Ed, r^>)
+//   g_w_post = sum EB alpha d g,   g_w_pre = sum grad_u EA,   g_gate = sum alpha d w_post EB
+//
+// As in the first pass a row is read once and has two reductions: EB, d and Ed
+// follow from the first four sums, everything else from the second four.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "norm_sums.hpp"
+
+namespace ctp {
+
+namespace {
+
+template <class T, int Lanes, int NV, int G>
+__global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a) {
+    constexpr int kRowsAtOnce = rows_at_once(Lanes);
+    __shared__ float part_s[2][4][kSumWaves<Lanes>];
+    __shared__ float part_t[2][4][kSumWaves<Lanes>];
+    extern __shared__ __align__(16) float row_buf[];
+    RowSum<Lanes, 4> sum_s{part_s}, sum_t{part_t};
+    const int lane = threadIdx.x % Lanes, sub = row_in_group<Lanes>();
+    const int C = a.channels, nvec = (C + kVec<T> - 1) / kVec<T>, nl = a.lmax + 1, comps = nl * nl;
+    const long W = (long)comps * C;
+    const bool has_h = a.h, has_post = a.w_post, has_pre = a.w_pre;
+    const float inv = 1.0f / ((float)nl * (float)C);
+    const Params<T> post{a.w_post, a.param_dtype != a.dtype, C}, pre{a.w_pre, post.wide, C}, shared{a.gate_p, post.wide, C};
+    Floats<T> acc_post[NV] = {}, acc_pre[NV] = {}, acc_gate[NV] = {};
+    auto place = [&](int i) { return place_of<T>(lane + i * Lanes, nvec, comps, C); };
+    auto ones = [] {
+        Floats<T> f;
+#pragma unroll
+        for (int k = 0; k < kVec<T>; ++k) f.v[k] = 1.0f;
+        return f;
+    };
+    for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
+        const long row = row0 + sub;
+        const bool live = row < a.n_rows;
+        vec_t<T> px[NV], qx[NV], hx[NV], rx[NV], grx[NV], gux[NV], gx[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place p = place(i);
+            px[i] = qx[i] = hx[i] = rx[i] = grx[i] = gux[i] = gx[i] = vec_t<T>{};
+            if (!p.on || !live) continue;
+            auto read = [&](const void* x, long stride, unsigned from) {
+                return read_at<T>(row_of<const T>(x, row, stride) + from, p.span, C);
+            };
+            if (a.a_d_r) px[i] = read(a.a_d_r, W, p.from);
+            if (a.a_d_h) qx[i] = read(a.a_d_h, W, p.from);
+            if (has_pre) rx[i] = read(a.r, a.r_stride, p.from);
+            if (a.grad_u) gux[i] = read(a.grad_u, a.grad_u_stride, p.from);
+            if (has_h) hx[i] = read(a.h, a.h_stride, p.from);
+            if (a.grad_r) grx[i] = read(a.grad_r, a.grad_r_stride, p.from);
+            if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p.par_from);
+        }
+        float s[4] = {};        // the squares of h and r', <A, r'>, <b Q, h>
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place p = place(i);
+            settle<T>(px[i], p.span), settle<T>(qx[i], p.span), settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
+            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span), settle<T>(gx[i], p.span);
+            const Floats<T> q = widen<T>(qx[i]), h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
+            const Floats<T> w = has_pre && p.on ? pre.load(p) : Floats<T>{};
+            const float b = inv / (float)(2 * p.l + 1);
+            float qh = 0.0f, qr = 0.0f, qq = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                qh = __builtin_fmaf(h.v[k], h.v[k], qh);
+                qr = __builtin_fmaf(r.v[k], r.v[k], qr);
+                qq = __builtin_fmaf(q.v[k], h.v[k], qq);
+                s[2] = __builtin_fmaf(w.v[k] * gu.v[k], r.v[k], s[2]);
+            }
+            s[0] = __builtin_fmaf(qh, b, s[0]);
+            s[1] = __builtin_fmaf(qr, b, s[1]);
+            s[3] = __builtin_fmaf(qq, b, s[3]);
+        }
+        sum_s(s);
+        const float s1 = has_post ? inv_root(s[0], a.eps) : 1.0f, s2 = has_pre ? inv_root(s[1], a.eps) : 0.0f;
+        const float ar = s2 * s[2], qh = has_post ? s1 * s[3] : 0.0f;      // <A, r^>, <b Q, h^>
+        float t[4] = {};        // <Q, B>, <B, h>, <Ed, A>, <b Ed, r'>
+        Floats<T> B[NV], Ed[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place p = place(i);
+            const bool on = p.on && live;
+            const float b = inv / (float)(2 * p.l + 1);
+            const Floats<T> q = widen<T>(qx[i]), h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
+            Floats<T> d = widen<T>(grx[i]), A{}, w = ones(), g = ones(), dg;
+            Ed[i] = widen<T>(px[i]);
+            if (has_pre && p.on) {
+                const Floats<T> wp = pre.load(p);
+#pragma unroll
+                for (int k = 0; k < kVec<T>; ++k) {
+                    A.v[k] = wp.v[k] * gu.v[k];
+                    d.v[k] = __builtin_fmaf(s2, __builtin_fmaf(-ar * b, r.v[k] * s2, A.v[k]), d.v[k]);
+                }
+            }
+            if (has_post && p.on) w = post.load(p);
+            if constexpr (G == kGateRow) g = widen<T>(gx[i]);
+            if constexpr (G == kGateChannel)
+                if (p.on) g = shared.load(p);
+            float be = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                const float EB = s1 * __builtin_fmaf(-qh, h.v[k] * s1, q.v[k]);
+                const float ad = a.alpha * d.v[k], dy = ad * g.v[k];
+                B[i].v[k] = dy * w.v[k];
+                dg.v[k] = ad * w.v[k] * EB;
+                if (has_h) {
+                    acc_post[i].v[k] = __builtin_fmaf(EB, dy, acc_post[i].v[k]);
+                    Ed[i].v[k] = __builtin_fmaf(a.alpha * g.v[k] * w.v[k], EB, Ed[i].v[k]);
+                }
+                if constexpr (G == kGateChannel) acc_gate[i].v[k] += dg.v[k];
+                t[0] = __builtin_fmaf(q.v[k], B[i].v[k], t[0]);
+                t[1] = __builtin_fmaf(B[i].v[k], h.v[k], t[1]);
+                t[2] = __builtin_fmaf(Ed[i].v[k], A.v[k], t[2]);
+                be = __builtin_fmaf(Ed[i].v[k], r.v[k], be);
+            }
+            t[3] = __builtin_fmaf(be, b, t[3]);
+            if (a.g_grad_r && on) store_left<T>(row_of<T>(a.g_grad_r, row, W) + p.to, p.left, narrow<T>(Ed[i]));
+            if constexpr (G == kGateRow) {
+                if (comps == 1) {
+                    if (on) store_left<T>(row_of<T>(a.d_gate, row, C) + p.to, p.left, narrow<T>(dg));
+                } else if (p.on) {
+                    float* at = row_buf + (sub * comps * nvec + lane + i * Lanes) * kVec<T>;
+#pragma unroll
+                    for (int k = 0; k < kVec<T>; ++k) at[k] = dg.v[k];
+                }
+            }
+        }
+        sum_t(t);
+        const float bh = s1 * t[1], er = s2 * t[3];     // <B, h^>, <b Ed, r^>
+        const float along_h = t[0] - 3.0f * qh * bh, along_r = t[2] - 3.0f * er * ar;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place p = place(i);
+            const bool on = p.on && live;
+            const float b = inv / (float)(2 * p.l + 1);
+            if (has_h) {
+                const Floats<T> q = widen<T>(qx[i]), h = widen<T>(hx[i]);
+                Floats<T> g;
+#pragma unroll
+                for (int k = 0; k < kVec<T>; ++k)
+                    g.v[k] = has_post ? -s1 * s1 * (b * (h.v[k] * s1 * along_h + q.v[k] * bh) + B[i].v[k] * qh) : 0.0f;
+                if (on) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(g));
+            }
+            if (!has_pre) continue;
+            const Floats<T> r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
+            const Floats<T> w = p.on ? pre.load(p) : Floats<T>{};
+            Floats<T> g, gg;
+#pragma unroll
+            for (int k = 0; k < kVec<T>; ++k) {
+                const float rs = r.v[k] * s2, EA = s2 * __builtin_fmaf(-er, rs, Ed[i].v[k]), A = w.v[k] * gu.v[k];
+                acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], EA, acc_pre[i].v[k]);
+                gg.v[k] = w.v[k] * EA;
+                g.v[k] = -s2 * s2 * (b * (rs * along_r + Ed[i].v[k] * ar) + A * er);
+            }
+            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(g));
+            if (on && a.g_grad_u) store_left<T>(row_of<T>(a.g_grad_u, row, W) + p.to, p.left, narrow<T>(gg));
+        }
+        if constexpr (G == kGateRow) {
+            if (comps > 1) {
+                // the components of a degree share the row's gate
+                lds_barrier();
+                for (int i = lane; live && i < nl * nvec; i += Lanes) {
+                    const int l = i / nvec, v = i - l * nvec;
+                    Floats<T> g = {};
+                    for (int d = l * l; d < (l + 1) * (l + 1); ++d) {
+                        const float* at = row_buf + ((sub * comps + d) * nvec + v) * kVec<T>;
+#pragma unroll
+                        for (int k = 0; k < kVec<T>; ++k) g.v[k] += at[k];
+                    }
+                    store_vec<T>(static_cast<T*>(a.d_gate) + (row * nl + l) * C, v, C, narrow<T>(g));
+                }
+                lds_barrier();
+            }
+        }
+    }
+    const GroupSums<T, Lanes, NV> leave{a, row_buf, lane, sub, nvec, nl};
+    if (a.d_w_post) leave(0, acc_post);
+    if (a.d_w_pre) leave(1, acc_pre);
+    if constexpr (G == kGateChannel) leave(2, acc_gate);
+}
+
+}  // namespace
+
+hipError_t launch_norm_bwd_bwd(const NormArgs& a, hipStream_t st) {
+    return with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        const int n = row_vectors(a.lmax, a.channels, kVec<T>);
+        return with_shape(n, [&](auto lanes, auto nv) {
+            const int grid = sums_grid(a.n_rows, lanes);
+            if (grid > 0) {
+                const size_t lds = sums_lds(a, n * kVec<T>, rows_at_once(lanes), false);
+                auto go = [&](auto kernel) { return launch_sums(kernel, grid, kNormThreads<lanes>, lds, st, a); };
+                const hipError_t e = a.gate == kGateRow ? go(k_norm_bwd_bwd<T, lanes, nv, kGateRow>)
+                                     : a.gate == kGateChannel ? go(k_norm_bwd_bwd<T, lanes, nv, kGateChannel>)
+                                                              : go(k_norm_bwd_bwd<T, lanes, nv, kGateNone>);
+                if (e != hipSuccess) return e;
+            }
+            return launch_join(a, kVec<T>, grid, st);
+        });
+    });
+}
+
+}  // namespace ctp

@@ -159,6 +159,51 @@ int check_workspace(const void* ws, int64_t bytes, int64_t wants) {
     return need(ws, wants, 16, "workspace");
 }
 
+// Checks the first backward pass's inputs and the workspace; fills them in.
+int first_bwd_args(const conv_tp_norm_problem* prob, const void* grad_r, const void* grad_u, const void* h,
+                   const void* r_out, const void* w_post, const void* w_pre, const void* gate, void* workspace,
+                   int64_t workspace_bytes, ctp::NormArgs* out) {
+    if (int r = check_norm(prob)) return r;
+    const int64_t row = (int64_t)(prob->lmax + 1) * (prob->lmax + 1) * prob->channels, n = prob->n_rows;
+    const uintptr_t e = size_of(prob->dtype);
+    if (int r = check_norm_arrays(prob, h, w_post, w_pre, gate)) return r;
+    if (int r = need(grad_r, 0, e, "grad_r")) return r;
+    if (int r = need(grad_u, 0, e, "grad_u")) return r;
+    if (grad_u != nullptr && w_pre == nullptr) return fail(CTP_EINVAL, "grad_u without w_pre");
+    if (grad_r != nullptr)
+        if (int r = check_stride(prob->grad_r_stride, row, n, "grad_r_stride")) return r;
+    if (grad_u != nullptr)
+        if (int r = check_stride(prob->grad_u_stride, row, n, "grad_u_stride")) return r;
+    if (w_pre != nullptr) {
+        if (int r = need(r_out, n, e, "r_out")) return r;
+        if (int r = check_stride(prob->r_stride, row, n, "r_stride")) return r;
+    }
+    const int64_t wants = ctp::norm_bwd_workspace(n, prob->lmax, prob->channels);
+    if (int r = check_workspace(workspace, workspace_bytes, wants)) return r;
+    *out = norm_args(prob, h, r_out, w_post, w_pre, gate);
+    out->grad_r = grad_r;
+    out->grad_u = grad_u;
+    out->workspace = workspace;
+    return CTP_OK;
+}
+
+// Checks and fills in the gradients that both backward passes write for h and the parameters.
+int gradient_args(const conv_tp_norm_problem* prob, ctp::NormArgs* a, void* d_h, void* d_w_post, void* d_w_pre, void* d_gate) {
+    const uintptr_t e = size_of(prob->dtype), q = size_of(prob->param_dtype);
+    const int64_t n = prob->n_rows, par = (int64_t)(prob->lmax + 1) * prob->channels;
+    const bool of_row = prob->gate == ctp::kGateRow;
+    if (int r = need(d_h, a->h ? n : 0, e, "the gradient of h")) return r;
+    if (int r = need(d_w_post, a->w_post ? par : 0, q, "the gradient of w_post")) return r;
+    if (int r = need(d_w_pre, a->w_pre ? par : 0, q, "the gradient of w_pre")) return r;
+    if (prob->gate != ctp::kGateNone)
+        if (int r = need(d_gate, of_row ? n : par, of_row ? e : q, "the gradient of gate")) return r;
+    a->d_h = a->h ? d_h : nullptr;
+    a->d_w_post = a->w_post ? d_w_post : nullptr;
+    a->d_w_pre = a->w_pre ? d_w_pre : nullptr;
+    a->d_gate = prob->gate != ctp::kGateNone ? d_gate : nullptr;
+    return CTP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -220,40 +265,36 @@ int32_t conv_tp_norm_bwd(const conv_tp_norm_problem* prob, const void* grad_r, c
                          const void* r_out, const void* w_post, const void* w_pre, const void* gate, void* d_h,
                          void* d_r, void* d_w_post, void* d_w_pre, void* d_gate, void* workspace,
                          int64_t workspace_bytes, void* stream) {
-    if (int r = check_norm(prob)) return r;
-    const int64_t row = (int64_t)(prob->lmax + 1) * (prob->lmax + 1) * prob->channels, par = (int64_t)(prob->lmax + 1) * prob->channels;
-    const uintptr_t e = size_of(prob->dtype), q = size_of(prob->param_dtype);
-    const int64_t n = prob->n_rows;
-    if (int r = check_norm_arrays(prob, h, w_post, w_pre, gate)) return r;
-    if (int r = need(grad_r, 0, e, "grad_r")) return r;
-    if (int r = need(grad_u, 0, e, "grad_u")) return r;
-    if (grad_u != nullptr && w_pre == nullptr) return fail(CTP_EINVAL, "grad_u without w_pre");
-    if (grad_r != nullptr)
-        if (int r = check_stride(prob->grad_r_stride, row, n, "grad_r_stride")) return r;
-    if (grad_u != nullptr)
-        if (int r = check_stride(prob->grad_u_stride, row, n, "grad_u_stride")) return r;
-    if (w_pre != nullptr) {
-        if (int r = need(r_out, n, e, "r_out")) return r;
-        if (int r = check_stride(prob->r_stride, row, n, "r_stride")) return r;
-    }
-    if (int r = need(d_r, n, e, "d_r")) return r;
-    if (int r = need(d_h, h ? n : 0, e, "d_h")) return r;
-    if (int r = need(d_w_post, w_post ? par : 0, q, "d_w_post")) return r;
-    if (int r = need(d_w_pre, w_pre ? par : 0, q, "d_w_pre")) return r;
-    if (prob->gate != ctp::kGateNone)
-        if (int r = need(d_gate, prob->gate == ctp::kGateChannel ? par : n, prob->gate == ctp::kGateChannel ? q : e, "d_gate")) return r;
-    const int64_t wants = ctp::norm_bwd_workspace(n, prob->lmax, prob->channels);
-    if (int r = check_workspace(workspace, workspace_bytes, wants)) return r;
-    ctp::NormArgs a = norm_args(prob, h, r_out, w_post, w_pre, gate);
-    a.grad_r = grad_r;
-    a.grad_u = grad_u;
-    a.d_h = h ? d_h : nullptr;
+    ctp::NormArgs a{};
+    if (int r = first_bwd_args(prob, grad_r, grad_u, h, r_out, w_post, w_pre, gate, workspace, workspace_bytes, &a)) return r;
+    if (int r = need(d_r, prob->n_rows, size_of(prob->dtype), "d_r")) return r;
+    if (int r = gradient_args(prob, &a, d_h, d_w_post, d_w_pre, d_gate)) return r;
     a.d_r = d_r;
-    a.d_w_post = w_post ? d_w_post : nullptr;
-    a.d_w_pre = w_pre ? d_w_pre : nullptr;
-    a.d_gate = prob->gate != ctp::kGateNone ? d_gate : nullptr;
-    a.workspace = workspace;
     return hip_status(ctp::launch_norm_bwd(a, (hipStream_t)stream), "conv_tp_norm_bwd");
+}
+
+int32_t conv_tp_norm_bwd_bwd(const conv_tp_norm_problem* prob, const void* a_d_h, const void* a_d_r, const void* grad_r,
+                             const void* grad_u, const void* h, const void* r_out, const void* w_post,
+                             const void* w_pre, const void* gate, void* g_grad_r, void* g_grad_u, void* g_h, void* g_r,
+                             void* g_w_post, void* g_w_pre, void* g_gate, void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+    ctp::NormArgs a{};
+    if (int r = first_bwd_args(prob, grad_r, grad_u, h, r_out, w_post, w_pre, gate, workspace, workspace_bytes, &a)) return r;
+    const uintptr_t e = size_of(prob->dtype);
+    const int64_t n = prob->n_rows;
+    if (int r = need(a_d_h, 0, e, "a_d_h")) return r;
+    if (int r = need(a_d_r, 0, e, "a_d_r")) return r;
+    if (n > 0 && a_d_h != nullptr && h == nullptr) return fail(CTP_EINVAL, "a_d_h without h");
+    if (int r = need(g_grad_r, 0, e, "g_grad_r")) return r;
+    if (int r = need(g_grad_u, 0, e, "g_grad_u")) return r;
+    if (int r = need(g_r, w_pre ? n : 0, e, "g_r")) return r;
+    if (int r = gradient_args(prob, &a, g_h, g_w_post, g_w_pre, g_gate)) return r;
+    a.a_d_h = a_d_h;
+    a.a_d_r = a_d_r;
+    a.g_grad_r = g_grad_r;
+    a.g_grad_u = w_pre ? g_grad_u : nullptr;
+    a.d_r = w_pre ? g_r : nullptr;
+    return hip_status(ctp::launch_norm_bwd_bwd(a, (hipStream_t)stream), "conv_tp_norm_bwd_bwd");
 }
 
 int64_t conv_tp_clip_workspace(int32_t n_tensors) { return ctp::clip_workspace(n_tensors < 0 ? 0 : n_tensors); }

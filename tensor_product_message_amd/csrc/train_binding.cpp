@@ -37,6 +37,7 @@ struct Library {
     decltype(&conv_tp_embed_bwd_workspace) embed_bwd_workspace;
     decltype(&conv_tp_norm_fwd) norm_fwd;
     decltype(&conv_tp_norm_bwd) norm_bwd;
+    decltype(&conv_tp_norm_bwd_bwd) norm_bwd_bwd;
     decltype(&conv_tp_norm_bwd_workspace) norm_bwd_workspace;
     decltype(&conv_tp_clip) clip;
     decltype(&conv_tp_clip_workspace) clip_workspace;
@@ -360,9 +361,8 @@ PyObject* norm_fwd(PyObject* const* a) {
     return tuple_of({r, wrap_or_none(u)});
 }
 
-// (grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax, workspace)
-PyObject* norm_bwd(PyObject* const* a) {
-    Norm n;
+// a: grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax.
+void read_first_bwd(Norm& n, PyObject* const* a) {
     n.grad_r = maybe_tensor(a[0], "grad_r");
     n.grad_u = maybe_tensor(a[1], "grad_u");
     n.h = maybe_tensor(a[2], "h");
@@ -371,21 +371,59 @@ PyObject* norm_bwd(PyObject* const* a) {
     if (n.grad_u && a[5] == Py_None) bad_value("grad_u without w_pre");
     if (a[5] != Py_None && !n.r) refuse(PyExc_TypeError, "r_out must be a tensor where there is w_pre");
     read_norm(n, a + 4);
-    const Tensor* given_ws = maybe_tensor(a[10], "workspace");
-    const c10::DeviceGuard guard(n.first->device());
+}
+
+std::optional<Tensor> like(const Tensor* t) {
+    if (!t) return std::nullopt;
+    return at::empty(t->sizes(), t->options().requires_grad(false));
+}
+
+void* address(const std::optional<Tensor>& t) { return t ? t->data_ptr() : nullptr; }
+
+Workspace norm_workspace(const Norm& n, const Tensor* given) {
     int64_t bytes = 0;
     check(lib.norm_bwd_workspace(&n.p, &bytes));
-    auto like = [](const Tensor* t) {
-        return t ? std::optional<Tensor>(at::empty(t->sizes(), t->options().requires_grad(false))) : std::nullopt;
-    };
+    return workspace(given, bytes, *n.first);
+}
+
+// (grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax, workspace)
+PyObject* norm_bwd(PyObject* const* a) {
+    Norm n;
+    read_first_bwd(n, a);
+    const Tensor* given_ws = maybe_tensor(a[10], "workspace");
+    const c10::DeviceGuard guard(n.first->device());
     const std::optional<Tensor> d_r = like(n.first), d_h = like(n.h), d_w_post = like(n.w_post), d_w_pre = like(n.w_pre),
                                 d_gate = like(n.gate);
-    auto to = [](const std::optional<Tensor>& t) { return t ? address(*t) : nullptr; };
-    const Workspace ws = workspace(given_ws, bytes, *n.first);
+    const Workspace ws = norm_workspace(n, given_ws);
     check(lib.norm_bwd(&n.p, address(n.grad_r), address(n.grad_u), address(n.h), address(n.r), address(n.w_post),
-                       address(n.w_pre), address(n.gate), to(d_h), to(d_r), to(d_w_post), to(d_w_pre), to(d_gate),
-                       address(ws.t), ws.bytes, stream_of(n.index)));
+                       address(n.w_pre), address(n.gate), address(d_h), address(d_r), address(d_w_post),
+                       address(d_w_pre), address(d_gate), address(ws.t), ws.bytes, stream_of(n.index)));
     return tuple_of({wrap_or_none(d_h), wrap_or_none(d_r), wrap_or_none(d_w_post), wrap_or_none(d_w_pre), wrap_or_none(d_gate)});
+}
+
+// (a_d_h, a_d_r, grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax, workspace)
+PyObject* norm_bwd_bwd(PyObject* const* a) {
+    Norm n;
+    read_first_bwd(n, a + 2);
+    const Tensor *a_d_h = maybe_tensor(a[0], "a_d_h"), *a_d_r = maybe_tensor(a[1], "a_d_r");
+    if (!a_d_h && !a_d_r) refuse(PyExc_TypeError, "a_d_h and a_d_r are both None");
+    if (a_d_h && !n.h) bad_value("a_d_h without h");
+    for (const Tensor* t : {a_d_h, a_d_r})
+        if (t && (t->sizes() != n.first->sizes() || t->scalar_type() != n.first->scalar_type() ||
+                  t->device() != n.first->device() || !t->is_contiguous()))
+            bad_value("a_d_h and a_d_r must be contiguous and of the features' type, shape and device");
+    const Tensor* given_ws = maybe_tensor(a[12], "workspace");
+    const c10::DeviceGuard guard(n.first->device());
+    const std::optional<Tensor> g_gr = like(n.grad_r), g_gu = like(n.grad_u), g_h = like(n.h),
+                                g_r = like(n.w_pre ? n.r : nullptr), g_w_post = like(n.w_post), g_w_pre = like(n.w_pre),
+                                g_gate = like(n.gate);
+    const Workspace ws = norm_workspace(n, given_ws);
+    check(lib.norm_bwd_bwd(&n.p, address(a_d_h), address(a_d_r), address(n.grad_r), address(n.grad_u), address(n.h),
+                           address(n.r), address(n.w_post), address(n.w_pre), address(n.gate), address(g_gr),
+                           address(g_gu), address(g_h), address(g_r), address(g_w_post), address(g_w_pre),
+                           address(g_gate), address(ws.t), ws.bytes, stream_of(n.index)));
+    return tuple_of({wrap_or_none(g_gr), wrap_or_none(g_gu), wrap_or_none(g_h), wrap_or_none(g_r), wrap_or_none(g_w_post),
+                     wrap_or_none(g_w_pre), wrap_or_none(g_gate)});
 }
 
 // ------------------------------------------------------------ clipping
@@ -464,6 +502,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     find(l.embed_bwd_workspace, "conv_tp_embed_bwd_workspace");
     find(l.norm_fwd, "conv_tp_norm_fwd");
     find(l.norm_bwd, "conv_tp_norm_bwd");
+    find(l.norm_bwd_bwd, "conv_tp_norm_bwd_bwd");
     find(l.norm_bwd_workspace, "conv_tp_norm_bwd_workspace");
     find(l.clip, "conv_tp_clip");
     find(l.clip_workspace, "conv_tp_clip_workspace");
@@ -485,6 +524,7 @@ PyMethodDef methods[] = {
     {"embed_bwd", fast(entry<embed_bwd, 7>), METH_FASTCALL, nullptr},
     {"norm_fwd", fast(entry<norm_fwd, 10>), METH_FASTCALL, nullptr},
     {"norm_bwd", fast(entry<norm_bwd, 11>), METH_FASTCALL, nullptr},
+    {"norm_bwd_bwd", fast(entry<norm_bwd_bwd, 13>), METH_FASTCALL, nullptr},
     {"clip", fast(entry<clip, 5>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

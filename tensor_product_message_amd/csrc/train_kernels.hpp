@@ -43,6 +43,8 @@ struct NormArgs {
     void *r_out, *u;        // forward
     const void *grad_r, *grad_u;                // backward (null: zero)
     void *d_h, *d_r, *d_w_post, *d_w_pre, *d_gate;
+    const void *a_d_h, *a_d_r;                  // second backward: cotangents of d_h and d_r, dense (null: zero);
+    void *g_grad_r, *g_grad_u;                  // its gradients in h, r' and the parameters are d_*, these in grad_*
     void* workspace;
     bool stream;            // set by the launch: reads are non-temporal
 };
@@ -52,6 +54,7 @@ constexpr int kMaxNormRow = 16384;
 long norm_bwd_workspace(long n_rows, int lmax, int channels);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st);
+hipError_t launch_norm_bwd_bwd(const NormArgs& a, hipStream_t st);
 
 struct ClipArgs {
     int n_tensors;

@@ -87,6 +87,15 @@ def norm_residual_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate=None, alpha:
     return native().norm_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax, workspace)
 
 
+def norm_residual_bwd_bwd(a_d_h, a_d_r, grad_r, grad_u, h, r_out, w_post, w_pre, gate=None, alpha: float = 1.0,
+                          eps: float = 1e-6, lmax: int = 0, workspace=None):
+    """Gradients (g_grad_r, g_grad_u, g_h, g_r_out, g_w_post, g_w_pre, g_gate) of <a_d_h, d_h> + <a_d_r, d_r> with
+    norm_residual_bwd's d_h and d_r, in its inputs; a_d_h or a_d_r may be None (zero).  None in the place of what
+    is absent."""
+    return native().norm_bwd_bwd(a_d_h, a_d_r, grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax,
+                                 workspace)
+
+
 class NormResidualFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, r, w_post, w_pre, gate, alpha, eps, lmax):
@@ -97,18 +106,40 @@ class NormResidualFunction(torch.autograd.Function):
         return (r_out.view_as(r_out) if h is None else r_out), u
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_r, grad_u):
         h, r_out, w_post, w_pre, gate = ctx.saved_tensors
         if grad_r is None and grad_u is None:
             return (None,) * 8
         grad_r, grad_u = (None if g is None else g.contiguous() for g in (grad_r, grad_u))
-        return (*norm_residual_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate, ctx.alpha, ctx.eps, ctx.lmax),
-                None, None, None)
+        return (*NormResidualBackward.apply(grad_r, grad_u, h, r_out, w_post, w_pre, gate, ctx.alpha, ctx.eps,
+                                            ctx.lmax), None, None, None)
+
+
+class NormResidualBackward(torch.autograd.Function):
+    """The VJP of norm_residual as a function of its own inputs, differentiable once more in the features' gradients
+    (a loss on forces); the parameters' gradients are not differentiated."""
+
+    @staticmethod
+    def forward(ctx, grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax):
+        ctx.save_for_backward(grad_r, grad_u, h, r_out, w_post, w_pre, gate)
+        ctx.alpha, ctx.eps, ctx.lmax = alpha, eps, lmax
+        ctx.set_materialize_grads(False)
+        return norm_residual_bwd(grad_r, grad_u, h, r_out, w_post, w_pre, gate, alpha, eps, lmax)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, a_d_h, a_d_r, *a_params):
+        if any(a is not None for a in a_params):
+            raise NotImplementedError("norm_residual: the gradients of its parameters cannot be differentiated again")
+        if a_d_h is None and a_d_r is None:
+            return (None,) * 10
+        a_d_h, a_d_r = (None if a is None else a.contiguous() for a in (a_d_h, a_d_r))
+        return (*norm_residual_bwd_bwd(a_d_h, a_d_r, *ctx.saved_tensors, ctx.alpha, ctx.eps, ctx.lmax), None, None,
+                None)
 
 
 def norm_residual(h, r, w_post, w_pre, gate=None, alpha: float = 1.0, eps: float = 1e-6, lmax: int = 0):
-    """Differentiable norm_residual_fwd (once)."""
+    """Differentiable norm_residual_fwd (twice in the features, as a loss on forces needs it)."""
     return NormResidualFunction.apply(h, r, w_post, w_pre, gate, float(alpha), float(eps), int(lmax))
 
 

@@ -14,6 +14,7 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t) { return a.n_rows =
 long norm_bwd_workspace(long n_rows, int, int channels) { return 16 * n_rows * channels; }
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t) { return a.n_rows == 0 ? hipSuccess : hipErrorNotSupported; }
 hipError_t launch_norm_bwd(const NormArgs&, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_norm_bwd_bwd(const NormArgs&, hipStream_t) { return hipErrorNotSupported; }
 long clip_workspace(int n_tensors) { return 256 + 8 * n_tensors; }
 hipError_t launch_clip(const ClipArgs&, hipStream_t) { return hipErrorNotSupported; }
 

@@ -598,3 +598,181 @@ def test_example_trains(dev):
     losses, norms = train_energy.train(steps=30, atoms=200, channels=16, lmax=2, log=None)
     assert all(np.isfinite(losses)) and all(np.isfinite(norms))
     assert losses[-1] < 0.5 * losses[0], (losses[0], losses[-1])
+
+
+# ---------------------------------------------------------------- the norms' second backward pass
+
+
+def norm_forward64(h, r, w_post, w_pre, gate, alpha, eps, lmax):
+    """The definition, differentiable: (r', u) of [n, D, C] features and [1 or n, L, C] parameters."""
+    l = degrees(lmax)
+    b = (1.0 / ((lmax + 1) * (2 * l + 1).double() * r.shape[2]))[:, None]
+    stat = lambda x: ((x.square() * b).sum((1, 2), keepdim=True) + eps).rsqrt()  # noqa: E731
+    if h is not None:
+        y = h if w_post is None else h * stat(h) * w_post[:, l]
+        r = r + alpha * (y if gate is None else y * gate[:, l])
+    return r, None if w_pre is None else r * stat(r) * w_pre[:, l]
+
+
+SECOND = ("g_grad_r", "g_grad_u", "g_h", "g_r", "g_w_post", "g_w_pre", "g_gate")
+
+
+def second_ref(w, alpha, eps, lmax, Q, P):
+    """float64 gradients of <Q, d_h> + <P, d_r> in the first backward's inputs, by differentiating the definition
+    twice: r' is a leaf, reached by grad_r directly and by grad_u through the second norm."""
+    leaf = {k: None if v is None else v.clone().requires_grad_() for k, v in w.items()}
+    keys = ("grad_r", "grad_u", "h", "r", "w_post", "w_pre", "gate")
+    rp = leaf["r"]
+    zero = torch.zeros_like(rp)
+    d = zero if leaf["grad_r"] is None else leaf["grad_r"]
+    if leaf["w_pre"] is not None and leaf["grad_u"] is not None:
+        u = norm_forward64(None, rp, None, leaf["w_pre"], None, alpha, eps, lmax)[1]
+        d = d + torch.autograd.grad(u, rp, leaf["grad_u"], create_graph=True)[0]
+    total = (d * P).sum() if P is not None else 0.0 * d.sum()
+    if leaf["h"] is not None and Q is not None:
+        out = norm_forward64(leaf["h"], zero, leaf["w_post"], None, leaf["gate"], alpha, eps, lmax)[0]
+        d_h, = torch.autograd.grad(out, leaf["h"], d, create_graph=True)
+        total = total + (d_h * Q).sum()
+    wants = [leaf[k] for k in keys if leaf[k] is not None]
+    got = iter(torch.autograd.grad(total, wants, allow_unused=True))
+    res = {}
+    for k, name in zip(keys, SECOND):
+        if leaf[k] is not None:
+            g = next(got)
+            res[name] = torch.zeros_like(leaf[k]) if g is None else g
+    return res
+
+
+def second_bounds(w, alpha, eps, lmax, Q, P):
+    """S of every output: the formulas with every term replaced by its absolute value."""
+    l = degrees(lmax)
+    some = next(w[k] for k in ("h", "grad_r", "r") if w[k] is not None)
+    n, D, C = some.shape
+    zero = torch.zeros(n, D, C, dtype=torch.float64)
+    b = (1.0 / ((lmax + 1) * (2 * l + 1).double() * C))[:, None]
+    mag = lambda x: zero if x is None else x.abs()  # noqa: E731
+    per = lambda x: torch.ones(1, D, C, dtype=torch.float64) if x is None else x.abs()[:, l]  # noqa: E731
+    dot = lambda x, y: (x * y).sum((1, 2), keepdim=True)  # noqa: E731
+    stat = lambda x: ((x.square() * b).sum((1, 2), keepdim=True) + eps).rsqrt()  # noqa: E731
+    fold = lambda x: torch.zeros(x.shape[0], lmax + 1, C, dtype=torch.float64).index_add_(1, l, x)  # noqa: E731
+    P, Q, h, r, gr, gu = (mag(x) for x in (P, Q, w["h"], w["r"], w["grad_r"], w["grad_u"]))
+    w1, w2, g = per(w["w_post"]), per(w["w_pre"]), abs(alpha) * per(w["gate"])
+    s1 = stat(h) if w["w_post"] is not None else torch.ones(n, 1, 1, dtype=torch.float64)
+    s2 = stat(r) if w["w_pre"] is not None else torch.zeros(n, 1, 1, dtype=torch.float64)
+    hs, rs, A = s1 * h, s2 * r, w2 * gu
+    ar, qh = dot(A, rs), dot(b * Q, hs) if w["w_post"] is not None else torch.zeros(n, 1, 1, dtype=torch.float64)
+    d, EB = gr + s2 * (A + b * rs * ar), s1 * (Q + hs * qh)
+    Ed, q = P + g * w1 * EB, d * g
+    B = w1 * q
+    bh, er = dot(B, hs), dot(b * Ed, rs)
+    EA = s2 * (Ed + rs * er)
+    dg = fold(abs(alpha) * d * w1 * EB)
+    shared = w["gate"] is None or w["gate"].shape[0] == 1
+    return dict(g_grad_r=Ed, g_grad_u=w2 * EA, g_h=s1 ** 2 * (b * (hs * (dot(Q, B) + 3 * qh * bh) + Q * bh) + B * qh),
+                g_r=s2 ** 2 * (b * (rs * (dot(Ed, A) + 3 * er * ar) + Ed * ar) + A * er),
+                g_w_post=fold(EB * q).sum(0, keepdim=True), g_w_pre=fold(gu * EA).sum(0, keepdim=True),
+                g_gate=dg.sum(0, keepdim=True) if shared else dg)
+
+
+@pytest.mark.parametrize("kind", ["none", "channel", "row"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,lmax,c", [(3, 0, 7), (65, 0, 250), (1100, 0, 130), (33, 0, 2048), (5, 0, 8191),
+                                         (3, 0, 16384), (64, 1, 16), (70, 2, 33), (90, 3, 128), (3, 3, 1024)])
+def test_norm_second_backward(ctp, dev, rows, lmax, c, dtype, kind):
+    """Against double differentiation in float64.  K = 512: a value passes through the first pass's sums and products
+    and as many again; sums over rows add one rounding a row."""
+    param = torch.float32 if (rows + c) % 2 else dtype
+    t, w = norm_case(rows, lmax, c, dtype, param, kind, rows + lmax + c + 7)
+    g = gen(rows)
+    Q, P = normal(g, t["h"].shape, dtype), normal(g, t["h"].shape, dtype)
+    tell("norm second", rows, lmax, c, dtype, param, kind)
+    d = {k: None if v is None else v.to(dev) for k, v in t.items()}
+    Q64, P64 = (x.double().reshape(w["h"].shape) for x in (Q, P))
+    ref, S = second_ref(w, 0.5, 1e-6, lmax, Q64, P64), second_bounds(w, 0.5, 1e-6, lmax, Q64, P64)
+    args = (Q.to(dev), P.to(dev), d["grad_r"], d["grad_u"], d["h"], d["r"], d["w_post"], d["w_pre"], d["gate"], 0.5, 1e-6, lmax)
+    got = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(*args)))
+    assert (got["g_gate"] is None) == (kind == "none")
+    for name, x in ref.items():
+        terms = rows * (2 * lmax + 1) if name.startswith("g_w") or (name == "g_gate" and kind == "channel") else 0
+        close(name, got[name].reshape(x.shape), x, S[name], 512 + terms)
+    again = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(*args)))
+    assert all(got[k] is None or torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("parts", ["no h", "no w_post", "no w_pre", "no grad_r", "no grad_u", "no P", "no Q"])
+def test_norm_second_backward_parts(ctp, dev, parts):
+    rows, lmax, c = 41, 1, 21
+    t, w = norm_case(rows, lmax, c, torch.float32, torch.float32, "none" if parts == "no h" else "channel", 8)
+    g = gen(8)
+    Q, P = (normal(g, t["h"].shape, torch.float32) for _ in range(2))
+    for k in {"no h": ["h", "w_post"], "no w_post": ["w_post"], "no w_pre": ["w_pre", "grad_u"],
+              "no grad_r": ["grad_r"], "no grad_u": ["grad_u"]}.get(parts, []):
+        t[k] = w[k] = None
+    Q = None if parts in ("no h", "no Q") else Q
+    P = None if parts == "no P" else P
+    wide = lambda x: None if x is None else x.double()  # noqa: E731
+    ref, S = second_ref(w, 0.7, 1e-5, lmax, wide(Q), wide(P)), second_bounds(w, 0.7, 1e-5, lmax, wide(Q), wide(P))
+    d = {k: None if v is None else v.to(dev) for k, v in t.items()}
+    to = lambda x: None if x is None else x.to(dev)  # noqa: E731
+    got = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(to(Q), to(P), d["grad_r"], d["grad_u"], d["h"], d["r"],
+                                                     d["w_post"], d["w_pre"], d["gate"], 0.7, 1e-5, lmax)))
+    for name, x in ref.items():
+        if parts == "no w_pre" and name == "g_r":
+            assert got[name] is None        # r' is not an input then
+            continue
+        close(name, got[name].reshape(x.shape), x, S[name], 512 + rows * 3)
+
+
+def test_norm_trains_on_first_gradients(ctp, dev):
+    """A loss on the gradient of an energy, differentiated again through autograd, against float64."""
+    rows, lmax, c = 30, 2, 10
+    t, w = norm_case(rows, lmax, c, torch.float32, torch.float32, "row", 15)
+    keys = ("h", "r", "w_post", "w_pre", "gate")
+
+    def loss_grads(x, forward, a, b):
+        r_out, u = forward(x["h"], x["r"], x["w_post"], x["w_pre"], x["gate"])
+        energy = (u.sin() * a).sum() + (r_out.square() * b).sum()
+        f_h, f_r = torch.autograd.grad(energy, (x["h"], x["r"]), create_graph=True)
+        return torch.autograd.grad(f_h.square().sum() + (f_r * a).sum(), [x[k] for k in keys])
+    x32 = {k: t[k].to(dev).requires_grad_() for k in keys}
+    x64 = {k: w[k].clone().requires_grad_() for k in keys}
+    got = loss_grads(x32, lambda *p: ctp.norm_residual(*p, 0.5, 1e-6, lmax), t["grad_r"].to(dev), t["grad_u"].to(dev))
+    ref = loss_grads(x64, lambda *p: norm_forward64(*p, 0.5, 1e-6, lmax), w["grad_r"], w["grad_u"])
+    for k, g, r in zip(keys, got, ref):
+        assert float((g.double().cpu().reshape(r.shape) - r).abs().max()) <= 2e-5 * float(r.abs().max()), k
+    u = ctp.norm_residual(x32["h"], x32["r"], x32["w_post"], x32["w_pre"], x32["gate"], 0.5, 1e-6, lmax)[1]
+    d_w, = torch.autograd.grad(u.sum(), x32["w_pre"], create_graph=True)
+    with pytest.raises(NotImplementedError):
+        d_w.sum().backward()
+
+
+def test_second_backward_refusals(ctp, dev):
+    f = lambda *s: torch.zeros(s, device=dev)  # noqa: E731
+    x, w = f(2, 8), f(8)
+    for call, err in ((lambda: ctp.norm_residual_bwd_bwd(None, None, x, x, x, x, w, w), TypeError),
+                      (lambda: ctp.norm_residual_bwd_bwd(x, x, x, x, None, x, None, w), ValueError),
+                      (lambda: ctp.norm_residual_bwd_bwd(f(2, 9), x, x, x, x, x, w, w), ValueError),
+                      (lambda: ctp.norm_residual_bwd_bwd(f(2, 16)[:, ::2], x, x, x, x, x, w, w), ValueError),
+                      (lambda: ctp.norm_residual_bwd_bwd(x, x, None, None, x, x, w, w), TypeError)):
+        with pytest.raises(err):
+            call()
+
+
+def test_wide_rows_in_a_graph(ctp, dev):
+    """Kernels that ask for more than 64 KB of LDS are launched in a capture too."""
+    t, _ = norm_case(12, 3, 1024, torch.float32, torch.float32, "row", 2)
+    n = {k: v.to(dev) for k, v in t.items()}
+
+    def step():
+        args = (n["grad_r"], n["grad_u"], n["h"], n["r"], n["w_post"], n["w_pre"], n["gate"], 0.5, 1e-6, 3)
+        return [*ctp.norm_residual_bwd(*args), *ctp.norm_residual_bwd_bwd(n["r"], n["h"], *args)]
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(3):
+        n["h"].normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in captured]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))

@@ -190,3 +190,22 @@ def test_binding_refuses_cpu_tensors():
     for call in (lambda: ctp.embed_fwd(None, ids), lambda: ctp.norm_residual_fwd(x, None, None, None)):
         with pytest.raises(TypeError):
             call()
+
+
+def second(L, p, a_d_h=A, a_d_r=A, grad_r=A, grad_u=A, h=A, r_out=A, w_post=B, w_pre=B, gate=None, g_grad_r=C, g_grad_u=C,
+           g_h=C, g_r=C, g_w_post=D, g_w_pre=D, g_gate=None, ws=D, nbytes=1 << 40):
+    return L.conv_tp_norm_bwd_bwd(ctypes.byref(p), a_d_h, a_d_r, grad_r, grad_u, h, r_out, w_post, w_pre, gate,
+                                  g_grad_r, g_grad_u, g_h, g_r, g_w_post, g_w_pre, g_gate, ws, nbytes, None)
+
+
+def test_norm_second_backward_rejects(capi, L):
+    E, AL = capi.CTP_EINVAL, capi.CTP_EALIGN
+    p = norm(capi)
+    for name in ("r_out", "g_h", "g_r", "g_w_post", "g_w_pre", "ws"):
+        assert second(L, p, **{name: None}) == E, name
+    for name in ("a_d_h", "a_d_r", "grad_r", "grad_u", "h", "r_out", "g_grad_r", "g_grad_u", "g_h", "g_r", "g_w_post", "g_w_pre"):
+        assert second(L, p, **{name: MIS4}) == AL, name
+    assert [second(L, p, w_pre=None), second(L, p, h=None, w_post=None), second(L, norm(capi, gate=1), gate=B),
+            second(L, norm(capi, grad_r_stride=31)), second(L, p, nbytes=0)] == [E] * 5
+    for bad, status in NORM_BAD:
+        assert second(L, norm(capi, **bad)) == getattr(capi, status), bad
