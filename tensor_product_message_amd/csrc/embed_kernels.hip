@@ -682,7 +682,7 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, hipStream_t st) {
         };
         // one row a group until the GPU is full, then four
         if (a.n_tokens <= 1024L * groups) go(k_embed_fwd<T, 1, false>, 1);
-        else if (streams(2 * a.n_tokens * a.channels * (long)sizeof(T))) go(k_embed_fwd<T, 4, true>, 4);
+        else if (streams_out(a.n_tokens * a.channels * (long)sizeof(T))) go(k_embed_fwd<T, 4, true>, 4);
         else go(k_embed_fwd<T, 4, false>, 4);
         return hipGetLastError();
     });

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             }
         };
         if (a.stream) {
+            keep_apart();
             read_row(std::true_type{});
             keep_apart();
         } else {
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
                     acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], rs, acc_pre[i].v[k]);
                 }
             }
-            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(d));
+            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(d), a.stream_out);
             if (!has_h) continue;
             const Floats<T> h = widen<T>(hx[i]);
             Floats<T> w, g, dg;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             }
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) dh.v[k] = s1 * __builtin_fmaf(-c, h.v[k] * s1, dh.v[k]);
-            if (p.on && live) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(dh));
+            if (p.on && live) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(dh), a.stream_out);
         }
         if constexpr (G == kGateRow) {
             if (comps > 1) {
@@ -243,6 +244,7 @@ hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
     NormArgs a = args;
     const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
     a.stream = streams(a.n_rows * row * (2 * !!a.h + !!a.grad_r + !!a.grad_u + !!a.w_pre + 1));
+    a.stream_out = streams_out(a.n_rows * row * (1 + !!a.h));
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         const int n = row_vectors(a.lmax, a.channels, kVec<T>);

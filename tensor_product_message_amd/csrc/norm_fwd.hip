@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_fwd(NormArgs a) {
         }
     };
     if (a.stream) {
+        keep_apart();
         read_row(std::true_type{});
         keep_apart();
     } else {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_fwd(NormArgs a) {
                 for (int k = 0; k < kVec<T>; ++k) f.v[k] *= wg[i].v[k];
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) y[i].v[k] = __builtin_fmaf(a.alpha, f.v[k], y[i].v[k]);
-            if (p[i].on) store_left<T>(out + p[i].to, p[i].left, narrow<T>(y[i]));
+            if (p[i].on) store_left<T>(out + p[i].to, p[i].left, narrow<T>(y[i]), a.stream_out);
         }
     }
     if (!has_pre) return;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_fwd(NormArgs a) {
         Floats<T> f;
 #pragma unroll
         for (int k = 0; k < kVec<T>; ++k) f.v[k] = y[i].v[k] * s2 * wp[i].v[k];
-        if (p[i].on) store_left<T>(u + p[i].to, p[i].left, narrow<T>(f));
+        if (p[i].on) store_left<T>(u + p[i].to, p[i].left, narrow<T>(f), a.stream_out);
     }
 }
 
@@ -132,6 +133,7 @@ hipError_t launch_norm_fwd(const NormArgs& args, hipStream_t st) {
     NormArgs a = args;
     const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
     a.stream = streams(a.n_rows * row * (2 * !!a.h + 1 + !!a.w_pre));
+    a.stream_out = streams_out(a.n_rows * row * (!!a.h + !!a.w_pre));
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         return with_shape(row_vectors(a.lmax, a.channels, kVec<T>), [&](auto lanes, auto nv) {

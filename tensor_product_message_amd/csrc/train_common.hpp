@@ -114,11 +114,22 @@ __device__ __forceinline__ void store_part(T* row, vec_t<T> x, int k) {
     *reinterpret_cast<part_t*>(row + k) = y;
 }
 
-// x to `to`, where `left` > 0 values have room.
+// Around the accesses of one of two branches that differ in cache policy alone: the
+// compiler would make one of them, and drop the policy.
+__device__ __forceinline__ void keep_apart() { asm volatile("; a cache policy of its own" ::: "memory"); }
+
+// x to `to`, where `left` > 0 values have room; stream: see streams_out.
 template <class T>
-__device__ __forceinline__ void store_left(T* to, int left, vec_t<T> x) {
+__device__ __forceinline__ void store_left(T* to, int left, vec_t<T> x, bool stream = false) {
     if (left >= kVec<T>) {
-        *reinterpret_cast<typename Vec<T>::unaligned*>(to) = x;
+        auto* at = reinterpret_cast<typename Vec<T>::unaligned*>(to);
+        if (stream) {
+            keep_apart();
+            __builtin_nontemporal_store(x, at);
+            keep_apart();
+        } else {
+            *at = x;
+        }
         return;
     }
     // the row's last values, in halves of halves of a vector
@@ -193,6 +204,13 @@ __device__ __forceinline__ Floats<T> load_param(const void* row, bool wide, int 
 constexpr long kStreamBytes = 256L << 20;
 inline bool streams(long bytes) { return bytes > kStreamBytes; }
 
+// Whether a call's outputs are written around that cache: where it would not
+// hold them until their consumer.  A norm's gradient and a pass over its two
+// outputs take 222 us with the mark and 238 without it for 268 MB of them, and
+// 166 and 156 us for 134 MB.
+constexpr long kStreamOutBytes = 192L << 20;
+inline bool streams_out(long bytes) { return bytes > kStreamOutBytes; }
+
 // Barrier of the workgroup for what it shares in LDS.  __syncthreads also waits
 // until the waves' stores to memory have arrived, which costs a row of a norm
 // another trip to memory at each of its reductions.
@@ -201,10 +219,6 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
-
-// Ends one of two branches that differ in their reads' cache policy alone: the
-// compiler would make one of them, and drop the policy.
-__device__ __forceinline__ void keep_apart() { asm volatile("; reads with a policy of their own" ::: "memory"); }
 
 // The value of another lane by a DPP control, 0 in rows of 16 lanes outside Rows.
 template <int Ctrl, int Rows = 0xf>

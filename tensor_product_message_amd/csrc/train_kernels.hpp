@@ -46,7 +46,7 @@ struct NormArgs {
     const void *a_d_h, *a_d_r;                  // second backward: cotangents of d_h and d_r, dense (null: zero);
     void *g_grad_r, *g_grad_u;                  // its gradients in h, r' and the parameters are d_*, these in grad_*
     void* workspace;
-    bool stream;            // set by the launch: reads are non-temporal
+    bool stream, stream_out;    // set by the launch: reads, writes are non-temporal
 };
 
 // Largest row: D * channels values.
