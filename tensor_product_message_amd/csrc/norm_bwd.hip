@@ -243,7 +243,8 @@ long norm_bwd_workspace(long n_rows, int lmax, int channels) {
 hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
     NormArgs a = args;
     const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
-    a.stream = streams(a.n_rows * row * (2 * !!a.h + !!a.grad_r + !!a.grad_u + !!a.w_pre + 1));
+    a.stream = streams(a.n_rows * (row * (2 * !!a.h + !!a.grad_r + !!a.grad_u + !!a.w_pre + 1) +
+                                   (a.gate == kGateRow ? 2 * row / (a.lmax + 1) : 0)));
     a.stream_out = streams_out(a.n_rows * row * (1 + !!a.h));
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);

@@ -124,7 +124,9 @@ __device__ __forceinline__ float inv_root(float mean, float eps) { return rsqrtf
 
 // Calls f(lanes, vectors a lane) for the smallest shape that holds a row of n
 // vectors: one vector a lane as long as a workgroup has lanes, since a lane
-// with two has twice the registers and half the waves to hide a row's latency.
+// with two has twice the registers and half the waves to hide a row's latency
+// (gradients of 16384 rows of 512 vectors: 137 us with one, 172 with two;
+// forward, 8192 rows of 512: 59 and 69 us).
 template <class F>
 auto with_shape(int n, F&& f) {
     using std::integral_constant;

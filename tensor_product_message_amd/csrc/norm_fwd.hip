@@ -132,7 +132,7 @@ hipError_t launch_norm_fwd(const NormArgs& args, hipStream_t st) {
     if (args.n_rows == 0) return hipSuccess;
     NormArgs a = args;
     const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
-    a.stream = streams(a.n_rows * row * (2 * !!a.h + 1 + !!a.w_pre));
+    a.stream = streams(a.n_rows * (row * (2 * !!a.h + 1 + !!a.w_pre) + (a.gate == kGateRow ? row / (a.lmax + 1) : 0)));
     a.stream_out = streams_out(a.n_rows * row * (!!a.h + !!a.w_pre));
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);

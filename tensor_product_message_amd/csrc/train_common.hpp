@@ -197,11 +197,11 @@ __device__ __forceinline__ Floats<T> load_param(const void* row, bool wide, int 
     return f;
 }
 
-// Whether a call's reads are marked non-temporal: where it moves more than the
-// 256 MB last-level cache holds, what it reads would only push out what it
-// writes.  Norm gradients over 805 MB take 129 us with the mark and 147 without
-// it; over 60 MB, which an earlier kernel leaves in that cache, 21 and 19 us.
-constexpr long kStreamBytes = 256L << 20;
+// Whether a call's reads are marked non-temporal: where it moves too much for
+// the 256 MB last-level cache to hold its inputs and what else a program uses,
+// they would only push that out.  Norm gradients that move 805, 153 and 93 MB
+// take 137, 36 and 28 us with the mark and 153, 40 and 27 without it.
+constexpr long kStreamBytes = 128L << 20;
 inline bool streams(long bytes) { return bytes > kStreamBytes; }
 
 // Whether a call's outputs are written around that cache: where it would not
