@@ -776,3 +776,19 @@ def test_wide_rows_in_a_graph(ctp, dev):
         torch.cuda.synchronize()
         got = [x.clone() for x in captured]
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,v,c,skew,pad", [
+    (8192, 5000, 40, 3, 0.1), (8192, 200001, 12, 30, 0.0), (8191, 3000, 300, 1, 0.5), (300, 150000, 64, 1, 0.1),
+    (8000, 2100, 1100, 60, 0.0), (8193, 5000, 40, 3, 0.1), (100, 2049, 4100, 1, 0.0), (4097, 70000, 9, 2, 0.0),
+    (5, 0, 16, 1, 0.0),
+])
+def test_embed_bwd_few_tokens_large_tables(ctp, dev, n, v, c, skew, pad, dtype):
+    g = gen(n + v)
+    grad, tok = normal(g, (n, c), dtype), draw_tokens(g, n, v, skew, pad)
+    tell("embed_bwd few", n, v, c, dtype)
+    ref, S, K = embed_bwd_ref(grad, tok, v, 2.0)
+    got = ctp.embed_bwd(grad.to(dev), tok.to(dev), v, 2.0)
+    close("d_table", got, ref, S, K)
+    assert torch.equal(got, ctp.embed_bwd(grad.to(dev), tok.to(torch.int32).to(dev), v, 2.0))
