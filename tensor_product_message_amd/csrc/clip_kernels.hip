@@ -13,6 +13,10 @@
 // The tensors' addresses travel in the kernel arguments (no table to copy to
 // the device, so a call can be captured in a graph); kPerLaunch of them fit
 // into one launch.
+//
+// Memory bounds both kernels: 604 MB of bf16 are read in 105 us (5.8 TB/s), and
+// read and written in 202 us (6.0 TB/s).  21 tensors of 850 KB take 4 and 5 us,
+// little more than an empty kernel.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
