@@ -11,9 +11,13 @@
 //   g_r = -s2^2 (b r^ (<Ed, A> - 3 <b Ed, r^> <A, r^>) + b Ed <A, r^> + A <b Ed, r^>)
 //   g_w_post = sum EB alpha d g,   g_w_pre = sum grad_u EA,   g_gate = sum alpha d w_post EB
 //
-// 16384 rows of 2048 floats take 284 us (1.34 GB, 4.7 TB/s), 8192 rows of 4096
-// bf16 with a gate each 204 us (3.9 TB/s).  As in the first pass a row is read once and has two reductions: EB, d and Ed
+// As in the first pass a row is read once and has two reductions: EB, d and Ed
 // follow from the first four sums, everything else from the second four.
+// Memory bounds it in fp32: 16384 rows of 2048 floats in 238 us (1.34 GB, 5.6
+// TB/s; 308 without marks on the reads and writes, with a branch before every
+// read and the parameters read at each use).  8192 rows of 4096 bf16 with a gate
+// each take 192 us (805 MB, 4.2 TB/s): dozens of operations a value, which only
+// two workgroups a CU hide; 215 with the registers of one.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -24,8 +28,9 @@ namespace ctp {
 
 namespace {
 
-template <class T, int Lanes, int NV, int G>
-__global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a) {
+// Full: everything is there, as in the first pass.
+template <class T, int Lanes, int NV, int G, bool Full>
+__global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd_bwd(NormArgs a) {
     constexpr int kRowsAtOnce = rows_at_once(Lanes);
     __shared__ float part_s[2][4][kSumWaves<Lanes>];
     __shared__ float part_t[2][4][kSumWaves<Lanes>];
@@ -34,11 +39,32 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
     const int lane = threadIdx.x % Lanes, sub = row_in_group<Lanes>();
     const int C = a.channels, nvec = (C + kVec<T> - 1) / kVec<T>, nl = a.lmax + 1, comps = nl * nl;
     const long W = (long)comps * C;
-    const bool has_h = a.h, has_post = a.w_post, has_pre = a.w_pre;
+    const bool has_h = Full || a.h, has_post = Full || a.w_post, has_pre = Full || a.w_pre;
     const float inv = 1.0f / ((float)nl * (float)C);
     const Params<T> post{a.w_post, a.param_dtype != a.dtype, C}, pre{a.w_pre, post.wide, C}, shared{a.gate_p, post.wide, C};
-    Floats<T> acc_post[NV] = {}, acc_pre[NV] = {}, acc_gate[NV] = {};
-    auto place = [&](int i) { return place_of<T>(lane + i * Lanes, nvec, comps, C); };
+    // Places and parameters are kept where a lane has one vector of four values,
+    // else worked out and read again: 128 registers, with which two workgroups of
+    // 512 fit on a CU, do not hold eight values of each.
+    constexpr bool kKeep = NV == 1 && kVec<T> == 4;
+    const Place p0 = place_of<T>(lane, nvec, comps, C);
+    auto place = [&](int i) {
+        if (kKeep) return p0;
+        __builtin_amdgcn_sched_barrier(0);
+        int at = lane + i * Lanes;
+        forget(at);
+        return place_of<T>(at, nvec, comps, C);
+    };
+    Floats<T> wq0{}, wp0{}, wg0{};
+    Floats<T> acc_post[NV] = {}, acc_pre[NV] = {}, acc_gate[G == kGateChannel ? NV : 1] = {};
+    if (kKeep && p0.on) {
+        if (has_post) wq0 = post.load(p0);
+        if (has_pre) wp0 = pre.load(p0);
+        if constexpr (G == kGateChannel) wg0 = shared.load(p0);
+    }
+    auto w_pre = [&](const Place& p) {
+        if (kKeep) return wp0;
+        return has_pre && p.on ? pre.load(p) : Floats<T>{};
+    };
     auto ones = [] {
         Floats<T> f;
 #pragma unroll
@@ -48,31 +74,47 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
     for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
         const long row = row0 + sub;
         const bool live = row < a.n_rows;
-        vec_t<T> px[NV], qx[NV], hx[NV], rx[NV], grx[NV], gux[NV], gx[NV];
+        vec_t<T> px[NV], qx[NV], hx[NV], rx[NV], grx[NV], gux[NV], gx[G == kGateRow ? NV : 1];
+        auto read_row = [&](auto stream) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Place p = place(i);
+                px[i] = qx[i] = hx[i] = rx[i] = grx[i] = gux[i] = vec_t<T>{};
+                if constexpr (G == kGateRow) gx[i] = vec_t<T>{};
+                if (!p.on || !live) continue;
+                auto read = [&](const void* x, long stride, unsigned from) {
+                    return read_at<T, Full, stream>(row_of<const T>(x, row, stride) + from, p.span, C);
+                };
+                if (Full || a.a_d_h) qx[i] = read(a.a_d_h, W, p.from);
+                if (has_pre) rx[i] = read(a.r, a.r_stride, p.from);
+                if (Full || a.grad_u) gux[i] = read(a.grad_u, a.grad_u_stride, p.from);
+                if (has_h) hx[i] = read(a.h, a.h_stride, p.from);
+                if (Full || a.grad_r) grx[i] = read(a.grad_r, a.grad_r_stride, p.from);
+                if (Full || a.a_d_r) px[i] = read(a.a_d_r, W, p.from);
+                if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p.par_from);
+            }
+        };
+        if (a.stream) {
+            keep_apart();
+            read_row(std::true_type{});
+            keep_apart();
+        } else {
+            read_row(std::false_type{});
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place p = place(i);
-            px[i] = qx[i] = hx[i] = rx[i] = grx[i] = gux[i] = gx[i] = vec_t<T>{};
-            if (!p.on || !live) continue;
-            auto read = [&](const void* x, long stride, unsigned from) {
-                return read_at<T>(row_of<const T>(x, row, stride) + from, p.span, C);
-            };
-            if (a.a_d_r) px[i] = read(a.a_d_r, W, p.from);
-            if (a.a_d_h) qx[i] = read(a.a_d_h, W, p.from);
-            if (has_pre) rx[i] = read(a.r, a.r_stride, p.from);
-            if (a.grad_u) gux[i] = read(a.grad_u, a.grad_u_stride, p.from);
-            if (has_h) hx[i] = read(a.h, a.h_stride, p.from);
-            if (a.grad_r) grx[i] = read(a.grad_r, a.grad_r_stride, p.from);
-            if constexpr (G == kGateRow) gx[i] = read(a.gate_p, a.gate_stride, p.par_from);
+            if (p.span.shift <= 0) continue;
+            settle<T>(px[i], p.span), settle<T>(qx[i], p.span), settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
+            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p.span);
         }
         float s[4] = {};        // the squares of h and r', <A, r'>, <b Q, h>
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place p = place(i);
-            settle<T>(px[i], p.span), settle<T>(qx[i], p.span), settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
-            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span), settle<T>(gx[i], p.span);
             const Floats<T> q = widen<T>(qx[i]), h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
-            const Floats<T> w = has_pre && p.on ? pre.load(p) : Floats<T>{};
+            const Floats<T> w = w_pre(p);
             const float b = inv / (float)(2 * p.l + 1);
             float qh = 0.0f, qr = 0.0f, qq = 0.0f;
 #pragma unroll
@@ -87,6 +129,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
             s[3] = __builtin_fmaf(qq, b, s[3]);
         }
         sum_s(s);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) forget(qx[i]), forget(hx[i]), forget(rx[i]), forget(gux[i]);
         const float s1 = has_post ? inv_root(s[0], a.eps) : 1.0f, s2 = has_pre ? inv_root(s[1], a.eps) : 0.0f;
         const float ar = s2 * s[2], qh = has_post ? s1 * s[3] : 0.0f;      // <A, r^>, <b Q, h^>
         float t[4] = {};        // <Q, B>, <B, h>, <Ed, A>, <b Ed, r'>
@@ -96,40 +140,36 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
             const Place p = place(i);
             const bool on = p.on && live;
             const float b = inv / (float)(2 * p.l + 1);
-            const Floats<T> q = widen<T>(qx[i]), h = widen<T>(hx[i]), r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
-            Floats<T> d = widen<T>(grx[i]), A{}, w = ones(), g = ones(), dg;
-            Ed[i] = widen<T>(px[i]);
-            if (has_pre && p.on) {
-                const Floats<T> wp = pre.load(p);
-#pragma unroll
-                for (int k = 0; k < kVec<T>; ++k) {
-                    A.v[k] = wp.v[k] * gu.v[k];
-                    d.v[k] = __builtin_fmaf(s2, __builtin_fmaf(-ar * b, r.v[k] * s2, A.v[k]), d.v[k]);
-                }
-            }
-            if (has_post && p.on) w = post.load(p);
-            if constexpr (G == kGateRow) g = widen<T>(gx[i]);
+            Floats<T> w = ones(), wp{}, g = ones(), dg;
+            if (has_pre) wp = w_pre(p);
+            if (has_post && p.on) w = kKeep ? wq0 : post.load(p);
             if constexpr (G == kGateChannel)
-                if (p.on) g = shared.load(p);
+                if (p.on) g = kKeep ? wg0 : shared.load(p);
             float be = 0.0f;
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) {
-                const float EB = s1 * __builtin_fmaf(-qh, h.v[k] * s1, q.v[k]);
-                const float ad = a.alpha * d.v[k], dy = ad * g.v[k];
+                if (k == 4) __builtin_amdgcn_sched_barrier(0);      // fp32 values of half a vector at a time
+                const float q = (float)qx[i][k], h = (float)hx[i][k], r = (float)rx[i][k];
+                const float A = wp.v[k] * (float)gux[i][k];
+                const float d = __builtin_fmaf(s2, __builtin_fmaf(-ar * b, r * s2, A), (float)grx[i][k]);
+                if constexpr (G == kGateRow) g.v[k] = (float)gx[i][k];
+                const float EB = s1 * __builtin_fmaf(-qh, h * s1, q);
+                const float ad = a.alpha * d, dy = ad * g.v[k];
                 B[i].v[k] = dy * w.v[k];
                 dg.v[k] = ad * w.v[k] * EB;
+                Ed[i].v[k] = (float)px[i][k];
                 if (has_h) {
                     acc_post[i].v[k] = __builtin_fmaf(EB, dy, acc_post[i].v[k]);
                     Ed[i].v[k] = __builtin_fmaf(a.alpha * g.v[k] * w.v[k], EB, Ed[i].v[k]);
                 }
                 if constexpr (G == kGateChannel) acc_gate[i].v[k] += dg.v[k];
-                t[0] = __builtin_fmaf(q.v[k], B[i].v[k], t[0]);
-                t[1] = __builtin_fmaf(B[i].v[k], h.v[k], t[1]);
-                t[2] = __builtin_fmaf(Ed[i].v[k], A.v[k], t[2]);
-                be = __builtin_fmaf(Ed[i].v[k], r.v[k], be);
+                t[0] = __builtin_fmaf(q, B[i].v[k], t[0]);
+                t[1] = __builtin_fmaf(B[i].v[k], h, t[1]);
+                t[2] = __builtin_fmaf(Ed[i].v[k], A, t[2]);
+                be = __builtin_fmaf(Ed[i].v[k], r, be);
             }
             t[3] = __builtin_fmaf(be, b, t[3]);
-            if (a.g_grad_r && on) store_left<T>(row_of<T>(a.g_grad_r, row, W) + p.to, p.left, narrow<T>(Ed[i]));
+            if (a.g_grad_r && on) store_left<T>(row_of<T>(a.g_grad_r, row, W) + p.to, p.left, narrow<T>(Ed[i]), a.stream_out);
             if constexpr (G == kGateRow) {
                 if (comps == 1) {
                     if (on) store_left<T>(row_of<T>(a.d_gate, row, C) + p.to, p.left, narrow<T>(dg));
@@ -141,6 +181,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
             }
         }
         sum_t(t);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) forget(qx[i]), forget(hx[i]), forget(rx[i]), forget(gux[i]);
         const float bh = s1 * t[1], er = s2 * t[3];     // <B, h^>, <b Ed, r^>
         const float along_h = t[0] - 3.0f * qh * bh, along_r = t[2] - 3.0f * er * ar;
 #pragma unroll
@@ -154,11 +196,11 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
 #pragma unroll
                 for (int k = 0; k < kVec<T>; ++k)
                     g.v[k] = has_post ? -s1 * s1 * (b * (h.v[k] * s1 * along_h + q.v[k] * bh) + B[i].v[k] * qh) : 0.0f;
-                if (on) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(g));
+                if (on) store_left<T>(row_of<T>(a.d_h, row, W) + p.to, p.left, narrow<T>(g), a.stream_out);
             }
             if (!has_pre) continue;
             const Floats<T> r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
-            const Floats<T> w = p.on ? pre.load(p) : Floats<T>{};
+            const Floats<T> w = w_pre(p);
             Floats<T> g, gg;
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) {
@@ -167,8 +209,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
                 gg.v[k] = w.v[k] * EA;
                 g.v[k] = -s2 * s2 * (b * (rs * along_r + Ed[i].v[k] * ar) + A * er);
             }
-            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(g));
-            if (on && a.g_grad_u) store_left<T>(row_of<T>(a.g_grad_u, row, W) + p.to, p.left, narrow<T>(gg));
+            if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(g), a.stream_out);
+            if (on && a.g_grad_u) store_left<T>(row_of<T>(a.g_grad_u, row, W) + p.to, p.left, narrow<T>(gg), a.stream_out);
         }
         if constexpr (G == kGateRow) {
             if (comps > 1) {
@@ -196,7 +238,13 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_bwd_bwd(NormArgs a
 
 }  // namespace
 
-hipError_t launch_norm_bwd_bwd(const NormArgs& a, hipStream_t st) {
+hipError_t launch_norm_bwd_bwd(const NormArgs& args, hipStream_t st) {
+    NormArgs a = args;
+    const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.channels * (a.dtype == kF32 ? 4 : 2);
+    const long outs = !!a.h + !!a.w_pre + !!a.g_grad_r + (a.w_pre && a.g_grad_u);
+    a.stream = streams(a.n_rows * (row * (outs + !!a.h + !!a.w_pre + !!a.grad_r + !!a.grad_u + !!a.a_d_r + !!a.a_d_h) +
+                                   (a.gate == kGateRow ? 2 * row / (a.lmax + 1) : 0)));
+    a.stream_out = streams_out(a.n_rows * row * outs);
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         const int n = row_vectors(a.lmax, a.channels, kVec<T>);
@@ -205,9 +253,13 @@ hipError_t launch_norm_bwd_bwd(const NormArgs& a, hipStream_t st) {
             if (grid > 0) {
                 const size_t lds = sums_lds(a, n * kVec<T>, rows_at_once(lanes), false);
                 auto go = [&](auto kernel) { return launch_sums(kernel, grid, kNormThreads<lanes>, lds, st, a); };
-                const hipError_t e = a.gate == kGateRow ? go(k_norm_bwd_bwd<T, lanes, nv, kGateRow>)
-                                     : a.gate == kGateChannel ? go(k_norm_bwd_bwd<T, lanes, nv, kGateChannel>)
-                                                              : go(k_norm_bwd_bwd<T, lanes, nv, kGateNone>);
+                const bool full = a.h && a.w_post && a.w_pre && a.grad_r && a.grad_u && a.a_d_r && a.a_d_h && a.channels >= kVec<T>;
+                auto gated = [&](auto g) {
+                    return full ? go(k_norm_bwd_bwd<T, lanes, nv, g, true>) : go(k_norm_bwd_bwd<T, lanes, nv, g, false>);
+                };
+                const hipError_t e = a.gate == kGateRow ? gated(std::integral_constant<int, kGateRow>{})
+                                     : a.gate == kGateChannel ? gated(std::integral_constant<int, kGateChannel>{})
+                                                              : gated(std::integral_constant<int, kGateNone>{});
                 if (e != hipSuccess) return e;
             }
             return launch_join(a, kVec<T>, grid, st);
