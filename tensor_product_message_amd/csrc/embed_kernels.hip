@@ -38,6 +38,7 @@ __device__ __forceinline__ int token_at(const void* tokens, int wide, long t, in
 // A row is shared by 2^lg lanes, one 16-byte vector each at a time; every
 // group of lanes looks up four rows at once so that four reads are in flight
 // (one by one is no faster for few rows either).
+// Memory bounds it: 32768 rows of 1024 bf16 in 23 us (134 MB at most, 5.8 TB/s).
 // Stream: an output that the last-level cache does not hold is written around
 // it, which leaves it to the table (262144 rows of 512 floats: 125 us, 162
 // without).
@@ -235,7 +236,8 @@ k_embed_few(const T* __restrict__ grad, const void* __restrict__ tokens, O* __re
 // tokens stably.  Up to 10 bits a pass: 2 passes sort a million-row table, 1 a
 // table of elements.  With one tile its own counts are all there are, and the
 // first kernel is left out.  At most 64 tiles: every tile reads the counts of
-// all of them, one digit a thread.
+// all of them, one digit a thread.  The two kernels of a pass over 131072 tokens
+// take 3 and 9 us, a few memory latencies each and not bandwidth.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 10;
@@ -397,7 +399,9 @@ __device__ __forceinline__ F* partial_row(F* base, long j, const Tile<Threads>& 
 }
 
 // Workgroups below `chunk_wgs` sum chunks, one a group of lanes; the others write
-// the zero rows of the table.
+// the zero rows of the table.  131072 rows of 128 floats under 100 ids take 15 us
+// (61 MB without the padding, 4.1 TB/s), 16384 rows of 2048 bf16 under 131072 ids
+// 106 us (604 MB, most of them zeros, 5.7 TB/s).
 template <class T, class O>
 __global__ void __launch_bounds__(kThreads)
 k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int channels, float scale, long grad_stride,
@@ -504,7 +508,8 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
 // reaches, which are those that begin with its id.  Every group of lanes looks
 // at one span and joins a run over a few of them by itself; longer runs (hot
 // tokens) are then joined by the whole workgroup one after the other, since
-// the longest decides how long the kernel takes.
+// the longest decides how long the kernel takes (6.6 us for 131072 tokens of 100
+// ids and 128 floats).
 constexpr int kJoinThreads = 1024;
 constexpr int kShortRun = 8;        // chunks that a short run reaches beyond its own
 

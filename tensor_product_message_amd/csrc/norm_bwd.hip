@@ -12,9 +12,10 @@ namespace {
 // Memory bounds it: 16384 rows of 2048 floats in 139 us (805 MB, 5.8 TB/s), 8192
 // rows of 4096 bf16 with a gate each in 107 us (537 MB, 5.0 TB/s); short of that,
 // 5001 rows of 1003 halves in 22 us (60 MB), a row's two reductions and the
-// partial sums.  Four waves a SIMD, 128 registers a lane, are what two workgroups of 512 a CU
-// need.  Full: everything is there (h, both norms, both gradients) and a row is no
-// shorter than a vector, so that a row's reads are issued in one straight line.
+// partial sums.  Four waves a SIMD, 128 registers a lane, are what two
+// workgroups of 512 a CU need.  Full: everything is there (h, both norms, both
+// gradients) and a row is no shorter than a vector, so that a row's reads are
+// issued in one straight line.
 template <class T, int Lanes, int NV, int G, bool Full>
 __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a) {
     constexpr int kRowsAtOnce = rows_at_once(Lanes);
