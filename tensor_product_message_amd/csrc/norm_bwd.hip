@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
     };
     for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
         const long row = row0 + sub;
-        const bool live = row < a.n_rows;
+        const bool live = is_row<Lanes>(row, a.n_rows);
         vec_t<T> hx[NV], rx[NV], grx[NV], gux[NV], gx[G == kGateRow ? NV : 1];
         auto read_row = [&](auto stream) {
 #pragma unroll
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             const Place p = place(i);
             const float b = NV == 1 ? b0 : weight(p);
             Floats<T> B{};
-            const bool on = p.on && live;    // the others work on zeros
+            const bool on = p.on && live;
             Floats<T> d = widen<T>(grx[i]);
             if (has_pre) {
                 const Floats<T> r = widen<T>(rx[i]), gu = widen<T>(gux[i]);
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
                 for (int k = 0; k < kVec<T>; ++k) {
                     const float rs = r.v[k] * s2;
                     d.v[k] = __builtin_fmaf(s2, __builtin_fmaf(-c, rs, w.v[k] * gu.v[k]), d.v[k]);
-                    acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], rs, acc_pre[i].v[k]);
+                    if (live) acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], rs, acc_pre[i].v[k]);
                 }
             }
             if (on) store_left<T>(row_of<T>(a.d_r, row, W) + p.to, p.left, narrow<T>(d), a.stream_out);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             for (int k = 0; k < kVec<T>; ++k) {
                 const float ad = a.alpha * d.v[k], hs = h.v[k] * s1, dy = ad * g.v[k];
                 dg.v[k] = ad * hs * w.v[k];
-                acc_post[i].v[k] = __builtin_fmaf(dy, hs, acc_post[i].v[k]);
+                if (live) acc_post[i].v[k] = __builtin_fmaf(dy, hs, acc_post[i].v[k]);
                 B.v[k] = dy * w.v[k];
                 t[0] = __builtin_fmaf(B.v[k], h.v[k], t[0]);
             }
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
             }
             if constexpr (G == kGateChannel) {
 #pragma unroll
-                for (int k = 0; k < kVec<T>; ++k) acc_gate[i].v[k] += dg.v[k];
+                for (int k = 0; k < kVec<T>; ++k)
+                    if (live) acc_gate[i].v[k] += dg.v[k];
             }
             if constexpr (G == kGateRow) {
                 if (comps == 1) {

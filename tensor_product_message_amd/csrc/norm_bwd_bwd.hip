@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd_bwd(NormArg
     };
     for (long row0 = (long)blockIdx.x * kRowsAtOnce; row0 < a.n_rows; row0 += (long)gridDim.x * kRowsAtOnce) {
         const long row = row0 + sub;
-        const bool live = row < a.n_rows;
+        const bool live = is_row<Lanes>(row, a.n_rows);
         vec_t<T> px[NV], qx[NV], hx[NV], rx[NV], grx[NV], gux[NV], gx[G == kGateRow ? NV : 1];
         auto read_row = [&](auto stream) {
 #pragma unroll
@@ -159,10 +159,11 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd_bwd(NormArg
                 dg.v[k] = ad * w.v[k] * EB;
                 Ed[i].v[k] = (float)px[i][k];
                 if (has_h) {
-                    acc_post[i].v[k] = __builtin_fmaf(EB, dy, acc_post[i].v[k]);
+                    if (live) acc_post[i].v[k] = __builtin_fmaf(EB, dy, acc_post[i].v[k]);
                     Ed[i].v[k] = __builtin_fmaf(a.alpha * g.v[k] * w.v[k], EB, Ed[i].v[k]);
                 }
-                if constexpr (G == kGateChannel) acc_gate[i].v[k] += dg.v[k];
+                if constexpr (G == kGateChannel)
+                    if (live) acc_gate[i].v[k] += dg.v[k];
                 t[0] = __builtin_fmaf(q, B[i].v[k], t[0]);
                 t[1] = __builtin_fmaf(B[i].v[k], h, t[1]);
                 t[2] = __builtin_fmaf(Ed[i].v[k], A, t[2]);
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd_bwd(NormArg
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) {
                 const float rs = r.v[k] * s2, EA = s2 * __builtin_fmaf(-er, rs, Ed[i].v[k]), A = w.v[k] * gu.v[k];
-                acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], EA, acc_pre[i].v[k]);
+                if (live) acc_pre[i].v[k] = __builtin_fmaf(gu.v[k], EA, acc_pre[i].v[k]);
                 gg.v[k] = w.v[k] * EA;
                 g.v[k] = -s2 * s2 * (b * (rs * along_r + Ed[i].v[k] * ar) + A * er);
             }

@@ -22,6 +22,15 @@ inline int sums_grid(long n_rows, int lanes) {
     return (int)std::min<long>((n_rows + at_once - 1) / at_once, kTotalThreads / threads);
 }
 
+// Whether a workgroup's place has a row.  Where rows share a workgroup the last
+// ones may have none: those places take part in the reductions with vectors of
+// zeros, but not in the column sums, since what multiplies the zeros may not be
+// finite (s without eps, a parameter of the caller's).
+template <int Lanes>
+__device__ __forceinline__ bool is_row(long row, long n_rows) {
+    return rows_at_once(Lanes) == 1 || row < n_rows;
+}
+
 // Bytes of LDS for the rows in work, in fp32, where lanes share sums or wait
 // with several vectors a lane (`waits`), and for both where they meet.
 inline size_t sums_lds(const NormArgs& a, int row_values, int at_once, bool waits) {

@@ -1,0 +1,77 @@
+"""The training-step operators at the ends of their documented ranges.  Forms,
+bounds and their derivation are test_gpu_train.py's."""
+import pytest
+import torch
+
+from tests.test_gpu_train import (SECOND, close, ctp, dev, gen, norm_case, norm_ref, normal,  # noqa: F401
+                                  second_bounds, second_ref, tell)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- rows that a workgroup has too many
+
+
+# Rows of up to 16, 64 and 128 vectors share a workgroup, 16, 4 and 2 at once; wider ones have it to themselves.
+UNEVEN = [  # rows, lmax, channels
+    (1, 0, 8), (5, 0, 64), (17, 0, 40), (3, 0, 250), (5, 0, 500), (1, 0, 1003), (3, 0, 1100), (3, 0, 2048), (5, 1, 5),
+    (17, 2, 9), (7, 3, 8), (31, 3, 16), (1, 2, 33),
+]
+
+
+@pytest.mark.parametrize("kind", ["none", "channel", "row"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,lmax,c", UNEVEN)
+def test_norm_gradients_without_eps(ctp, dev, rows, lmax, c, dtype, kind):
+    """eps = 0 and no row of zeros: everything is finite, whatever a workgroup's places without a row hold."""
+    t, w = norm_case(rows, lmax, c, dtype, torch.float32 if c % 2 else dtype, kind, rows + lmax + c + 1)
+    tell("norm eps 0", rows, lmax, c, dtype, kind)
+    d = {k: None if v is None else v.to(dev) for k, v in t.items()}
+    args = (d["grad_r"], d["grad_u"], d["h"], d["r"], d["w_post"], d["w_pre"], d["gate"], 0.5, 0.0, lmax)
+    terms = rows * (2 * lmax + 1)
+
+    def shared(name):
+        return "_w_" in name or (name.endswith("gate") and kind == "channel")
+    got = dict(zip(("d_h", "d_r", "d_w_post", "d_w_pre", "d_gate"), ctp.norm_residual_bwd(*args)))
+    ref = norm_ref(w["h"], w["r"], w["w_post"], w["w_pre"], w["gate"], 0.5, 0.0, lmax, w["grad_r"], w["grad_u"])
+    for name, (x, S) in ref.items():
+        close(name, got[name].reshape(x.shape), x, S, 256 + terms * shared(name))
+    g = gen(rows + c)
+    Q, P = normal(g, t["h"].shape, dtype), normal(g, t["h"].shape, dtype)
+    Q64, P64 = (x.double().reshape(w["h"].shape) for x in (Q, P))
+    got = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(Q.to(dev), P.to(dev), *args)))
+    ref, S = second_ref(w, 0.5, 0.0, lmax, Q64, P64), second_bounds(w, 0.5, 0.0, lmax, Q64, P64)
+    for name, x in ref.items():
+        close(name, got[name].reshape(x.shape), x, S[name], 512 + terms * shared(name))
+
+
+@pytest.mark.parametrize("c", [8, 250, 500])
+def test_norm_gradients_of_infinite_parameters(ctp, dev, c):
+    """One row in a workgroup of 16, 4 or 2: an infinite parameter gives the other one's gradient infinity in its
+    channel, as the formula does, and not NaN."""
+    t, w = norm_case(1, 0, c, torch.float32, torch.float32, "channel", c)
+    tell("norm infinite", c)
+    g = gen(c + 1)
+    Q, P = normal(g, (1, c), torch.float32), normal(g, (1, c), torch.float32)
+    for param, first, second in (("gate", "d_w_post", "g_w_post"), ("w_post", "d_gate", "g_gate")):
+        x, x64 = dict(t), dict(w)
+        x[param] = t[param].clone()
+        x[param][3] = float("inf")
+        x64[param] = x[param].double().reshape(w[param].shape)
+        d = {k: v.to(dev) for k, v in x.items()}
+        args = (d["grad_r"], d["grad_u"], d["h"], d["r"], d["w_post"], d["w_pre"], d["gate"], 0.5, 1e-6, 0)
+        got = dict(zip(("d_h", "d_r", "d_w_post", "d_w_pre", "d_gate"), ctp.norm_residual_bwd(*args)))
+        ref, S = norm_ref(x64["h"], x64["r"], x64["w_post"], x64["w_pre"], x64["gate"], 0.5, 1e-6, 0, x64["grad_r"],
+                          x64["grad_u"])[first]
+        rest = [k for k in range(c) if k != 3]
+        assert bool(ref[0, 3].isinf())
+        assert float(got[first][3]) == float(ref[0, 3])
+        close(first, got[first][rest], ref[0, rest], S[0, rest], 257)
+        # the second pass: EB alpha d times the other parameter, EB = s1 (Q - h^ <b Q, h^>)
+        d64 = norm_ref(None, x64["r"], None, x64["w_pre"], None, 0.5, 1e-6, 0, x64["grad_r"], x64["grad_u"])["d_r"][0]
+        h = x64["h"] * (x64["h"].square().mean() + 1e-6).rsqrt()
+        eb = (x64["h"].square().mean() + 1e-6).rsqrt() * (Q.double() - h * (Q.double() * h).mean())
+        ref = (eb * 0.5 * d64 * x64[param])[0, 0]
+        got = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(Q.to(dev), P.to(dev), *args)))
+        assert float(got[second][3]) == float(ref[3])
+        assert bool(got[second].isfinite()[rest].all())
