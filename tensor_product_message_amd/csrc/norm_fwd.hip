@@ -130,6 +130,22 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_fwd(NormArgs a) {
     }
 }
 
+// The arguments for rows [first, first + n) alone.
+NormArgs rows_from(const NormArgs& all, long first, long n) {
+    NormArgs a = all;
+    const long nl = a.lmax + 1, row = nl * nl * a.channels, size = a.dtype == kF32 ? 4 : 2;
+    auto move = [&](auto& p, long stride) {
+        if (p) p = reinterpret_cast<std::decay_t<decltype(p)>>(reinterpret_cast<uintptr_t>(p) + first * stride * size);
+    };
+    a.n_rows = n;
+    move(a.h, a.h_stride);
+    move(a.r, a.r_stride);
+    if (a.gate == kGateRow) move(a.gate_p, a.gate_stride);
+    move(a.r_out, row);
+    move(a.u, row);
+    return a;
+}
+
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormArgs& args, hipStream_t st) {
@@ -142,9 +158,15 @@ hipError_t launch_norm_fwd(const NormArgs& args, hipStream_t st) {
         using T = decltype(t);
         return with_shape(row_vectors(a.lmax, a.channels, kVec<T>), [&](auto lanes, auto nv) {
             constexpr int kAtOnce = rows_at_once(lanes);
-            const unsigned grid = (unsigned)((a.n_rows + kAtOnce - 1) / kAtOnce);
             const bool full = a.h && a.w_post && a.w_pre && a.channels >= kVec<T>;
-            auto go = [&](auto kernel) { kernel<<<grid, kNormThreads<lanes>, 0, st>>>(a); };
+            auto go = [&](auto kernel) {
+                // 2^28 rows of 16 lanes, 2^22 of 1024, are more than a launch takes
+                constexpr long kMost = max_groups(kNormThreads<lanes>) * kAtOnce;
+                for (long first = 0; first < a.n_rows; first += kMost) {
+                    const NormArgs part = rows_from(a, first, std::min(kMost, a.n_rows - first));
+                    kernel<<<(unsigned)((part.n_rows + kAtOnce - 1) / kAtOnce), kNormThreads<lanes>, 0, st>>>(part);
+                }
+            };
             auto gated = [&](auto g) {
                 if (full) go(k_norm_fwd<T, lanes, nv, g, true>);
                 else go(k_norm_fwd<T, lanes, nv, g, false>);

@@ -250,7 +250,8 @@ __device__ __forceinline__ double wave_sum(double x) {
     return x;
 }
 
-// Bounds of a launch: workgroups are counted in 31 bits.
-constexpr long kMaxGrid = 0x7fffffffL;
+// Workgroups that a launch may have: its threads are counted in 32 bits, and a
+// larger launch starts the remainder modulo 2^32 without an error.
+constexpr long max_groups(int threads) { return 0xffffffffL / threads; }
 
 }  // namespace ctp

@@ -75,3 +75,23 @@ def test_norm_gradients_of_infinite_parameters(ctp, dev, c):
         got = dict(zip(SECOND, ctp.norm_residual_bwd_bwd(Q.to(dev), P.to(dev), *args)))
         assert float(got[second][3]) == float(ref[3])
         assert bool(got[second].isfinite()[rest].all())
+
+
+# ---------------------------------------------------------------- more than one launch
+
+
+def test_norm_rows_beyond_a_launch(ctp, dev):
+    """2^28 + 21 rows of one value, 16 lanes each: more than the 2^32 - 1 threads of a launch."""
+    n = 2 ** 28 + 21
+    g = torch.Generator(device=dev).manual_seed(3)
+    h, r, gate = (torch.randn((n, 1), generator=g, device=dev, dtype=torch.float16) for _ in range(3))
+    w = torch.tensor([1.5], dtype=torch.float16, device=dev)
+    out = tuple(torch.full((n, 1), float("nan"), dtype=torch.float16, device=dev) for _ in range(2))
+    tell("norm rows", n)
+    ctp.norm_residual_fwd(h, r, w, w, gate, 0.5, out=out)
+    assert not any(bool(x.isnan().any()) for x in out)
+    at = torch.cat([torch.arange(n - 40, n, device=dev), torch.arange(40, device=dev),
+                    torch.arange(2 ** 28 - 60, 2 ** 28 + 20, device=dev),
+                    torch.randint(0, n, (4096,), generator=g, device=dev)])
+    part = ctp.norm_residual_fwd(h[at], r[at], w, w, gate[at], 0.5)
+    assert all(torch.equal(x[at], y) for x, y in zip(out, part))
