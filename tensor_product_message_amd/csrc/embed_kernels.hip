@@ -410,19 +410,21 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
     __shared__ __align__(16) float head_lds[kThreads * kVec<T>];    // each chunk's share of the run that it begins with
     const Tile<kThreads> tl(lg, channels, kVec<T>);
     if (blockIdx.x >= chunk_wgs) {
-        // which of 32 table rows have a token: a binary search in the sorted ids, one row a lane
-        const long v0 = (blockIdx.x - chunk_wgs) * kZeroRows;
-        const int row = (int)min(v0 + (threadIdx.x & (kZeroRows - 1)), (long)s.rows - 1);
-        int lo = 0, hi = s.n;
-        while (lo < hi) {
-            const int mid = lo + (hi - lo) / 2;
-            if (s.keys[mid] < row) lo = mid + 1;
-            else hi = mid;
+        // 32 table rows a time, and more than once where a launch has not a workgroup for all of them
+        for (long v0 = (blockIdx.x - chunk_wgs) * kZeroRows; v0 < s.rows; v0 += (gridDim.x - chunk_wgs) * kZeroRows) {
+            // which of them have a token: a binary search in the sorted ids, one row a lane
+            const int row = (int)min(v0 + (threadIdx.x & (kZeroRows - 1)), (long)s.rows - 1);
+            int lo = 0, hi = s.n;
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                if (s.keys[mid] < row) lo = mid + 1;
+                else hi = mid;
+            }
+            const uint64_t present = __ballot(lo < s.n && s.keys[lo] == row);
+            for (int k = tl.group; k < kZeroRows && v0 + k < s.rows; k += tl.groups)
+                if (tl.v < tl.nvec && !(present >> k & 1))
+                    store_zeros<T, O>(d_table + (v0 + k) * table_stride, tl.v, channels);
         }
-        const uint64_t present = __ballot(lo < s.n && s.keys[lo] == row);
-        if (tl.v >= tl.nvec) return;
-        for (int k = tl.group; k < kZeroRows && v0 + k < s.rows; k += tl.groups)
-            if (!(present >> k & 1)) store_zeros<T, O>(d_table + (v0 + k) * table_stride, tl.v, channels);
         return;
     }
     const long wg_begin = (long)blockIdx.x * tl.groups * s.chunk;
@@ -633,7 +635,7 @@ hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* 
     const unsigned tiles = (unsigned)((nvec + (1 << lg) - 1) >> lg);
     const long chunks = (a.n_tokens + chunk - 1) / chunk;
     const long chunk_wgs = (chunks + groups - 1) / groups;     // spans too
-    const long zero_wgs = (a.n_rows + kZeroRows - 1) / kZeroRows;
+    const long zero_wgs = std::min((a.n_rows + kZeroRows - 1) / kZeroRows, max_groups(kThreads) - chunk_wgs);
     if (chunk_wgs + zero_wgs > 0)
         k_embed_sum<T, O><<<dim3((unsigned)(chunk_wgs + zero_wgs), tiles), kThreads, (2 * groups * chunk + 2) * sizeof(int32_t), st>>>(
             s, static_cast<const T*>(a.src), static_cast<O*>(a.dst), a.channels, a.scale, a.src_stride, a.dst_stride,

@@ -95,3 +95,15 @@ def test_norm_rows_beyond_a_launch(ctp, dev):
                     torch.randint(0, n, (4096,), generator=g, device=dev)])
     part = ctp.norm_residual_fwd(h[at], r[at], w, w, gate[at], 0.5)
     assert all(torch.equal(x[at], y) for x, y in zip(out, part))
+
+
+def test_table_rows_beyond_a_launch(ctp, dev):
+    """The gradient of a table of 2^29 + 77 rows: the workgroups that write its zero rows."""
+    v = 2 ** 29 + 77
+    tok = torch.tensor([0, v - 1, 2 ** 29, 5, -1], device=dev)
+    grad = torch.arange(1, 6, dtype=torch.float16, device=dev)[:, None]
+    table = torch.full((v, 1), float("nan"), dtype=torch.float16, device=dev)
+    tell("table rows", v)
+    ctp.embed_bwd(grad, tok, v, out=table)
+    assert torch.equal(table[tok[:4]], grad[:4])
+    assert int((table != 0).sum()) == 4
