@@ -686,11 +686,16 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, hipStream_t st) {
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         const int lg = lanes_log2(a.channels, kVec<T>), groups = kThreads >> lg;
-        const int n = (int)a.n_tokens;
-        const unsigned grid = (unsigned)((a.n_tokens + groups * kLookups - 1) / (groups * kLookups));
         auto* kernel = streams_out(a.n_tokens * a.channels * (long)sizeof(T)) ? k_embed_fwd<T, true> : k_embed_fwd<T, false>;
-        kernel<<<grid, kThreads, 0, st>>>(static_cast<const T*>(a.src), a.tokens, static_cast<T*>(a.dst), n,
-                                          (int)a.n_rows, a.channels, a.wide_index, a.scale, a.src_stride, a.dst_stride, lg);
+        // 2^26 tokens of 256 lanes are more than a launch takes (a lane looks up four)
+        const long at_once = groups * kLookups, most = max_groups(kThreads) * at_once;
+        for (long first = 0; first < a.n_tokens; first += most) {
+            const long n = std::min(most, a.n_tokens - first);
+            kernel<<<(unsigned)((n + at_once - 1) / at_once), kThreads, 0, st>>>(
+                static_cast<const T*>(a.src), static_cast<const char*>(a.tokens) + first * (a.wide_index ? 8 : 4),
+                static_cast<T*>(a.dst) + first * a.dst_stride, (int)n, (int)a.n_rows, a.channels, a.wide_index, a.scale,
+                a.src_stride, a.dst_stride, lg);
+        }
         return hipGetLastError();
     });
 }

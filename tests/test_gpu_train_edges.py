@@ -107,3 +107,21 @@ def test_table_rows_beyond_a_launch(ctp, dev):
     ctp.embed_bwd(grad, tok, v, out=table)
     assert torch.equal(table[tok[:4]], grad[:4])
     assert int((table != 0).sum()) == 4
+
+
+def test_lookups_beyond_a_launch(ctp, dev):
+    """2^26 + 3 tokens of 1025 channels, a quarter of a workgroup of 256 each."""
+    n, c = 2 ** 26 + 3, 1025
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160 * 2 ** 30:
+        pytest.skip("needs 160 GiB of GPU memory")
+    g = torch.Generator(device=dev).manual_seed(5)
+    table = torch.randn((50, c), generator=g, device=dev, dtype=torch.float16)
+    tok = torch.randint(0, 50, (n,), generator=g, device=dev, dtype=torch.int32)
+    out = torch.full((n, c), float("nan"), dtype=torch.float16, device=dev)
+    tell("lookups", n)
+    ctp.embed_fwd(table, tok, out=out)
+    for k in range(0, n, 2 ** 20):
+        assert torch.equal(out[k:k + 2 ** 20], table[tok[k:k + 2 ** 20].long()]), k
+    del out
+    torch.cuda.empty_cache()
