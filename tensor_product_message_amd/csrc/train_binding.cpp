@@ -169,6 +169,12 @@ Workspace workspace(const Tensor* given, int64_t bytes, const Tensor& like) {
     return {*given, (int64_t)given->nbytes()};
 }
 
+// After a call has written a tensor that the caller gave: a backward pass that saved it must see that it has
+// changed.  Inference tensors cannot be saved and have no version.
+void written(const Tensor* t) {
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 void* address(const Tensor& t) { return t.data_ptr(); }
 void* address(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
@@ -212,6 +218,7 @@ PyObject* embed_fwd(PyObject* const* a) {
     if (given) p.dst_stride = row_stride(*given, "out", shape, 1, c, table.scalar_type(), index);
     const Tensor out = given ? *given : dense(nullptr, "out", shape, table);
     check(lib.embed_fwd(&p, address(table), address(tokens), address(out), stream_of(index)));
+    written(given);
     return THPVariable_Wrap(out);
 }
 
@@ -250,6 +257,8 @@ PyObject* embed_bwd(PyObject* const* a) {
     const Tensor out = given ? *given : at::empty(shape, grad.options().dtype(type).requires_grad(false));
     const Workspace ws = workspace(given_ws, bytes, grad);
     check(lib.embed_bwd(&p, address(grad), address(tokens), address(out), address(ws.t), ws.bytes, stream_of(index)));
+    written(given);
+    written(given_ws);
     return THPVariable_Wrap(out);
 }
 
@@ -351,6 +360,8 @@ PyObject* norm_fwd(PyObject* const* a) {
     if (n.w_pre) u = dense(given_u, "u", n.first->sizes(), *n.first);
     check(lib.norm_fwd(&n.p, address(n.h), address(n.r), address(n.w_post), address(n.w_pre), address(n.gate),
                        r_out ? address(*r_out) : nullptr, u ? address(*u) : nullptr, stream_of(n.index)));
+    if (r_out) written(given_r);
+    if (u) written(given_u);
     PyObject* r;
     if (n.h) {
         r = THPVariable_Wrap(*r_out);
@@ -398,6 +409,7 @@ PyObject* norm_bwd(PyObject* const* a) {
     check(lib.norm_bwd(&n.p, address(n.grad_r), address(n.grad_u), address(n.h), address(n.r), address(n.w_post),
                        address(n.w_pre), address(n.gate), address(d_h), address(d_r), address(d_w_post),
                        address(d_w_pre), address(d_gate), address(ws.t), ws.bytes, stream_of(n.index)));
+    written(given_ws);
     return tuple_of({wrap_or_none(d_h), wrap_or_none(d_r), wrap_or_none(d_w_post), wrap_or_none(d_w_pre), wrap_or_none(d_gate)});
 }
 
@@ -422,6 +434,7 @@ PyObject* norm_bwd_bwd(PyObject* const* a) {
                            address(n.r), address(n.w_post), address(n.w_pre), address(n.gate), address(g_gr),
                            address(g_gu), address(g_h), address(g_r), address(g_w_post), address(g_w_pre),
                            address(g_gate), address(ws.t), ws.bytes, stream_of(n.index)));
+    written(given_ws);
     return tuple_of({wrap_or_none(g_gr), wrap_or_none(g_gu), wrap_or_none(g_h), wrap_or_none(g_r), wrap_or_none(g_w_post),
                      wrap_or_none(g_w_pre), wrap_or_none(g_gate)});
 }
@@ -469,6 +482,9 @@ PyObject* clip(PyObject* const* a) {
     const Workspace ws = workspace(nullptr, lib.clip_workspace(n), first);
     check(lib.clip(n, in.at.data(), out ? out->at.data() : nullptr, in.numel.data(), in.dtype.data(), (float)number_of(a[2]),
                    (float)number_of(a[3]), norm.data_ptr<float>(), address(ws.t), ws.bytes, stream_of(index)));
+    if (out)
+        for (Py_ssize_t k = 0; k < PyList_GET_SIZE(a[1]); ++k) written(&tensor_of(PyList_GET_ITEM(a[1], k), "out"));
+    written(given);
     return THPVariable_Wrap(norm);
 }
 

@@ -8,7 +8,9 @@ current HIP stream.
 Types: float32, bfloat16, float16; every sum is formed in 32 bits or more and
 every output rounded once.  A tensor's rows may lie any stride apart (a slice
 of a wider tensor), but within a row values are contiguous.  Wrong metadata
-raises TypeError or ValueError, what the library refuses ConvTPError.
+raises TypeError or ValueError, what the library refuses ConvTPError.  A
+tensor given to write into counts as modified in place: a backward pass that
+saved it raises.
 
 Shapes (lmax = 0: plain rows; else D = (lmax + 1)^2 components a row):
     h, r, grad_r, grad_u, d_h, d_r  : [..., C], or [..., D, C]

@@ -125,3 +125,53 @@ def test_lookups_beyond_a_launch(ctp, dev):
         assert torch.equal(out[k:k + 2 ** 20], table[tok[k:k + 2 ** 20].long()]), k
     del out
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- outputs that autograd watches
+
+
+def test_given_outputs_count_as_written(ctp, dev):
+    """Every output that the caller gives gets a new version, so that a backward pass which saved it refuses it."""
+    f = lambda *s: torch.ones(s, device=dev)  # noqa: E731
+    ids = torch.zeros(4, dtype=torch.int64, device=dev)
+    outs = [f(4, 8), f(3, 8), f(4, 8), f(4, 8), f(4, 8), torch.ones((), device=dev)]
+    before = [x._version for x in outs]
+    ctp.embed_fwd(f(3, 8), ids, out=outs[0])
+    ctp.embed_bwd(f(4, 8), ids, 3, out=outs[1])
+    ctp.norm_residual_fwd(f(4, 8), f(4, 8), f(8), f(8), out=(outs[2], outs[3]))
+    ctp.clip_grad_norm([f(4, 8)], 1.0, out=[outs[4]])
+    ctp.grad_norm([f(4, 8)], out=outs[5])
+    assert all(x._version > v for x, v in zip(outs, before)), [x._version - v for x, v in zip(outs, before)]
+    x, w = f(4, 8), f(8)
+    for call in (lambda ws: ctp.embed_bwd(x, ids, 3, workspace=ws),
+                 lambda ws: ctp.norm_residual_bwd(x, x, x, x, w, w, workspace=ws),
+                 lambda ws: ctp.norm_residual_bwd_bwd(x, x, x, x, x, x, w, w, workspace=ws)):
+        ws = torch.zeros(1 << 20, dtype=torch.uint8, device=dev)
+        call(ws)
+        assert ws._version > 0
+
+
+@pytest.mark.parametrize("how", ["clip", "norm", "embed_fwd", "embed_bwd", "grad_norm"])
+def test_a_saved_tensor_that_is_written_is_refused(ctp, dev, how):
+    x = torch.randn((4, 8) if how != "grad_norm" else (), device=dev, requires_grad=True)
+    y = 2 * x
+    loss = y.square().sum()                 # saves y
+    to, one, ids = y.detach(), torch.ones(8, device=dev), torch.arange(4, device=dev)
+    {"clip": lambda: ctp.clip_grad_norm([to], 0.1, out=[to]),
+     "norm": lambda: ctp.norm_residual_fwd(torch.ones_like(to), to, one, one, out=(to, None)),
+     "embed_fwd": lambda: ctp.embed_fwd(torch.ones(4, 8, device=dev), ids, out=to),
+     "embed_bwd": lambda: ctp.embed_bwd(torch.ones(4, 8, device=dev), ids, 4, out=to),
+     "grad_norm": lambda: ctp.grad_norm([torch.ones(4, device=dev)], out=to)}[how]()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_inference_tensors_are_written(ctp, dev):
+    """They have no version; writing them needs none."""
+    ids = torch.arange(4, device=dev)
+    with torch.inference_mode():
+        table, out = torch.randn(4, 8, device=dev), torch.zeros(4, 8, device=dev)
+        ctp.embed_fwd(table, ids, out=out)
+        assert torch.equal(out, table)
+    out2 = ctp.embed_fwd(table, ids, 2.0, out=out)
+    assert out2 is out and torch.equal(out, 2 * table)
