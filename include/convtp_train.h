@@ -129,8 +129,9 @@ int32_t conv_tp_norm_bwd_bwd(const conv_tp_norm_problem *prob, const void *a_d_h
  * n_tensors entries, read before the call returns.  out NULL: the norm alone.
  * out[k] may be in[k] (in place; where nothing is clipped it is not rewritten)
  * and has in[k]'s type; other overlaps are not allowed.  norm: device, one
- * float.  Squares are summed in 64 bits.  A norm that is not finite gives what
- * the formula gives.  workspace: 16-byte aligned, at least
+ * float.  Squares are summed in 64 bits, and out is the formula's also where the
+ * norm leaves a float's range (it is then reported as infinity) or the factor
+ * does.  A norm that is not finite gives what the formula gives.  workspace: 16-byte aligned, at least
  * conv_tp_clip_workspace(n_tensors) bytes. */
 int32_t conv_tp_clip(int32_t n_tensors, const void *const *in, void *const *out, const int64_t *numel,
                      const int32_t *dtype, float max_norm, float eps, float *norm, void *workspace,

@@ -96,16 +96,32 @@ __device__ __forceinline__ double squares(const T* x, long n) {
     return s;
 }
 
+// What a value is multiplied by, in two steps.  The norm may be above fp32's
+// largest number and the factor below its smallest normal one where the clipped
+// values are neither: then `factor` is 2^64 times it, and `then` 2^-64.  Else
+// `then` is 1, which leaves the first product as it is.
+struct Factor {
+    float factor, then;
+};
+
+__device__ __forceinline__ Factor factor_of(double norm, float max_norm, float eps) {
+    float f = max_norm / ((float)norm + eps);
+    if (f > 1.0f) f = 1.0f;       // a NaN norm stays NaN
+    if (f < 0x1p-126f && norm < __builtin_inf())
+        return {(float)(0x1p64 * ((double)max_norm / (norm + (double)eps))), 0x1p-64f};
+    return {f, 1.0f};
+}
+
 // y = factor x.
 template <class T, bool Stream>
-__device__ __forceinline__ void scaled(const T* x, T* y, long n, float factor) {
+__device__ __forceinline__ void scaled(const T* x, T* y, long n, Factor by) {
     const long whole = n / kVec<T>;
     auto* xv = reinterpret_cast<const typename Vec<T>::unaligned*>(x);
     auto* yv = reinterpret_cast<typename Vec<T>::unaligned*>(y);
     auto put = [&](long v, const vec_t<T>& q) {
         Floats<T> f = widen<T>(q);
 #pragma unroll
-        for (int k = 0; k < kVec<T>; ++k) f.v[k] *= factor;
+        for (int k = 0; k < kVec<T>; ++k) f.v[k] = f.v[k] * by.factor * by.then;
         if (Stream) __builtin_nontemporal_store(narrow<T>(f), yv + v);
         else yv[v] = narrow<T>(f);
     };
@@ -122,7 +138,7 @@ __device__ __forceinline__ void scaled(const T* x, T* y, long n, float factor) {
         put(v, q);
     }
     const long at = whole * kVec<T> + threadIdx.x;
-    if (at < n) y[at] = (T)((float)x[at] * factor);
+    if (at < n) y[at] = (T)((float)x[at] * by.factor * by.then);
 }
 
 // Calls f with a value of the type of a code.
@@ -157,16 +173,16 @@ __global__ void __launch_bounds__(kThreads) k_clip_squares(Batch b, double* __re
 }
 
 // Every workgroup adds all partial sums for itself; the first one writes the norm.
-__device__ __forceinline__ float total_norm(const double* partial, int n_partial, double* part) {
+__device__ __forceinline__ double total_norm(const double* partial, int n_partial, double* part) {
     double s = 0.0;
     for (int k = threadIdx.x; k < n_partial; k += kThreads) s += partial[k];
-    return (float)sqrt(group_sum(s, part));
+    return sqrt(group_sum(s, part));
 }
 
 __global__ void __launch_bounds__(kThreads) k_clip_norm(const double* __restrict__ partial, int n_partial, float* norm) {
     __shared__ double part[kThreads / 64];
-    const float x = total_norm(partial, n_partial, part);
-    if (threadIdx.x == 0) *norm = x;
+    const double x = total_norm(partial, n_partial, part);
+    if (threadIdx.x == 0) *norm = (float)x;
 }
 
 // Stream: where much is moved, neither what is read here nor what is written
@@ -177,16 +193,15 @@ template <bool Stream>
 __global__ void __launch_bounds__(kThreads)
 k_clip_scale(Batch b, const double* __restrict__ partial, int n_partial, float max_norm, float eps, float* norm) {
     __shared__ double part[kThreads / 64];
-    const float x = total_norm(partial, n_partial, part);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = x;
-    float factor = max_norm / (x + eps);
-    if (factor > 1.0f) factor = 1.0f;       // a NaN norm stays NaN
+    const double x = total_norm(partial, n_partial, part);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = (float)x;
+    const Factor by = factor_of(x, max_norm, eps);
     each_span(b, [&](int t, long begin, long end) {
         // in place with nothing to clip: the values stay as they are
-        if (factor == 1.0f && b.in[t] == b.out[t]) return;
+        if (by.factor == 1.0f && by.then == 1.0f && b.in[t] == b.out[t]) return;
         typed(b.dtype[t], [&](auto q) {
             using T = decltype(q);
-            scaled<T, Stream>(static_cast<const T*>(b.in[t]) + begin, static_cast<T*>(b.out[t]) + begin, end - begin, factor);
+            scaled<T, Stream>(static_cast<const T*>(b.in[t]) + begin, static_cast<T*>(b.out[t]) + begin, end - begin, by);
         });
     });
 }

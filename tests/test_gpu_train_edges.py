@@ -175,3 +175,32 @@ def test_inference_tensors_are_written(ctp, dev):
         assert torch.equal(out, table)
     out2 = ctp.embed_fwd(table, ids, 2.0, out=out)
     assert out2 is out and torch.equal(out, 2 * table)
+
+
+# ---------------------------------------------------------------- norms and factors outside float32
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value,n,max_norm", [
+    (3e38, 4, 1.0),             # the norm is above float32's largest number
+    (3e38, 5003, 0.125),        # so is the norm, and the factor below its smallest
+    (1e37, 100, 0.5),           # the norm fits, the factor is subnormal
+    (1e30, 20000, 1e-9), (2e38, 2, 1e-3),
+])
+def test_clip_norms_beyond_float32(ctp, dev, value, n, max_norm, dtype):
+    """The squares are summed in 64 bits, so the clipped gradients are the formula's although the norm, one float,
+    overflows or the factor is no normal one.  Two products and a sum of 64 bits: K = 8."""
+    x = torch.full((n,), value).to(dtype)
+    x[::3] *= -0.5
+    small = torch.linspace(-1e-3, 1e3, 77).to(dtype)
+    tell("clip", value, n, max_norm, dtype)
+    norm = float(torch.cat([x.double(), small.double()]).norm())
+    max64 = float(torch.tensor(max_norm, dtype=torch.float32))
+    for in_place in (False, True):
+        d = [x.to(dev), small.to(dev)]
+        out, got = ctp.clip_grad_norm(d, max_norm, out=d if in_place else None)
+        ref = torch.tensor(norm, dtype=torch.float64).float()
+        assert float(got) == float(ref) if ref.isinf() else abs(float(got) - norm) <= 2 ** -23 * norm
+        for o, i in zip(out, (x, small)):
+            want = i.double() * (max64 / (norm + 1e-6))
+            close("out", o, want, want.abs(), 8)
