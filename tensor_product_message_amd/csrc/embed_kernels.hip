@@ -69,7 +69,7 @@ k_embed_fwd(const T* __restrict__ table, const void* __restrict__ tokens, T* __r
         for (int u = 0; u < kLookups; ++u) {
             const long t = t0 + u * groups;
             if (t >= n) break;
-            settle<T>(x[u], span);
+            settle<T>(x[u], span, true);
             Floats<T> f = widen<T>(x[u]);
 #pragma unroll
             for (int k = 0; k < kVec<T>; ++k) f.v[k] *= scale;
@@ -212,7 +212,7 @@ k_embed_few(const T* __restrict__ grad, const void* __restrict__ tokens, O* __re
         }
 #pragma unroll
         for (int q = 0; q < kAtOnce; ++q) {
-            settle<T>(x[q], span);
+            settle<T>(x[q], span, on);
             add_vec<T>(acc, x[q]);
         }
     }
@@ -470,7 +470,7 @@ k_embed_sum(Sorted s, const T* __restrict__ grad, O* __restrict__ d_table, int c
                     head = false;
                     acc = Floats<T>{};
                 }
-                settle<T>(x[q], span);
+                settle<T>(x[q], span, true);
                 add_vec<T>(acc, x[q]);
             }
 #pragma unroll

@@ -92,10 +92,10 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd(NormArgs a)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place p = place(i);
-            if (p.span.shift <= 0) continue;
-            settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
-            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span);
-            if constexpr (G == kGateRow) settle<T>(gx[i], p.span);
+            if (!p.on || p.span.shift <= 0) continue;
+            settle<T>(rx[i], p.span, true), settle<T>(gux[i], p.span, true);
+            settle<T>(hx[i], p.span, true), settle<T>(grx[i], p.span, true);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p.span, true);
         }
         // the squares of h and r' and <A, r'>
         float s[3] = {0.0f, 0.0f, 0.0f};

@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>, 4) k_norm_bwd_bwd(NormArg
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place p = place(i);
-            if (p.span.shift <= 0) continue;
-            settle<T>(px[i], p.span), settle<T>(qx[i], p.span), settle<T>(rx[i], p.span), settle<T>(gux[i], p.span);
-            settle<T>(hx[i], p.span), settle<T>(grx[i], p.span);
-            if constexpr (G == kGateRow) settle<T>(gx[i], p.span);
+            if (!p.on || p.span.shift <= 0) continue;
+            settle<T>(px[i], p.span, true), settle<T>(qx[i], p.span, true), settle<T>(rx[i], p.span, true);
+            settle<T>(gux[i], p.span, true), settle<T>(hx[i], p.span, true), settle<T>(grx[i], p.span, true);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p.span, true);
         }
         float s[4] = {};        // the squares of h and r', <A, r'>, <b Q, h>
 #pragma unroll

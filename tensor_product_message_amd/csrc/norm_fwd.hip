@@ -67,9 +67,9 @@ __global__ void __launch_bounds__(kNormThreads<Lanes>) k_norm_fwd(NormArgs a) {
     Floats<T> y[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (p[i].span.shift > 0) {
-            settle<T>(hx[i], p[i].span), settle<T>(rx[i], p[i].span);
-            if constexpr (G == kGateRow) settle<T>(gx[i], p[i].span);
+        if (p[i].on && p[i].span.shift > 0) {
+            settle<T>(hx[i], p[i].span, true), settle<T>(rx[i], p[i].span, true);
+            if constexpr (G == kGateRow) settle<T>(gx[i], p[i].span, true);
         }
         y[i] = widen<T>(rx[i]);
     }

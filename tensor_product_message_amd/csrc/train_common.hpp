@@ -62,7 +62,7 @@ struct Span {
 };
 
 template <class T>
-__device__ __forceinline__ Span span_of(int v, int n) {
+__host__ __device__ __forceinline__ Span span_of(int v, int n) {
     const int at = v * kVec<T>, over = at + kVec<T> - n;
     if (n < kVec<T>) return Span{at, 0, v == 0 ? n : 0};
     return over > 0 ? Span{at - over, over * 8 * (int)sizeof(T), 0} : Span{at, 0, 0};
@@ -86,16 +86,18 @@ __device__ __forceinline__ vec_t<T> read_span(const T* row, const Span& s, int n
 }
 
 // (Whole: the caller knows that rows are no shorter; Stream: see streams.)  What lies past the row's end becomes 0.
+// on: the vector begins in the row.  Others are zeros that nothing was read into, and their shift is 128 bits or
+// more, which is no shift.
 template <class T>
-__device__ __forceinline__ void settle(vec_t<T>& x, const Span& s) {
-    if (s.shift > 0) x = __builtin_bit_cast(vec_t<T>, __builtin_bit_cast(unsigned __int128, x) >> s.shift);
+__host__ __device__ __forceinline__ void settle(vec_t<T>& x, const Span& s, bool on) {
+    if (on && s.shift > 0) x = __builtin_bit_cast(vec_t<T>, __builtin_bit_cast(unsigned __int128, x) >> s.shift);
 }
 
 template <class T>
 __device__ __forceinline__ vec_t<T> load_vec(const T* row, int v, int n) {
     const Span s = span_of<T>(v, n);
     vec_t<T> x = read_span<T>(row, s, n);
-    settle<T>(x, s);
+    settle<T>(x, s, true);
     return x;
 }
 
