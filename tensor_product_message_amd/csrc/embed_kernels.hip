@@ -156,13 +156,12 @@ __device__ __forceinline__ void store_zeros(O* row, int v, int n) {
 
 // One workgroup a table row and tile of channels goes through all tokens,
 // keeps the places of its own in order and sums their rows.  Every workgroup
-// reads all tokens, so this is for a few thousand of them and workgroups; it
-// saves the sort's launches (100 rows of 128 floats: 6.5 us for the water box's
-// 1503 tokens and 12.9 for 8000, 15.7 and 19.6 with the sort; 8000 tokens of
-// one id 22.8 and 22.1, and 16000 of one id 44 and 23).
+// reads all tokens, so this is for a few thousand of them and few rounds of
+// workgroups (see few); it saves the sort's launches (100 rows of 128 floats:
+// 6.5 us for the water box's 1503 tokens and 12.9 for 8000, 15.7 and 19.6 with
+// the sort; 8000 tokens of one id 22.8 and 22.1, and 16000 of one id 44 and 23).
 constexpr int kFewThreads = 1024;
 constexpr int kFewTokens = 8192;
-constexpr int kFewGroups = 2048;    // workgroups
 constexpr int kFewLanes = 3;        // log2 of the lanes of a row
 
 template <class T, class O>
@@ -595,8 +594,16 @@ int lanes_log2(int channels, int kvec) { return std::clamp(log2_up((channels + k
 
 int few_tiles(int channels, int kvec) { return ((channels + kvec - 1) / kvec + (1 << kFewLanes) - 1) >> kFewLanes; }
 
+// Whether k_embed_few takes a call: where its workgroups, of which a CU holds
+// two with the registers of fp32 and one with those of 16-bit types, all get
+// their turn in four rounds, or in two with more than half of its tokens.
+// Uniform ids, us here and with the sort: 512 tokens of 128 floats 6 and 15 in
+// one round, 14 and 16 in four, 26 and 19 in eight; 8192 tokens 13 and 20 in one,
+// 21 and 20 in two, 37 and 21 in four.  Of 256 bf16 channels: 512 tokens 13 and
+// 16 in four, 23 and 17 in eight; 8192 tokens 16 and 20 in two, 28 and 21 in four.
 bool few(long n, long rows, int channels, int kvec) {
-    return n <= kFewTokens && rows * few_tiles(channels, kvec) <= kFewGroups;
+    const long at_once = kvec == 4 ? 512 : 256, rounds = n > kFewTokens / 2 ? 2 : 4;
+    return n <= kFewTokens && rows * few_tiles(channels, kvec) <= rounds * at_once;
 }
 
 struct Plan {

@@ -3,8 +3,8 @@ bounds and their derivation are test_gpu_train.py's."""
 import pytest
 import torch
 
-from tests.test_gpu_train import (SECOND, close, ctp, dev, gen, norm_case, norm_ref, normal,  # noqa: F401
-                                  second_bounds, second_ref, tell)
+from tests.test_gpu_train import (SECOND, close, ctp, dev, draw_tokens, embed_bwd_ref, gen, norm_case,  # noqa: F401
+                                  norm_ref, normal, second_bounds, second_ref, tell)
 
 pytestmark = pytest.mark.gpu
 
@@ -204,3 +204,21 @@ def test_clip_norms_beyond_float32(ctp, dev, value, n, max_norm, dtype):
         for o, i in zip(out, (x, small)):
             want = i.double() * (max64 / (norm + 1e-6))
             close("out", o, want, want.abs(), 8)
+
+
+# ---------------------------------------------------------------- the embedding gradient's choices
+
+
+@pytest.mark.parametrize("dtype,out,c,rows", [  # a workgroup a row and 8 vectors: both sides of 2 and 4 rounds
+    (torch.float32, None, 32, 1024), (torch.float32, None, 32, 1025), (torch.float32, None, 30, 2048),
+    (torch.float32, None, 30, 2049), (torch.float32, None, 1000, 64), (torch.float32, None, 1000, 65),
+    (torch.bfloat16, None, 64, 512), (torch.bfloat16, None, 64, 513), (torch.float16, None, 61, 1024),
+    (torch.float16, torch.float32, 61, 1025), (torch.bfloat16, torch.float32, 250, 256),
+])
+@pytest.mark.parametrize("n", [4096, 4097, 8192, 8193])
+def test_embed_bwd_at_the_ends_of_the_one_launch_form(ctp, dev, n, dtype, out, c, rows):
+    g = gen(n + rows)
+    grad, tok = normal(g, (n, c), dtype), draw_tokens(g, n, rows, 2, 0.1)
+    tell("embed_bwd ends", n, dtype, out, c, rows)
+    ref, S, K = embed_bwd_ref(grad, tok, rows, 0.7)
+    close("d_table", ctp.embed_bwd(grad.to(dev), tok.to(dev), rows, 0.7, dtype=out), ref, S, K)
