@@ -633,12 +633,15 @@ template <class T, class O>
 hipError_t sum_and_join(const EmbedArgs& a, const int32_t* keys, const int32_t* pos, float* heads, float* tails,
                         hipStream_t st) {
     const int lg = lanes_log2(a.channels, kVec<T>), groups = kThreads >> lg;
-    // chunks of 16 rows keep thousands of groups busy; longer ones, as n grows, read more at a time (131072 rows of
-    // 128 floats: 34, 32 and 37 us with 16, 32 and 64)
-    int chunk = a.n_tokens <= 65536 ? kShortChunk : a.n_tokens <= 262144 ? 2 * kShortChunk : 4 * kShortChunk;
+    const int nvec = (a.channels + kVec<T> - 1) / kVec<T>;
+    // Chunks of 16 rows keep the GPU busy where there are few vectors; longer ones, as these grow in number, leave
+    // fewer partial sums.  With chunks of 16, 32 and 64 (100 ids, us): 1 M vectors, 131072 rows of 32 floats, 30, 33
+    // and 40; 2 M, 65536 of 128, 27.9, 27.9 and 34.5; 4 M, 131072 of 128, 34.7, 33.6 and 37.5; 8 M, 262144 of 128,
+    // 50, 51 and 50, and 16384 of 2048, 50, 43 and 40; 34 M, 65536 of 2048, 173, 141 and 131.
+    const long vectors = a.n_tokens * nvec;
+    int chunk = vectors < 1L << 21 ? kShortChunk : vectors < 1L << 23 ? 2 * kShortChunk : 4 * kShortChunk;
     chunk = std::min(chunk, kEntries / groups);
     const Sorted s{keys, pos, (int)a.n_tokens, (int)a.n_rows, chunk};
-    const int nvec = (a.channels + kVec<T> - 1) / kVec<T>;
     const unsigned tiles = (unsigned)((nvec + (1 << lg) - 1) >> lg);
     const long chunks = (a.n_tokens + chunk - 1) / chunk;
     const long chunk_wgs = (chunks + groups - 1) / groups;     // spans too

@@ -222,3 +222,18 @@ def test_embed_bwd_at_the_ends_of_the_one_launch_form(ctp, dev, n, dtype, out, c
     tell("embed_bwd ends", n, dtype, out, c, rows)
     ref, S, K = embed_bwd_ref(grad, tok, rows, 0.7)
     close("d_table", ctp.embed_bwd(grad.to(dev), tok.to(dev), rows, 0.7, dtype=out), ref, S, K)
+
+
+@pytest.mark.parametrize("n,v,c,dtype", [  # both sides of 2^21 and 2^23 vectors
+    (2 ** 20 - 1, 700, 8, torch.float32), (2 ** 20, 700, 8, torch.float32), (4095, 900, 2048, torch.float32),
+    (4096, 900, 2045, torch.float32), (16383, 300, 2048, torch.float32), (16384, 300, 2047, torch.float32),
+    (131071, 5000, 121, torch.bfloat16), (131072, 5000, 121, torch.bfloat16), (2 ** 19, 60000, 126, torch.float16),
+])
+def test_embed_bwd_of_every_chunk_length(ctp, dev, n, v, c, dtype):
+    g = gen(n + c)
+    grad, tok = normal(g, (n, c), dtype), draw_tokens(g, n, v, 2, 0.05)
+    tell("embed_bwd chunks", n, v, c, dtype)
+    ref, S, K = embed_bwd_ref(grad, tok, v, -1.5)
+    got = ctp.embed_bwd(grad.to(dev), tok.to(dev), v, -1.5)
+    close("d_table", got, ref, S, K)
+    assert torch.equal(got, ctp.embed_bwd(grad.to(dev), tok.to(dev), v, -1.5))
