@@ -324,7 +324,8 @@ void read_norm(Norm& n, PyObject* const* a) {
     parameter(n.w_post, "w_post");
     parameter(n.w_pre, "w_pre");
     if (!n.gate) return;
-    if (n.gate->sizes() == IntArrayRef(per) && lead > 0) {
+    // a single row without a batch: its gate may have either type, and a batch's gate of every row has the features'
+    if (n.gate->sizes() == IntArrayRef(per) && (lead > 0 || n.gate->scalar_type() != type)) {
         p.gate = 1;
         parameter(n.gate, "gate");
         return;

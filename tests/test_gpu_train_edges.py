@@ -237,3 +237,25 @@ def test_embed_bwd_of_every_chunk_length(ctp, dev, n, v, c, dtype):
     got = ctp.embed_bwd(grad.to(dev), tok.to(dev), v, -1.5)
     close("d_table", got, ref, S, K)
     assert torch.equal(got, ctp.embed_bwd(grad.to(dev), tok.to(dev), v, -1.5))
+
+
+# ---------------------------------------------------------------- one row without a batch
+
+
+@pytest.mark.parametrize("lmax,c", [(0, 24), (2, 7)])
+@pytest.mark.parametrize("kind", ["float32", "own"])
+def test_norm_of_a_single_row(ctp, dev, lmax, c, kind):
+    """[C] or [D, C] alone: a gate of the parameters' shape may have their type or the features', as in a batch."""
+    t, _ = norm_case(1, lmax, c, torch.bfloat16, torch.float32, "channel", 6)
+    if kind == "own":
+        t["gate"] = t["gate"].bfloat16()
+    d = {k: v.to(dev) for k, v in t.items()}
+    one = {k: v[0] if k in ("h", "r", "grad_r", "grad_u") else v for k, v in d.items()}
+    in_batch = d["gate"] if kind == "float32" else d["gate"][None]      # in the features' type it is a gate of every row
+
+    def passes(x, gate):
+        fwd = ctp.norm_residual_fwd(x["h"], x["r"], x["w_post"], x["w_pre"], gate, 0.5, 1e-6, lmax)
+        bwd = ctp.norm_residual_bwd(x["grad_r"], x["grad_u"], x["h"], x["r"], x["w_post"], x["w_pre"], gate, 0.5, 1e-6, lmax)
+        return [*fwd, *bwd]
+    for got, want in zip(passes(one, d["gate"]), passes(d, in_batch)):
+        assert got.dtype == want.dtype and torch.equal(got, want.reshape(got.shape))
