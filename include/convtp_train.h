@@ -131,8 +131,8 @@ int32_t conv_tp_norm_bwd_bwd(const conv_tp_norm_problem *prob, const void *a_d_h
  * and has in[k]'s type; other overlaps are not allowed.  norm: device, one
  * float.  Squares are summed in 64 bits, and out is the formula's also where the
  * norm leaves a float's range (it is then reported as infinity) or the factor
- * does.  A norm that is not finite gives what the formula gives.  workspace: 16-byte aligned, at least
- * conv_tp_clip_workspace(n_tensors) bytes. */
+ * does.  A norm that is not finite gives what the formula gives.  workspace:
+ * 16-byte aligned, at least conv_tp_clip_workspace(n_tensors) bytes. */
 int32_t conv_tp_clip(int32_t n_tensors, const void *const *in, void *const *out, const int64_t *numel,
                      const int32_t *dtype, float max_norm, float eps, float *norm, void *workspace,
                      int64_t workspace_bytes, void *stream);

@@ -15,7 +15,7 @@ saved it raises.
 Shapes (lmax = 0: plain rows; else D = (lmax + 1)^2 components a row):
     h, r, grad_r, grad_u, d_h, d_r  : [..., C], or [..., D, C]
     w_post, w_pre, gate of channels : [C], or [lmax + 1, C]
-    gate of rows                    : [..., C], or [..., lmax + 1, C]
+    gate of rows                    : [..., C], or [..., lmax + 1, C]; in the features' type
 """
 from __future__ import annotations
 
@@ -77,7 +77,8 @@ def norm_residual_fwd(h, r, w_post, w_pre, gate=None, alpha: float = 1.0, eps: f
     """(r', u) with r' = r + alpha * gate * N(h; w_post) and u = N(r'; w_pre), N the root-mean-square norm over a
     row (balanced over the degrees for lmax > 0; see include/convtp_train.h).  h None: u = N(r; w_pre) alone, r'
     is r itself.  w_post None: h is added without a norm.  w_pre None: u is None.  gate: one row, or one for every
-    row.  out: (r', u) to write into, None for a new one; r' may be r."""
+    row.  out: (r', u) to write into, None for a new one; r' may be r.  What is not computed is not written: r'
+    without h, u without w_pre."""
     r_out, u = (None, None) if out is None else out
     return native().norm_fwd(h, r, w_post, w_pre, gate, alpha, eps, lmax, r_out, u)
 
