@@ -1,5 +1,5 @@
-"""ctypes declarations of libconvtp.so (include/convtp.h, include/convtp_train.h) and
-the loading of the training-step operators' binding module, nothing else.
+"""ctypes declarations of libconvtp.so (include/convtp.h, include/convtp_train.h,
+include/convtp_dense.h) and the loading of the binding modules, nothing else.
 
 Loading fails loudly if the HIP library has not been built: there is no
 fallback implementation of any entry point.
@@ -32,6 +32,11 @@ TRAIN_EXPORTS = ("conv_tp_embed_fwd", "conv_tp_embed_bwd", "conv_tp_embed_bwd_wo
                  "conv_tp_norm_bwd", "conv_tp_norm_bwd_bwd", "conv_tp_norm_bwd_workspace", "conv_tp_clip", "conv_tp_clip_workspace",
                  "conv_tp_train_last_error")
 
+# Every symbol include/convtp_dense.h declares.
+DENSE_EXPORTS = ("conv_tp_linear_fwd", "conv_tp_linear_fwd_workspace", "conv_tp_linear_bwd", "conv_tp_linear_bwd_workspace",
+                 "conv_tp_linear_bwd_bwd", "conv_tp_linear_bwd_bwd_workspace", "conv_tp_orthogonalise",
+                 "conv_tp_orthogonalise_workspace", "conv_tp_dense_last_error")
+
 
 class Problem(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("n_edges", ctypes.c_int32),
@@ -57,6 +62,12 @@ class NormProblem(ctypes.Structure):
                 ("lmax", ctypes.c_int32), ("channels", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("param_dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("alpha", ctypes.c_float),
                 ("eps", ctypes.c_float)]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("grad_stride", ctypes.c_int64), ("lmax", ctypes.c_int32), ("inner", ctypes.c_int32),
+                ("outer", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("gated", ctypes.c_int32)]
 
 
 class ConvTPError(RuntimeError):
@@ -156,6 +167,46 @@ def train_check(status: int) -> None:
         raise ConvTPError(status, train_lib().conv_tp_train_last_error().decode())
 
 
+_dense_lib = None
+
+
+def dense_lib() -> ctypes.CDLL:
+    """The library with the entry points of include/convtp_dense.h declared."""
+    global _dense_lib
+    if _dense_lib is not None:
+        return _dense_lib
+    L = lib()
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    i64p, lp = ctypes.POINTER(i64), ctypes.POINTER(LinearProblem)
+    sig = {
+        "conv_tp_linear_fwd": ([lp] + [vp] * 7 + [i64, vp], i32),
+        "conv_tp_linear_fwd_workspace": ([lp, i64p], i32),
+        "conv_tp_linear_bwd": ([lp] + [vp] * 8 + [i64, vp], i32),
+        "conv_tp_linear_bwd_workspace": ([lp, i64p], i32),
+        "conv_tp_linear_bwd_bwd": ([lp] + [vp] * 10 + [i64, vp], i32),
+        "conv_tp_linear_bwd_bwd_workspace": ([lp, i64p], i32),
+        "conv_tp_orthogonalise": ([i32] + [vp] * 6 + [i32, f32, f32, vp, i64, vp], i32),
+        "conv_tp_orthogonalise_workspace": ([i32] + [vp] * 3 + [i64p], i32),
+        "conv_tp_dense_last_error": ([], ctypes.c_char_p),
+    }
+    for name, (args, res) in sig.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = res
+    _dense_lib = L
+    return L
+
+
+def dense_check(status: int) -> None:
+    if status != CTP_OK:
+        raise ConvTPError(status, dense_lib().conv_tp_dense_last_error().decode())
+
+
+def _missing(module: str, e: ImportError) -> RuntimeError:
+    return RuntimeError(f"{os.path.join(HERE, module)} is missing or does not load ({e}): build it with "
+                        "`python -m tensor_product_message_amd.build`")
+
+
 _native = None
 
 
@@ -167,8 +218,24 @@ def native():
         try:
             from . import _train
         except ImportError as e:
-            raise RuntimeError(f"{os.path.join(HERE, '_train.so')} is missing or does not load ({e}): build it with "
-                               "`python -m tensor_product_message_amd.build`") from e
+            raise _missing("_train.so", e) from e
         _train.bind(train_lib()._handle, train_check)
         _native = _train
     return _native
+
+
+_native_dense = None
+
+
+def dense_native():
+    """The binding module of the dense operators (csrc/dense_binding.cpp), on the loaded library."""
+    global _native_dense
+    if _native_dense is None:
+        import torch  # noqa: F401  (the module links to its libraries)
+        try:
+            from . import _dense as module
+        except ImportError as e:
+            raise _missing("_dense.so", e) from e
+        module.bind(dense_lib()._handle, dense_check)
+        _native_dense = module
+    return _native_dense

@@ -1,5 +1,6 @@
-"""Build libconvtp.so (HIP, gfx950) in-tree with hipcc, and the Python binding of
-the training-step operators (_train.so, host code) with g++.
+"""Build libconvtp.so (HIP, gfx950) in-tree with hipcc, and the Python bindings of
+the training-step and the dense operators (_train.so, _dense.so, host code) with
+g++.
 
     python -m tensor_product_message_amd.build [--incremental]
 
@@ -9,7 +10,8 @@ no implicit multiply-add contraction (-ffp-contract=off: every fused
 multiply-add is an explicit __builtin_fmaf in the source).
 The convolution kernels are compiled once per degree triple (l_in, l_sh,
 l_out), 64 objects from csrc/convtp_triple.hip with -DCTP_L1/-DCTP_L2/-DCTP_L3,
-in parallel, largest first.  --incremental skips objects newer than every
+in parallel, largest first; the linear layers once per element type (-DCTP_DENSE_TYPE).
+--incremental skips objects newer than every
 source (for development; the default rebuilds everything).
 """
 from __future__ import annotations
@@ -30,9 +32,14 @@ SOURCES = ["convtp_common.hip", "nodetp_kernels.hip", "graph_kernels.hip", "stre
 TRAIN_SOURCES = ["embed_kernels.hip", "norm_fwd.hip", "norm_bwd.hip", "norm_bwd_bwd.hip", "clip_kernels.hip", "train_api.hip"]
 TRAIN_HEADERS = ["csrc/train_common.hpp", "csrc/train_kernels.hpp", "csrc/norm_common.hpp", "csrc/norm_sums.hpp",
                  "../include/convtp_train.h", "../include/convtp.h"]
-# their Python binding, an extension module next to the package's other files
-BINDING_SOURCE = "train_binding.cpp"
-BINDING = os.path.join(HERE, "_train.so")
+# the dense operators (include/convtp_dense.h)
+DENSE_SOURCES = ["ortho_kernels.hip", "dense_dispatch.hip", "dense_api.hip"]
+DENSE_TYPED_SOURCE, DENSE_TYPES = "dense_linear.hip", ("f32", "bf16", "f16")
+DENSE_HEADERS = ["csrc/dense_common.hpp", "csrc/dense_direct.hpp", "csrc/dense_kernels.hpp", "csrc/dense_linear.hpp",
+                 "csrc/train_common.hpp", "../include/convtp_dense.h", "../include/convtp_train.h", "../include/convtp.h"]
+# the Python bindings, extension modules next to the package's other files: source, module
+BINDINGS = [("train_binding.cpp", os.path.join(HERE, "_train.so")), ("dense_binding.cpp", os.path.join(HERE, "_dense.so"))]
+BINDING_HEADERS = ["csrc/binding_common.hpp", "../include/convtp_dense.h", "../include/convtp_train.h", "../include/convtp.h"]
 TRIPLE_SOURCE = "convtp_triple.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -70,10 +77,12 @@ def _jobs(objdir: str):
     single = lambda names: [(s, os.path.join(objdir, s.replace(".hip", ".o")), []) for s in names]  # noqa: E731
     triples = [(TRIPLE_SOURCE, os.path.join(objdir, f"triple_{a}{b}{c}.o"),
                 [f"-DCTP_L1={a}", f"-DCTP_L2={b}", f"-DCTP_L3={c}"]) for a, b, c in TRIPLES]
-    return single(TRAIN_SOURCES) + triples + single(SOURCES)     # the longest first
+    typed = [(DENSE_TYPED_SOURCE, os.path.join(objdir, f"dense_linear_{t}.o"), [f"-DCTP_DENSE_TYPE={k}"])
+             for k, t in enumerate(DENSE_TYPES)]
+    return single(TRAIN_SOURCES) + typed + triples + single(DENSE_SOURCES + SOURCES)     # the longest first
 
 
-def _build_binding() -> None:
+def _build_binding(source: str, module: str) -> None:
     """Host code only (g++): torch's and Python's headers, the library's entry points are looked up at run time."""
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     include, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
@@ -83,14 +92,14 @@ def _build_binding() -> None:
     for path in (include, os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(rocm, "include"),
                  sysconfig.get_paths()["include"]):
         cmd += ["-isystem", path]
-    tmp = BINDING + ".tmp"
-    cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    tmp = module + ".tmp"
+    cmd += [os.path.join(CSRC, source), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}{r.stderr}")
+        raise RuntimeError(f"g++ failed on {source}:\n{r.stdout}{r.stderr}")
     if r.stderr:
         print(r.stderr, file=sys.stderr)
-    os.replace(tmp, BINDING)
+    os.replace(tmp, module)
 
 
 def build(verbose: bool = True, incremental: bool = False, workers: int = None) -> str:
@@ -99,23 +108,24 @@ def build(verbose: bool = True, incremental: bool = False, workers: int = None) 
     os.makedirs(objdir, exist_ok=True)
     jobs = _jobs(objdir)
     todo = jobs
+    bindings = BINDINGS
     if incremental:
-        train = [os.path.normpath(os.path.join(HERE, p)) for p in TRAIN_HEADERS]
-        conv = [p for p in glob.glob(os.path.join(CSRC, "*.hpp")) if p not in train]
-        conv.append(os.path.normpath(os.path.join(HERE, "..", "include", "convtp.h")))
-        newest_train, newest_conv = (max(os.path.getmtime(p) for p in ps) for ps in (train, conv))
+        full = lambda paths: [os.path.normpath(os.path.join(HERE, p)) for p in paths]  # noqa: E731
+        newest = lambda paths: max(os.path.getmtime(p) for p in paths)  # noqa: E731
+        train, dense = full(TRAIN_HEADERS), full(DENSE_HEADERS)
+        others = train + dense + full(BINDING_HEADERS)
+        conv = [p for p in glob.glob(os.path.join(CSRC, "*.hpp")) if p not in others] + full(["../include/convtp.h"])
 
-        def stale(job):
-            src, obj, _ = job
-            newest = max(newest_train if src in TRAIN_SOURCES else newest_conv,
-                         os.path.getmtime(os.path.join(CSRC, src)))
-            return not os.path.exists(obj) or os.path.getmtime(obj) < newest
-        todo = [j for j in jobs if stale(j)]
+        def stale(src, target, headers):
+            return not os.path.exists(target) or os.path.getmtime(target) < newest([os.path.join(CSRC, src), *headers])
+
+        def headers_of(src):
+            return train if src in TRAIN_SOURCES else dense if src in (*DENSE_SOURCES, DENSE_TYPED_SOURCE) else conv
+        todo = [j for j in jobs if stale(j[0], j[1], headers_of(j[0]))]
+        bindings = [b for b in BINDINGS if stale(*b, full(BINDING_HEADERS))]
     n = workers or min(16, os.cpu_count() or 8)
-    binding = not incremental or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(
-        newest_train, os.path.getmtime(os.path.join(CSRC, BINDING_SOURCE)))
     with ThreadPoolExecutor(max_workers=n) as ex:
-        jobs_done = [ex.submit(_build_binding)] if binding else []
+        jobs_done = [ex.submit(_build_binding, *b) for b in bindings]
         list(ex.map(_compile, todo))
         for f in jobs_done:
             f.result()

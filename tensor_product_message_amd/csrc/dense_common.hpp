@@ -1,0 +1,307 @@
+// Matrix products of the dense operators: tiles, their way through LDS, matrix
+// instructions, and the way of their results back to rows.
+//
+//   out(m, n) = sum over k of A(m, k) B(n, k)
+//
+// An operand lies in memory with k contiguous ("along": rows of x or w) or
+// with m or n contiguous ("across": what a gradient sums over are rows of
+// storage).  Operands of 16 bits go to the matrix cores as they are.  Floats are
+// taken apart into three bfloat16, x = h + m + l, each the rest rounded to
+// nearest: 24 bits, so h + m + l is x (what underflows, 2^-133 and less, aside).
+// Of the nine products of the parts those below 2^-23 of the whole (m l, l m,
+// l l) are left out; the other six are summed in fp32, which is a float
+// product's accuracy at 2.7 times the rate of the fp32 matrix instructions
+// (2.5 PFLOP/s over six against 157 TFLOP/s).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "dense_kernels.hpp"
+#include "train_common.hpp"
+
+namespace ctp {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// What the matrix cores see of an element type: parts of type E.
+template <class T>
+struct Parts {
+    typedef T E;
+    static constexpr int count = 1;
+};
+template <>
+struct Parts<float> {
+    typedef __bf16 E;
+    static constexpr int count = 3;
+};
+
+template <class E>
+struct Frag {
+    typedef E type __attribute__((ext_vector_type(8)));
+    typedef E half __attribute__((ext_vector_type(4)));
+};
+
+__device__ __forceinline__ f32x16 mfma(Frag<__bf16>::type a, Frag<__bf16>::type b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(Frag<_Float16>::type a, Frag<_Float16>::type b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// A tile of Rows values of m (or n) by Depth of k in LDS, one plane for each
+// part.  Along: [row][k]; the 16-byte chunks of a row trade places by the row, so
+// that the 8 rows that one phase of a b128 read takes lie in different banks.
+// Across: [k][row]; units of 16 values trade places by k, for the transposing
+// reads, whose 16 lanes take 32 bytes of four values of k each.
+template <class E, int Parts_, bool Along, int Rows, int Depth>
+struct Tile {
+    static constexpr int kPlane = Rows * Depth;     // elements
+    static constexpr int kBytes = Parts_ * kPlane * 2;
+    typedef typename Frag<E>::type frag_t;
+
+    static __device__ __forceinline__ int chunk_of(int row, int c) {
+        return Depth == 64 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+    }
+    // element offset of value (row, k)
+    static __device__ __forceinline__ int at(int row, int k) {
+        if constexpr (Along) return row * Depth + chunk_of(row, k >> 3) * 8 + (k & 7);
+        return k * Rows + (((row >> 4) ^ (k & 3)) << 4) + (row & 15);
+    }
+    // The fragment of 32 rows from `row` and 16 k from `k`: lane i has row i % 32, 8 values of k from 8 (i / 32).
+    static __device__ __forceinline__ frag_t read(const E* plane, int row, int k, int lane) {
+        if constexpr (Along) {
+            return *reinterpret_cast<const frag_t*>(plane + at(row + (lane & 31), k + 8 * (lane >> 5)));
+        } else {
+            // 16 lanes read 4 rows of 16 values, lane i the values 4 (i % 4) of row i / 4, and get the columns
+            const int i = lane & 15, k0 = k + 8 * (lane >> 5) + (i >> 2), r0 = row + (lane & 16) + 4 * (i & 3);
+            typedef __attribute__((address_space(3))) s16x4* lds_t;
+            union {
+                s16x4 h[2];
+                frag_t f;
+            } u;
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(plane + at(r0, k0)));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(plane + at(r0, k0 + 4)));
+            return u.f;
+        }
+    }
+};
+
+// A tile's way from memory: 16-byte reads into registers, then into LDS as parts.
+// n_rows: how many m (or n) there are, values past which are any; k_end: where k ends, zeros past it.
+template <class T, bool Along, int Rows, int Depth, int Threads>
+struct Staged {
+    typedef typename Parts<T>::E E;
+    typedef Tile<E, Parts<T>::count, Along, Rows, Depth> tile_t;
+    static constexpr int kPerRow = (Along ? Depth : Rows) / kVec<T>;        // 16-byte vectors
+    static constexpr int kVecs = Rows * Depth / kVec<T> / Threads;          // a thread's
+    static_assert(kVecs * Threads * kVec<T> == Rows * Depth);
+    vec_t<T> v[kVecs];
+
+    // The tile's rows from row0, k from k0.  row_of(r): where row r of the tile lies among the operand's rows
+    // (Along), which may be any permutation.
+    template <class F>
+    __device__ __forceinline__ void load(const T* base, long ld, int row0, int n_rows, int k0, int k_end, F&& row_of) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow;
+            if constexpr (Along) {
+                const T* row = base + (long)row_of(row0, r) * ld;
+                const int k = k0 + c * kVec<T>;
+                if (k + kVec<T> <= k_end) {
+                    v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + k);
+                } else if (k < k_end) {
+                    v[i] = load_vec<T>(row, k / kVec<T>, k_end);
+                } else {
+                    v[i] = vec_t<T>{};
+                }
+            } else {
+                const int k = k0 + r, n = row0 + c * kVec<T>;
+                const T* row = base + (long)k * ld;
+                if (k >= k_end || n >= n_rows) {
+                    v[i] = vec_t<T>{};
+                } else if (n + kVec<T> <= n_rows) {
+                    v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + n);
+                } else {
+                    v[i] = load_vec<T>(row, n / kVec<T>, n_rows);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(E* lds) const {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow * kVec<T>;
+            E* to = lds + (Along ? tile_t::at(r, c) : tile_t::at(c, r));
+            if constexpr (Parts<T>::count == 1) {
+                *reinterpret_cast<vec_t<T>*>(to) = v[i];
+            } else {
+                typename Frag<E>::half h, m, l;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // a value whose rounding would be infinite is cut instead
+                    const float x = v[i][q];
+                    h[q] = (E)__builtin_amdgcn_fmed3f(x, -kLargest, kLargest);
+                    const float rest = x - (float)h[q];
+                    m[q] = (E)rest;
+                    l[q] = (E)(rest - (float)m[q]);
+                }
+                *reinterpret_cast<typename Frag<E>::half*>(to) = h;
+                *reinterpret_cast<typename Frag<E>::half*>(to + tile_t::kPlane) = m;
+                *reinterpret_cast<typename Frag<E>::half*>(to + 2 * tile_t::kPlane) = l;
+            }
+        }
+    }
+    static constexpr float kLargest = 3.3895313892515355e38f;      // of bfloat16
+};
+
+// One step of k through the matrix cores: the wave's tile of (32 MT) x (32 NT).  The matrix instruction's own rows are
+// n, so that a lane's four consecutive results lie beside each other in a row of the output.
+template <class TileA, class TileB, int NParts, int MT, int NT, int Depth, class E>
+__device__ __forceinline__ void multiply_step(f32x16 (&acc)[NT][MT], const E* a, const E* b, int m0, int n0, int lane) {
+    typedef typename Frag<E>::type frag_t;
+#pragma unroll
+    for (int k = 0; k < Depth; k += 16) {
+        frag_t fa[MT][NParts], fb[NT][NParts];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int p = 0; p < NParts; ++p) fa[i][p] = TileA::read(a + p * TileA::kPlane, m0 + 32 * i, k, lane);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int p = 0; p < NParts; ++p) fb[j][p] = TileB::read(b + p * TileB::kPlane, n0 + 32 * j, k, lane);
+        // the parts' smallest products first
+#pragma unroll
+        for (int s = NParts - 1; s >= 0; --s)
+#pragma unroll
+            for (int p = 0; p <= s; ++p)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) acc[j][i] = mfma(fb[j][s - p], fa[i][p], acc[j][i]);
+    }
+}
+
+// The wave's results by rows: for every row of its tile f(m, n, first), where first[0 .. V) are the values of the
+// columns n .. n + V - 1 of the wave's tile, in fp32.  slab: the wave's own piece of LDS, 32 rows of kSlab floats.
+// Pairs: the halves of each 64 columns belong together, f(m, n, first, second) for the columns n, n + 32 of them.
+template <int NT>
+constexpr int kSlab = 32 * NT + 4;
+
+__device__ __forceinline__ void wave_lds_fence() {
+    // LDS accesses of one wave stay in order; this keeps the compiler from moving them
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Rows 32 i .. 32 i + 31 of the wave's tile into its slab.
+template <int NT, int MT>
+__device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i, float* slab, int lane) {
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 x;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = acc[j][i][4 * g + q];
+            *reinterpret_cast<f32x4*>(slab + (lane & 31) * kSlab<NT> + 32 * j + 8 * g + 4 * (lane >> 5)) = x;
+        }
+    wave_lds_fence();
+}
+
+template <int V, bool Pairs, int MT, int NT, class F>
+__device__ __forceinline__ void by_rows(const f32x16 (&acc)[NT][MT], float* slab, int lane, F&& f) {
+    constexpr int kCols = 32 * NT / (Pairs ? 2 : 1), kLanes = kCols / V, kRows = 64 / kLanes;
+    static_assert(!Pairs || NT % 2 == 0);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        by_rows_block(acc, i, slab, lane);
+#pragma unroll
+        for (int r = 0; r < 32; r += kRows) {
+            const int m = r + lane / kLanes, n = lane % kLanes * V;
+            const float* from = slab + m * kSlab<NT> + (Pairs ? n / 32 * 64 + n % 32 : n);
+            float x[V], y[V];
+#pragma unroll
+            for (int q = 0; q < V; q += 4) {
+                *reinterpret_cast<f32x4*>(x + q) = *reinterpret_cast<const f32x4*>(from + q);
+                if constexpr (Pairs) *reinterpret_cast<f32x4*>(y + q) = *reinterpret_cast<const f32x4*>(from + 32 + q);
+            }
+            f(32 * i + m, n, x, y);
+        }
+    }
+}
+
+// Where workgroup `id` of `total` works: the workgroups of one of the 8 XCDs, which get every eighth, take
+// consecutive tiles, and those go through up to kGroup rows of tiles before the next column, so that an XCD's L2 sees
+// the same operands again.
+constexpr unsigned kXcds = 8, kGroup = 8;
+
+__device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned total) {
+    const unsigned q = total / kXcds, r = total % kXcds, xcd = id % kXcds;
+    return (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + id / kXcds;
+}
+
+struct TileAt {
+    unsigned m, n, outer;       // tile row, tile column, batch and split
+};
+__device__ __forceinline__ TileAt tile_at(unsigned id, unsigned tiles_m, unsigned tiles_n) {
+    TileAt t;
+    const unsigned per = tiles_m * tiles_n;
+    t.outer = id / per;
+    id -= t.outer * per;
+    const unsigned in_group = kGroup * tiles_n, group = id / in_group, first = group * kGroup;
+    const unsigned rows = min(tiles_m - first, kGroup);
+    id -= group * in_group;
+    t.m = first + id % rows;
+    t.n = id / rows;
+    return t;
+}
+
+// ---------------------------------------------------------------- activations
+
+// act(z), its first and its second derivative.
+__device__ __forceinline__ void activation(int act, float z, float& f, float& d1, float& d2) {
+    switch (act) {
+        case kActRelu:
+            f = z > 0.0f ? z : (z != z ? z : 0.0f);
+            d1 = z > 0.0f ? 1.0f : 0.0f;
+            d2 = 0.0f;
+            return;
+        case kActSilu:
+        case kActSigmoid: {
+            // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
+            const float e = expf(-fabsf(z)), large = 1.0f / (1.0f + e), small = e * large;
+            const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
+            if (act == kActSigmoid) {
+                f = s, d1 = t, d2 = t * u;
+            } else {
+                f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
+            }
+            return;
+        }
+        case kActGelu: {
+            const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * expf(-0.5f * z * z);
+            f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
+            return;
+        }
+        case kActTanh: {
+            const float e = expf(-2.0f * fabsf(z)), r = 1.0f / (1.0f + e);
+            f = tanhf(z);
+            d1 = 4.0f * e * r * r;
+            d2 = -2.0f * f * d1;
+            return;
+        }
+        default: f = z, d1 = 1.0f, d2 = 0.0f; return;
+    }
+}
+
+// l of component d = l^2 .. l^2 + 2 l
+__host__ __device__ __forceinline__ int degree_of(int d) { return d < 1 ? 0 : d < 4 ? 1 : d < 9 ? 2 : 3; }
+
+}  // namespace ctp

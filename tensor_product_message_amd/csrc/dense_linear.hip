@@ -1,0 +1,624 @@
+// Linear layers with their epilogue, the gated feed-forward form, and their first
+// and second gradients.  One object for each element type (-DCTP_DENSE_TYPE),
+// the dispatch by type in dense_dispatch.hip.
+//
+//   z = x W^T + b,   y = act(z) + r                or  h = act(z0) z1 (gated)
+//   s = G act'(z)    d_x = s W   d_W = s^T x   d_b = sum of s
+//   v = u W^T        g_G = v act'(z)   g_z = v G act''(z)
+//                    g_x = g_z W   g_W = g_z^T x + s^T u   g_b = sum of g_z
+//
+// s, g_z (and the gated form's pairs of them) are rounded to the features' type
+// before they enter a product, as the stored z is: they are operands of the
+// matrix cores.  What is summed is in fp32.
+#include "dense_common.hpp"
+#include "dense_linear.hpp"
+
+namespace ctp {
+namespace {
+
+#if CTP_DENSE_TYPE == 0
+typedef float T;
+#elif CTP_DENSE_TYPE == 1
+typedef __bf16 T;
+#else
+typedef _Float16 T;
+#endif
+typedef Parts<T>::E E;
+constexpr int kParts = Parts<T>::count, V = kVec<T>;
+constexpr int kDepth = kParts == 1 ? 64 : 32;       // of k a tile: 128 bytes of a row
+
+// ---------------------------------------------------------------- products
+
+struct Gemm {
+    const T *a, *b;
+    long a_ld, b_ld;            // elements from row to row of storage
+    long a_batch, b_batch;      // from batch to batch; b_batch by degree where b_degree is set
+    int b_degree;
+    long m, k;
+    int n;                      // Pairs: columns of one half
+    long pair;                  // Pairs: elements of B from a column to its partner
+    long k_split;               // k of a split, a multiple of kDepth
+    unsigned splits, tiles_m, tiles_n, total;
+};
+
+// A tile of BM x BN by 4 waves, WM x (4 / WM) of them.  One buffer in LDS: the next tiles' reads are in flight in
+// registers while the matrix cores work, and the workgroups that share a CU fill each other's pauses.
+template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
+__global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
+    constexpr int WN = 4 / WM, MT = BM / 32 / WM, NT = BN / 32 / WN;
+    typedef Staged<T, AlongA, BM, kDepth, 256> SA;
+    typedef Staged<T, AlongB, BN, kDepth, 256> SB;
+    constexpr int kTiles = SA::tile_t::kBytes + SB::tile_t::kBytes, kSlabs = 4 * 32 * kSlab<NT> * 4;
+    __shared__ __attribute__((aligned(16))) char lds[kTiles > kSlabs ? kTiles : kSlabs];
+    E* la = reinterpret_cast<E*>(lds);
+    E* lb = reinterpret_cast<E*>(lds + SA::tile_t::kBytes);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave % WM * 32 * MT, wn = wave / WM * 32 * NT;
+
+    for (unsigned id = blockIdx.x; id < g.total; id += gridDim.x) {
+        const TileAt t = tile_at(xcd_order(id, g.total), g.tiles_m, g.tiles_n);
+        const unsigned batch = t.outer / g.splits, split = t.outer % g.splits;
+        const long m0 = (long)t.m * BM, k0 = split * g.k_split;
+        const int n0 = t.n * (Pairs ? BN / 2 : BN);
+        const int k_end = (int)min(g.k_split, g.k - k0);    // from here on k counts from k0
+        const T* a = g.a + batch * g.a_batch + (AlongA ? m0 * g.a_ld + k0 : k0 * g.a_ld + m0);
+        const T* b = g.b + (g.b_degree ? degree_of(batch) : (int)batch) * g.b_batch +
+                     (AlongB ? (long)n0 * g.b_ld + k0 : k0 * g.b_ld + n0);
+        const int m_left = (int)min((long)BM, g.m - m0), n_left = min(g.n - n0, BN);
+        // rows past the last give results that nobody stores
+        auto row_a = [&](int, int r) { return (long)min(r, m_left - 1); };
+        auto row_b = [&](int, int r) {
+            if constexpr (Pairs) {
+                const int col = min((r >> 6 << 5) + (r & 31), n_left - 1);
+                return (long)col + (r >> 5 & 1) * g.pair;
+            }
+            return (long)min(r, n_left - 1);
+        };
+        f32x16 acc[NT][MT] = {};
+        SA sa;
+        SB sb;
+        sa.load(a, g.a_ld, 0, m_left, 0, k_end, row_a);
+        sb.load(b, g.b_ld, 0, n_left, 0, k_end, row_b);
+        for (int k = 0; k < k_end; k += kDepth) {
+            lds_barrier();
+            sa.store(la);
+            sb.store(lb);
+            lds_barrier();
+            if (k + kDepth < k_end) {
+                sa.load(a, g.a_ld, 0, m_left, k + kDepth, k_end, row_a);
+                sb.load(b, g.b_ld, 0, n_left, k + kDepth, k_end, row_b);
+            }
+            multiply_step<typename SA::tile_t, typename SB::tile_t, kParts, MT, NT, kDepth>(acc, la, lb, wm, wn, lane);
+        }
+        lds_barrier();
+        by_rows<V, Pairs, MT, NT>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>, lane,
+                                  [&](int mr, int nc, const float* x, const float* y) {
+                                      const int m = wm + mr, n = (Pairs ? wn / 2 : wn) + nc;
+                                      if (m < m_left && n < n_left) epi(t.outer, batch, m0 + m, n0 + n, x, y);
+                                  });
+        lds_barrier();
+    }
+}
+
+// V floats, the same width as a vector of T.
+struct Values {
+    float v[V];
+};
+
+__device__ __forceinline__ Values read_values(const T* row, int n, int width) {
+    const Floats<T> f = widen<T>(load_vec<T>(row, n / V, width));
+    Values x;
+#pragma unroll
+    for (int q = 0; q < V; ++q) x.v[q] = f.v[q];
+    return x;
+}
+__device__ __forceinline__ void write_values(T* row, int n, int width, const float* x) {
+    Floats<T> f;
+#pragma unroll
+    for (int q = 0; q < V; ++q) f.v[q] = x[q];
+    store_left<T>(row + n, width - n, narrow<T>(f));
+}
+
+// y = act(x + bias) + residual, z = x + bias
+struct EpiLinear {
+    T *y, *z;
+    const T *bias, *residual;
+    long row, residual_row;     // elements from row to row
+    int n, act;
+    __device__ __forceinline__ void operator()(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
+        Values v;
+#pragma unroll
+        for (int q = 0; q < V; ++q) v.v[q] = x[q];
+        if (bias != nullptr && batch == 0) {
+            const Values b = read_values(bias, at, n);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v.v[q] += b.v[q];
+        }
+        const long to = m * row + (long)batch * n;
+        if (z != nullptr) write_values(z + to, at, n, v.v);
+        if (act != kActNone) {
+            float d1, d2;
+#pragma unroll
+            for (int q = 0; q < V; ++q) activation(act, v.v[q], v.v[q], d1, d2);
+        }
+        if (residual != nullptr) {
+            const Values r = read_values(residual + m * residual_row + (long)batch * n, at, n);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v.v[q] += r.v[q];
+        }
+        write_values(y + to, at, n, v.v);
+    }
+};
+
+// h = act(x + bias[0]) (y + bias[1]), z the two sums
+struct EpiGated {
+    T *h, *z;
+    const T* bias;
+    int n, act;
+    __device__ __forceinline__ void operator()(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
+        Values a, b;
+#pragma unroll
+        for (int q = 0; q < V; ++q) a.v[q] = x[q], b.v[q] = y[q];
+        if (bias != nullptr) {
+            const Values p = read_values(bias, at, n), r = read_values(bias + n, at, n);
+#pragma unroll
+            for (int q = 0; q < V; ++q) a.v[q] += p.v[q], b.v[q] += r.v[q];
+        }
+        if (z != nullptr) {
+            write_values(z + m * 2 * n, at, n, a.v);
+            write_values(z + m * 2 * n + n, at, n, b.v);
+        }
+        Values f;
+        float d1, d2;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            activation(act, a.v[q], f.v[q], d1, d2);
+            f.v[q] *= b.v[q];
+        }
+        write_values(h + m * n, at, n, f.v);
+    }
+};
+
+// out = x
+struct EpiPlain {
+    T* out;
+    long row;
+    int n;
+    __device__ __forceinline__ void operator()(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
+        write_values(out + m * row + (long)batch * n, at, n, x);
+    }
+};
+
+// A split's share of a sum, in fp32.
+struct EpiPart {
+    float* parts;
+    long size;      // of one part: rows n values wide
+    int n;
+    __device__ __forceinline__ void operator()(unsigned outer, unsigned, long m, int at, const float* x, const float*) const {
+        float* to = parts + outer * size + m * n + at;
+#pragma unroll
+        for (int q = 0; q < V; q += 4)
+            if (at + q < n) {
+                vec_t<float> w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = x[q + e];
+                store_left<float>(to + q, n - at - q, w);
+            }
+    }
+};
+
+// The second backward pass's middle: v = x (gated: x and y) in, g_G, g_z and s out.
+template <bool Gated>
+struct EpiSecond {
+    const T *grad, *z;
+    T *g_grad, *g_z, *s;
+    long grad_row;
+    int n, act;
+    __device__ __forceinline__ void operator()(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
+        const Values g = read_values(grad + m * grad_row, at, n);
+        const long zr = m * n * (Gated ? 2 : 1);
+        const Values a = read_values(z + zr, at, n);
+        Values b{}, o, p, q, pb, qb;
+        if constexpr (Gated) b = read_values(z + zr + n, at, n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f, d1, d2;
+            activation(act, a.v[i], f, d1, d2);
+            if constexpr (Gated) {
+                const float gb = g.v[i] * b.v[i];
+                o.v[i] = __builtin_fmaf(x[i] * b.v[i], d1, y[i] * f);
+                p.v[i] = __builtin_fmaf(x[i] * gb, d2, y[i] * g.v[i] * d1);
+                pb.v[i] = x[i] * g.v[i] * d1;
+                q.v[i] = gb * d1;
+                qb.v[i] = g.v[i] * f;
+            } else {
+                o.v[i] = x[i] * d1;
+                p.v[i] = x[i] * g.v[i] * d2;
+                q.v[i] = g.v[i] * d1;
+            }
+        }
+        if (g_grad != nullptr) write_values(g_grad + m * n, at, n, o.v);
+        if (g_z != nullptr) {
+            write_values(g_z + zr, at, n, p.v);
+            if constexpr (Gated) write_values(g_z + zr + n, at, n, pb.v);
+        }
+        if (s != nullptr) {
+            write_values(s + zr, at, n, q.v);
+            if constexpr (Gated) write_values(s + zr + n, at, n, qb.v);
+        }
+    }
+};
+
+// ---------------------------------------------------------------- passes over values
+
+// s = grad act'(z) for the products of the backward pass, and its columns' sums, a part for each chunk of rows.
+// Gated: s and the sums have both halves beside each other.  A workgroup is `across` lanes wide, a vector of columns
+// each, and 256 / across rows high.
+struct ActBwd {
+    const T *grad, *z;
+    T* s;               // null: the sums alone, of grad itself
+    float* sums;        // null: none; [chunk][columns]
+    long grad_row, rows, chunk;
+    int n, act, across;
+};
+
+template <bool Gated>
+__global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
+    constexpr int H = Gated ? 2 : 1;
+    __shared__ float part[256 * H * V];
+    const int tx = threadIdx.x % p.across, ty = threadIdx.x / p.across, high = 256 / p.across;
+    const int at = (blockIdx.x * p.across + tx) * V;
+    const long first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.rows);
+    Values sum[H] = {};
+    if (at < p.n) {
+        for (long m = first + ty; m < last; m += high) {
+            Values g = read_values(p.grad + m * p.grad_row, at, p.n), u{};
+            if (p.s != nullptr) {
+                const long zr = m * p.n * H;
+                const Values a = read_values(p.z + zr, at, p.n);
+                if constexpr (Gated) {
+                    const Values b = read_values(p.z + zr + p.n, at, p.n);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        float f, d1, d2;
+                        activation(p.act, a.v[q], f, d1, d2);
+                        u.v[q] = g.v[q] * f;
+                        g.v[q] = g.v[q] * b.v[q] * d1;
+                    }
+                    write_values(p.s + zr + p.n, at, p.n, u.v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        float f, d1, d2;
+                        activation(p.act, a.v[q], f, d1, d2);
+                        g.v[q] *= d1;
+                    }
+                }
+                write_values(p.s + zr, at, p.n, g.v);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                sum[0].v[q] += g.v[q];
+                if constexpr (Gated) sum[1].v[q] += u.v[q];
+            }
+        }
+    }
+    if (p.sums == nullptr) return;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int q = 0; q < V; ++q) part[((h * high + ty) * V + q) * p.across + tx] = sum[h].v[q];
+    lds_barrier();
+    // value i of the workgroup's across * V columns, summed over its rows in order
+    for (int i = threadIdx.x; i < H * V * p.across; i += 256) {
+        const int h = i / (V * p.across), c = i % (V * p.across), col = blockIdx.x * p.across * V + c;
+        if (col >= p.n) continue;
+        float s = 0.0f;
+        for (int r = 0; r < high; ++r) s += part[((h * high + r) * V + c % V) * p.across + c / V];
+        p.sums[(long)blockIdx.y * p.n * H + h * p.n + col] = s;
+    }
+}
+
+// Parts joined in their order, 16 at a time: out[l][i] = sum over the parts of degree l.
+struct Join {
+    const float* parts;
+    T* out;
+    long size;              // of one part
+    int degrees;            // part p belongs to the degree of p / per_component
+    unsigned per_component;
+    unsigned groups;        // of 64 values, each degree's own
+};
+
+__global__ __launch_bounds__(1024) void k_join(Join first, Join second) {
+    __shared__ float part[16][64];
+    const bool is_first = blockIdx.x < first.groups * first.degrees;
+    const Join& j = is_first ? first : second;
+    const unsigned id = is_first ? blockIdx.x : blockIdx.x - first.groups * first.degrees;
+    const unsigned l = id / j.groups, c = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const long i = (long)(id % j.groups) * 64 + c;
+    const unsigned p0 = l * l * j.per_component, p1 = (l + 1) * (l + 1) * j.per_component;
+    float s = 0.0f;
+    if (i < j.size)
+        for (unsigned p = p0 + q; p < p1; p += 16) s += j.parts[p * j.size + i];
+    part[q][c] = s;
+    lds_barrier();
+    if (q == 0 && i < j.size) {
+#pragma unroll
+        for (int r = 1; r < 16; ++r) s += part[r][c];
+        j.out[l * j.size + i] = (T)s;
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
+constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
+
+// Workgroups that fill the card: two for each of 256 CUs.
+constexpr long kFill = 512;
+
+template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
+hipError_t run_tiles(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
+    g.tiles_m = (unsigned)div_up(g.m, BM);
+    g.tiles_n = (unsigned)div_up(g.n, Pairs ? BN / 2 : BN);
+    const long total = (long)g.tiles_m * g.tiles_n * outer;
+    if (total == 0) return hipSuccess;
+    g.total = (unsigned)total;
+    k_gemm<AlongA, AlongB, BM, BN, WM, Pairs><<<dim3((unsigned)min(total, max_groups(256))), 256, 0, st>>>(g, epi);
+    return hipGetLastError();
+}
+
+// Whether tiles of 128 fill the card; those of 64 reach half their rate, and are for what has too few of them.
+bool wide_tiles(long m, long n, long outer) { return div_up(m, 128) * div_up(n, 128) * outer >= kFill / 2; }
+
+template <bool AlongA, bool AlongB, class Epi>
+hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
+    g.splits = 1;
+    g.k_split = div_up(g.k, kDepth) * kDepth;
+    if (wide_tiles(g.m, g.n, batches)) return run_tiles<AlongA, AlongB, 128, 128, 2, false>(g, batches, epi, st);
+    return run_tiles<AlongA, AlongB, 64, 64, 2, false>(g, batches, epi, st);
+}
+template <class Epi>
+hipError_t run_pairs(Gemm g, const Epi& epi, hipStream_t st) {
+    g.splits = 1;
+    g.k_split = div_up(g.k, kDepth) * kDepth;
+    if (wide_tiles(g.m, 2L * g.n, 1)) return run_tiles<true, true, 128, 128, 2, true>(g, 1, epi, st);
+    return run_tiles<true, true, 64, 128, 2, true>(g, 1, epi, st);
+}
+
+// How d_W[outer][inner] = sum over rows is cut: every component by itself, and its rows into `splits`.
+struct WeightCut {
+    bool wide;
+    unsigned splits;
+    long k_split;
+    bool direct;        // one part alone: no join
+};
+WeightCut weight_cut(const LinearArgs& a, bool twice) {
+    const long comps = (long)(a.lmax + 1) * (a.lmax + 1), out = (long)a.outer * (a.gated ? 2 : 1);
+    WeightCut c;
+    // large matrices fill the card by themselves
+    c.wide = div_up(out, 128) * div_up(a.inner, 128) * comps >= kFill / 8 && a.inner > 64 && out > 64;
+    const long tile = c.wide ? 128 : 64, tiles = div_up(out, tile) * div_up(a.inner, tile) * comps;
+    long splits = max(1L, min(kFill / tiles, a.n_rows / (4 * kDepth)));
+    splits = max(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
+    c.k_split = max(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
+    c.splits = (unsigned)max(1L, div_up(a.n_rows, c.k_split));
+    c.direct = c.splits == 1 && comps == 1 && !twice;
+    return c;
+}
+
+struct BiasCut {
+    long chunk;
+    unsigned chunks;
+    int across;
+    unsigned groups;
+};
+BiasCut bias_cut(long rows, int n) {
+    BiasCut c;
+    c.across = 1;
+    while (c.across < 64 && c.across * V < n) c.across *= 2;
+    c.groups = (unsigned)div_up(n, (long)c.across * V);
+    const long high = 256 / c.across;
+    // enough workgroups for the card, at most 1024 chunks, which are joined afterwards
+    const long most = max(1L, min(1024L, div_up(4 * kFill, c.groups)));
+    c.chunk = max(1L, div_up(div_up(rows, most), high)) * high;
+    c.chunks = (unsigned)max(1L, div_up(rows, c.chunk));
+    return c;
+}
+
+struct Layout {
+    long s, g_z, sums, parts, bytes;
+};
+Layout layout_of(const LinearArgs& a, bool second) {
+    const long z_bytes = align256(a.n_rows * a.outer * (a.gated ? 2 : 1) * (long)sizeof(T));
+    const bool act = a.act != kActNone || a.gated;
+    const long out = (long)a.outer * (a.gated ? 2 : 1), comps = (long)(a.lmax + 1) * (a.lmax + 1);
+    const WeightCut w = weight_cut(a, second && act);
+    const BiasCut b = bias_cut(a.n_rows, a.outer);
+    Layout y;
+    y.s = 0;
+    y.g_z = act ? z_bytes : 0;
+    y.sums = y.g_z + (act && second ? z_bytes : 0);
+    y.parts = y.sums + align256(b.chunks * out * 4);
+    y.bytes = y.parts + (w.direct ? 0 : align256(w.splits * comps * out * a.inner * 4 * (second && act ? 2 : 1)));
+    return y;
+}
+
+Gemm forward_product(const LinearArgs& a, const T* x, long x_row) {
+    Gemm g{};
+    g.a = x;
+    g.a_ld = x_row;
+    g.a_batch = a.inner;
+    g.b = static_cast<const T*>(a.w);
+    g.b_ld = a.inner;
+    g.b_degree = 1;
+    g.b_batch = (long)a.outer * a.inner;
+    g.m = a.n_rows;
+    g.n = a.outer;
+    g.k = a.inner;
+    g.pair = a.outer;
+    return g;
+}
+
+// out[row][inner] = s W
+hipError_t input_gradient(const LinearArgs& a, const T* s, long s_row, void* out, hipStream_t st) {
+    const int comps = (a.lmax + 1) * (a.lmax + 1);
+    Gemm g{};
+    g.a = s;
+    g.a_ld = s_row;
+    g.a_batch = a.outer;
+    g.b = static_cast<const T*>(a.w);
+    g.b_ld = a.inner;
+    g.b_degree = 1;
+    g.b_batch = (long)a.outer * a.inner;
+    g.m = a.n_rows;
+    g.n = a.inner;
+    g.k = (long)a.outer * (a.gated ? 2 : 1);
+    return run_gemm<true, false>(g, comps, EpiPlain{static_cast<T*>(out), (long)comps * a.inner, a.inner}, st);
+}
+
+// The parts of s^T x over the rows (direct: d_w itself).
+hipError_t weight_gradient(const LinearArgs& a, const T* s, long s_row, const T* x, long x_row, const WeightCut& c,
+                           float* parts, T* d_w, hipStream_t st) {
+    const unsigned comps = (a.lmax + 1) * (a.lmax + 1);
+    const long out = (long)a.outer * (a.gated ? 2 : 1);
+    Gemm g{};
+    g.a = s;
+    g.a_ld = s_row;
+    g.a_batch = a.outer;
+    g.b = x;
+    g.b_ld = x_row;
+    g.b_batch = a.inner;
+    g.m = out;
+    g.n = a.inner;
+    g.k = a.n_rows;
+    g.splits = c.splits;
+    g.k_split = c.k_split;
+    if (c.direct) {
+        const EpiPlain epi{d_w, a.inner, a.inner};
+        return c.wide ? run_tiles<false, false, 128, 128, 2, false>(g, 1, epi, st)
+                      : run_tiles<false, false, 64, 64, 2, false>(g, 1, epi, st);
+    }
+    const EpiPart epi{parts, out * a.inner, a.inner};
+    return c.wide ? run_tiles<false, false, 128, 128, 2, false>(g, comps * c.splits, epi, st)
+                  : run_tiles<false, false, 64, 64, 2, false>(g, comps * c.splits, epi, st);
+}
+
+hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, float* sums, bool gated, int n, const BiasCut& c,
+                   hipStream_t st) {
+    const ActBwd p{grad, static_cast<const T*>(a.z), s, sums, grad_row, a.n_rows, c.chunk, n, a.act, c.across};
+    if (a.n_rows == 0 && sums == nullptr) return hipSuccess;
+    if (gated)
+        k_act_bwd<true><<<dim3(c.groups, c.chunks), 256, 0, st>>>(p);
+    else
+        k_act_bwd<false><<<dim3(c.groups, c.chunks), 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+Join join_of(const float* parts, void* out, long size, int degrees, unsigned per_component) {
+    return Join{parts, static_cast<T*>(out), size, degrees, per_component, (unsigned)div_up(size, 64)};
+}
+hipError_t join(const Join& a, const Join& b, hipStream_t st) {
+    const unsigned groups = a.groups * a.degrees + b.groups * b.degrees;
+    if (groups == 0) return hipSuccess;
+    k_join<<<groups, 1024, 0, st>>>(a, b);
+    return hipGetLastError();
+}
+
+#define CTP_TRY(call)                                                 \
+    do {                                                              \
+        if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+    } while (0)
+
+hipError_t fwd(const LinearArgs& a, hipStream_t st) {
+    const int comps = (a.lmax + 1) * (a.lmax + 1);
+    const Gemm g = forward_product(a, static_cast<const T*>(a.x), a.x_stride);
+    if (a.gated)
+        return run_pairs(g, EpiGated{static_cast<T*>(a.y), static_cast<T*>(a.z_out), static_cast<const T*>(a.bias), a.outer, a.act}, st);
+    return run_gemm<true, true>(g, comps,
+                                EpiLinear{static_cast<T*>(a.y), static_cast<T*>(a.z_out), static_cast<const T*>(a.bias),
+                                          static_cast<const T*>(a.residual), (long)comps * a.outer, a.residual_stride,
+                                          a.outer, a.act},
+                                st);
+}
+
+hipError_t bwd(const LinearArgs& a, hipStream_t st) {
+    const Layout y = layout_of(a, false);
+    char* ws = static_cast<char*>(a.workspace);
+    const bool act = a.act != kActNone || a.gated;
+    const long out = (long)a.outer * (a.gated ? 2 : 1);
+    float *sums = a.d_bias ? reinterpret_cast<float*>(ws + y.sums) : nullptr, *parts = reinterpret_cast<float*>(ws + y.parts);
+    const BiasCut b = bias_cut(a.n_rows, a.outer);
+    const T* s = static_cast<const T*>(a.grad);
+    long s_row = a.grad_stride;
+    if (act || sums) { CTP_TRY(act_bwd(a, s, s_row, act ? reinterpret_cast<T*>(ws + y.s) : nullptr, sums, a.gated, a.outer, b, st)); }
+    if (act) s = reinterpret_cast<const T*>(ws + y.s), s_row = out;
+    if (a.d_x) CTP_TRY(input_gradient(a, s, s_row, a.d_x, st));
+    Join of_w{}, of_b{};
+    if (a.d_w) {
+        const WeightCut c = weight_cut(a, false);
+        CTP_TRY(weight_gradient(a, s, s_row, static_cast<const T*>(a.x), a.x_stride, c, parts, static_cast<T*>(a.d_w), st));
+        if (!c.direct) of_w = join_of(parts, a.d_w, out * a.inner, a.lmax + 1, c.splits);
+    }
+    if (a.d_bias) of_b = join_of(sums, a.d_bias, out, 1, b.chunks);
+    return join(of_w, of_b, st);
+}
+
+hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
+    const Layout y = layout_of(a, true);
+    char* ws = static_cast<char*>(a.workspace);
+    const int comps = (a.lmax + 1) * (a.lmax + 1);
+    const bool act = a.act != kActNone || a.gated;
+    const long out = (long)a.outer * (a.gated ? 2 : 1);
+    const T *u = static_cast<const T*>(a.a_d_x), *grad = static_cast<const T*>(a.grad), *z = static_cast<const T*>(a.z);
+    T *s = reinterpret_cast<T*>(ws + y.s), *g_z = reinterpret_cast<T*>(ws + y.g_z);
+    float *sums = reinterpret_cast<float*>(ws + y.sums), *parts = reinterpret_cast<float*>(ws + y.parts);
+    const Gemm v = forward_product(a, u, (long)comps * a.inner);
+    const WeightCut c = weight_cut(a, act);
+    if (!act) {
+        if (a.g_grad) CTP_TRY((run_gemm<true, true>(v, comps, EpiPlain{static_cast<T*>(a.g_grad), (long)comps * a.outer, a.outer}, st)));
+        if (a.g_w == nullptr) return hipSuccess;
+        CTP_TRY(weight_gradient(a, grad, a.grad_stride, u, (long)comps * a.inner, c, parts, static_cast<T*>(a.g_w), st));
+        return c.direct ? hipSuccess : join(join_of(parts, a.g_w, out * a.inner, a.lmax + 1, c.splits), Join{}, st);
+    }
+    const bool need_z = a.g_x || a.g_w || a.g_bias;
+    if (a.gated)
+        CTP_TRY(run_pairs(v, EpiSecond<true>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr, a.g_w ? s : nullptr,
+                                             a.grad_stride, a.outer, a.act}, st));
+    else
+        CTP_TRY((run_gemm<true, true>(v, 1, EpiSecond<false>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
+                                                            a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, st)));
+    if (a.g_x) CTP_TRY(input_gradient(a, g_z, out, a.g_x, st));
+    Join of_w{}, of_b{};
+    if (a.g_w) {
+        CTP_TRY(weight_gradient(a, g_z, out, static_cast<const T*>(a.x), a.x_stride, c, parts, nullptr, st));
+        CTP_TRY(weight_gradient(a, s, out, u, a.inner, c, parts + c.splits * out * a.inner, nullptr, st));
+        of_w = join_of(parts, a.g_w, out * a.inner, 1, 2 * c.splits);
+    }
+    if (a.g_bias) {
+        const int half = a.outer;
+        const BiasCut b = bias_cut(a.n_rows, half);
+        // the halves of a gated z as columns side by side: summed one half at a time
+        for (int h = 0; h < (a.gated ? 2 : 1); ++h) {
+            CTP_TRY(act_bwd(a, g_z + (long)h * half, out, nullptr, sums + (long)h * b.chunks * half, false, half, b, st));
+            const Join of = join_of(sums + (long)h * b.chunks * half, static_cast<T*>(a.g_bias) + (long)h * half, half, 1, b.chunks);
+            if (h + 1 == (a.gated ? 2 : 1))
+                of_b = of;
+            else
+                CTP_TRY(join(of, Join{}, st));
+        }
+    }
+    return join(of_w, of_b, st);
+}
+
+long workspace(const LinearArgs& a, bool second) { return layout_of(a, second).bytes; }
+
+}  // namespace
+
+template <>
+const LinearOps& linear_ops<CTP_DENSE_TYPE>() {
+    static constexpr LinearOps ops{fwd, bwd, bwd_bwd, workspace};
+    return ops;
+}
+
+}  // namespace ctp

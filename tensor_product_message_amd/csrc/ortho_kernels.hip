@@ -1,0 +1,386 @@
+// Orthogonalising matrices by Newton-Schulz products.
+//
+//   X = M / (|M| + eps)       |M| the root of the sum of squares
+//   A = X X^T,  X <- a X + (b A + c A A) X      `steps` times
+//
+// which takes every singular value s of X to a s + b s^3 + c s^5 and leaves the
+// singular vectors.  With a, b, c = 3.4445, -4.7750, 2.0315 the values between
+// some 0.003 and 1 are between 0.7 and 1.2 after five steps.
+//
+// X lies with its short side S first, [S][L]: a tall matrix is turned on its way
+// in and on its way out.  Small singular values grow some 3.4 times a step, and
+// the noise that a rounding of X puts beside them grows alike: with X in
+// bfloat16 or float16 a matrix of few strong directions comes out wrong by 22%
+// and 4%.  So X, A and b A + c A A are held in 32 bits whatever the matrix's
+// type, as two float16, v 2^12 = h + l: 22 bits, and with entries below 1.3, 1.8
+// and 3 nothing overflows and nothing above 2^-36 is lost.  A product is three
+// of the matrix cores', h h + h l + l h (l l is below 2^-22 of it).
+//
+// All matrices of a call go through the same launches, three a step.
+#include "dense_direct.hpp"
+
+namespace ctp {
+namespace {
+
+typedef _Float16 E;
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScale = 4096.0f;
+constexpr int kPad = 64, kDepth = 32;
+constexpr int kMostGroups = 32;     // tensors of one launch
+constexpr int kMostSums = 64;       // shares of a matrix's sum of squares
+
+// One tensor: `batch` matrices.  Places are elements from the workspace's start; each matrix has two planes.
+struct Group {
+    const void* in;
+    void* out;
+    long x[2], a, b;        // X and the next X, A, b A + c A A of the first matrix
+    long sums;              // doubles from the sums' start
+    int rows, cols, dtype;  // of a matrix as it is given
+    int s, l;               // padded sides
+    unsigned batch;
+    unsigned chunks;        // shares of the sum of squares
+    bool tall;
+};
+struct Groups {
+    int n;
+    float eps, scale;
+    E* base;
+    double* sums;
+    Group g[kMostGroups];
+    unsigned first[kMostGroups + 1];    // of this launch's workgroups, each group's first
+};
+
+__device__ __forceinline__ int group_of(const Groups& p, unsigned id) {
+    int k = 0;
+    while (k + 1 < p.n && id >= p.first[k + 1]) ++k;
+    return k;
+}
+
+__device__ __forceinline__ float value_at(const void* p, int dtype, long i) {
+    if (dtype == kF32) return static_cast<const float*>(p)[i];
+    if (dtype == kBF16) return (float)static_cast<const __bf16*>(p)[i];
+    return (float)static_cast<const _Float16*>(p)[i];
+}
+
+// Calls f(T{}) for an element type's code.
+template <class F>
+__device__ __forceinline__ void of_type(int code, F&& f) {
+    if (code == kF32)
+        f(float{});
+    else if (code == kBF16)
+        f(__bf16{});
+    else
+        f(_Float16{});
+}
+
+// Shares of the sums of squares, in 64 bits.
+__global__ __launch_bounds__(256) void k_squares(Groups p) {
+    __shared__ double part[4];
+    const int k = group_of(p, blockIdx.x);
+    const Group& g = p.g[k];
+    const unsigned id = blockIdx.x - p.first[k], matrix = id / g.chunks, chunk = id % g.chunks;
+    const long size = (long)g.rows * g.cols, per = (size + g.chunks - 1) / g.chunks;
+    const long from = matrix * size, first = chunk * per, last = min(first + per, size);
+    double s = 0.0;
+    of_type(g.dtype, [&](auto type) {
+        typedef decltype(type) T;
+        const T* x = static_cast<const T*>(g.in) + from;
+        for (long i = first + (long)threadIdx.x * kVec<T>; i < last; i += 256 * kVec<T>) {
+            if (i + kVec<T> <= last) {
+                const vec_t<T> v = *reinterpret_cast<const typename Vec<T>::unaligned*>(x + i);
+                // squares of floats are exact in 64 bits
+#pragma unroll
+                for (int q = 0; q < kVec<T>; ++q) s += (double)(float)v[q] * (double)(float)v[q];
+            } else {
+                for (long j = i; j < last; ++j) s += (double)(float)x[j] * (double)(float)x[j];
+            }
+        }
+    });
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) p.sums[g.sums + (long)matrix * g.chunks + chunk] = part[0] + part[1] + part[2] + part[3];
+}
+
+__device__ __forceinline__ void write_parts(E* hi, long plane, float v) {
+    const E h = (E)v;
+    hi[0] = h;
+    hi[plane] = (E)(v - (float)h);
+}
+
+// X 2^12 as two planes, 64 x 64 values a workgroup, turned for a tall matrix; the padding is zeros.
+__global__ __launch_bounds__(256) void k_begin(Groups p) {
+    __shared__ float tile[64][65];
+    const int k = group_of(p, blockIdx.x);
+    const Group& g = p.g[k];
+    const unsigned across = g.l / 64, per = (g.s / 64) * across, id = blockIdx.x - p.first[k], matrix = id / per;
+    const int s0 = id % per / across * 64, l0 = id % across * 64;
+    double sum = 0.0;
+    for (unsigned c = 0; c < g.chunks; ++c) sum += p.sums[g.sums + (long)matrix * g.chunks + c];
+    const double factor = (double)kScale / (sqrt(sum) + (double)p.eps);
+    const long size = (long)g.rows * g.cols, plane = (long)g.s * g.l;
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    // the tile as it lies in the matrix: rows r0.., columns c0..
+    const int r0 = g.tall ? l0 : s0, c0 = g.tall ? s0 : l0;
+    for (int r = ty; r < 64; r += 4) {
+        const bool in = r0 + r < g.rows && c0 + tx < g.cols;
+        const float v = in ? value_at(g.in, g.dtype, matrix * size + (long)(r0 + r) * g.cols + c0 + tx) : 0.0f;
+        tile[r][tx] = (float)((double)v * factor);
+    }
+    __syncthreads();
+    E* x = p.base + g.x[0] + matrix * 2 * plane;
+    for (int r = ty; r < 64; r += 4) write_parts(x + (long)(s0 + r) * g.l + l0 + tx, plane, g.tall ? tile[tx][r] : tile[r][tx]);
+}
+
+enum Kind : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
+
+__device__ __forceinline__ void write_out(void* p, int dtype, long i, float v) {
+    if (dtype == kF32)
+        static_cast<float*>(p)[i] = v;
+    else if (dtype == kBF16)
+        static_cast<__bf16*>(p)[i] = (__bf16)v;
+    else
+        static_cast<_Float16*>(p)[i] = (_Float16)v;
+}
+
+// 8 values at a place of two planes.
+struct Eight {
+    float v[8];
+};
+__device__ __forceinline__ Eight read_parts(const E* hi, long plane) {
+    const vec_t<E> h = *reinterpret_cast<const vec_t<E>*>(hi), l = *reinterpret_cast<const vec_t<E>*>(hi + plane);
+    Eight x;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x.v[q] = (float)h[q] + (float)l[q];
+    return x;
+}
+__device__ __forceinline__ void write_parts(E* hi, long plane, const Eight& x) {
+    vec_t<E> h, l;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        h[q] = (E)x.v[q];
+        l[q] = (E)(x.v[q] - (float)h[q]);
+    }
+    *reinterpret_cast<vec_t<E>*>(hi) = h;
+    *reinterpret_cast<vec_t<E>*>(hi + plane) = l;
+}
+
+// A tile of Side x Side of one of the products by 4 waves; from: which of the X buffers is X.
+template <int K, int Side>
+__global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
+    constexpr int MT = Side / 64;       // 32 x 32 tiles of a wave, in each direction
+    constexpr bool kAlong = K == kGram || K == kPoly;       // of the second operand
+    typedef Tile<E, 2, true, Side, kDepth> TA;
+    typedef Tile<E, 2, kAlong, Side, kDepth> TB;
+    constexpr int kBuffer = TA::kBytes + TB::kBytes, kSlabs = 4 * 32 * kSlab<MT> * 4;
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBuffer > kSlabs ? 2 * kBuffer : kSlabs];
+    const int k = group_of(p, blockIdx.x);
+    const Group& g = p.g[k];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave & 1) * 32 * MT, wn = (wave >> 1) * 32 * MT;
+    const int width = K == kGram || K == kPoly ? g.s : g.l;     // of the output
+    const unsigned tiles_m = (g.s + Side - 1) / Side, tiles_n = (width + Side - 1) / Side;
+    const unsigned count = (k + 1 < p.n ? p.first[k + 1] : gridDim.x) - p.first[k];
+    const TileAt t = tile_at(xcd_order(blockIdx.x - p.first[k], count), tiles_m, tiles_n);
+    const long x_plane = (long)g.s * g.l, a_plane = (long)g.s * g.s;
+    E* x = p.base + g.x[from] + t.outer * 2 * x_plane;
+    E* a = p.base + g.a + t.outer * 2 * a_plane;
+    E* b = p.base + g.b + t.outer * 2 * a_plane;
+    const int m0 = t.m * Side, n0 = t.n * Side;
+    // the operands; rows of a tile past the matrix's last are read where the matrix's last is, and their results dropped
+    const int a_ld = K == kGram ? g.l : g.s, b_ld = K == kPoly ? g.s : g.l, depth = K == kGram ? g.l : g.s;
+    const E* pa = (K == kGram ? x : K == kPoly ? a : b) + (long)m0 * a_ld;
+    const E* pb = (K == kPoly ? a : x) + (kAlong ? (long)n0 * b_ld : 0);
+    const long a_step = K == kGram ? x_plane : a_plane, b_step = K == kPoly ? a_plane : x_plane;
+    Direct<true, Side, kDepth, 4> da;
+    Direct<kAlong, Side, kDepth, 4> db;
+    da.init(a_ld, [&](int r) { return (long)min(r, g.s - 1 - m0); });
+    db.init(b_ld, [&](int r) { return (long)min(r, g.s - 1 - n0); });
+    const unsigned base = lds_address(lds);
+    auto issue = [&](int k0, int buffer) {
+        const unsigned to = base + buffer * kBuffer;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            da.issue(buffer_at(pa + q * a_step + k0, 0x7ffffff0u), to + q * TA::kPlane * 2, kDepth);
+            // Across: past the last column of a row lies the next row, past the last row's the buffer's end
+            const E* from_b = pb + q * b_step + (kAlong ? k0 : (long)k0 * b_ld + n0);
+            const long left = kAlong ? 0x7ffffff0L : 2 * ((long)(g.s - k0) * b_ld - n0);
+            db.issue(buffer_at(from_b, (unsigned)min(left, 0x7ffffff0L)), to + TA::kBytes + q * TB::kPlane * 2, kDepth);
+        }
+    };
+    f32x16 acc[MT][MT] = {};
+    issue(0, 0);
+    for (int k0 = 0, s = 0; k0 < depth; k0 += kDepth, s ^= 1) {
+        loads_arrived<0>();
+        tile_barrier();
+        if (k0 + kDepth < depth) issue(k0 + kDepth, s ^ 1);
+        const E* la = reinterpret_cast<const E*>(lds + s * kBuffer);
+        multiply_step<TA, TB, 2, MT, MT, kDepth>(acc, la, la + TA::kBytes / 2, wm, wn, lane);
+    }
+    tile_barrier();
+    float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<MT>;
+    if (K == kLast && g.tall) {
+        // the output's rows are the columns here
+        const float unscale = p.scale / kScale;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            by_rows_block<MT>(acc, i, slab, lane);
+            for (int r = lane >> 5; r < 32 * MT; r += 2) {
+                const int m = m0 + wm + 32 * i + (lane & 31), n = n0 + wn + r;
+                if (m < g.cols && n < g.rows) {
+                    const long at = (long)m * g.l + n;
+                    const float v = __builtin_fmaf(kA, (float)x[at] + (float)x[at + x_plane], slab[(lane & 31) * kSlab<MT> + r] * (1.0f / kScale));
+                    write_out(g.out, g.dtype, ((long)t.outer * g.rows + n) * g.cols + m, v * unscale);
+                }
+            }
+        }
+        return;
+    }
+    by_rows<8, false, MT, MT>(acc, slab, lane, [&](int mr, int nc, const float* v, const float*) {
+        const int m = m0 + wm + mr, n = n0 + wn + nc;
+        if (m >= g.s || n >= width) return;
+        Eight y;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y.v[q] = v[q] * (1.0f / kScale);
+        if constexpr (K == kGram) {
+            write_parts(a + (long)m * g.s + n, a_plane, y);
+        } else if constexpr (K == kPoly) {
+            const Eight z = read_parts(a + (long)m * g.s + n, a_plane);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y.v[q] = __builtin_fmaf(kB, z.v[q], kC * y.v[q]);
+            write_parts(b + (long)m * g.s + n, a_plane, y);
+        } else {
+            const Eight z = read_parts(x + (long)m * g.l + n, x_plane);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y.v[q] = __builtin_fmaf(kA, z.v[q], y.v[q]);
+            if constexpr (K == kStep) {
+                write_parts(p.base + g.x[from ^ 1] + t.outer * 2 * x_plane + (long)m * g.l + n, x_plane, y);
+            } else if (m < g.rows) {
+                const float unscale = p.scale / kScale;
+                const int some = g.cols - n;
+                if (some > 0)
+                    of_type(g.dtype, [&](auto type) {
+                        typedef decltype(type) T;
+                        T* to = static_cast<T*>(g.out) + ((long)t.outer * g.rows + m) * g.cols + n;
+#pragma unroll
+                        for (int h = 0; h < 8; h += kVec<T>) {
+                            Floats<T> f;
+#pragma unroll
+                            for (int q = 0; q < kVec<T>; ++q) f.v[q] = y.v[h + q] * unscale;
+                            if (some > h) store_left<T>(to + h, some - h, narrow<T>(f));
+                        }
+                    });
+            }
+        }
+    });
+}
+
+constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
+constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
+
+// Places of the tensors first .. first + n - 1 (n at most kMostGroups) and the bytes they take.
+long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* rows, const int* cols) {
+    long at = 0, sums = 0;
+    p.n = 0;
+    for (int k = first; k < n_tensors && p.n < kMostGroups; ++k) {
+        Group& g = p.g[p.n++];
+        g = Group{};
+        g.rows = rows[k], g.cols = cols[k];
+        g.batch = (unsigned)batch[k];
+        g.tall = rows[k] > cols[k];
+        g.s = (int)div_up(min(rows[k], cols[k]), kPad) * kPad;
+        g.l = (int)div_up(max(rows[k], cols[k]), kPad) * kPad;
+        if (rows[k] == 0 || cols[k] == 0) g.batch = 0;
+        const long size = (long)rows[k] * cols[k];
+        g.chunks = (unsigned)max(1L, min((long)kMostSums, size / 16384));
+        for (long* q : {&g.x[0], &g.x[1], &g.a, &g.b}) {
+            *q = at;
+            at += 2 * g.batch * (long)g.s * (q < &g.a ? g.l : g.s);
+        }
+        g.sums = sums;
+        sums += (long)g.batch * g.chunks;
+    }
+    return align256(2 * at) + align256(8 * sums);
+}
+
+template <class F>
+unsigned place(Groups& p, F&& tiles) {
+    long total = 0;
+    for (int k = 0; k < p.n; ++k) {
+        p.first[k] = (unsigned)total;
+        total += p.g[k].batch * tiles(p.g[k]);
+    }
+    p.first[p.n] = (unsigned)total;
+    return (unsigned)total;
+}
+
+template <int K, int Side>
+hipError_t product(Groups& p, int from, hipStream_t st) {
+    const unsigned total = place(p, [](const Group& g) {
+        return div_up(g.s, Side) * div_up(K == kGram || K == kPoly ? g.s : g.l, Side);
+    });
+    k_product<K, Side><<<total, 256, 0, st>>>(p, from);
+    return hipGetLastError();
+}
+template <int K>
+hipError_t product(Groups& p, int from, bool wide, hipStream_t st) {
+    return wide ? product<K, 128>(p, from, st) : product<K, 64>(p, from, st);
+}
+
+#define CTP_TRY(call)                                                 \
+    do {                                                              \
+        if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+    } while (0)
+
+hipError_t run(Groups& p, int steps, hipStream_t st) {
+    unsigned total = place(p, [](const Group& g) { return (long)g.chunks; });
+    if (total == 0) return hipSuccess;
+    k_squares<<<total, 256, 0, st>>>(p);
+    CTP_TRY(hipGetLastError());
+    total = place(p, [](const Group& g) { return (long)(g.s / 64) * (g.l / 64); });
+    k_begin<<<total, 256, 0, st>>>(p);
+    CTP_TRY(hipGetLastError());
+    // tiles of 128 where those of the smallest product fill the card
+    const bool wide = place(p, [](const Group& g) { return div_up(g.s, 128) * div_up(g.s, 128); }) >= 256;
+    for (int s = 0; s < steps; ++s) {
+        CTP_TRY(product<kGram>(p, s & 1, wide, st));
+        CTP_TRY(product<kPoly>(p, s & 1, wide, st));
+        if (s + 1 < steps) {
+            CTP_TRY(product<kStep>(p, s & 1, wide, st));
+        } else {
+            CTP_TRY(product<kLast>(p, s & 1, wide, st));
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+long ortho_workspace(int n_tensors, const long* batch, const int* rows, const int* cols) {
+    Groups p;
+    long most = 0;
+    for (int k = 0; k < n_tensors; k += kMostGroups) most = max(most, lay_out(p, k, n_tensors, batch, rows, cols));
+    return most;
+}
+
+hipError_t launch_ortho(const OrthoArgs& a, hipStream_t st) {
+    for (int k = 0; k < a.n_tensors; k += kMostGroups) {
+        Groups p;
+        lay_out(p, k, a.n_tensors, a.batch, a.rows, a.cols);
+        long at = 0;
+        for (int i = 0; i < p.n; ++i) {
+            Group& g = p.g[i];
+            g.in = a.in[k + i];
+            g.out = a.out[k + i];
+            g.dtype = a.dtype[k + i];
+            at += 4 * g.batch * (long)g.s * (g.l + g.s);
+        }
+        p.eps = a.eps, p.scale = a.scale;
+        p.base = static_cast<E*>(a.workspace);
+        p.sums = reinterpret_cast<double*>(static_cast<char*>(a.workspace) + align256(2 * at));
+        CTP_TRY(run(p, a.steps, st));
+    }
+    return hipSuccess;
+}
+
+}  // namespace ctp
