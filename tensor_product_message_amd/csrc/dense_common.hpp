@@ -99,34 +99,24 @@ struct Staged {
     static_assert(kVecs * Threads * kVec<T> == Rows * Depth);
     vec_t<T> v[kVecs];
 
-    // The tile's rows from row0, k from k0.  row_of(r): where row r of the tile lies among the operand's rows
-    // (Along), which may be any permutation.
-    template <class F>
-    __device__ __forceinline__ void load(const T* base, long ld, int row0, int n_rows, int k0, int k_end, F&& row_of) {
+    // The tile's k from k0 on, base being the tile's first row (Along) or column and k = 0.  row_of(r): where row r of
+    // the tile lies among the operand's rows (Along), which may be any permutation.  Whole: nothing of the tile lies
+    // past k_end or n_left, and the reads are straight-line code.
+    template <bool Whole, class F>
+    __device__ __forceinline__ void load(const T* base, long ld, int n_left, int k0, int k_end, F&& row_of) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow;
-            if constexpr (Along) {
-                const T* row = base + (long)row_of(row0, r) * ld;
-                const int k = k0 + c * kVec<T>;
-                if (k + kVec<T> <= k_end) {
-                    v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + k);
-                } else if (k < k_end) {
-                    v[i] = load_vec<T>(row, k / kVec<T>, k_end);
-                } else {
-                    v[i] = vec_t<T>{};
-                }
+            // a vector of the row `row` of `width` values, from value `at`
+            const long row = Along ? row_of(r) : k0 + r;
+            const int at = (Along ? k0 : 0) + c * kVec<T>, width = Along ? k_end : n_left;
+            if (Whole || (at + kVec<T> <= width && (Along || row < k_end))) {
+                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + row * ld + at);
+            } else if (at < width && (Along || row < k_end)) {
+                v[i] = load_vec<T>(base + row * ld, at / kVec<T>, width);
             } else {
-                const int k = k0 + r, n = row0 + c * kVec<T>;
-                const T* row = base + (long)k * ld;
-                if (k >= k_end || n >= n_rows) {
-                    v[i] = vec_t<T>{};
-                } else if (n + kVec<T> <= n_rows) {
-                    v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + n);
-                } else {
-                    v[i] = load_vec<T>(row, n / kVec<T>, n_rows);
-                }
+                v[i] = vec_t<T>{};
             }
         }
     }
@@ -266,38 +256,48 @@ __device__ __forceinline__ TileAt tile_at(unsigned id, unsigned tiles_m, unsigne
 // ---------------------------------------------------------------- activations
 
 // act(z), its first and its second derivative.
-__device__ __forceinline__ void activation(int act, float z, float& f, float& d1, float& d2) {
+template <int Act_>
+__device__ __forceinline__ void activation(float z, float& f, float& d1, float& d2) {
+    if constexpr (Act_ == kActRelu) {
+        f = z > 0.0f ? z : (z != z ? z : 0.0f);
+        d1 = z > 0.0f ? 1.0f : 0.0f;
+        d2 = 0.0f;
+    } else if constexpr (Act_ == kActSilu || Act_ == kActSigmoid) {
+        // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
+        const float e = expf(-fabsf(z)), large = 1.0f / (1.0f + e), small = e * large;
+        const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
+        if constexpr (Act_ == kActSigmoid) {
+            f = s, d1 = t, d2 = t * u;
+        } else {
+            f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
+        }
+    } else if constexpr (Act_ == kActGelu) {
+        const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * expf(-0.5f * z * z);
+        f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
+    } else if constexpr (Act_ == kActTanh) {
+        const float e = expf(-2.0f * fabsf(z)), r = 1.0f / (1.0f + e);
+        f = tanhf(z);
+        d1 = 4.0f * e * r * r;
+        d2 = -2.0f * f * d1;
+    } else {
+        f = z, d1 = 1.0f, d2 = 0.0f;
+    }
+}
+
+// Calls f(integral constant) for an activation: one branch for all values that f goes through.
+template <int N>
+struct ActIs {
+    static constexpr int value = N;
+};
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        case kActRelu:
-            f = z > 0.0f ? z : (z != z ? z : 0.0f);
-            d1 = z > 0.0f ? 1.0f : 0.0f;
-            d2 = 0.0f;
-            return;
-        case kActSilu:
-        case kActSigmoid: {
-            // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
-            const float e = expf(-fabsf(z)), large = 1.0f / (1.0f + e), small = e * large;
-            const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
-            if (act == kActSigmoid) {
-                f = s, d1 = t, d2 = t * u;
-            } else {
-                f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
-            }
-            return;
-        }
-        case kActGelu: {
-            const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * expf(-0.5f * z * z);
-            f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
-            return;
-        }
-        case kActTanh: {
-            const float e = expf(-2.0f * fabsf(z)), r = 1.0f / (1.0f + e);
-            f = tanhf(z);
-            d1 = 4.0f * e * r * r;
-            d2 = -2.0f * f * d1;
-            return;
-        }
-        default: f = z, d1 = 1.0f, d2 = 0.0f; return;
+        case kActRelu: f(ActIs<kActRelu>{}); break;
+        case kActSilu: f(ActIs<kActSilu>{}); break;
+        case kActGelu: f(ActIs<kActGelu>{}); break;
+        case kActSigmoid: f(ActIs<kActSigmoid>{}); break;
+        case kActTanh: f(ActIs<kActTanh>{}); break;
+        default: f(ActIs<kActNone>{}); break;
     }
 }
 

@@ -11,6 +11,7 @@
 // before they enter a product, as the stored z is: they are operands of the
 // matrix cores.  What is summed is in fp32.
 #include "dense_common.hpp"
+#include "dense_direct.hpp"
 #include "dense_linear.hpp"
 
 namespace ctp {
@@ -41,6 +42,51 @@ struct Gemm {
     unsigned splits, tiles_m, tiles_n, total;
 };
 
+// V floats, the same width as a vector of T.
+struct Values {
+    float v[V];
+};
+
+// Whole: the vector lies in the row.
+template <bool Whole>
+__device__ __forceinline__ Values read_values(const T* row, int n, int width) {
+    vec_t<T> r;
+    if constexpr (Whole)
+        r = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + n);
+    else
+        r = load_vec<T>(row, n / V, width);
+    const Floats<T> f = widen<T>(r);
+    Values x;
+#pragma unroll
+    for (int q = 0; q < V; ++q) x.v[q] = f.v[q];
+    return x;
+}
+template <bool Whole>
+__device__ __forceinline__ void write_values(T* row, int n, int width, const float* x) {
+    Floats<T> f;
+#pragma unroll
+    for (int q = 0; q < V; ++q) f.v[q] = x[q];
+    if constexpr (Whole)
+        *reinterpret_cast<typename Vec<T>::unaligned*>(row + n) = narrow<T>(f);
+    else
+        store_left<T>(row + n, width - n, narrow<T>(f));
+}
+
+// A wave's results through its epilogue: epi.run<Whole>(outer, batch, m, n, x, y) for V columns of a row.
+template <bool Pairs, int MT, int NT, class Epi>
+__device__ __forceinline__ void write_tile(const f32x16 (&acc)[NT][MT], float* slab, int lane, int wm, int wn, int m_left,
+                                           int n_left, bool whole, const Epi& epi, unsigned outer, unsigned batch, long m0, int n0) {
+    if (whole) {
+        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int n, const float* x, const float* y) {
+            epi.template run<true>(outer, batch, m0 + wm + m, n0 + wn + n, x, y);
+        });
+    } else {
+        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int n, const float* x, const float* y) {
+            if (wm + m < m_left && wn + n < n_left) epi.template run<false>(outer, batch, m0 + wm + m, n0 + wn + n, x, y);
+        });
+    }
+}
+
 // A tile of BM x BN by 4 waves, WM x (4 / WM) of them.  One buffer in LDS: the next tiles' reads are in flight in
 // registers while the matrix cores work, and the workgroups that share a CU fill each other's pauses.
 template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
@@ -66,57 +112,96 @@ __global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
                      (AlongB ? (long)n0 * g.b_ld + k0 : k0 * g.b_ld + n0);
         const int m_left = (int)min((long)BM, g.m - m0), n_left = min(g.n - n0, BN);
         // rows past the last give results that nobody stores
-        auto row_a = [&](int, int r) { return (long)min(r, m_left - 1); };
-        auto row_b = [&](int, int r) {
-            if constexpr (Pairs) {
-                const int col = min((r >> 6 << 5) + (r & 31), n_left - 1);
-                return (long)col + (r >> 5 & 1) * g.pair;
-            }
+        auto row_a = [&](int r) { return (long)min(r, m_left - 1); };
+        auto row_b = [&](int r) {
+            if constexpr (Pairs) return (long)min((r >> 6 << 5) + (r & 31), n_left - 1) + (r >> 5 & 1) * g.pair;
             return (long)min(r, n_left - 1);
         };
-        f32x16 acc[NT][MT] = {};
+        const bool whole_m = m_left == BM, whole_n = n_left >= (Pairs ? BN / 2 : BN);
         SA sa;
         SB sb;
-        sa.load(a, g.a_ld, 0, m_left, 0, k_end, row_a);
-        sb.load(b, g.b_ld, 0, n_left, 0, k_end, row_b);
+        auto load = [&](int k) {
+            if (k + kDepth <= k_end && (AlongA || whole_m) && (AlongB || whole_n)) {
+                sa.template load<true>(a, g.a_ld, m_left, k, k_end, row_a);
+                sb.template load<true>(b, g.b_ld, n_left, k, k_end, row_b);
+            } else {
+                sa.template load<false>(a, g.a_ld, m_left, k, k_end, row_a);
+                sb.template load<false>(b, g.b_ld, n_left, k, k_end, row_b);
+            }
+        };
+        f32x16 acc[NT][MT] = {};
+        load(0);
         for (int k = 0; k < k_end; k += kDepth) {
             lds_barrier();
             sa.store(la);
             sb.store(lb);
             lds_barrier();
-            if (k + kDepth < k_end) {
-                sa.load(a, g.a_ld, 0, m_left, k + kDepth, k_end, row_a);
-                sb.load(b, g.b_ld, 0, n_left, k + kDepth, k_end, row_b);
-            }
+            if (k + kDepth < k_end) load(k + kDepth);
             multiply_step<typename SA::tile_t, typename SB::tile_t, kParts, MT, NT, kDepth>(acc, la, lb, wm, wn, lane);
         }
         lds_barrier();
-        by_rows<V, Pairs, MT, NT>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>, lane,
-                                  [&](int mr, int nc, const float* x, const float* y) {
-                                      const int m = wm + mr, n = (Pairs ? wn / 2 : wn) + nc;
-                                      if (m < m_left && n < n_left) epi(t.outer, batch, m0 + m, n0 + n, x, y);
-                                  });
+        float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
+        write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left, whole_m && whole_n, epi, t.outer, batch, m0, n0);
         lds_barrier();
     }
 }
 
-// V floats, the same width as a vector of T.
-struct Values {
-    float v[V];
-};
+// The same for operands of 16 bits whose rows begin on 16 bytes and are whole vectors long: memory to LDS without
+// registers between, in two buffers, the next tiles' reads under way while the matrix cores work on these.  Side is 256
+// with 8 waves (2 x 4) or 128 with 4 (2 x 2).
+template <bool AlongA, bool AlongB, int Side, bool Pairs, class Epi>
+__global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
+    constexpr int Waves = Side / 32, WN = Waves / 2, MT = Side / 64, NT = Side / 32 / WN;
+    typedef Tile<E, 1, AlongA, Side, kDepth> TA;
+    typedef Tile<E, 1, AlongB, Side, kDepth> TB;
+    constexpr int kBuffer = TA::kBytes + TB::kBytes, kSlabs = Waves * 32 * kSlab<NT> * 4;
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBuffer > kSlabs ? 2 * kBuffer : kSlabs];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = (wave & 1) * 32 * MT, wn = (wave >> 1) * 32 * NT;
+    const unsigned base = lds_address(lds);
 
-__device__ __forceinline__ Values read_values(const T* row, int n, int width) {
-    const Floats<T> f = widen<T>(load_vec<T>(row, n / V, width));
-    Values x;
-#pragma unroll
-    for (int q = 0; q < V; ++q) x.v[q] = f.v[q];
-    return x;
-}
-__device__ __forceinline__ void write_values(T* row, int n, int width, const float* x) {
-    Floats<T> f;
-#pragma unroll
-    for (int q = 0; q < V; ++q) f.v[q] = x[q];
-    store_left<T>(row + n, width - n, narrow<T>(f));
+    for (unsigned id = blockIdx.x; id < g.total; id += gridDim.x) {
+        const TileAt t = tile_at(xcd_order(id, g.total), g.tiles_m, g.tiles_n);
+        const unsigned batch = t.outer / g.splits, split = t.outer % g.splits;
+        const long m0 = (long)t.m * Side, k0 = split * g.k_split;
+        const int n0 = t.n * (Pairs ? Side / 2 : Side);
+        const int k_end = (int)min(g.k_split, g.k - k0);    // from here on k counts from k0
+        const T* a = g.a + batch * g.a_batch + (AlongA ? m0 * g.a_ld + k0 : k0 * g.a_ld + m0);
+        const T* b = g.b + (g.b_degree ? degree_of(batch) : (int)batch) * g.b_batch +
+                     (AlongB ? (long)n0 * g.b_ld + k0 : k0 * g.b_ld + n0);
+        const int m_left = (int)min((long)Side, g.m - m0), n_left = min(g.n - n0, Side);
+        Direct<AlongA, Side, kDepth, Waves> da;
+        Direct<AlongB, Side, kDepth, Waves> db;
+        // rows past the last give results that nobody stores
+        da.init(g.a_ld, [&](int r) { return (long)min(r, m_left - 1); });
+        db.init(g.b_ld, [&](int r) {
+            if constexpr (Pairs) return (long)min((r >> 6 << 5) + (r & 31), n_left - 1) + (r >> 5 & 1) * g.pair;
+            return (long)min(r, n_left - 1);
+        });
+        auto issue = [&](int k, int buffer) {
+            // Across: what lies past the last k is the buffer's end
+            const long rows = min(k_end - k, kDepth) - 1;
+            const long a_left = AlongA ? 0x7ffffff0L : 2 * (rows * g.a_ld + m_left);
+            const long b_left = AlongB ? 0x7ffffff0L : 2 * (rows * g.b_ld + n_left);
+            da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), (unsigned)min(a_left, 0x7ffffff0L)), base + buffer * kBuffer, k_end - k);
+            db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), (unsigned)min(b_left, 0x7ffffff0L)),
+                     base + buffer * kBuffer + TA::kBytes, k_end - k);
+        };
+        f32x16 acc[NT][MT] = {};
+        issue(0, 0);
+        for (int k = 0, s = 0; k < k_end; k += kDepth, s ^= 1) {
+            loads_arrived<0>();
+            tile_barrier();
+            if (k + kDepth < k_end) issue(k + kDepth, s ^ 1);
+            const E* la = reinterpret_cast<const E*>(lds + s * kBuffer);
+            multiply_step<TA, TB, 1, MT, NT, kDepth>(acc, la, la + TA::kBytes / 2, wm, wn, lane);
+        }
+        tile_barrier();
+        float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
+        write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left,
+                                  m_left == Side && n_left >= (Pairs ? Side / 2 : Side), epi, t.outer, batch, m0, n0);
+        tile_barrier();
+    }
 }
 
 // y = act(x + bias) + residual, z = x + bias
@@ -125,28 +210,29 @@ struct EpiLinear {
     const T *bias, *residual;
     long row, residual_row;     // elements from row to row
     int n, act;
-    __device__ __forceinline__ void operator()(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
+    template <bool Whole>
+    __device__ __forceinline__ void run(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
         Values v;
 #pragma unroll
         for (int q = 0; q < V; ++q) v.v[q] = x[q];
         if (bias != nullptr && batch == 0) {
-            const Values b = read_values(bias, at, n);
+            const Values b = read_values<Whole>(bias, at, n);
 #pragma unroll
             for (int q = 0; q < V; ++q) v.v[q] += b.v[q];
         }
         const long to = m * row + (long)batch * n;
-        if (z != nullptr) write_values(z + to, at, n, v.v);
-        if (act != kActNone) {
+        if (z != nullptr) write_values<Whole>(z + to, at, n, v.v);
+        with_act(act, [&](auto is) {
             float d1, d2;
 #pragma unroll
-            for (int q = 0; q < V; ++q) activation(act, v.v[q], v.v[q], d1, d2);
-        }
+            for (int q = 0; q < V; ++q) activation<decltype(is)::value>(v.v[q], v.v[q], d1, d2);
+        });
         if (residual != nullptr) {
-            const Values r = read_values(residual + m * residual_row + (long)batch * n, at, n);
+            const Values r = read_values<Whole>(residual + m * residual_row + (long)batch * n, at, n);
 #pragma unroll
             for (int q = 0; q < V; ++q) v.v[q] += r.v[q];
         }
-        write_values(y + to, at, n, v.v);
+        write_values<Whole>(y + to, at, n, v.v);
     }
 };
 
@@ -155,27 +241,30 @@ struct EpiGated {
     T *h, *z;
     const T* bias;
     int n, act;
-    __device__ __forceinline__ void operator()(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
+    template <bool Whole>
+    __device__ __forceinline__ void run(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
         Values a, b;
 #pragma unroll
         for (int q = 0; q < V; ++q) a.v[q] = x[q], b.v[q] = y[q];
         if (bias != nullptr) {
-            const Values p = read_values(bias, at, n), r = read_values(bias + n, at, n);
+            const Values p = read_values<Whole>(bias, at, n), r = read_values<Whole>(bias + n, at, n);
 #pragma unroll
             for (int q = 0; q < V; ++q) a.v[q] += p.v[q], b.v[q] += r.v[q];
         }
         if (z != nullptr) {
-            write_values(z + m * 2 * n, at, n, a.v);
-            write_values(z + m * 2 * n + n, at, n, b.v);
+            write_values<Whole>(z + m * 2 * n, at, n, a.v);
+            write_values<Whole>(z + m * 2 * n + n, at, n, b.v);
         }
         Values f;
-        float d1, d2;
+        with_act(act, [&](auto is) {
+            float d1, d2;
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            activation(act, a.v[q], f.v[q], d1, d2);
-            f.v[q] *= b.v[q];
-        }
-        write_values(h + m * n, at, n, f.v);
+            for (int q = 0; q < V; ++q) {
+                activation<decltype(is)::value>(a.v[q], f.v[q], d1, d2);
+                f.v[q] *= b.v[q];
+            }
+        });
+        write_values<Whole>(h + m * n, at, n, f.v);
     }
 };
 
@@ -184,8 +273,9 @@ struct EpiPlain {
     T* out;
     long row;
     int n;
-    __device__ __forceinline__ void operator()(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
-        write_values(out + m * row + (long)batch * n, at, n, x);
+    template <bool Whole>
+    __device__ __forceinline__ void run(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
+        write_values<Whole>(out + m * row + (long)batch * n, at, n, x);
     }
 };
 
@@ -194,16 +284,19 @@ struct EpiPart {
     float* parts;
     long size;      // of one part: rows n values wide
     int n;
-    __device__ __forceinline__ void operator()(unsigned outer, unsigned, long m, int at, const float* x, const float*) const {
+    template <bool Whole>
+    __device__ __forceinline__ void run(unsigned outer, unsigned, long m, int at, const float* x, const float*) const {
         float* to = parts + outer * size + m * n + at;
 #pragma unroll
-        for (int q = 0; q < V; q += 4)
-            if (at + q < n) {
-                vec_t<float> w;
+        for (int q = 0; q < V; q += 4) {
+            vec_t<float> w;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = x[q + e];
+            for (int e = 0; e < 4; ++e) w[e] = x[q + e];
+            if constexpr (Whole)
+                *reinterpret_cast<Vec<float>::unaligned*>(to + q) = w;
+            else if (at + q < n)
                 store_left<float>(to + q, n - at - q, w);
-            }
+        }
     }
 };
 
@@ -214,37 +307,40 @@ struct EpiSecond {
     T *g_grad, *g_z, *s;
     long grad_row;
     int n, act;
-    __device__ __forceinline__ void operator()(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
-        const Values g = read_values(grad + m * grad_row, at, n);
+    template <bool Whole>
+    __device__ __forceinline__ void run(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
+        const Values g = read_values<Whole>(grad + m * grad_row, at, n);
         const long zr = m * n * (Gated ? 2 : 1);
-        const Values a = read_values(z + zr, at, n);
+        const Values a = read_values<Whole>(z + zr, at, n);
         Values b{}, o, p, q, pb, qb;
-        if constexpr (Gated) b = read_values(z + zr + n, at, n);
+        if constexpr (Gated) b = read_values<Whole>(z + zr + n, at, n);
+        with_act(act, [&](auto is) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float f, d1, d2;
-            activation(act, a.v[i], f, d1, d2);
-            if constexpr (Gated) {
-                const float gb = g.v[i] * b.v[i];
-                o.v[i] = __builtin_fmaf(x[i] * b.v[i], d1, y[i] * f);
-                p.v[i] = __builtin_fmaf(x[i] * gb, d2, y[i] * g.v[i] * d1);
-                pb.v[i] = x[i] * g.v[i] * d1;
-                q.v[i] = gb * d1;
-                qb.v[i] = g.v[i] * f;
-            } else {
-                o.v[i] = x[i] * d1;
-                p.v[i] = x[i] * g.v[i] * d2;
-                q.v[i] = g.v[i] * d1;
+            for (int i = 0; i < V; ++i) {
+                float f, d1, d2;
+                activation<decltype(is)::value>(a.v[i], f, d1, d2);
+                if constexpr (Gated) {
+                    const float gb = g.v[i] * b.v[i];
+                    o.v[i] = __builtin_fmaf(x[i] * b.v[i], d1, y[i] * f);
+                    p.v[i] = __builtin_fmaf(x[i] * gb, d2, y[i] * g.v[i] * d1);
+                    pb.v[i] = x[i] * g.v[i] * d1;
+                    q.v[i] = gb * d1;
+                    qb.v[i] = g.v[i] * f;
+                } else {
+                    o.v[i] = x[i] * d1;
+                    p.v[i] = x[i] * g.v[i] * d2;
+                    q.v[i] = g.v[i] * d1;
+                }
             }
-        }
-        if (g_grad != nullptr) write_values(g_grad + m * n, at, n, o.v);
+        });
+        if (g_grad != nullptr) write_values<Whole>(g_grad + m * n, at, n, o.v);
         if (g_z != nullptr) {
-            write_values(g_z + zr, at, n, p.v);
-            if constexpr (Gated) write_values(g_z + zr + n, at, n, pb.v);
+            write_values<Whole>(g_z + zr, at, n, p.v);
+            if constexpr (Gated) write_values<Whole>(g_z + zr + n, at, n, pb.v);
         }
         if (s != nullptr) {
-            write_values(s + zr, at, n, q.v);
-            if constexpr (Gated) write_values(s + zr + n, at, n, qb.v);
+            write_values<Whole>(s + zr, at, n, q.v);
+            if constexpr (Gated) write_values<Whole>(s + zr + n, at, n, qb.v);
         }
     }
 };
@@ -272,29 +368,27 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
     Values sum[H] = {};
     if (at < p.n) {
         for (long m = first + ty; m < last; m += high) {
-            Values g = read_values(p.grad + m * p.grad_row, at, p.n), u{};
+            Values g = read_values<false>(p.grad + m * p.grad_row, at, p.n), u{};
             if (p.s != nullptr) {
                 const long zr = m * p.n * H;
-                const Values a = read_values(p.z + zr, at, p.n);
-                if constexpr (Gated) {
-                    const Values b = read_values(p.z + zr + p.n, at, p.n);
+                const Values a = read_values<false>(p.z + zr, at, p.n);
+                Values b{};
+                if constexpr (Gated) b = read_values<false>(p.z + zr + p.n, at, p.n);
+                with_act(p.act, [&](auto is) {
+                    float f, d1, d2;
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
-                        float f, d1, d2;
-                        activation(p.act, a.v[q], f, d1, d2);
-                        u.v[q] = g.v[q] * f;
-                        g.v[q] = g.v[q] * b.v[q] * d1;
+                        activation<decltype(is)::value>(a.v[q], f, d1, d2);
+                        if constexpr (Gated) {
+                            u.v[q] = g.v[q] * f;
+                            g.v[q] = g.v[q] * b.v[q] * d1;
+                        } else {
+                            g.v[q] *= d1;
+                        }
                     }
-                    write_values(p.s + zr + p.n, at, p.n, u.v);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        float f, d1, d2;
-                        activation(p.act, a.v[q], f, d1, d2);
-                        g.v[q] *= d1;
-                    }
-                }
-                write_values(p.s + zr, at, p.n, g.v);
+                });
+                if constexpr (Gated) write_values<false>(p.s + zr + p.n, at, p.n, u.v);
+                write_values<false>(p.s + zr, at, p.n, g.v);
             }
 #pragma unroll
             for (int q = 0; q < V; ++q) {
@@ -357,38 +451,71 @@ constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 // Workgroups that fill the card: two for each of 256 CUs.
 constexpr long kFill = 512;
 
+bool set_tiles(Gemm& g, long rows, long cols, unsigned outer) {
+    g.tiles_m = (unsigned)div_up(g.m, rows);
+    g.tiles_n = (unsigned)div_up(g.n, cols);
+    const long total = (long)g.tiles_m * g.tiles_n;
+    if (total > 0xffffffffL || total * outer > 0xffffffffL) return false;
+    g.total = (unsigned)(total * outer);
+    return true;
+}
+
 template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
-hipError_t run_tiles(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
-    g.tiles_m = (unsigned)div_up(g.m, BM);
-    g.tiles_n = (unsigned)div_up(g.n, Pairs ? BN / 2 : BN);
-    const long total = (long)g.tiles_m * g.tiles_n * outer;
-    if (total == 0) return hipSuccess;
-    g.total = (unsigned)total;
-    k_gemm<AlongA, AlongB, BM, BN, WM, Pairs><<<dim3((unsigned)min(total, max_groups(256))), 256, 0, st>>>(g, epi);
+hipError_t run_staged(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
+    if (!set_tiles(g, BM, Pairs ? BN / 2 : BN, outer)) return hipErrorInvalidValue;
+    if (g.total == 0) return hipSuccess;
+    k_gemm<AlongA, AlongB, BM, BN, WM, Pairs><<<dim3((unsigned)min((long)g.total, max_groups(256))), 256, 0, st>>>(g, epi);
+    return hipGetLastError();
+}
+template <bool AlongA, bool AlongB, int Side, bool Pairs, class Epi>
+hipError_t run_direct(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
+    if (!set_tiles(g, Side, Pairs ? Side / 2 : Side, outer)) return hipErrorInvalidValue;
+    if (g.total == 0) return hipSuccess;
+    k_gemm_direct<AlongA, AlongB, Side, Pairs>
+        <<<dim3((unsigned)min((long)g.total, max_groups(2 * Side))), 2 * Side, 0, st>>>(g, epi);
     return hipGetLastError();
 }
 
-// Whether tiles of 128 fill the card; those of 64 reach half their rate, and are for what has too few of them.
-bool wide_tiles(long m, long n, long outer) { return div_up(m, 128) * div_up(n, 128) * outer >= kFill / 2; }
+// Whether tiles may go to LDS directly: 16-byte pieces, whole in every row.
+template <bool AlongA, bool AlongB>
+bool direct(const Gemm& g) {
+    const auto whole = [](const T* p, long ld, long batch, long n) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && batch % V == 0 && n % V == 0;
+    };
+    return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m) && whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n);
+}
+
+// Tiles of 256 reuse an operand most, and are taken where they fill the card; tiles of 64 are for what has too few of
+// the others.
+template <bool AlongA, bool AlongB, bool Pairs, class Epi>
+hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t st) {
+    const long n = Pairs ? 2L * g.n : g.n;
+    if constexpr (kParts == 1) {
+        if (direct<AlongA, AlongB>(g)) {
+            if (div_up(g.m, 256) * div_up(n, 256) * outer >= kFill * 3 / 8) return run_direct<AlongA, AlongB, 256, Pairs>(g, outer, epi, st);
+            if (div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
+        }
+    }
+    if (g.m > 64 && n > 64 && g.k > 256 && div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 2)
+        return run_staged<AlongA, AlongB, 128, 128, 2, Pairs>(g, outer, epi, st);
+    return run_staged<AlongA, AlongB, 64, Pairs ? 128 : 64, 2, Pairs>(g, outer, epi, st);
+}
 
 template <bool AlongA, bool AlongB, class Epi>
 hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
     g.splits = 1;
     g.k_split = div_up(g.k, kDepth) * kDepth;
-    if (wide_tiles(g.m, g.n, batches)) return run_tiles<AlongA, AlongB, 128, 128, 2, false>(g, batches, epi, st);
-    return run_tiles<AlongA, AlongB, 64, 64, 2, false>(g, batches, epi, st);
+    return run_tiles<AlongA, AlongB, false>(g, batches, epi, st);
 }
 template <class Epi>
 hipError_t run_pairs(Gemm g, const Epi& epi, hipStream_t st) {
     g.splits = 1;
     g.k_split = div_up(g.k, kDepth) * kDepth;
-    if (wide_tiles(g.m, 2L * g.n, 1)) return run_tiles<true, true, 128, 128, 2, true>(g, 1, epi, st);
-    return run_tiles<true, true, 64, 128, 2, true>(g, 1, epi, st);
+    return run_tiles<true, true, true>(g, 1, epi, st);
 }
 
 // How d_W[outer][inner] = sum over rows is cut: every component by itself, and its rows into `splits`.
 struct WeightCut {
-    bool wide;
     unsigned splits;
     long k_split;
     bool direct;        // one part alone: no join
@@ -397,8 +524,8 @@ WeightCut weight_cut(const LinearArgs& a, bool twice) {
     const long comps = (long)(a.lmax + 1) * (a.lmax + 1), out = (long)a.outer * (a.gated ? 2 : 1);
     WeightCut c;
     // large matrices fill the card by themselves
-    c.wide = div_up(out, 128) * div_up(a.inner, 128) * comps >= kFill / 8 && a.inner > 64 && out > 64;
-    const long tile = c.wide ? 128 : 64, tiles = div_up(out, tile) * div_up(a.inner, tile) * comps;
+    const bool wide = div_up(out, 128) * div_up(a.inner, 128) * comps >= kFill / 8 && a.inner > 64 && out > 64;
+    const long tile = wide ? 128 : 64, tiles = div_up(out, tile) * div_up(a.inner, tile) * comps;
     long splits = max(1L, min(kFill / tiles, a.n_rows / (4 * kDepth)));
     splits = max(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
     c.k_split = max(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
@@ -494,14 +621,8 @@ hipError_t weight_gradient(const LinearArgs& a, const T* s, long s_row, const T*
     g.k = a.n_rows;
     g.splits = c.splits;
     g.k_split = c.k_split;
-    if (c.direct) {
-        const EpiPlain epi{d_w, a.inner, a.inner};
-        return c.wide ? run_tiles<false, false, 128, 128, 2, false>(g, 1, epi, st)
-                      : run_tiles<false, false, 64, 64, 2, false>(g, 1, epi, st);
-    }
-    const EpiPart epi{parts, out * a.inner, a.inner};
-    return c.wide ? run_tiles<false, false, 128, 128, 2, false>(g, comps * c.splits, epi, st)
-                  : run_tiles<false, false, 64, 64, 2, false>(g, comps * c.splits, epi, st);
+    if (c.direct) return run_tiles<false, false, false>(g, 1, EpiPlain{d_w, a.inner, a.inner}, st);
+    return run_tiles<false, false, false>(g, comps * c.splits, EpiPart{parts, out * a.inner, a.inner}, st);
 }
 
 hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, float* sums, bool gated, int n, const BiasCut& c,

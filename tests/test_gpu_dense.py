@@ -250,6 +250,29 @@ def test_linear(ctp, dev, rows, inner, outer, dtype):
                 close(n, a, *ref)
 
 
+WIDE = [  # enough tiles of 256 and of 128 for the card, in each direction's product; sums that end inside a tile
+    (3400, 72, 3600, False), (1500, 80, 1400, False), (3400, 3600, 40, False), (2600, 2608, 40, False), (40, 3400, 3600, False),
+    (72, 1400, 1504, False), (3400, 72, 1800, True), (1500, 136, 712, True), (40, 3400, 1800, True),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer,gated", WIDE)
+def test_wide(ctp, dev, rows, inner, outer, gated, dtype):
+    c = Case(rows, inner, outer, dtype, "silu", gated=gated)
+    tell("wide", rows, inner, outer, gated, dtype)
+    x, w, b, grad = to(dev, c.x, c.w, c.bias, c.grad)
+    f, back = (ctp.gated_linear_fwd, ctp.gated_linear_bwd) if gated else (ctp.linear_fwd, ctp.linear_bwd)
+    y, z = f(x, w, b, act="silu", keep_z=True)
+    z_ref, ez, y_ref, ey = c.forward()
+    close("z", z, z_ref, ez)
+    close("y", y, y_ref, ey)
+    got = back(grad, x, w, z, act="silu")
+    for n, a, (ref, bound) in zip(("d_x", "d_w", "d_bias"), got, c.backward(z.double().cpu())):
+        close(n, a, ref, bound)
+    assert all(torch.equal(a, b2) for a, b2 in zip(got, back(grad, x, w, z, act="silu")))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lmax,rows,inner,outer", [(1, 1, 16, 16), (1, 64, 16, 16), (2, 77, 33, 20), (3, 100, 128, 128),
                                                    (3, 301, 9, 65), (2, 700, 64, 136)])
