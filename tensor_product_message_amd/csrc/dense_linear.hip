@@ -345,6 +345,115 @@ struct EpiSecond {
     }
 };
 
+// ---------------------------------------------------------------- few rows
+
+// Up to 16 MB rows, where the weights' way from memory is all there is: no tile of x fills the matrix cores, and no
+// weight is used twice.  Each wave takes 32 rows of w (Pairs: 16 and their partners) and one of Waves shares of k,
+// straight from memory into the matrix instruction's registers, kAhead reads of each row under way at once; the
+// waves' sums meet in LDS, in the waves' order.  Within 4 lanes' reads a row of w is 128 bytes in one piece: which k
+// goes to which lane does not matter as long as w and x agree.
+template <class U>
+struct Small;
+template <>
+struct Small<float> {
+    // fp32 matrix instructions: their rate is no limit here
+    static __device__ __forceinline__ f32x4 mul(vec_t<float> w, vec_t<float> x, f32x4 c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[q], x[q], c, 0, 0, 0);
+        return c;
+    }
+};
+template <>
+struct Small<__bf16> {
+    static __device__ __forceinline__ f32x4 mul(vec_t<__bf16> w, vec_t<__bf16> x, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
+    }
+};
+template <>
+struct Small<_Float16> {
+    static __device__ __forceinline__ f32x4 mul(vec_t<_Float16> w, vec_t<_Float16> x, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, c, 0, 0, 0);
+    }
+};
+
+template <int MB, int Waves, bool Pairs, class Epi>
+__global__ __launch_bounds__(64 * Waves) void k_few(Gemm g, Epi epi) {
+    constexpr int kStep = 8 * V, kAhead = 4 / MB, kRow = 36;
+    __shared__ __attribute__((aligned(16))) float part[Waves][16 * MB][kRow];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, from = (lane >> 4) * 2 * V;
+    const unsigned batch = blockIdx.y;
+    const int n0 = blockIdx.x * (Pairs ? 16 : 32), k_end = (int)g.k;
+    const T *a[MB], *b[2];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) a[i] = g.a + batch * g.a_batch + min((long)(16 * i + r), g.m - 1) * g.a_ld;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const T* w = g.b + degree_of(batch) * g.b_batch + (long)min(n0 + r + (Pairs ? 0 : 16 * j), g.n - 1) * g.b_ld;
+        b[j] = Pairs ? w + j * g.pair * g.b_ld : w;
+    }
+    f32x4 acc[2][MB] = {};
+    // kAhead steps at a time, the waves in turn
+    for (int k0 = wave * kAhead * kStep; k0 < k_end; k0 += Waves * kAhead * kStep) {
+        vec_t<T> va[kAhead][2][MB], vb[kAhead][2][2];
+        if (k0 + kAhead * kStep <= k_end) {
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + s * kStep + from + h * V;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) vb[s][h][j] = *reinterpret_cast<const typename Vec<T>::unaligned*>(b[j] + k);
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) va[s][h][i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(a[i] + k);
+                }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + s * kStep + from + h * V;
+                    const bool in = k < k_end;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) vb[s][h][j] = in ? load_vec<T>(b[j], k / V, k_end) : vec_t<T>{};
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) va[s][h][i] = in ? load_vec<T>(a[i], k / V, k_end) : vec_t<T>{};
+                }
+        }
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) acc[j][i] = Small<T>::mul(vb[s][h][j], va[s][h][i], acc[j][i]);
+    }
+    // lane: row 16 i + lane % 16 of x, columns 16 j + 4 (lane / 16) .. + 3
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) *reinterpret_cast<f32x4*>(&part[wave][16 * i + r][16 * j + 4 * (lane >> 4)]) = acc[j][i];
+    lds_barrier();
+    constexpr int kCols = Pairs ? 16 : 32, kLanes = kCols / V;
+    for (int id = threadIdx.x; id < 16 * MB * kLanes; id += 64 * Waves) {
+        const int m = id / kLanes, n = id % kLanes * V;
+        if (m >= g.m || n0 + n >= g.n) continue;
+        float x[V], y[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            x[q] = part[0][m][n + q];
+            if constexpr (Pairs) y[q] = part[0][m][16 + n + q];
+        }
+        for (int w = 1; w < Waves; ++w)
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                x[q] += part[w][m][n + q];
+                if constexpr (Pairs) y[q] += part[w][m][16 + n + q];
+            }
+        epi.template run<false>(batch, batch, m, n0 + n, x, y);
+    }
+}
+
 // ---------------------------------------------------------------- passes over values
 
 // s = grad act'(z) for the products of the backward pass, and its columns' sums, a part for each chunk of rows.
@@ -358,22 +467,52 @@ struct ActBwd {
     int n, act, across;
 };
 
+// One row's vector of columns.
 template <bool Gated>
+struct ActRow {
+    vec_t<T> g, a, b;
+};
+
+// Whole: n is whole vectors.  Rows: so many of a lane's rows are read at once.
+template <bool Gated, bool Whole>
 __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
-    constexpr int H = Gated ? 2 : 1;
+    constexpr int H = Gated ? 2 : 1, Rows = 4;
     __shared__ float part[256 * H * V];
     const int tx = threadIdx.x % p.across, ty = threadIdx.x / p.across, high = 256 / p.across;
     const int at = (blockIdx.x * p.across + tx) * V;
     const long first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.rows);
     Values sum[H] = {};
-    if (at < p.n) {
-        for (long m = first + ty; m < last; m += high) {
-            Values g = read_values<false>(p.grad + m * p.grad_row, at, p.n), u{};
+    auto read = [&](const T* row) {
+        if constexpr (Whole) return (vec_t<T>)*reinterpret_cast<const typename Vec<T>::unaligned*>(row + at);
+        return load_vec<T>(row, at / V, p.n);
+    };
+    auto values = [](vec_t<T> x) {
+        const Floats<T> f = widen<T>(x);
+        Values v;
+#pragma unroll
+        for (int q = 0; q < V; ++q) v.v[q] = f.v[q];
+        return v;
+    };
+    for (long m0 = at < p.n ? first + ty : last; m0 < last; m0 += Rows * high) {
+        ActRow<Gated> rows[Rows];
+#pragma unroll
+        for (int i = 0; i < Rows; ++i) {
+            const long m = min(m0 + (long)i * high, last - 1);      // past the last row: the last again, not used
+            rows[i].g = read(p.grad + m * p.grad_row);
             if (p.s != nullptr) {
-                const long zr = m * p.n * H;
-                const Values a = read_values<false>(p.z + zr, at, p.n);
+                rows[i].a = read(p.z + m * p.n * H);
+                if constexpr (Gated) rows[i].b = read(p.z + m * p.n * H + p.n);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Rows; ++i) {
+            const long m = m0 + (long)i * high;
+            if (m >= last) break;
+            Values g = values(rows[i].g), u{};
+            if (p.s != nullptr) {
+                const Values a = values(rows[i].a);
                 Values b{};
-                if constexpr (Gated) b = read_values<false>(p.z + zr + p.n, at, p.n);
+                if constexpr (Gated) b = values(rows[i].b);
                 with_act(p.act, [&](auto is) {
                     float f, d1, d2;
 #pragma unroll
@@ -387,8 +526,9 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
                         }
                     }
                 });
-                if constexpr (Gated) write_values<false>(p.s + zr + p.n, at, p.n, u.v);
-                write_values<false>(p.s + zr, at, p.n, g.v);
+                T* to = p.s + m * p.n * H;
+                write_values<Whole>(to, at, p.n, g.v);
+                if constexpr (Gated) write_values<Whole>(to + p.n, at, p.n, u.v);
             }
 #pragma unroll
             for (int q = 0; q < V; ++q) {
@@ -413,32 +553,43 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
     }
 }
 
-// Parts joined in their order, 16 at a time: out[l][i] = sum over the parts of degree l.
+// Parts joined: out[l][i] = sum over the parts of degree l, `ways` sums of every ways-th part first, then those.
 struct Join {
     const float* parts;
     T* out;
     long size;              // of one part
     int degrees;            // part p belongs to the degree of p / per_component
     unsigned per_component;
-    unsigned groups;        // of 64 values, each degree's own
+    int ways;               // 1, 4 or 16
+    unsigned groups;        // of 256 / ways values, each degree's own
 };
 
-__global__ __launch_bounds__(1024) void k_join(Join first, Join second) {
-    __shared__ float part[16][64];
+__global__ __launch_bounds__(256) void k_join(Join first, Join second) {
+    __shared__ float part[256];
     const bool is_first = blockIdx.x < first.groups * first.degrees;
-    const Join& j = is_first ? first : second;
+    const Join j = is_first ? first : second;
     const unsigned id = is_first ? blockIdx.x : blockIdx.x - first.groups * first.degrees;
-    const unsigned l = id / j.groups, c = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const long i = (long)(id % j.groups) * 64 + c;
-    const unsigned p0 = l * l * j.per_component, p1 = (l + 1) * (l + 1) * j.per_component;
+    const int wide = 256 / j.ways, c = threadIdx.x % wide, q = threadIdx.x / wide;
+    const unsigned l = id / j.groups;
+    const long i = (long)(id % j.groups) * wide + c;
+    const unsigned p1 = (l + 1) * (l + 1) * j.per_component;
+    unsigned p = l * l * j.per_component + q;
     float s = 0.0f;
-    if (i < j.size)
-        for (unsigned p = p0 + q; p < p1; p += 16) s += j.parts[p * j.size + i];
-    part[q][c] = s;
+    if (i < j.size) {
+        // eight reads at once
+        for (; p + 7 * j.ways < p1; p += 8 * j.ways) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = j.parts[(p + e * j.ways) * j.size + i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += x[e];
+        }
+        for (; p < p1; p += j.ways) s += j.parts[p * j.size + i];
+    }
+    part[threadIdx.x] = s;
     lds_barrier();
     if (q == 0 && i < j.size) {
-#pragma unroll
-        for (int r = 1; r < 16; ++r) s += part[r][c];
+        for (int r = 1; r < j.ways; ++r) s += part[r * wide + c];
         j.out[l * j.size + i] = (T)s;
     }
 }
@@ -501,16 +652,35 @@ hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t 
     return run_staged<AlongA, AlongB, 64, Pairs ? 128 : 64, 2, Pairs>(g, outer, epi, st);
 }
 
+template <int MB, bool Pairs, class Epi>
+hipError_t run_few(const Gemm& g, unsigned batches, const Epi& epi, hipStream_t st) {
+    const unsigned groups = (unsigned)div_up(g.n, Pairs ? 16 : 32);
+    // more shares of k where few columns would leave the card empty
+    if ((long)groups * batches < kFill / 2 && g.k >= 8 * (4 / MB) * 8 * V)
+        k_few<MB, 16, Pairs><<<dim3(groups, batches), 64 * 16, 0, st>>>(g, epi);
+    else
+        k_few<MB, 4, Pairs><<<dim3(groups, batches), 64 * 4, 0, st>>>(g, epi);
+    return hipGetLastError();
+}
+
 template <bool AlongA, bool AlongB, class Epi>
 hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
+    if (g.m == 0) return hipSuccess;
     g.splits = 1;
     g.k_split = div_up(g.k, kDepth) * kDepth;
+    if constexpr (AlongB) {
+        if (g.m <= 16) return run_few<1, false>(g, batches, epi, st);
+        if (g.m <= 32) return run_few<2, false>(g, batches, epi, st);
+    }
     return run_tiles<AlongA, AlongB, false>(g, batches, epi, st);
 }
 template <class Epi>
 hipError_t run_pairs(Gemm g, const Epi& epi, hipStream_t st) {
+    if (g.m == 0) return hipSuccess;
     g.splits = 1;
     g.k_split = div_up(g.k, kDepth) * kDepth;
+    if (g.m <= 16) return run_few<1, true>(g, 1, epi, st);
+    if (g.m <= 32) return run_few<2, true>(g, 1, epi, st);
     return run_tiles<true, true, true>(g, 1, epi, st);
 }
 
@@ -546,9 +716,9 @@ BiasCut bias_cut(long rows, int n) {
     while (c.across < 64 && c.across * V < n) c.across *= 2;
     c.groups = (unsigned)div_up(n, (long)c.across * V);
     const long high = 256 / c.across;
-    // enough workgroups for the card, at most 1024 chunks, which are joined afterwards
-    const long most = max(1L, min(1024L, div_up(4 * kFill, c.groups)));
-    c.chunk = max(1L, div_up(div_up(rows, most), high)) * high;
+    // enough workgroups for the card, at most 512 chunks, which are joined afterwards; a lane reads 4 rows at once
+    const long most = max(1L, min(512L, div_up(4 * kFill, c.groups)));
+    c.chunk = max(1L, div_up(div_up(rows, most), 4 * high)) * 4 * high;
     c.chunks = (unsigned)max(1L, div_up(rows, c.chunk));
     return c;
 }
@@ -629,20 +799,22 @@ hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, floa
                    hipStream_t st) {
     const ActBwd p{grad, static_cast<const T*>(a.z), s, sums, grad_row, a.n_rows, c.chunk, n, a.act, c.across};
     if (a.n_rows == 0 && sums == nullptr) return hipSuccess;
-    if (gated)
-        k_act_bwd<true><<<dim3(c.groups, c.chunks), 256, 0, st>>>(p);
+    const dim3 grid(c.groups, c.chunks);
+    if (n % V == 0)
+        gated ? k_act_bwd<true, true><<<grid, 256, 0, st>>>(p) : k_act_bwd<false, true><<<grid, 256, 0, st>>>(p);
     else
-        k_act_bwd<false><<<dim3(c.groups, c.chunks), 256, 0, st>>>(p);
+        gated ? k_act_bwd<true, false><<<grid, 256, 0, st>>>(p) : k_act_bwd<false, false><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
 Join join_of(const float* parts, void* out, long size, int degrees, unsigned per_component) {
-    return Join{parts, static_cast<T*>(out), size, degrees, per_component, (unsigned)div_up(size, 64)};
+    const int ways = per_component <= 4 ? 1 : per_component <= 64 ? 4 : 16;
+    return Join{parts, static_cast<T*>(out), size, degrees, per_component, ways, (unsigned)div_up(size, 256 / ways)};
 }
 hipError_t join(const Join& a, const Join& b, hipStream_t st) {
     const unsigned groups = a.groups * a.degrees + b.groups * b.degrees;
     if (groups == 0) return hipSuccess;
-    k_join<<<groups, 1024, 0, st>>>(a, b);
+    k_join<<<groups, 256, 0, st>>>(a, b);
     return hipGetLastError();
 }
 

@@ -27,25 +27,31 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScale = 4096.0f;
 constexpr int kPad = 64, kDepth = 32;
 constexpr int kMostGroups = 32;     // tensors of one launch
-constexpr int kMostSums = 64;       // shares of a matrix's sum of squares
+constexpr int kMostSums = 512;      // shares of a matrix's sum of squares
+constexpr int kLeastCut = 256;      // of the long side, a share of A
 
 // One tensor: `batch` matrices.  Places are elements from the workspace's start; each matrix has two planes.
 struct Group {
     const void* in;
     void* out;
     long x[2], a, b;        // X and the next X, A, b A + c A A of the first matrix
+    long parts;             // shares of A, floats from the workspace's start (splits > 1)
     long sums;              // doubles from the sums' start
     int rows, cols, dtype;  // of a matrix as it is given
     int s, l;               // padded sides
     unsigned batch;
     unsigned chunks;        // shares of the sum of squares
+    unsigned splits;        // of A's sums, each over `cut` of the long side
+    int cut;
     bool tall;
 };
 struct Groups {
     int n;
+    bool wide;              // tiles of 128, else of 64
     float eps, scale;
     E* base;
     double* sums;
+    long sums_at;           // bytes from the workspace's start
     Group g[kMostGroups];
     unsigned first[kMostGroups + 1];    // of this launch's workgroups, each group's first
 };
@@ -54,12 +60,6 @@ __device__ __forceinline__ int group_of(const Groups& p, unsigned id) {
     int k = 0;
     while (k + 1 < p.n && id >= p.first[k + 1]) ++k;
     return k;
-}
-
-__device__ __forceinline__ float value_at(const void* p, int dtype, long i) {
-    if (dtype == kF32) return static_cast<const float*>(p)[i];
-    if (dtype == kBF16) return (float)static_cast<const __bf16*>(p)[i];
-    return (float)static_cast<const _Float16*>(p)[i];
 }
 
 // Calls f(T{}) for an element type's code.
@@ -102,47 +102,6 @@ __global__ __launch_bounds__(256) void k_squares(Groups p) {
     if (threadIdx.x == 0) p.sums[g.sums + (long)matrix * g.chunks + chunk] = part[0] + part[1] + part[2] + part[3];
 }
 
-__device__ __forceinline__ void write_parts(E* hi, long plane, float v) {
-    const E h = (E)v;
-    hi[0] = h;
-    hi[plane] = (E)(v - (float)h);
-}
-
-// X 2^12 as two planes, 64 x 64 values a workgroup, turned for a tall matrix; the padding is zeros.
-__global__ __launch_bounds__(256) void k_begin(Groups p) {
-    __shared__ float tile[64][65];
-    const int k = group_of(p, blockIdx.x);
-    const Group& g = p.g[k];
-    const unsigned across = g.l / 64, per = (g.s / 64) * across, id = blockIdx.x - p.first[k], matrix = id / per;
-    const int s0 = id % per / across * 64, l0 = id % across * 64;
-    double sum = 0.0;
-    for (unsigned c = 0; c < g.chunks; ++c) sum += p.sums[g.sums + (long)matrix * g.chunks + c];
-    const double factor = (double)kScale / (sqrt(sum) + (double)p.eps);
-    const long size = (long)g.rows * g.cols, plane = (long)g.s * g.l;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    // the tile as it lies in the matrix: rows r0.., columns c0..
-    const int r0 = g.tall ? l0 : s0, c0 = g.tall ? s0 : l0;
-    for (int r = ty; r < 64; r += 4) {
-        const bool in = r0 + r < g.rows && c0 + tx < g.cols;
-        const float v = in ? value_at(g.in, g.dtype, matrix * size + (long)(r0 + r) * g.cols + c0 + tx) : 0.0f;
-        tile[r][tx] = (float)((double)v * factor);
-    }
-    __syncthreads();
-    E* x = p.base + g.x[0] + matrix * 2 * plane;
-    for (int r = ty; r < 64; r += 4) write_parts(x + (long)(s0 + r) * g.l + l0 + tx, plane, g.tall ? tile[tx][r] : tile[r][tx]);
-}
-
-enum Kind : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
-
-__device__ __forceinline__ void write_out(void* p, int dtype, long i, float v) {
-    if (dtype == kF32)
-        static_cast<float*>(p)[i] = v;
-    else if (dtype == kBF16)
-        static_cast<__bf16*>(p)[i] = (__bf16)v;
-    else
-        static_cast<_Float16*>(p)[i] = (_Float16)v;
-}
-
 // 8 values at a place of two planes.
 struct Eight {
     float v[8];
@@ -165,32 +124,123 @@ __device__ __forceinline__ void write_parts(E* hi, long plane, const Eight& x) {
     *reinterpret_cast<vec_t<E>*>(hi + plane) = l;
 }
 
-// A tile of Side x Side of one of the products by 4 waves; from: which of the X buffers is X.
+// X 2^12 as two planes, 64 x 64 values a workgroup, turned for a tall matrix; the padding is zeros.
+__global__ __launch_bounds__(256) void k_begin(Groups p) {
+    __shared__ float tile[64][65];
+    const int k = group_of(p, blockIdx.x);
+    const Group& g = p.g[k];
+    const unsigned across = g.l / 64, per = (g.s / 64) * across, id = blockIdx.x - p.first[k], matrix = id / per;
+    const int s0 = id % per / across * 64, l0 = id % across * 64;
+    // every wave sums the shares, in the same order
+    double sum = 0.0;
+    for (unsigned c = threadIdx.x & 63; c < g.chunks; c += 64) sum += p.sums[g.sums + (long)matrix * g.chunks + c];
+    const double factor = (double)kScale / (sqrt(wave_sum(sum)) + (double)p.eps);
+    const long size = (long)g.rows * g.cols, plane = (long)g.s * g.l;
+    // the tile as it lies in the matrix: rows r0.., columns c0..
+    const int r0 = g.tall ? l0 : s0, c0 = g.tall ? s0 : l0;
+    of_type(g.dtype, [&](auto type) {
+        typedef decltype(type) T;
+        constexpr int kLanes = 64 / kVec<T>, kRows = 256 / kLanes;
+        const T* in = static_cast<const T*>(g.in) + matrix * size;
+        const int c = threadIdx.x % kLanes * kVec<T>;
+        vec_t<T> v[64 / kRows];
+#pragma unroll
+        for (int i = 0; i < 64 / kRows; ++i) {
+            const int r = threadIdx.x / kLanes + i * kRows;
+            const T* row = in + (long)(r0 + r) * g.cols;
+            v[i] = vec_t<T>{};
+            if (r0 + r < g.rows && c0 + c < g.cols) v[i] = load_vec<T>(row, (c0 + c) / kVec<T>, g.cols);
+        }
+#pragma unroll
+        for (int i = 0; i < 64 / kRows; ++i)
+#pragma unroll
+            for (int q = 0; q < kVec<T>; ++q)
+                tile[threadIdx.x / kLanes + i * kRows][c + q] = (float)((double)(float)v[i][q] * factor);
+    });
+    __syncthreads();
+    E* x = p.base + g.x[0] + matrix * 2 * plane;
+    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+        const int r = i / 8, c = i % 8 * 8;
+        Eight y;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y.v[q] = g.tall ? tile[c + q][r] : tile[r][c + q];
+        write_parts(x + (long)(s0 + r) * g.l + l0 + c, plane, y);
+    }
+}
+
+// A of the matrices whose sums are cut, from the shares in their order; 8 values a thread.
+__global__ __launch_bounds__(256) void k_join_gram(Groups p) {
+    const int k = group_of(p, blockIdx.x);
+    const Group& g = p.g[k];
+    const long plane = (long)g.s * g.s, i = ((long)(blockIdx.x - p.first[k]) * 256 + threadIdx.x) * 8, matrix = i / plane, at = i % plane;
+    if (matrix >= g.batch) return;
+    const float* from = reinterpret_cast<const float*>(p.base) + g.parts + matrix * g.splits * plane + at;
+    Eight y{};
+#pragma unroll 4
+    for (unsigned s = 0; s < g.splits; ++s) {
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(from + s * plane), hi = *reinterpret_cast<const f32x4*>(from + s * plane + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y.v[q] += lo[q], y.v[4 + q] += hi[q];
+    }
+    write_parts(p.base + g.a + matrix * 2 * plane + at, plane, y);
+}
+
+enum Kind : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
+
+__device__ __forceinline__ void write_out(void* p, int dtype, long i, float v) {
+    if (dtype == kF32)
+        static_cast<float*>(p)[i] = v;
+    else if (dtype == kBF16)
+        static_cast<__bf16*>(p)[i] = (__bf16)v;
+    else
+        static_cast<_Float16*>(p)[i] = (_Float16)v;
+}
+
+// Place of a triangle's tile: row m, column n <= m of them, row after row.
+__device__ __forceinline__ TileAt triangle_at(unsigned id) {
+    unsigned m = (unsigned)((sqrtf(8.0f * id + 1.0f) - 1.0f) * 0.5f);
+    while (m * (m + 1) / 2 > id) --m;
+    while ((m + 1) * (m + 2) / 2 <= id) ++m;
+    return TileAt{m, id - m * (m + 1) / 2, 0};
+}
+
+// A tile of Side x Side of one of the products by 4 waves; from: which of the X buffers is X.  A and b A + c A A are
+// symmetric: the tiles on and below the diagonal are computed and written twice.
 template <int K, int Side>
 __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
     constexpr int MT = Side / 64;       // 32 x 32 tiles of a wave, in each direction
-    constexpr bool kAlong = K == kGram || K == kPoly;       // of the second operand
+    constexpr bool kSymmetric = K == kGram || K == kPoly, kAlong = kSymmetric;      // kAlong: the second operand
     typedef Tile<E, 2, true, Side, kDepth> TA;
     typedef Tile<E, 2, kAlong, Side, kDepth> TB;
     constexpr int kBuffer = TA::kBytes + TB::kBytes, kSlabs = 4 * 32 * kSlab<MT> * 4;
     __shared__ __attribute__((aligned(16))) char lds[2 * kBuffer > kSlabs ? 2 * kBuffer : kSlabs];
     const int k = group_of(p, blockIdx.x);
     const Group& g = p.g[k];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = (wave & 1) * 32 * MT, wn = (wave >> 1) * 32 * MT;
-    const int width = K == kGram || K == kPoly ? g.s : g.l;     // of the output
+    const int width = kSymmetric ? g.s : g.l;       // of the output
     const unsigned tiles_m = (g.s + Side - 1) / Side, tiles_n = (width + Side - 1) / Side;
-    const unsigned count = (k + 1 < p.n ? p.first[k + 1] : gridDim.x) - p.first[k];
-    const TileAt t = tile_at(xcd_order(blockIdx.x - p.first[k], count), tiles_m, tiles_n);
+    const unsigned id = xcd_order(blockIdx.x - p.first[k], p.first[k + 1] - p.first[k]);
+    TileAt t;
+    unsigned split = 0;
+    if constexpr (kSymmetric) {
+        const unsigned per = tiles_m * (tiles_m + 1) / 2, splits = K == kGram ? g.splits : 1;
+        t = triangle_at(id % per);
+        split = id / per % splits;
+        t.outer = id / per / splits;
+    } else {
+        t = tile_at(id, tiles_m, tiles_n);
+    }
     const long x_plane = (long)g.s * g.l, a_plane = (long)g.s * g.s;
     E* x = p.base + g.x[from] + t.outer * 2 * x_plane;
     E* a = p.base + g.a + t.outer * 2 * a_plane;
     E* b = p.base + g.b + t.outer * 2 * a_plane;
     const int m0 = t.m * Side, n0 = t.n * Side;
     // the operands; rows of a tile past the matrix's last are read where the matrix's last is, and their results dropped
-    const int a_ld = K == kGram ? g.l : g.s, b_ld = K == kPoly ? g.s : g.l, depth = K == kGram ? g.l : g.s;
-    const E* pa = (K == kGram ? x : K == kPoly ? a : b) + (long)m0 * a_ld;
-    const E* pb = (K == kPoly ? a : x) + (kAlong ? (long)n0 * b_ld : 0);
+    const int a_ld = K == kGram ? g.l : g.s, b_ld = K == kPoly ? g.s : g.l;
+    const int first = K == kGram ? split * g.cut : 0, depth = K == kGram ? min(g.cut, g.l - first) : g.s;
+    const E* pa = (K == kGram ? x : K == kPoly ? a : b) + (long)m0 * a_ld + first;
+    const E* pb = (K == kPoly ? a : x) + (kAlong ? (long)n0 * b_ld + first : 0);
     const long a_step = K == kGram ? x_plane : a_plane, b_step = K == kPoly ? a_plane : x_plane;
     Direct<true, Side, kDepth, 4> da;
     Direct<kAlong, Side, kDepth, 4> db;
@@ -219,31 +269,18 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
     }
     tile_barrier();
     float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<MT>;
-    if (K == kLast && g.tall) {
-        // the output's rows are the columns here
-        const float unscale = p.scale / kScale;
+    // 8 values of row m of the output, from column n on
+    auto finish = [&](int m, int n, Eight y) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            by_rows_block<MT>(acc, i, slab, lane);
-            for (int r = lane >> 5; r < 32 * MT; r += 2) {
-                const int m = m0 + wm + 32 * i + (lane & 31), n = n0 + wn + r;
-                if (m < g.cols && n < g.rows) {
-                    const long at = (long)m * g.l + n;
-                    const float v = __builtin_fmaf(kA, (float)x[at] + (float)x[at + x_plane], slab[(lane & 31) * kSlab<MT> + r] * (1.0f / kScale));
-                    write_out(g.out, g.dtype, ((long)t.outer * g.rows + n) * g.cols + m, v * unscale);
-                }
-            }
-        }
-        return;
-    }
-    by_rows<8, false, MT, MT>(acc, slab, lane, [&](int mr, int nc, const float* v, const float*) {
-        const int m = m0 + wm + mr, n = n0 + wn + nc;
-        if (m >= g.s || n >= width) return;
-        Eight y;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) y.v[q] = v[q] * (1.0f / kScale);
+        for (int q = 0; q < 8; ++q) y.v[q] *= 1.0f / kScale;
         if constexpr (K == kGram) {
-            write_parts(a + (long)m * g.s + n, a_plane, y);
+            if (g.splits > 1) {
+                float* to = reinterpret_cast<float*>(p.base) + g.parts + (t.outer * (long)g.splits + split) * a_plane + (long)m * g.s + n;
+                *reinterpret_cast<f32x4*>(to) = f32x4{y.v[0], y.v[1], y.v[2], y.v[3]};
+                *reinterpret_cast<f32x4*>(to + 4) = f32x4{y.v[4], y.v[5], y.v[6], y.v[7]};
+            } else {
+                write_parts(a + (long)m * g.s + n, a_plane, y);
+            }
         } else if constexpr (K == kPoly) {
             const Eight z = read_parts(a + (long)m * g.s + n, a_plane);
 #pragma unroll
@@ -272,13 +309,65 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
                     });
             }
         }
-    });
+    };
+    const bool turned = K == kLast && g.tall;       // the output's rows are the columns here
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        by_rows_block(acc, i, slab, lane);
+        constexpr int kLanes = 4 * MT, kRows = 64 / kLanes;
+#pragma unroll
+        for (int r = 0; r < 32; r += kRows) {
+            const int mr = r + lane / kLanes, nc = lane % kLanes * 8, m = m0 + wm + 32 * i + mr, n = n0 + wn + nc;
+            float* v = slab + mr * kSlab<MT> + nc;
+            Eight y;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y.v[q] = v[q];
+            if (m >= g.s || n >= width) continue;
+            if (turned) {
+                const Eight z = read_parts(x + (long)m * g.l + n, x_plane);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(kA, z.v[q], y.v[q] * (1.0f / kScale));
+            } else {
+                finish(m, n, y);
+            }
+        }
+        wave_lds_fence();
+        if (turned || (kSymmetric && t.m != t.n)) {
+            // columns of the tile: 4 lanes have 32 rows of one
+#pragma unroll
+            for (int r = 0; r < 32 * MT; r += 16) {
+                const int nc = r + lane / 4, mr = lane % 4 * 8, n = n0 + wn + nc, m = m0 + wm + 32 * i + mr;
+                const float* v = slab + mr * kSlab<MT> + nc;
+                Eight y;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y.v[q] = v[q * kSlab<MT>];
+                if constexpr (kSymmetric) {
+                    if (m < g.s && n < g.s) finish(n, m, y);
+                } else if (n < g.rows && m < g.cols) {
+                    of_type(g.dtype, [&](auto type) {
+                        typedef decltype(type) T;
+                        T* to = static_cast<T*>(g.out) + ((long)t.outer * g.rows + n) * g.cols + m;
+                        const int some = g.cols - m;
+#pragma unroll
+                        for (int h = 0; h < 8; h += kVec<T>) {
+                            Floats<T> f;
+#pragma unroll
+                            for (int q = 0; q < kVec<T>; ++q) f.v[q] = y.v[h + q] * (p.scale / kScale);
+                            if (some > h) store_left<T>(to + h, some - h, narrow<T>(f));
+                        }
+                    });
+                }
+            }
+        }
+    }
 }
 
 constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
 constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 
-// Places of the tensors first .. first + n - 1 (n at most kMostGroups) and the bytes they take.
+long triangle(long tiles) { return tiles * (tiles + 1) / 2; }
+
+// Places of the tensors from `first` on (at most kMostGroups) and the bytes they take.
 long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* rows, const int* cols) {
     long at = 0, sums = 0;
     p.n = 0;
@@ -300,31 +389,54 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
         g.sums = sums;
         sums += (long)g.batch * g.chunks;
     }
+    // tiles of 128 where those of the smallest product fill the card
+    long tiles = 0, terms = 0;
+    for (int k = 0; k < p.n; ++k) tiles += p.g[k].batch * triangle(div_up(p.g[k].s, 128));
+    p.wide = tiles >= 256;
+    // A's sums are cut where a long side would keep few workgroups busy for long
+    for (int k = 0; k < p.n; ++k) terms += p.g[k].batch * triangle(div_up(p.g[k].s, p.wide ? 128 : 64)) * p.g[k].l;
+    const long cut = max((long)kLeastCut, div_up(terms, 512));
+    for (int k = 0; k < p.n; ++k) {
+        Group& g = p.g[k];
+        g.splits = (unsigned)max(1L, g.l / cut);
+        g.cut = (int)div_up(div_up(g.l, g.splits), kPad) * kPad;
+        g.splits = (unsigned)max(1L, div_up(g.l, g.cut));
+        g.parts = at / 2;       // a float for two E; at is a multiple of the padding's square
+        if (g.splits > 1) at += 2 * g.batch * g.splits * (long)g.s * g.s;
+    }
+    p.sums_at = align256(2 * at);
     return align256(2 * at) + align256(8 * sums);
 }
 
+// Sets every group's first workgroup, of(g) of them each; their number.
 template <class F>
-unsigned place(Groups& p, F&& tiles) {
+unsigned place_groups(Groups& p, F&& of) {
     long total = 0;
     for (int k = 0; k < p.n; ++k) {
         p.first[k] = (unsigned)total;
-        total += p.g[k].batch * tiles(p.g[k]);
+        total += of(p.g[k]);
     }
     p.first[p.n] = (unsigned)total;
     return (unsigned)total;
+}
+// per(g) for each matrix.
+template <class F>
+unsigned place(Groups& p, F&& per) {
+    return place_groups(p, [&](const Group& g) { return g.batch * (long)per(g); });
 }
 
 template <int K, int Side>
 hipError_t product(Groups& p, int from, hipStream_t st) {
     const unsigned total = place(p, [](const Group& g) {
-        return div_up(g.s, Side) * div_up(K == kGram || K == kPoly ? g.s : g.l, Side);
+        if (K == kStep || K == kLast) return div_up(g.s, Side) * div_up(g.l, Side);
+        return triangle(div_up(g.s, Side)) * (K == kGram ? (long)g.splits : 1);
     });
     k_product<K, Side><<<total, 256, 0, st>>>(p, from);
     return hipGetLastError();
 }
 template <int K>
-hipError_t product(Groups& p, int from, bool wide, hipStream_t st) {
-    return wide ? product<K, 128>(p, from, st) : product<K, 64>(p, from, st);
+hipError_t product(Groups& p, int from, hipStream_t st) {
+    return p.wide ? product<K, 128>(p, from, st) : product<K, 64>(p, from, st);
 }
 
 #define CTP_TRY(call)                                                 \
@@ -340,16 +452,22 @@ hipError_t run(Groups& p, int steps, hipStream_t st) {
     total = place(p, [](const Group& g) { return (long)(g.s / 64) * (g.l / 64); });
     k_begin<<<total, 256, 0, st>>>(p);
     CTP_TRY(hipGetLastError());
-    // tiles of 128 where those of the smallest product fill the card
-    const bool wide = place(p, [](const Group& g) { return div_up(g.s, 128) * div_up(g.s, 128); }) >= 256;
+    bool cut = false;
+    for (int k = 0; k < p.n; ++k) cut |= p.g[k].batch && p.g[k].splits > 1;
     for (int s = 0; s < steps; ++s) {
-        CTP_TRY(product<kGram>(p, s & 1, wide, st));
-        CTP_TRY(product<kPoly>(p, s & 1, wide, st));
-        if (s + 1 < steps) {
-            CTP_TRY(product<kStep>(p, s & 1, wide, st));
-        } else {
-            CTP_TRY(product<kLast>(p, s & 1, wide, st));
+        CTP_TRY(product<kGram>(p, s & 1, st));
+        if (cut) {
+            total = place_groups(p, [](const Group& g) {
+                return g.splits > 1 ? div_up(g.batch * (long)g.s * g.s, 256 * 8) : 0L;
+            });
+            k_join_gram<<<total, 256, 0, st>>>(p);
+            CTP_TRY(hipGetLastError());
         }
+        CTP_TRY(product<kPoly>(p, s & 1, st));
+        if (s + 1 < steps)
+            CTP_TRY(product<kStep>(p, s & 1, st));
+        else
+            CTP_TRY(product<kLast>(p, s & 1, st));
     }
     return hipSuccess;
 }
@@ -367,17 +485,15 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t st) {
     for (int k = 0; k < a.n_tensors; k += kMostGroups) {
         Groups p;
         lay_out(p, k, a.n_tensors, a.batch, a.rows, a.cols);
-        long at = 0;
         for (int i = 0; i < p.n; ++i) {
             Group& g = p.g[i];
             g.in = a.in[k + i];
             g.out = a.out[k + i];
             g.dtype = a.dtype[k + i];
-            at += 4 * g.batch * (long)g.s * (g.l + g.s);
         }
         p.eps = a.eps, p.scale = a.scale;
         p.base = static_cast<E*>(a.workspace);
-        p.sums = reinterpret_cast<double*>(static_cast<char*>(a.workspace) + align256(2 * at));
+        p.sums = reinterpret_cast<double*>(static_cast<char*>(a.workspace) + p.sums_at);
         CTP_TRY(run(p, a.steps, st));
     }
     return hipSuccess;
