@@ -52,9 +52,11 @@ __device__ __forceinline__ f32x16 mfma(Frag<_Float16>::type a, Frag<_Float16>::t
 
 // A tile of Rows values of m (or n) by Depth of k in LDS, one plane for each
 // part.  Along: [row][k]; the 16-byte chunks of a row trade places by the row, so
-// that the 8 rows that one phase of a b128 read takes lie in different banks.
+// that the 16 rows that one clock of a b128 read takes lie in all 64 banks.
 // Across: [k][row]; units of 16 values trade places by k, for the transposing
-// reads, whose 16 lanes take 32 bytes of four values of k each.
+// reads, of which a clock takes two units of four values of k each.  (With the
+// places traded for 32 banks half of LDS's clocks were conflicts, and products of
+// 8192 x 16384 x 2048 bf16 took @@.)
 template <class E, int Parts_, bool Along, int Rows, int Depth>
 struct Tile {
     static constexpr int kPlane = Rows * Depth;     // elements
@@ -62,12 +64,13 @@ struct Tile {
     typedef typename Frag<E>::type frag_t;
 
     static __device__ __forceinline__ int chunk_of(int row, int c) {
-        return Depth == 64 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+        return Depth == 64 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
     }
+    static __device__ __forceinline__ int unit_of(int k, int u) { return u ^ (Rows >= 128 ? (k & 3) << 1 : k & 2); }
     // element offset of value (row, k)
     static __device__ __forceinline__ int at(int row, int k) {
         if constexpr (Along) return row * Depth + chunk_of(row, k >> 3) * 8 + (k & 7);
-        return k * Rows + (((row >> 4) ^ (k & 3)) << 4) + (row & 15);
+        return k * Rows + (unit_of(k, row >> 4) << 4) + (row & 15);
     }
     // The fragment of 32 rows from `row` and 16 k from `k`: lane i has row i % 32, 8 values of k from 8 (i / 32).
     static __device__ __forceinline__ frag_t read(const E* plane, int row, int k, int lane) {

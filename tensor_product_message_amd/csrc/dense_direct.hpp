@@ -45,6 +45,7 @@ template <bool Along, int Rows, int Depth, int Waves>
 struct Direct {
     static constexpr int kLoads = Rows * Depth / 8 / 64 / Waves;
     static_assert(kLoads * Waves * 64 * 8 == Rows * Depth);
+    typedef Tile<_Float16, 1, Along, Rows, Depth> tile_t;       // (the places are the same for any 16-bit type)
     static constexpr unsigned kNowhere = 0xfffffff0u;       // past the end of any buffer
     unsigned at[kLoads];        // byte offsets from the tile's first value
     int k[kLoads];              // Along: the chunk's first k
@@ -58,11 +59,11 @@ struct Direct {
             const int chunk = (wave * kLoads + j) * 64 + lane;
             if constexpr (Along) {
                 const int row = chunk / (Depth / 8), c = chunk % (Depth / 8);
-                k[j] = 8 * (Depth == 64 ? c ^ (row & 7) : c ^ ((row >> 1) & 3));
+                k[j] = 8 * tile_t::chunk_of(row, c);
                 at[j] = (unsigned)((row_of(row) * ld + k[j]) * 2);
             } else {
                 const int kr = chunk / (Rows / 8), c = chunk % (Rows / 8);
-                at[j] = (unsigned)((kr * ld + 8 * (c ^ ((kr & 3) << 1))) * 2);
+                at[j] = (unsigned)((kr * ld + 16 * tile_t::unit_of(kr, c >> 1) + 8 * (c & 1)) * 2);
                 k[j] = 0;
             }
         }
@@ -75,5 +76,62 @@ struct Direct {
             load_lds(buffer, !Along || k[j] < left ? at[j] : kNowhere, lds + (wave * kLoads + j) * 1024);
     }
 };
+
+// A wave's tile of (32 MT) x (32 NT) over `steps` (>= 1) tiles of k that issue(step, buffer) brings into one of two
+// buffers in LDS.  The fragments of the next 16 k are read while the matrix cores work on these, and across the end of a
+// tile too: its barrier stands before its last 16 k are multiplied, so that the cores have work while the first
+// fragments of the next tile come.  Without that they would wait for those at each barrier, all waves at once.
+template <class TA, class TB, int NParts, int MT, int NT, int Depth, class E, class Issue>
+__device__ __forceinline__ void multiply_tiles(f32x16 (&acc)[NT][MT], const E* lds, int steps, int wm, int wn, int lane, Issue&& issue) {
+    typedef typename Frag<E>::type frag_t;
+    constexpr int kBuffer = (TA::kBytes + TB::kBytes) / 2, kParts16 = Depth / 16;       // elements; even
+    frag_t fa[2][MT][NParts], fb[2][NT][NParts];
+    auto read = [&](int set, const E* tile, int k) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int p = 0; p < NParts; ++p) fb[set][j][p] = TB::read(tile + TA::kBytes / 2 + p * TB::kPlane, wn + 32 * j, k, lane);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int p = 0; p < NParts; ++p) fa[set][i][p] = TA::read(tile + p * TA::kPlane, wm + 32 * i, k, lane);
+    };
+    auto multiply = [&](int set) {
+        // the parts' smallest products first
+#pragma unroll
+        for (int s = NParts - 1; s >= 0; --s)
+#pragma unroll
+            for (int p = 0; p <= s; ++p)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[j][i] = mfma(fb[set][j][s - p], fa[set][i][p], acc[j][i]);
+    };
+    issue(0, 0);
+    loads_arrived<0>();
+    tile_barrier();
+    if (steps > 1) issue(1, 1);
+    read(0, lds, 0);
+    for (int step = 0; step < steps; ++step) {
+        const E* tile = lds + (step & 1) * kBuffer;
+#pragma unroll
+        for (int q = 0; q < kParts16 - 1; ++q) {
+            read((q + 1) & 1, tile, 16 * (q + 1));
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(q & 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (step + 1 < steps) {
+            // the next tile is there, and no wave reads this one any more
+            loads_arrived<0>();
+            tile_barrier();
+            if (step + 2 < steps) issue(step + 2, step & 1);
+            read(0, lds + ((step + 1) & 1) * kBuffer, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        multiply((kParts16 - 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
 
 }  // namespace ctp

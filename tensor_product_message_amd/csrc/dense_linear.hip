@@ -178,7 +178,8 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
             if constexpr (Pairs) return (long)min((r >> 6 << 5) + (r & 31), n_left - 1) + (r >> 5 & 1) * g.pair;
             return (long)min(r, n_left - 1);
         });
-        auto issue = [&](int k, int buffer) {
+        auto issue = [&](int step, int buffer) {
+            const int k = step * kDepth;
             // Across: what lies past the last k is the buffer's end
             const long rows = min(k_end - k, kDepth) - 1;
             const long a_left = AlongA ? 0x7ffffff0L : 2 * (rows * g.a_ld + m_left);
@@ -188,14 +189,8 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
                      base + buffer * kBuffer + TA::kBytes, k_end - k);
         };
         f32x16 acc[NT][MT] = {};
-        issue(0, 0);
-        for (int k = 0, s = 0; k < k_end; k += kDepth, s ^= 1) {
-            loads_arrived<0>();
-            tile_barrier();
-            if (k + kDepth < k_end) issue(k + kDepth, s ^ 1);
-            const E* la = reinterpret_cast<const E*>(lds + s * kBuffer);
-            multiply_step<TA, TB, 1, MT, NT, kDepth>(acc, la, la + TA::kBytes / 2, wm, wn, lane);
-        }
+        if (k_end > 0)
+            multiply_tiles<TA, TB, 1, MT, NT, kDepth>(acc, reinterpret_cast<const E*>(lds), (k_end + kDepth - 1) / kDepth, wm, wn, lane, issue);
         tile_barrier();
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
         write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left,

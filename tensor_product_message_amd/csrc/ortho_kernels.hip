@@ -247,7 +247,8 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
     da.init(a_ld, [&](int r) { return (long)min(r, g.s - 1 - m0); });
     db.init(b_ld, [&](int r) { return (long)min(r, g.s - 1 - n0); });
     const unsigned base = lds_address(lds);
-    auto issue = [&](int k0, int buffer) {
+    auto issue = [&](int step, int buffer) {
+        const int k0 = step * kDepth;
         const unsigned to = base + buffer * kBuffer;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -259,14 +260,7 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
         }
     };
     f32x16 acc[MT][MT] = {};
-    issue(0, 0);
-    for (int k0 = 0, s = 0; k0 < depth; k0 += kDepth, s ^= 1) {
-        loads_arrived<0>();
-        tile_barrier();
-        if (k0 + kDepth < depth) issue(k0 + kDepth, s ^ 1);
-        const E* la = reinterpret_cast<const E*>(lds + s * kBuffer);
-        multiply_step<TA, TB, 2, MT, MT, kDepth>(acc, la, la + TA::kBytes / 2, wm, wn, lane);
-    }
+    multiply_tiles<TA, TB, 2, MT, MT, kDepth>(acc, reinterpret_cast<const E*>(lds), depth / kDepth, wm, wn, lane, issue);
     tile_barrier();
     float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<MT>;
     // 8 values of row m of the output, from column n on
@@ -395,7 +389,7 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
     p.wide = tiles >= 256;
     // A's sums are cut where a long side would keep few workgroups busy for long
     for (int k = 0; k < p.n; ++k) terms += p.g[k].batch * triangle(div_up(p.g[k].s, p.wide ? 128 : 64)) * p.g[k].l;
-    const long cut = max((long)kLeastCut, div_up(terms, 512));
+    const long cut = max((long)kLeastCut, div_up(terms, 768));
     for (int k = 0; k < p.n; ++k) {
         Group& g = p.g[k];
         g.splits = (unsigned)max(1L, g.l / cut);
