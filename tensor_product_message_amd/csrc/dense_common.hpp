@@ -64,7 +64,7 @@ struct Tile {
     typedef typename Frag<E>::type frag_t;
 
     static __device__ __forceinline__ int chunk_of(int row, int c) {
-        return Depth == 64 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
+        return Depth == 128 ? c ^ (row & 15) : Depth == 64 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
     }
     static __device__ __forceinline__ int unit_of(int k, int u) { return u ^ (Rows >= 128 ? (k & 3) << 1 : k & 2); }
     // element offset of value (row, k)
@@ -72,13 +72,15 @@ struct Tile {
         if constexpr (Along) return row * Depth + chunk_of(row, k >> 3) * 8 + (k & 7);
         return k * Rows + (unit_of(k, row >> 4) << 4) + (row & 15);
     }
-    // The fragment of 32 rows from `row` and 16 k from `k`: lane i has row i % 32, 8 values of k from 8 (i / 32).
+    // The fragment of 32 rows from `row` and 16 k: lane i has row i % 32, 8 values of k from k + Half (i / 32).  Which
+    // k a lane has does not matter as long as both operands' lanes agree.
+    template <int Half = 8>
     static __device__ __forceinline__ frag_t read(const E* plane, int row, int k, int lane) {
         if constexpr (Along) {
-            return *reinterpret_cast<const frag_t*>(plane + at(row + (lane & 31), k + 8 * (lane >> 5)));
+            return *reinterpret_cast<const frag_t*>(plane + at(row + (lane & 31), k + Half * (lane >> 5)));
         } else {
             // 16 lanes read 4 rows of 16 values, lane i the values 4 (i % 4) of row i / 4, and get the columns
-            const int i = lane & 15, k0 = k + 8 * (lane >> 5) + (i >> 2), r0 = row + (lane & 16) + 4 * (i & 3);
+            const int i = lane & 15, k0 = k + Half * (lane >> 5) + (i >> 2), r0 = row + (lane & 16) + 4 * (i & 3);
             typedef __attribute__((address_space(3))) s16x4* lds_t;
             union {
                 s16x4 h[2];
@@ -90,6 +92,20 @@ struct Tile {
         }
     }
 };
+
+// x = p[0] + p[1] + p[2].
+struct ThreeParts {
+    __bf16 p[3];
+};
+__device__ __forceinline__ ThreeParts take_apart(float x) {
+    constexpr float kLargest = 3.3895313892515355e38f;      // of bfloat16: a value that rounds beyond it is cut instead
+    ThreeParts t;
+    t.p[0] = (__bf16)__builtin_amdgcn_fmed3f(x, -kLargest, kLargest);
+    const float rest = x - (float)t.p[0];
+    t.p[1] = (__bf16)rest;
+    t.p[2] = (__bf16)(rest - (float)t.p[1]);
+    return t;
+}
 
 // A tile's way from memory: 16-byte reads into registers, then into LDS as parts.
 // n_rows: how many m (or n) there are, values past which are any; k_end: where k ends, zeros past it.
@@ -133,23 +149,18 @@ struct Staged {
             if constexpr (Parts<T>::count == 1) {
                 *reinterpret_cast<vec_t<T>*>(to) = v[i];
             } else {
-                typename Frag<E>::half h, m, l;
+                typename Frag<E>::half part[3];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    // a value whose rounding would be infinite is cut instead
-                    const float x = v[i][q];
-                    h[q] = (E)__builtin_amdgcn_fmed3f(x, -kLargest, kLargest);
-                    const float rest = x - (float)h[q];
-                    m[q] = (E)rest;
-                    l[q] = (E)(rest - (float)m[q]);
+                    const ThreeParts t = take_apart(v[i][q]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) part[p][q] = t.p[p];
                 }
-                *reinterpret_cast<typename Frag<E>::half*>(to) = h;
-                *reinterpret_cast<typename Frag<E>::half*>(to + tile_t::kPlane) = m;
-                *reinterpret_cast<typename Frag<E>::half*>(to + 2 * tile_t::kPlane) = l;
+#pragma unroll
+                for (int p = 0; p < 3; ++p) *reinterpret_cast<typename Frag<E>::half*>(to + p * tile_t::kPlane) = part[p];
             }
         }
     }
-    static constexpr float kLargest = 3.3895313892515355e38f;      // of bfloat16
 };
 
 // One step of k through the matrix cores: the wave's tile of (32 MT) x (32 NT).  The matrix instruction's own rows are
@@ -180,9 +191,9 @@ __device__ __forceinline__ void multiply_step(f32x16 (&acc)[NT][MT], const E* a,
     }
 }
 
-// The wave's results by rows: for every row of its tile f(m, n, first), where first[0 .. V) are the values of the
-// columns n .. n + V - 1 of the wave's tile, in fp32.  slab: the wave's own piece of LDS, 32 rows of kSlab floats.
-// Pairs: the halves of each 64 columns belong together, f(m, n, first, second) for the columns n, n + 32 of them.
+// The wave's results by rows: f(m, step, n, x, y), where x[r][0 .. V) are the values of row m + r step of the wave's
+// tile in the columns n .. n + V - 1, in fp32.  slab: the wave's own piece of LDS, 32 rows of kSlab floats.
+// Pairs: the halves of each 64 columns belong together, x and y for the columns n, n + 32 of them.
 template <int NT>
 constexpr int kSlab = 32 * NT + 4;
 
@@ -210,23 +221,23 @@ __device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i
 
 template <int V, bool Pairs, int MT, int NT, class F>
 __device__ __forceinline__ void by_rows(const f32x16 (&acc)[NT][MT], float* slab, int lane, F&& f) {
-    constexpr int kCols = 32 * NT / (Pairs ? 2 : 1), kLanes = kCols / V, kRows = 64 / kLanes;
+    constexpr int kCols = 32 * NT / (Pairs ? 2 : 1), kLanes = kCols / V, kRows = 64 / kLanes, R = 32 / kRows;
     static_assert(!Pairs || NT % 2 == 0);
+    const int n = lane % kLanes * V;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         by_rows_block(acc, i, slab, lane);
+        float x[R][V], y[R][V];
 #pragma unroll
-        for (int r = 0; r < 32; r += kRows) {
-            const int m = r + lane / kLanes, n = lane % kLanes * V;
-            const float* from = slab + m * kSlab<NT> + (Pairs ? n / 32 * 64 + n % 32 : n);
-            float x[V], y[V];
+        for (int r = 0; r < R; ++r) {
+            const float* from = slab + (r * kRows + lane / kLanes) * kSlab<NT> + (Pairs ? n / 32 * 64 + n % 32 : n);
 #pragma unroll
             for (int q = 0; q < V; q += 4) {
-                *reinterpret_cast<f32x4*>(x + q) = *reinterpret_cast<const f32x4*>(from + q);
-                if constexpr (Pairs) *reinterpret_cast<f32x4*>(y + q) = *reinterpret_cast<const f32x4*>(from + 32 + q);
+                *reinterpret_cast<f32x4*>(x[r] + q) = *reinterpret_cast<const f32x4*>(from + q);
+                if constexpr (Pairs) *reinterpret_cast<f32x4*>(y[r] + q) = *reinterpret_cast<const f32x4*>(from + 32 + q);
             }
-            f(32 * i + m, n, x, y);
         }
+        f(32 * i + lane / kLanes, kRows, n, x, y);
     }
 }
 
@@ -258,6 +269,20 @@ __device__ __forceinline__ TileAt tile_at(unsigned id, unsigned tiles_m, unsigne
 
 // ---------------------------------------------------------------- activations
 
+// exp(x) for x <= 0 and 1 / d for 1 <= d <= 2, each off by some two roundings: the product with log2(e) is carried in
+// two floats, and one Newton step follows the hardware's reciprocal.  (expf and a division are three times the
+// instructions, which a layer's epilogue does not hide.)
+__device__ __forceinline__ float exp_falling(float x) {
+    x = x < -104.0f ? -104.0f : x;      // exp(-104) is below every float; NaN stays
+    const float t = x * 1.44269502f, rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
+    const float y = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(y, rest * 0.693147181f, y);
+}
+__device__ __forceinline__ float one_over(float d) {
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
 // act(z), its first and its second derivative.
 template <int Act_>
 __device__ __forceinline__ void activation(float z, float& f, float& d1, float& d2) {
@@ -267,7 +292,7 @@ __device__ __forceinline__ void activation(float z, float& f, float& d1, float& 
         d2 = 0.0f;
     } else if constexpr (Act_ == kActSilu || Act_ == kActSigmoid) {
         // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
-        const float e = expf(-fabsf(z)), large = 1.0f / (1.0f + e), small = e * large;
+        const float e = exp_falling(-fabsf(z)), large = one_over(1.0f + e), small = e * large;
         const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
         if constexpr (Act_ == kActSigmoid) {
             f = s, d1 = t, d2 = t * u;
@@ -275,10 +300,10 @@ __device__ __forceinline__ void activation(float z, float& f, float& d1, float& 
             f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
         }
     } else if constexpr (Act_ == kActGelu) {
-        const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * expf(-0.5f * z * z);
+        const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * exp_falling(-0.5f * z * z);
         f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
     } else if constexpr (Act_ == kActTanh) {
-        const float e = expf(-2.0f * fabsf(z)), r = 1.0f / (1.0f + e);
+        const float e = exp_falling(-2.0f * fabsf(z)), r = one_over(1.0f + e);
         f = tanhf(z);
         d1 = 4.0f * e * r * r;
         d2 = -2.0f * f * d1;

@@ -42,47 +42,87 @@ struct Gemm {
     unsigned splits, tiles_m, tiles_n, total;
 };
 
-// V floats, the same width as a vector of T.
-struct Values {
-    float v[V];
+// Rows of V values each, of which the first `some` are there (Whole: all, and their columns too).
+template <bool Whole, int R>
+struct Rows {
+    int some;
+    int at, width;      // first column, columns of a row
+
+    __device__ __forceinline__ vec_t<T> read(const T* row) const {
+        if constexpr (Whole) return *reinterpret_cast<const typename Vec<T>::unaligned*>(row + at);
+        return load_vec<T>(row, at / V, width);
+    }
+    // to[r step]: row r
+    __device__ __forceinline__ void write(T* to, long step, const float (&x)[R][V], bool stream) const {
+        if (stream) {
+            keep_apart();
+            write<true>(to, step, x);
+            keep_apart();
+        } else {
+            write<false>(to, step, x);
+        }
+    }
+    template <bool Stream>
+    __device__ __forceinline__ void write(T* to, long step, const float (&x)[R][V]) const {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            Floats<T> f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) f.v[q] = x[r][q];
+            const vec_t<T> v = narrow<T>(f);
+            auto* place = reinterpret_cast<typename Vec<T>::unaligned*>(to + r * step + at);
+            if constexpr (Whole) {
+                if constexpr (Stream)
+                    __builtin_nontemporal_store(v, place);
+                else
+                    *place = v;
+            } else if (r < some) {
+                store_left<T>(to + r * step + at, width - at, v);
+            }
+        }
+    }
+    // row r: what is at from[r step], zeros where there is none
+    __device__ __forceinline__ void read(const T* from, long step, float (&x)[R][V]) const {
+        vec_t<T> v[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            v[r] = vec_t<T>{};
+            if (Whole || r < some) v[r] = read(from + r * step);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[r][q] = (float)v[r][q];
+    }
+    // one vector added to every row
+    __device__ __forceinline__ void add(const T* from, float (&x)[R][V]) const {
+        const Floats<T> f = widen<T>(read(from));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[r][q] += f.v[q];
+    }
 };
 
-// Whole: the vector lies in the row.
-template <bool Whole>
-__device__ __forceinline__ Values read_values(const T* row, int n, int width) {
-    vec_t<T> r;
-    if constexpr (Whole)
-        r = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + n);
-    else
-        r = load_vec<T>(row, n / V, width);
-    const Floats<T> f = widen<T>(r);
-    Values x;
-#pragma unroll
-    for (int q = 0; q < V; ++q) x.v[q] = f.v[q];
-    return x;
-}
-template <bool Whole>
-__device__ __forceinline__ void write_values(T* row, int n, int width, const float* x) {
-    Floats<T> f;
-#pragma unroll
-    for (int q = 0; q < V; ++q) f.v[q] = x[q];
-    if constexpr (Whole)
-        *reinterpret_cast<typename Vec<T>::unaligned*>(row + n) = narrow<T>(f);
-    else
-        store_left<T>(row + n, width - n, narrow<T>(f));
-}
+// A place in the output: rows m, m + step, .., of which `some` are there, and V columns from `at` on.
+struct Place {
+    unsigned outer, batch;
+    long m;
+    int step, some, at;
+};
 
-// A wave's results through its epilogue: epi.run<Whole>(outer, batch, m, n, x, y) for V columns of a row.
+// A wave's results through its epilogue.
 template <bool Pairs, int MT, int NT, class Epi>
 __device__ __forceinline__ void write_tile(const f32x16 (&acc)[NT][MT], float* slab, int lane, int wm, int wn, int m_left,
                                            int n_left, bool whole, const Epi& epi, unsigned outer, unsigned batch, long m0, int n0) {
     if (whole) {
-        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int n, const float* x, const float* y) {
-            epi.template run<true>(outer, batch, m0 + wm + m, n0 + wn + n, x, y);
+        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int step, int n, auto& x, auto& y) {
+            epi.template run<true>(Place{outer, batch, m0 + wm + m, step, 0, n0 + wn + n}, x, y);
         });
     } else {
-        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int n, const float* x, const float* y) {
-            if (wm + m < m_left && wn + n < n_left) epi.template run<false>(outer, batch, m0 + wm + m, n0 + wn + n, x, y);
+        by_rows<V, Pairs, MT, NT>(acc, slab, lane, [&](int m, int step, int n, auto& x, auto& y) {
+            const int left = wn + n < n_left ? (m_left - wm - m + step - 1) / step : 0;
+            if (left > 0) epi.template run<false>(Place{outer, batch, m0 + wm + m, step, left, n0 + wn + n}, x, y);
         });
     }
 }
@@ -205,29 +245,28 @@ struct EpiLinear {
     const T *bias, *residual;
     long row, residual_row;     // elements from row to row
     int n, act;
-    template <bool Whole>
-    __device__ __forceinline__ void run(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
-        Values v;
-#pragma unroll
-        for (int q = 0; q < V; ++q) v.v[q] = x[q];
-        if (bias != nullptr && batch == 0) {
-            const Values b = read_values<Whole>(bias, at, n);
-#pragma unroll
-            for (int q = 0; q < V; ++q) v.v[q] += b.v[q];
-        }
-        const long to = m * row + (long)batch * n;
-        if (z != nullptr) write_values<Whole>(z + to, at, n, v.v);
+    bool stream;                // see streams_out
+    template <bool Whole, int R>
+    __device__ __forceinline__ void run(const Place& p, float (&x)[R][V], float (&)[R][V]) const {
+        const Rows<Whole, R> rows{p.some, p.at, n};
+        float r[R][V];
+        if (residual != nullptr) rows.read(residual + p.m * residual_row + (long)p.batch * n, p.step * residual_row, r);
+        if (bias != nullptr && p.batch == 0) rows.add(bias, x);
+        const long to = p.m * row + (long)p.batch * n;
+        if (z != nullptr) rows.write(z + to, p.step * row, x, stream);
         with_act(act, [&](auto is) {
             float d1, d2;
 #pragma unroll
-            for (int q = 0; q < V; ++q) activation<decltype(is)::value>(v.v[q], v.v[q], d1, d2);
-        });
-        if (residual != nullptr) {
-            const Values r = read_values<Whole>(residual + m * residual_row + (long)batch * n, at, n);
+            for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int q = 0; q < V; ++q) v.v[q] += r.v[q];
-        }
-        write_values<Whole>(y + to, at, n, v.v);
+                for (int q = 0; q < V; ++q) activation<decltype(is)::value>(x[i][q], x[i][q], d1, d2);
+        });
+        if (residual != nullptr)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int q = 0; q < V; ++q) x[i][q] += r[i][q];
+        rows.write(y + to, p.step * row, x, stream);
     }
 };
 
@@ -236,30 +275,29 @@ struct EpiGated {
     T *h, *z;
     const T* bias;
     int n, act;
-    template <bool Whole>
-    __device__ __forceinline__ void run(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
-        Values a, b;
-#pragma unroll
-        for (int q = 0; q < V; ++q) a.v[q] = x[q], b.v[q] = y[q];
+    bool stream;
+    template <bool Whole, int R>
+    __device__ __forceinline__ void run(const Place& p, float (&x)[R][V], float (&y)[R][V]) const {
+        const Rows<Whole, R> rows{p.some, p.at, n};
         if (bias != nullptr) {
-            const Values p = read_values<Whole>(bias, at, n), r = read_values<Whole>(bias + n, at, n);
-#pragma unroll
-            for (int q = 0; q < V; ++q) a.v[q] += p.v[q], b.v[q] += r.v[q];
+            rows.add(bias, x);
+            rows.add(bias + n, y);
         }
         if (z != nullptr) {
-            write_values<Whole>(z + m * 2 * n, at, n, a.v);
-            write_values<Whole>(z + m * 2 * n + n, at, n, b.v);
+            rows.write(z + p.m * 2 * n, p.step * 2L * n, x, stream);
+            rows.write(z + p.m * 2 * n + n, p.step * 2L * n, y, stream);
         }
-        Values f;
         with_act(act, [&](auto is) {
             float d1, d2;
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                activation<decltype(is)::value>(a.v[q], f.v[q], d1, d2);
-                f.v[q] *= b.v[q];
-            }
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    activation<decltype(is)::value>(x[i][q], x[i][q], d1, d2);
+                    x[i][q] *= y[i][q];
+                }
         });
-        write_values<Whole>(h + m * n, at, n, f.v);
+        rows.write(h + p.m * n, (long)p.step * n, x, stream);
     }
 };
 
@@ -268,9 +306,10 @@ struct EpiPlain {
     T* out;
     long row;
     int n;
-    template <bool Whole>
-    __device__ __forceinline__ void run(unsigned, unsigned batch, long m, int at, const float* x, const float*) const {
-        write_values<Whole>(out + m * row + (long)batch * n, at, n, x);
+    bool stream;
+    template <bool Whole, int R>
+    __device__ __forceinline__ void run(const Place& p, float (&x)[R][V], float (&)[R][V]) const {
+        Rows<Whole, R>{p.some, p.at, n}.write(out + p.m * row + (long)p.batch * n, p.step * row, x, stream);
     }
 };
 
@@ -279,19 +318,21 @@ struct EpiPart {
     float* parts;
     long size;      // of one part: rows n values wide
     int n;
-    template <bool Whole>
-    __device__ __forceinline__ void run(unsigned outer, unsigned, long m, int at, const float* x, const float*) const {
-        float* to = parts + outer * size + m * n + at;
+    template <bool Whole, int R>
+    __device__ __forceinline__ void run(const Place& p, float (&x)[R][V], float (&)[R][V]) const {
+        float* to = parts + p.outer * size + p.m * n + p.at;
 #pragma unroll
-        for (int q = 0; q < V; q += 4) {
-            vec_t<float> w;
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = x[q + e];
-            if constexpr (Whole)
-                *reinterpret_cast<Vec<float>::unaligned*>(to + q) = w;
-            else if (at + q < n)
-                store_left<float>(to + q, n - at - q, w);
-        }
+            for (int q = 0; q < V; q += 4) {
+                vec_t<float> w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = x[i][q + e];
+                if constexpr (Whole)
+                    *reinterpret_cast<Vec<float>::unaligned*>(to + (long)i * p.step * n + q) = w;
+                else if (i < p.some && p.at + q < n)
+                    store_left<float>(to + (long)i * p.step * n + q, n - p.at - q, w);
+            }
     }
 };
 
@@ -302,43 +343,166 @@ struct EpiSecond {
     T *g_grad, *g_z, *s;
     long grad_row;
     int n, act;
-    template <bool Whole>
-    __device__ __forceinline__ void run(unsigned, unsigned, long m, int at, const float* x, const float* y) const {
-        const Values g = read_values<Whole>(grad + m * grad_row, at, n);
-        const long zr = m * n * (Gated ? 2 : 1);
-        const Values a = read_values<Whole>(z + zr, at, n);
-        Values b{}, o, p, q, pb, qb;
-        if constexpr (Gated) b = read_values<Whole>(z + zr + n, at, n);
-        with_act(act, [&](auto is) {
+    template <bool Whole, int R>
+    __device__ __forceinline__ void run(const Place& place, float (&x)[R][V], float (&y)[R][V]) const {
+        // a row at a time: its many values would not all find registers
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float f, d1, d2;
-                activation<decltype(is)::value>(a.v[i], f, d1, d2);
-                if constexpr (Gated) {
-                    const float gb = g.v[i] * b.v[i];
-                    o.v[i] = __builtin_fmaf(x[i] * b.v[i], d1, y[i] * f);
-                    p.v[i] = __builtin_fmaf(x[i] * gb, d2, y[i] * g.v[i] * d1);
-                    pb.v[i] = x[i] * g.v[i] * d1;
-                    q.v[i] = gb * d1;
-                    qb.v[i] = g.v[i] * f;
-                } else {
-                    o.v[i] = x[i] * d1;
-                    p.v[i] = x[i] * g.v[i] * d2;
-                    q.v[i] = g.v[i] * d1;
+        for (int i = 0; i < R; ++i) {
+            if (!Whole && i >= place.some) break;
+            const Rows<Whole, 1> row{1, place.at, n};
+            const long m = place.m + (long)i * place.step, zr = m * n * (Gated ? 2 : 1);
+            float g[1][V], a[1][V], b[1][V], o[1][V], p[1][V], q[1][V], pb[1][V], qb[1][V];
+            row.read(grad + m * grad_row, 0, g);
+            row.read(z + zr, 0, a);
+            if constexpr (Gated) row.read(z + zr + n, 0, b);
+            with_act(act, [&](auto is) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float f, d1, d2;
+                    activation<decltype(is)::value>(a[0][e], f, d1, d2);
+                    const float u = x[i][e], h = g[0][e];
+                    if constexpr (Gated) {
+                        const float w = y[i][e], c = b[0][e], hc = h * c;
+                        o[0][e] = __builtin_fmaf(u * c, d1, w * f);
+                        p[0][e] = __builtin_fmaf(u * hc, d2, w * h * d1);
+                        pb[0][e] = u * h * d1;
+                        q[0][e] = hc * d1;
+                        qb[0][e] = h * f;
+                    } else {
+                        o[0][e] = u * d1;
+                        p[0][e] = u * h * d2;
+                        q[0][e] = h * d1;
+                    }
                 }
+            });
+            if (g_grad != nullptr) row.write(g_grad + m * n, 0, o, false);
+            if (g_z != nullptr) {
+                row.write(g_z + zr, 0, p, false);
+                if constexpr (Gated) row.write(g_z + zr + n, 0, pb, false);
             }
-        });
-        if (g_grad != nullptr) write_values<Whole>(g_grad + m * n, at, n, o.v);
-        if (g_z != nullptr) {
-            write_values<Whole>(g_z + zr, at, n, p.v);
-            if constexpr (Gated) write_values<Whole>(g_z + zr + n, at, n, pb.v);
-        }
-        if (s != nullptr) {
-            write_values<Whole>(s + zr, at, n, q.v);
-            if constexpr (Gated) write_values<Whole>(s + zr + n, at, n, qb.v);
+            if (s != nullptr) {
+                row.write(s + zr, 0, q, false);
+                if constexpr (Gated) row.write(s + zr + n, 0, qb, false);
+            }
         }
     }
 };
+
+// ---------------------------------------------------------------- floats, short sums
+
+#if CTP_DENSE_TYPE == 0
+
+// Floats with at most 64 Blocks terms a sum, where taking the operands apart and what is done with the results cost
+// more than the products: a wave keeps 32 rows of A in registers, taken apart once, and goes through the columns, 64
+// (Pairs: 32 and their partners) at a time, whose parts the workgroup's waves share in LDS.  Results go from the matrix
+// cores' registers to memory, 16 bytes a lane.
+template <int Blocks, bool AlongB, bool Pairs, class Epi>
+__global__ __launch_bounds__(256, Blocks == 1 ? 3 : 2) void k_rows(Gemm g, Epi epi, unsigned tiles_a_group) {
+    constexpr int kLong = 64 * Blocks, kCols = Pairs ? 32 : 64;
+    typedef Staged<T, AlongB, 64, kLong, 256> SB;
+    typedef typename SB::tile_t TB;
+    typedef typename Frag<E>::type frag_t;
+    __shared__ __attribute__((aligned(16))) char lds[TB::kBytes];
+    __shared__ __attribute__((aligned(16))) float slabs[4][32 * kSlab<1>];
+    E* lb = reinterpret_cast<E*>(lds);
+    float* slab = slabs[threadIdx.x >> 6];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const TileAt t = tile_at(xcd_order(blockIdx.x, g.total), g.tiles_m, g.tiles_n);
+    const unsigned batch = t.outer;
+    const long m = (long)t.m * 128 + wave * 32 + (lane & 31);
+    const int k_end = (int)g.k;
+    const T* row = g.a + batch * g.a_batch + min(m, g.m - 1) * g.a_ld;
+    // 16 values of k a lane and 32: 64 bytes in one piece
+    frag_t a[kLong / 16][kParts];
+#pragma unroll
+    for (int k = 0; k < kLong; k += 32) {
+        vec_t<T> v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int at = k + 16 * (lane >> 5) + 4 * q;
+            if (at + V <= k_end)
+                v[q] = *reinterpret_cast<const typename Vec<T>::unaligned*>(row + at);
+            else
+                v[q] = at < k_end ? load_vec<T>(row, at / V, k_end) : vec_t<T>{};
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const ThreeParts x = take_apart(v[2 * s + q / 4][q % 4]);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) a[k / 16 + s][p][q] = x.p[p];
+            }
+    }
+    const T* b = g.b + (g.b_degree ? degree_of(batch) : (int)batch) * g.b_batch;
+    const int n_first = t.n * tiles_a_group * kCols, n_last = min(g.n, n_first + (int)tiles_a_group * kCols);
+    SB sb;
+    auto load = [&](int n0) {
+        const T* from = b + (AlongB ? (long)n0 * g.b_ld : n0);
+        const int n_left = g.n - n0;
+        auto row_b = [&](int r) {
+            if constexpr (Pairs) return (long)min(r & 31, n_left - 1) + (r >> 5) * g.pair;
+            return (long)min(r, n_left - 1);
+        };
+        if (k_end == kLong && n_left >= kCols)
+            sb.template load<true>(from, g.b_ld, n_left, 0, k_end, row_b);
+        else
+            sb.template load<false>(from, g.b_ld, n_left, 0, k_end, row_b);
+    };
+    load(n_first);
+    for (int n0 = n_first; n0 < n_last; n0 += kCols) {
+        lds_barrier();
+        sb.store(lb);
+        lds_barrier();
+        if (n0 + kCols < n_last) load(n0 + kCols);
+        f32x16 acc[2] = {};
+#pragma unroll
+        for (int k = 0; k < kLong; k += 16) {
+            frag_t f[2][kParts];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    f[j][p] = TB::template read<16>(lb + p * TB::kPlane, 32 * j, k / 32 * 32 + k % 32 / 2, lane);
+            // the parts' smallest products first
+#pragma unroll
+            for (int s = kParts - 1; s >= 0; --s)
+#pragma unroll
+                for (int p = 0; p <= s; ++p)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[j] = mfma(f[j][s - p], a[k / 16][p], acc[j]);
+        }
+        // 32 columns at a time: a row of them is 128 bytes
+        const long m0 = (long)t.m * 128 + wave * 32;
+        auto write = [&](auto whole) {
+            constexpr bool Whole = decltype(whole)::value != 0;
+            float x[4][4], y[4][4];
+            const int nc = lane % 8 * 4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                wave_lds_fence();
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4*>(slab + (lane & 31) * kSlab<1> + 8 * q + 4 * (lane >> 5)) =
+                        f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+                wave_lds_fence();
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<f32x4*>((Pairs && j ? y : x)[r]) = *reinterpret_cast<const f32x4*>(slab + (8 * r + lane / 8) * kSlab<1> + nc);
+                if (Pairs && j == 0) continue;
+                const int n = n0 + nc + (Pairs ? 0 : 32 * j);
+                const long m = m0 + lane / 8;
+                const int some = Whole || n < g.n ? (int)min(4L, (g.m - m + 7) / 8) : 0;
+                if (Whole || some > 0) epi.template run<Whole>(Place{batch, batch, m, 8, some, n}, x, y);
+            }
+        };
+        if (n0 + kCols <= g.n && m0 + 32 <= g.m)
+            write(ActIs<1>{});
+        else
+            write(ActIs<0>{});
+    }
+}
+#endif
 
 // ---------------------------------------------------------------- few rows
 
@@ -433,19 +597,19 @@ __global__ __launch_bounds__(64 * Waves) void k_few(Gemm g, Epi epi) {
     for (int id = threadIdx.x; id < 16 * MB * kLanes; id += 64 * Waves) {
         const int m = id / kLanes, n = id % kLanes * V;
         if (m >= g.m || n0 + n >= g.n) continue;
-        float x[V], y[V];
+        float x[1][V], y[1][V];
 #pragma unroll
         for (int q = 0; q < V; ++q) {
-            x[q] = part[0][m][n + q];
-            if constexpr (Pairs) y[q] = part[0][m][16 + n + q];
+            x[0][q] = part[0][m][n + q];
+            if constexpr (Pairs) y[0][q] = part[0][m][16 + n + q];
         }
         for (int w = 1; w < Waves; ++w)
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                x[q] += part[w][m][n + q];
-                if constexpr (Pairs) y[q] += part[w][m][16 + n + q];
+                x[0][q] += part[w][m][n + q];
+                if constexpr (Pairs) y[0][q] += part[w][m][16 + n + q];
             }
-        epi.template run<false>(batch, batch, m, n0 + n, x, y);
+        epi.template run<false>(Place{batch, batch, m, 1, 1, n0 + n}, x, y);
     }
 }
 
@@ -462,81 +626,78 @@ struct ActBwd {
     int n, act, across;
 };
 
-// One row's vector of columns.
-template <bool Gated>
-struct ActRow {
-    vec_t<T> g, a, b;
-};
+// As the members of Rows, for rows whose columns are whole vectors but whose number is `some`.
+template <bool Whole, int R>
+__device__ __forceinline__ void read_rows(const Rows<Whole, R>& rows, const T* from, long step, float (&x)[R][V]) {
+    vec_t<T> v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        v[r] = vec_t<T>{};
+        if (r < rows.some) v[r] = rows.read(from + r * step);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int q = 0; q < V; ++q) x[r][q] = (float)v[r][q];
+}
+template <bool Whole, int R>
+__device__ __forceinline__ void write_rows(const Rows<Whole, R>& rows, T* to, long step, const float (&x)[R][V]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r < rows.some) Rows<Whole, 1>{1, rows.at, rows.width}.write(to + r * step, 0, reinterpret_cast<const float(&)[1][V]>(x[r]), false);
+}
 
-// Whole: n is whole vectors.  Rows: so many of a lane's rows are read at once.
+// Whole: n is whole vectors.
 template <bool Gated, bool Whole>
 __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
-    constexpr int H = Gated ? 2 : 1, Rows = 4;
+    constexpr int H = Gated ? 2 : 1, R = 4;     // rows that a lane reads at once
     __shared__ float part[256 * H * V];
     const int tx = threadIdx.x % p.across, ty = threadIdx.x / p.across, high = 256 / p.across;
     const int at = (blockIdx.x * p.across + tx) * V;
     const long first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.rows);
-    Values sum[H] = {};
-    auto read = [&](const T* row) {
-        if constexpr (Whole) return (vec_t<T>)*reinterpret_cast<const typename Vec<T>::unaligned*>(row + at);
-        return load_vec<T>(row, at / V, p.n);
-    };
-    auto values = [](vec_t<T> x) {
-        const Floats<T> f = widen<T>(x);
-        Values v;
+    float sum[H][V] = {};
+    for (long m = at < p.n ? first + ty : last; m < last; m += R * high) {
+        // past the chunk's last row: zeros
+        const Rows<Whole, R> rows{(int)min((long)R, (last - m + high - 1) / high), at, p.n};
+        float g[R][V], a[R][V], u[R][V];
+        read_rows(rows, p.grad + m * p.grad_row, high * p.grad_row, g);
+        if (p.s != nullptr) {
+            const long zr = m * p.n * H, step = (long)high * p.n * H;
+            read_rows(rows, p.z + zr, step, a);
+            if constexpr (Gated) read_rows(rows, p.z + zr + p.n, step, u);
+            with_act(p.act, [&](auto is) {
+                float f, d1, d2;
 #pragma unroll
-        for (int q = 0; q < V; ++q) v.v[q] = f.v[q];
-        return v;
-    };
-    for (long m0 = at < p.n ? first + ty : last; m0 < last; m0 += Rows * high) {
-        ActRow<Gated> rows[Rows];
-#pragma unroll
-        for (int i = 0; i < Rows; ++i) {
-            const long m = min(m0 + (long)i * high, last - 1);      // past the last row: the last again, not used
-            rows[i].g = read(p.grad + m * p.grad_row);
-            if (p.s != nullptr) {
-                rows[i].a = read(p.z + m * p.n * H);
-                if constexpr (Gated) rows[i].b = read(p.z + m * p.n * H + p.n);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < Rows; ++i) {
-            const long m = m0 + (long)i * high;
-            if (m >= last) break;
-            Values g = values(rows[i].g), u{};
-            if (p.s != nullptr) {
-                const Values a = values(rows[i].a);
-                Values b{};
-                if constexpr (Gated) b = values(rows[i].b);
-                with_act(p.act, [&](auto is) {
-                    float f, d1, d2;
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
-                        activation<decltype(is)::value>(a.v[q], f, d1, d2);
+                        activation<decltype(is)::value>(a[i][q], f, d1, d2);
                         if constexpr (Gated) {
-                            u.v[q] = g.v[q] * f;
-                            g.v[q] = g.v[q] * b.v[q] * d1;
+                            const float b = u[i][q];
+                            u[i][q] = g[i][q] * f;
+                            g[i][q] = g[i][q] * b * d1;
                         } else {
-                            g.v[q] *= d1;
+                            g[i][q] *= d1;
                         }
                     }
-                });
-                T* to = p.s + m * p.n * H;
-                write_values<Whole>(to, at, p.n, g.v);
-                if constexpr (Gated) write_values<Whole>(to + p.n, at, p.n, u.v);
-            }
+            });
+            write_rows(rows, p.s + zr, step, g);
+            if constexpr (Gated) write_rows(rows, p.s + zr + p.n, step, u);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                sum[0].v[q] += g.v[q];
-                if constexpr (Gated) sum[1].v[q] += u.v[q];
+                if (i >= rows.some) continue;
+                sum[0][q] += g[i][q];
+                if constexpr (Gated) sum[1][q] += u[i][q];
             }
-        }
     }
     if (p.sums == nullptr) return;
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int q = 0; q < V; ++q) part[((h * high + ty) * V + q) * p.across + tx] = sum[h].v[q];
+        for (int q = 0; q < V; ++q) part[((h * high + ty) * V + q) * p.across + tx] = sum[h][q];
     lds_barrier();
     // value i of the workgroup's across * V columns, summed over its rows in order
     for (int i = threadIdx.x; i < H * V * p.across; i += 256) {
@@ -631,6 +792,20 @@ bool direct(const Gemm& g) {
     return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m) && whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n);
 }
 
+#if CTP_DENSE_TYPE == 0
+template <int Blocks, bool AlongB, bool Pairs, class Epi>
+hipError_t run_rows(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
+    // columns are cut into groups where the rows alone would leave the card empty
+    const long cols = Pairs ? 32 : 64, tiles = div_up(g.n, cols), rows = div_up(g.m, 128) * batches;
+    const long groups = max(1L, min(tiles, div_up(4 * kFill, rows)));
+    const long per = div_up(tiles, groups);
+    if (!set_tiles(g, 128, per * cols, batches)) return hipErrorInvalidValue;
+    if (g.total > max_groups(256)) return hipErrorInvalidValue;
+    k_rows<Blocks, AlongB, Pairs><<<dim3(g.total), 256, 0, st>>>(g, epi, (unsigned)per);
+    return hipGetLastError();
+}
+#endif
+
 // Tiles of 256 reuse an operand most, and are taken where they fill the card; tiles of 64 are for what has too few of
 // the others.
 template <bool AlongA, bool AlongB, bool Pairs, class Epi>
@@ -642,6 +817,15 @@ hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t 
             if (div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
         }
     }
+#if CTP_DENSE_TYPE == 0
+    if constexpr (AlongA) {
+        // many columns for few terms: 83325 x 64 -> 1024 takes 94 us so and 135 us in tiles of 64, -> 256 30 and 33
+        if (g.splits == 1 && div_up(g.m, 128) * outer * div_up(n, 64) >= kFill) {
+            if (g.k <= 64 && n >= 256) return run_rows<1, AlongB, Pairs>(g, outer, epi, st);
+            if (g.k <= 128 && n >= 512) return run_rows<2, AlongB, Pairs>(g, outer, epi, st);
+        }
+    }
+#endif
     if (g.m > 64 && n > 64 && g.k > 256 && div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 2)
         return run_staged<AlongA, AlongB, 128, 128, 2, Pairs>(g, outer, epi, st);
     return run_staged<AlongA, AlongB, 64, Pairs ? 128 : 64, 2, Pairs>(g, outer, epi, st);
@@ -766,7 +950,7 @@ hipError_t input_gradient(const LinearArgs& a, const T* s, long s_row, void* out
     g.m = a.n_rows;
     g.n = a.inner;
     g.k = (long)a.outer * (a.gated ? 2 : 1);
-    return run_gemm<true, false>(g, comps, EpiPlain{static_cast<T*>(out), (long)comps * a.inner, a.inner}, st);
+    return run_gemm<true, false>(g, comps, EpiPlain{static_cast<T*>(out), (long)comps * a.inner, a.inner, streams_out(a.n_rows * comps * a.inner * (long)sizeof(T))}, st);
 }
 
 // The parts of s^T x over the rows (direct: d_w itself).
@@ -786,7 +970,7 @@ hipError_t weight_gradient(const LinearArgs& a, const T* s, long s_row, const T*
     g.k = a.n_rows;
     g.splits = c.splits;
     g.k_split = c.k_split;
-    if (c.direct) return run_tiles<false, false, false>(g, 1, EpiPlain{d_w, a.inner, a.inner}, st);
+    if (c.direct) return run_tiles<false, false, false>(g, 1, EpiPlain{d_w, a.inner, a.inner, false}, st);
     return run_tiles<false, false, false>(g, comps * c.splits, EpiPart{parts, out * a.inner, a.inner}, st);
 }
 
@@ -821,13 +1005,14 @@ hipError_t join(const Join& a, const Join& b, hipStream_t st) {
 hipError_t fwd(const LinearArgs& a, hipStream_t st) {
     const int comps = (a.lmax + 1) * (a.lmax + 1);
     const Gemm g = forward_product(a, static_cast<const T*>(a.x), a.x_stride);
-    if (a.gated)
-        return run_pairs(g, EpiGated{static_cast<T*>(a.y), static_cast<T*>(a.z_out), static_cast<const T*>(a.bias), a.outer, a.act}, st);
-    return run_gemm<true, true>(g, comps,
-                                EpiLinear{static_cast<T*>(a.y), static_cast<T*>(a.z_out), static_cast<const T*>(a.bias),
-                                          static_cast<const T*>(a.residual), (long)comps * a.outer, a.residual_stride,
-                                          a.outer, a.act},
-                                st);
+    T *y = static_cast<T*>(a.y), *z = static_cast<T*>(a.z_out);
+    const T *bias = static_cast<const T*>(a.bias), *residual = static_cast<const T*>(a.residual);
+    const long row = (long)comps * a.outer;
+    const bool stream = streams_out(a.n_rows * row * (long)sizeof(T) * (1 + (z ? a.gated ? 2 : 1 : 0)));
+    if (a.gated) return run_pairs(g, EpiGated{y, z, bias, a.outer, a.act, stream}, st);
+    // without anything to do the epilogue's questions cost a layer that writes much (83325 x 64 -> 4352: 408 instead of 340 us) a sixth of its time
+    if (!z && !bias && !residual && a.act == kActNone) return run_gemm<true, true>(g, comps, EpiPlain{y, row, a.outer, stream}, st);
+    return run_gemm<true, true>(g, comps, EpiLinear{y, z, bias, residual, row, a.residual_stride, a.outer, a.act, stream}, st);
 }
 
 hipError_t bwd(const LinearArgs& a, hipStream_t st) {
@@ -864,7 +1049,7 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
     const Gemm v = forward_product(a, u, (long)comps * a.inner);
     const WeightCut c = weight_cut(a, act);
     if (!act) {
-        if (a.g_grad) CTP_TRY((run_gemm<true, true>(v, comps, EpiPlain{static_cast<T*>(a.g_grad), (long)comps * a.outer, a.outer}, st)));
+        if (a.g_grad) CTP_TRY((run_gemm<true, true>(v, comps, EpiPlain{static_cast<T*>(a.g_grad), (long)comps * a.outer, a.outer, false}, st)));
         if (a.g_w == nullptr) return hipSuccess;
         CTP_TRY(weight_gradient(a, grad, a.grad_stride, u, (long)comps * a.inner, c, parts, static_cast<T*>(a.g_w), st));
         return c.direct ? hipSuccess : join(join_of(parts, a.g_w, out * a.inner, a.lmax + 1, c.splits), Join{}, st);
