@@ -54,9 +54,7 @@ __device__ __forceinline__ f32x16 mfma(Frag<_Float16>::type a, Frag<_Float16>::t
 // part.  Along: [row][k]; the 16-byte chunks of a row trade places by the row, so
 // that the 16 rows that one clock of a b128 read takes lie in all 64 banks.
 // Across: [k][row]; units of 16 values trade places by k, for the transposing
-// reads, of which a clock takes two units of four values of k each.  (With the
-// places traded for 32 banks half of LDS's clocks were conflicts, and products of
-// 8192 x 16384 x 2048 bf16 took @@.)
+// reads, of which a clock takes two units of four values of k each.
 template <class E, int Parts_, bool Along, int Rows, int Depth>
 struct Tile {
     static constexpr int kPlane = Rows * Depth;     // elements
@@ -219,26 +217,42 @@ __device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i
     wave_lds_fence();
 }
 
+// f(Is<0>{}), .., f(Is<N - 1>{}): a loop that is unrolled whatever its body's size.
+template <int N>
+struct Is {
+    static constexpr int value = N;
+};
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+        f(Is<I>{});
+        each<N, I + 1>(f);
+    }
+}
+
 template <int V, bool Pairs, int MT, int NT, class F>
 __device__ __forceinline__ void by_rows(const f32x16 (&acc)[NT][MT], float* slab, int lane, F&& f) {
-    constexpr int kCols = 32 * NT / (Pairs ? 2 : 1), kLanes = kCols / V, kRows = 64 / kLanes, R = 32 / kRows;
+    // B rows at once: one where the results themselves take half of the registers
+    constexpr int kCols = 32 * NT / (Pairs ? 2 : 1), kLanes = kCols / V, kRows = 64 / kLanes, R = 32 / kRows, B = MT > 2 ? 1 : R;
     static_assert(!Pairs || NT % 2 == 0);
     const int n = lane % kLanes * V;
+    each<MT>([&](auto i) {
+        by_rows_block(acc, decltype(i)::value, slab, lane);
+#pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += B) {
+            float x[B][V], y[B][V];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        by_rows_block(acc, i, slab, lane);
-        float x[R][V], y[R][V];
+            for (int r = 0; r < B; ++r) {
+                const float* from = slab + ((r0 + r) * kRows + lane / kLanes) * kSlab<NT> + (Pairs ? n / 32 * 64 + n % 32 : n);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float* from = slab + (r * kRows + lane / kLanes) * kSlab<NT> + (Pairs ? n / 32 * 64 + n % 32 : n);
-#pragma unroll
-            for (int q = 0; q < V; q += 4) {
-                *reinterpret_cast<f32x4*>(x[r] + q) = *reinterpret_cast<const f32x4*>(from + q);
-                if constexpr (Pairs) *reinterpret_cast<f32x4*>(y[r] + q) = *reinterpret_cast<const f32x4*>(from + 32 + q);
+                for (int q = 0; q < V; q += 4) {
+                    *reinterpret_cast<f32x4*>(x[r] + q) = *reinterpret_cast<const f32x4*>(from + q);
+                    if constexpr (Pairs) *reinterpret_cast<f32x4*>(y[r] + q) = *reinterpret_cast<const f32x4*>(from + 32 + q);
+                }
             }
+            f(32 * decltype(i)::value + r0 * kRows + lane / kLanes, kRows, n, x, y);
         }
-        f(32 * i + lane / kLanes, kRows, n, x, y);
-    }
+    });
 }
 
 // Where workgroup `id` of `total` works: the workgroups of one of the 8 XCDs, which get every eighth, take
@@ -312,20 +326,16 @@ __device__ __forceinline__ void activation(float z, float& f, float& d1, float& 
     }
 }
 
-// Calls f(integral constant) for an activation: one branch for all values that f goes through.
-template <int N>
-struct ActIs {
-    static constexpr int value = N;
-};
+// Calls f(Is<act>{}): one branch for all values that f goes through.
 template <class F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        case kActRelu: f(ActIs<kActRelu>{}); break;
-        case kActSilu: f(ActIs<kActSilu>{}); break;
-        case kActGelu: f(ActIs<kActGelu>{}); break;
-        case kActSigmoid: f(ActIs<kActSigmoid>{}); break;
-        case kActTanh: f(ActIs<kActTanh>{}); break;
-        default: f(ActIs<kActNone>{}); break;
+        case kActRelu: f(Is<kActRelu>{}); break;
+        case kActSilu: f(Is<kActSilu>{}); break;
+        case kActGelu: f(Is<kActGelu>{}); break;
+        case kActSigmoid: f(Is<kActSigmoid>{}); break;
+        case kActTanh: f(Is<kActTanh>{}); break;
+        default: f(Is<kActNone>{}); break;
     }
 }
 

@@ -14,6 +14,8 @@
 #include "dense_direct.hpp"
 #include "dense_linear.hpp"
 
+#include <type_traits>
+
 namespace ctp {
 namespace {
 
@@ -396,14 +398,18 @@ struct EpiSecond {
 // more than the products: a wave keeps 32 rows of A in registers, taken apart once, and goes through the columns, 64
 // (Pairs: 32 and their partners) at a time, whose parts the workgroup's waves share in LDS.  Results go from the matrix
 // cores' registers to memory, 16 bytes a lane.
+template <class Epi>
+constexpr bool kIsPlain = std::is_same<Epi, EpiPlain>::value;
+
 template <int Blocks, bool AlongB, bool Pairs, class Epi>
-__global__ __launch_bounds__(256, Blocks == 1 ? 3 : 2) void k_rows(Gemm g, Epi epi, unsigned tiles_a_group) {
+__global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> ? 3 : 2) void k_rows(Gemm g, Epi epi, unsigned tiles_a_group) {
     constexpr int kLong = 64 * Blocks, kCols = Pairs ? 32 : 64;
     typedef Staged<T, AlongB, 64, kLong, 256> SB;
     typedef typename SB::tile_t TB;
     typedef typename Frag<E>::type frag_t;
     __shared__ __attribute__((aligned(16))) char lds[TB::kBytes];
-    __shared__ __attribute__((aligned(16))) float slabs[4][32 * kSlab<1>];
+    constexpr int kWide = kSlab<Pairs ? 2 : 1>;
+    __shared__ __attribute__((aligned(16))) float slabs[4][32 * kWide];
     E* lb = reinterpret_cast<E*>(lds);
     float* slab = slabs[threadIdx.x >> 6];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -476,30 +482,37 @@ __global__ __launch_bounds__(256, Blocks == 1 ? 3 : 2) void k_rows(Gemm g, Epi e
         const long m0 = (long)t.m * 128 + wave * 32;
         auto write = [&](auto whole) {
             constexpr bool Whole = decltype(whole)::value != 0;
-            float x[4][4], y[4][4];
+            constexpr int B = kIsPlain<Epi> ? 4 : 1;       // rows of a lane at once
             const int nc = lane % 8 * 4;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                wave_lds_fence();
+                if (!Pairs || j == 0) wave_lds_fence();
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<f32x4*>(slab + (lane & 31) * kSlab<1> + 8 * q + 4 * (lane >> 5)) =
+                    *reinterpret_cast<f32x4*>(slab + (lane & 31) * kWide + (Pairs ? 32 * j : 0) + 8 * q + 4 * (lane >> 5)) =
                         f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
-                wave_lds_fence();
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<f32x4*>((Pairs && j ? y : x)[r]) = *reinterpret_cast<const f32x4*>(slab + (8 * r + lane / 8) * kSlab<1> + nc);
                 if (Pairs && j == 0) continue;
+                wave_lds_fence();
                 const int n = n0 + nc + (Pairs ? 0 : 32 * j);
-                const long m = m0 + lane / 8;
-                const int some = Whole || n < g.n ? (int)min(4L, (g.m - m + 7) / 8) : 0;
-                if (Whole || some > 0) epi.template run<Whole>(Place{batch, batch, m, 8, some, n}, x, y);
+#pragma unroll 1
+                for (int r0 = 0; r0 < 4; r0 += B) {
+                    float x[B][4], y[B][4];
+#pragma unroll
+                    for (int r = 0; r < B; ++r) {
+                        const float* from = slab + (8 * (r0 + r) + lane / 8) * kWide + nc;
+                        *reinterpret_cast<f32x4*>(x[r]) = *reinterpret_cast<const f32x4*>(from);
+                        if constexpr (Pairs) *reinterpret_cast<f32x4*>(y[r]) = *reinterpret_cast<const f32x4*>(from + 32);
+                    }
+                    const long m = m0 + 8 * r0 + lane / 8;
+                    const int some = Whole || n < g.n ? (int)min((long)B, (g.m - m + 7) / 8) : 0;
+                    if (Whole || some > 0) epi.template run<Whole>(Place{batch, batch, m, 8, some, n}, x, y);
+                }
             }
         };
         if (n0 + kCols <= g.n && m0 + 32 <= g.m)
-            write(ActIs<1>{});
+            write(Is<1>{});
         else
-            write(ActIs<0>{});
+            write(Is<0>{});
     }
 }
 #endif
@@ -650,7 +663,7 @@ __device__ __forceinline__ void write_rows(const Rows<Whole, R>& rows, T* to, lo
 // Whole: n is whole vectors.
 template <bool Gated, bool Whole>
 __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
-    constexpr int H = Gated ? 2 : 1, R = 4;     // rows that a lane reads at once
+    constexpr int H = Gated ? 2 : 1, R = Gated ? 2 : 4;      // rows that a lane reads at once
     __shared__ float part[256 * H * V];
     const int tx = threadIdx.x % p.across, ty = threadIdx.x / p.across, high = 256 / p.across;
     const int at = (blockIdx.x * p.across + tx) * V;
@@ -835,8 +848,8 @@ template <int MB, bool Pairs, class Epi>
 hipError_t run_few(const Gemm& g, unsigned batches, const Epi& epi, hipStream_t st) {
     const unsigned groups = (unsigned)div_up(g.n, Pairs ? 16 : 32);
     // more shares of k where few columns would leave the card empty
-    if ((long)groups * batches < kFill / 2 && g.k >= 8 * (4 / MB) * 8 * V)
-        k_few<MB, 16, Pairs><<<dim3(groups, batches), 64 * 16, 0, st>>>(g, epi);
+    if ((long)groups * batches < kFill / 2 && g.k >= 4 * (4 / MB) * 8 * V)
+        k_few<MB, 8, Pairs><<<dim3(groups, batches), 64 * 8, 0, st>>>(g, epi);
     else
         k_few<MB, 4, Pairs><<<dim3(groups, batches), 64 * 4, 0, st>>>(g, epi);
     return hipGetLastError();
