@@ -91,6 +91,90 @@ struct Tile {
     }
 };
 
+// f(Is<0>{}), .., f(Is<N - 1>{}): a loop that is unrolled whatever its body's size.
+template <int N>
+struct Is {
+    static constexpr int value = N;
+};
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+        f(Is<I>{});
+        each<N, I + 1>(f);
+    }
+}
+
+// ---------------------------------------------------------------- activations
+
+// exp(x) for x <= 0 and 1 / d for d >= 1, each off by some two roundings: the product with log2(e) is carried in
+// two floats, and one Newton step follows the hardware's reciprocal.  (expf and a division are three times the
+// instructions, which a layer's epilogue does not hide.)
+__device__ __forceinline__ float exp_falling(float x) {
+    x = x < -104.0f ? -104.0f : x;      // exp(-104) is below every float; NaN stays
+    const float t = x * 1.44269502f, rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
+    const float y = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(y, rest * 0.693147181f, y);
+}
+__device__ __forceinline__ float one_over(float d) {
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
+// act(z), its first and its second derivative.
+template <int Act_>
+__device__ __forceinline__ void activation(float z, float& f, float& d1, float& d2) {
+    if constexpr (Act_ == kActRelu) {
+        f = z > 0.0f ? z : (z != z ? z : 0.0f);
+        d1 = z > 0.0f ? 1.0f : 0.0f;
+        d2 = 0.0f;
+    } else if constexpr (Act_ == kActSilu || Act_ == kActSigmoid) {
+        // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
+        const float e = exp_falling(-fabsf(z)), large = one_over(1.0f + e), small = e * large;
+        const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
+        if constexpr (Act_ == kActSigmoid) {
+            f = s, d1 = t, d2 = t * u;
+        } else {
+            f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
+        }
+    } else if constexpr (Act_ == kActGelu) {
+        // Phi(-|z|) = exp(-z^2 / 2) times a function that a polynomial in t = 1 / (1 + 0.4 |z| / sqrt(2)) follows to
+        // 1.3 2^-23 of it (least squares at Chebyshev points, reweighted to even out the error), 4.4e-7 with the
+        // evaluation's roundings; erfcf is four times the instructions.  Past 42 the exponential is zero anyway.
+        const float g = exp_falling(-0.5f * z * z), t = one_over(__builtin_fmaf(0.28284271f, fminf(fabsf(z), 42.0f), 1.0f));
+        constexpr float kPoly[9] = {0.22567586600780487f, 0.22566959261894226f, 0.20784272253513336f, 0.1685418039560318f,
+                                    0.14143219590187073f, -0.005609337240457535f, 0.169087752699852f, -0.1829030066728592f,
+                                    0.050262536853551865f};
+        float q = kPoly[8];
+#pragma unroll
+        for (int k = 7; k >= 0; --k) q = __builtin_fmaf(q, t, kPoly[k]);
+        q *= 0.5f * t * g;
+        const float c = z < 0.0f ? q : 1.0f - q, p = 0.39894228040143268f * g;
+        f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
+    } else if constexpr (Act_ == kActTanh) {
+        const float e = exp_falling(-2.0f * fabsf(z)), r = one_over(1.0f + e);
+        f = tanhf(z);
+        d1 = 4.0f * e * r * r;
+        d2 = -2.0f * f * d1;
+    } else {
+        f = z, d1 = 1.0f, d2 = 0.0f;
+    }
+}
+
+// Calls f(Is<act>{}): one branch for all values that f goes through.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    switch (act) {
+        case kActRelu: f(Is<kActRelu>{}); break;
+        case kActSilu: f(Is<kActSilu>{}); break;
+        case kActGelu: f(Is<kActGelu>{}); break;
+        case kActSigmoid: f(Is<kActSigmoid>{}); break;
+        case kActTanh: f(Is<kActTanh>{}); break;
+        default: f(Is<kActNone>{}); break;
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+
 // x = p[0] + p[1] + p[2].
 struct ThreeParts {
     __bf16 p[3];
@@ -136,6 +220,28 @@ struct Staged {
                 v[i] = vec_t<T>{};
             }
         }
+    }
+
+    // Every value times act'(z).
+    __device__ __forceinline__ void curve(const Staged& z, int act) {
+        with_act(act, [&](auto is) {
+            float f, d1, d2;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                for (int q = 0; q < kVec<T>; ++q) {
+                    activation<decltype(is)::value>((float)z.v[i][q], f, d1, d2);
+                    v[i][q] = (T)((float)v[i][q] * d1);
+                }
+        });
+    }
+    // Across: adds to the sums of the thread's columns, which are the same for all of its vectors.
+    __device__ __forceinline__ void add_columns(float (&sum)[kVec<T>]) const {
+        static_assert(Along || Threads % kPerRow == 0);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int q = 0; q < kVec<T>; ++q) sum[q] += (float)v[i][q];
     }
 
     __device__ __forceinline__ void store(E* lds) const {
@@ -217,19 +323,6 @@ __device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i
     wave_lds_fence();
 }
 
-// f(Is<0>{}), .., f(Is<N - 1>{}): a loop that is unrolled whatever its body's size.
-template <int N>
-struct Is {
-    static constexpr int value = N;
-};
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void each(F&& f) {
-    if constexpr (I < N) {
-        f(Is<I>{});
-        each<N, I + 1>(f);
-    }
-}
-
 template <int V, bool Pairs, int MT, int NT, class F>
 __device__ __forceinline__ void by_rows(const f32x16 (&acc)[NT][MT], float* slab, int lane, F&& f) {
     // B rows at once: one where the results themselves take half of the registers
@@ -279,64 +372,6 @@ __device__ __forceinline__ TileAt tile_at(unsigned id, unsigned tiles_m, unsigne
     t.m = first + id % rows;
     t.n = id / rows;
     return t;
-}
-
-// ---------------------------------------------------------------- activations
-
-// exp(x) for x <= 0 and 1 / d for 1 <= d <= 2, each off by some two roundings: the product with log2(e) is carried in
-// two floats, and one Newton step follows the hardware's reciprocal.  (expf and a division are three times the
-// instructions, which a layer's epilogue does not hide.)
-__device__ __forceinline__ float exp_falling(float x) {
-    x = x < -104.0f ? -104.0f : x;      // exp(-104) is below every float; NaN stays
-    const float t = x * 1.44269502f, rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269502f, -t));
-    const float y = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(y, rest * 0.693147181f, y);
-}
-__device__ __forceinline__ float one_over(float d) {
-    const float r = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-}
-
-// act(z), its first and its second derivative.
-template <int Act_>
-__device__ __forceinline__ void activation(float z, float& f, float& d1, float& d2) {
-    if constexpr (Act_ == kActRelu) {
-        f = z > 0.0f ? z : (z != z ? z : 0.0f);
-        d1 = z > 0.0f ? 1.0f : 0.0f;
-        d2 = 0.0f;
-    } else if constexpr (Act_ == kActSilu || Act_ == kActSigmoid) {
-        // from exp(-|z|): nothing overflows, and sigmoid and its complement keep their relative accuracy
-        const float e = exp_falling(-fabsf(z)), large = one_over(1.0f + e), small = e * large;
-        const float s = z >= 0.0f ? large : small, t = large * small, u = z >= 0.0f ? small - large : large - small;
-        if constexpr (Act_ == kActSigmoid) {
-            f = s, d1 = t, d2 = t * u;
-        } else {
-            f = z * s, d1 = __builtin_fmaf(z, t, s), d2 = t * __builtin_fmaf(z, u, 2.0f);
-        }
-    } else if constexpr (Act_ == kActGelu) {
-        const float c = 0.5f * erfcf(z * -0.70710678118654752f), p = 0.39894228040143268f * exp_falling(-0.5f * z * z);
-        f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
-    } else if constexpr (Act_ == kActTanh) {
-        const float e = exp_falling(-2.0f * fabsf(z)), r = one_over(1.0f + e);
-        f = tanhf(z);
-        d1 = 4.0f * e * r * r;
-        d2 = -2.0f * f * d1;
-    } else {
-        f = z, d1 = 1.0f, d2 = 0.0f;
-    }
-}
-
-// Calls f(Is<act>{}): one branch for all values that f goes through.
-template <class F>
-__device__ __forceinline__ void with_act(int act, F&& f) {
-    switch (act) {
-        case kActRelu: f(Is<kActRelu>{}); break;
-        case kActSilu: f(Is<kActSilu>{}); break;
-        case kActGelu: f(Is<kActGelu>{}); break;
-        case kActSigmoid: f(Is<kActSigmoid>{}); break;
-        case kActTanh: f(Is<kActTanh>{}); break;
-        default: f(Is<kActNone>{}); break;
-    }
 }
 
 // l of component d = l^2 .. l^2 + 2 l

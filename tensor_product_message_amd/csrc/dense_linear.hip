@@ -39,6 +39,8 @@ struct Gemm {
     int b_degree;
     long m, k;
     int n;                      // Pairs: columns of one half
+    long m_read;                // Across: values of a row of A, of B, that may be read, at least m, n
+    int n_read;
     long pair;                  // Pairs: elements of B from a column to its partner
     long k_split;               // k of a split, a multiple of kDepth
     unsigned splits, tiles_m, tiles_n, total;
@@ -129,21 +131,39 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[NT][MT], float* s
     }
 }
 
-// A tile of BM x BN by 4 waves, WM x (4 / WM) of them.  One buffer in LDS: the next tiles' reads are in flight in
-// registers while the matrix cores work, and the workgroups that share a CU fill each other's pauses.
-template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
-__global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
-    constexpr int WN = 4 / WM, MT = BM / 32 / WM, NT = BN / 32 / WN;
+// What a gradient's first operand is made of on its way into LDS: A times act'(z), z dense rows of z_ld values, and
+// (Across) the sums of A's columns over each split's k, parts of m values.
+struct Curve {
+    const T* z;
+    long z_ld;
+    int act;
+    float* sums;        // null: none
+};
+
+// Tiles of BM x BN by 4 waves, WM x (4 / WM) of them, the block-th of every `blocks`.  One buffer in LDS: the next
+// tiles' reads are in flight in registers while the matrix cores work, and the workgroups that share a CU fill each
+// other's pauses.
+template <bool AlongA, bool AlongB, int BM, int BN, int WM>
+struct StagedTiles {
+    static constexpr int WN = 4 / WM, MT = BM / 32 / WM, NT = BN / 32 / WN;
     typedef Staged<T, AlongA, BM, kDepth, 256> SA;
     typedef Staged<T, AlongB, BN, kDepth, 256> SB;
-    constexpr int kTiles = SA::tile_t::kBytes + SB::tile_t::kBytes, kSlabs = 4 * 32 * kSlab<NT> * 4;
-    __shared__ __attribute__((aligned(16))) char lds[kTiles > kSlabs ? kTiles : kSlabs];
+    static constexpr int kTiles = SA::tile_t::kBytes + SB::tile_t::kBytes, kSlabs = 4 * 32 * kSlab<NT> * 4;
+    static constexpr int kBytes = kTiles > kSlabs ? kTiles : kSlabs;
+};
+
+template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, bool Curved, bool Summed, class Epi>
+__device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, const Curve& c, char* lds, unsigned block, unsigned blocks) {
+    typedef StagedTiles<AlongA, AlongB, BM, BN, WM> S;
+    constexpr int MT = S::MT, NT = S::NT;
+    typedef typename S::SA SA;
+    typedef typename S::SB SB;
     E* la = reinterpret_cast<E*>(lds);
     E* lb = reinterpret_cast<E*>(lds + SA::tile_t::kBytes);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave % WM * 32 * MT, wn = wave / WM * 32 * NT;
 
-    for (unsigned id = blockIdx.x; id < g.total; id += gridDim.x) {
+    for (unsigned id = block; id < g.total; id += blocks) {
         const TileAt t = tile_at(xcd_order(id, g.total), g.tiles_m, g.tiles_n);
         const unsigned batch = t.outer / g.splits, split = t.outer % g.splits;
         const long m0 = (long)t.m * BM, k0 = split * g.k_split;
@@ -152,6 +172,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
         const T* a = g.a + batch * g.a_batch + (AlongA ? m0 * g.a_ld + k0 : k0 * g.a_ld + m0);
         const T* b = g.b + (g.b_degree ? degree_of(batch) : (int)batch) * g.b_batch +
                      (AlongB ? (long)n0 * g.b_ld + k0 : k0 * g.b_ld + n0);
+        const T* z = Curved ? c.z + (AlongA ? m0 * c.z_ld + k0 : k0 * c.z_ld + m0) : nullptr;
         const int m_left = (int)min((long)BM, g.m - m0), n_left = min(g.n - n0, BN);
         // rows past the last give results that nobody stores
         auto row_a = [&](int r) { return (long)min(r, m_left - 1); };
@@ -160,20 +181,28 @@ __global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
             return (long)min(r, n_left - 1);
         };
         const bool whole_m = m_left == BM, whole_n = n_left >= (Pairs ? BN / 2 : BN);
-        SA sa;
+        SA sa, sz;
         SB sb;
         auto load = [&](int k) {
-            if (k + kDepth <= k_end && (AlongA || whole_m) && (AlongB || whole_n)) {
-                sa.template load<true>(a, g.a_ld, m_left, k, k_end, row_a);
-                sb.template load<true>(b, g.b_ld, n_left, k, k_end, row_b);
-            } else {
-                sa.template load<false>(a, g.a_ld, m_left, k, k_end, row_a);
-                sb.template load<false>(b, g.b_ld, n_left, k, k_end, row_b);
-            }
+            auto read = [&](auto whole) {
+                constexpr bool Whole = decltype(whole)::value != 0;
+                sa.template load<Whole>(a, g.a_ld, m_left, k, k_end, row_a);
+                if constexpr (Curved) sz.template load<Whole>(z, c.z_ld, m_left, k, k_end, row_a);
+                sb.template load<Whole>(b, g.b_ld, n_left, k, k_end, row_b);
+            };
+            if (k + kDepth <= k_end && (AlongA || whole_m) && (AlongB || whole_n))
+                read(Is<1>{});
+            else
+                read(Is<0>{});
         };
+        const bool sums = Summed && c.sums != nullptr && t.n == 0 && batch == 0;
+        float sum[V] = {};
         f32x16 acc[NT][MT] = {};
         load(0);
         for (int k = 0; k < k_end; k += kDepth) {
+            if constexpr (Curved) sa.curve(sz, c.act);
+            if constexpr (Summed)
+                if (sums) sa.add_columns(sum);
             lds_barrier();
             sa.store(la);
             sb.store(lb);
@@ -185,7 +214,30 @@ __global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
         write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left, whole_m && whole_n, epi, t.outer, batch, m0, n0);
         lds_barrier();
+        if constexpr (Summed) {
+            if (sums) {
+                // the threads of a column, in their order
+                constexpr int kHigh = 256 / SA::kPerRow;
+                static_assert(kHigh * BM * 4 <= S::kBytes);
+                float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+                for (int q = 0; q < V; ++q) part[threadIdx.x / SA::kPerRow * BM + threadIdx.x % SA::kPerRow * V + q] = sum[q];
+                lds_barrier();
+                if ((int)threadIdx.x < m_left) {
+                    float s = 0.0f;
+                    for (int r = 0; r < kHigh; ++r) s += part[r * BM + threadIdx.x];
+                    c.sums[split * g.m + m0 + threadIdx.x] = s;
+                }
+                lds_barrier();
+            }
+        }
     }
+}
+
+template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Epi>
+__global__ __launch_bounds__(256, 2) void k_gemm(Gemm g, Epi epi) {
+    __shared__ __attribute__((aligned(16))) char lds[StagedTiles<AlongA, AlongB, BM, BN, WM>::kBytes];
+    staged_tiles<AlongA, AlongB, BM, BN, WM, Pairs, false, false>(g, epi, Curve{}, lds, blockIdx.x, gridDim.x);
 }
 
 // The same for operands of 16 bits whose rows begin on 16 bytes and are whole vectors long: memory to LDS without
@@ -224,8 +276,8 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
             const int k = step * kDepth;
             // Across: what lies past the last k is the buffer's end
             const long rows = min(k_end - k, kDepth) - 1;
-            const long a_left = AlongA ? 0x7ffffff0L : 2 * (rows * g.a_ld + m_left);
-            const long b_left = AlongB ? 0x7ffffff0L : 2 * (rows * g.b_ld + n_left);
+            const long a_left = AlongA ? 0x7ffffff0L : 2 * (rows * g.a_ld + min((long)Side, g.m_read - m0));
+            const long b_left = AlongB ? 0x7ffffff0L : 2 * (rows * g.b_ld + min(Side, g.n_read - n0));
             da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), (unsigned)min(a_left, 0x7ffffff0L)), base + buffer * kBuffer, k_end - k);
             db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), (unsigned)min(b_left, 0x7ffffff0L)),
                      base + buffer * kBuffer + TA::kBytes, k_end - k);
@@ -389,6 +441,55 @@ struct EpiSecond {
         }
     }
 };
+
+// ---------------------------------------------------------------- small layers' gradients
+
+// Both gradients of a layer whose matrices are small, in one launch: d_W's parts by the first workgroups, d_x by the
+// others, each forming s = grad act'(z) on its way (the layer is few tiles wide, so s is not formed often), and the
+// bias's sums beside d_W's.  Neither product fills the card by itself, and s is neither written nor read: the gradients
+// of 83325 rows of 64 -> 64 floats take 30 us so and 44 us in four launches.
+template <bool Curved>
+__global__ __launch_bounds__(256, 2) void k_small_bwd(Gemm of_w, EpiPart to_w, Gemm of_x, EpiPlain to_x, Curve c) {
+    typedef StagedTiles<false, false, 64, 64, 2> W;
+    typedef StagedTiles<true, false, 64, 64, 2> X;
+    __shared__ __attribute__((aligned(16))) char lds[W::kBytes > X::kBytes ? W::kBytes : X::kBytes];
+    if (blockIdx.x < of_w.total)
+        staged_tiles<false, false, 64, 64, 2, false, Curved, true>(of_w, to_w, c, lds, blockIdx.x, of_w.total);
+    else
+        staged_tiles<true, false, 64, 64, 2, false, Curved, false>(of_x, to_x, c, lds, blockIdx.x - of_w.total, of_x.total);
+}
+
+// ---------------------------------------------------------------- long sums, few tiles
+
+// The epilogue of a product whose k was cut: V columns of a row a thread, the parts summed in their order.  Pairs: a
+// row's halves lie beside each other.
+template <bool Pairs, class Epi>
+__global__ __launch_bounds__(256) void k_finish(const float* parts, unsigned splits, int m, int n, unsigned batches, Epi epi) {
+    const int vecs = (n + V - 1) / V, width = Pairs ? 2 * n : n;
+    const long size = (long)m * width, total = (long)batches * m * vecs;
+    for (long id = (long)blockIdx.x * 256 + threadIdx.x; id < total; id += 256L * gridDim.x) {
+        const int at = (int)(id % vecs) * V;
+        const long row = id / vecs;
+        const unsigned batch = (unsigned)(row / m);
+        const float* from = parts + batch * splits * size + row % m * width;
+        float x[1][V] = {}, y[1][V] = {};
+        auto add = [&](float (&sum)[1][V], const float* p) {
+#pragma unroll
+            for (int q = 0; q < V; q += 4)
+                if (at + q < n) {
+                    const vec_t<float> v = load_vec<float>(p, (at + q) / 4, n);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[0][q + e] += v[e];
+                }
+        };
+#pragma unroll 4
+        for (unsigned s = 0; s < splits; ++s) {
+            add(x, from + s * size);
+            if constexpr (Pairs) add(y, from + s * size + n);
+        }
+        epi.template run<false>(Place{batch, batch, row % m, 1, 1, at}, x, y);
+    }
+}
 
 // ---------------------------------------------------------------- floats, short sums
 
@@ -637,6 +738,7 @@ struct ActBwd {
     float* sums;        // null: none; [chunk][columns]
     long grad_row, rows, chunk;
     int n, act, across;
+    long s_row;         // elements from row to row of s; above what a row has: whole vectors, zeros past its end
 };
 
 // As the members of Rows, for rows whose columns are whole vectors but whose number is `some`.
@@ -675,7 +777,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
         float g[R][V], a[R][V], u[R][V];
         read_rows(rows, p.grad + m * p.grad_row, high * p.grad_row, g);
         if (p.s != nullptr) {
-            const long zr = m * p.n * H, step = (long)high * p.n * H;
+            const long zr = m * p.n * H, step = (long)high * p.n * H, sr = m * p.s_row, s_step = high * p.s_row;
             read_rows(rows, p.z + zr, step, a);
             if constexpr (Gated) read_rows(rows, p.z + zr + p.n, step, u);
             with_act(p.act, [&](auto is) {
@@ -694,8 +796,11 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
                         }
                     }
             });
-            write_rows(rows, p.s + zr, step, g);
-            if constexpr (Gated) write_rows(rows, p.s + zr + p.n, step, u);
+            if (!Gated && p.s_row > p.n)
+                write_rows(Rows<true, R>{rows.some, at, p.n}, p.s + sr, s_step, g);
+            else
+                write_rows(rows, p.s + sr, s_step, g);
+            if constexpr (Gated) write_rows(rows, p.s + sr + p.n, s_step, u);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -719,6 +824,31 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
         float s = 0.0f;
         for (int r = 0; r < high; ++r) s += part[((h * high + r) * V + c % V) * p.across + c / V];
         p.sums[(long)blockIdx.y * p.n * H + h * p.n + col] = s;
+    }
+}
+
+// Rows laid out for 16-byte pieces: to[i][j][0 .. padded) = from[i][j][0 .. width), zeros past the width and for
+// j >= there.  A few rows of which none begins on 16 bytes cost a product's tiles more than this pass: the gradients of
+// 5001 rows of 1003 -> 777 float16 take 75 us with it and 140 us without.
+struct Pack {
+    const T* from;
+    T* to;
+    long n_i, from_i, from_j;   // elements from i to i and from j to j
+    int n_j, there, width, padded;
+};
+
+__global__ __launch_bounds__(256) void k_pack(Pack first, Pack second, unsigned groups_first) {
+    const bool is_first = blockIdx.x < groups_first;
+    const Pack p = is_first ? first : second;
+    const unsigned group = is_first ? blockIdx.x : blockIdx.x - groups_first, groups = is_first ? groups_first : gridDim.x - groups_first;
+    const int vecs = p.padded / V;
+    const long total = p.n_i * p.n_j * vecs;
+    for (long id = (long)group * 256 + threadIdx.x; id < total; id += 256L * groups) {
+        const long row = id / vecs, i = row / p.n_j;
+        const int v = (int)(id % vecs), j = (int)(row % p.n_j);
+        vec_t<T> x{};
+        if (j < p.there && v * V < p.width) x = load_vec<T>(p.from + i * p.from_i + j * p.from_j, v, p.width);
+        *reinterpret_cast<vec_t<T>*>(p.to + id * V) = x;
     }
 }
 
@@ -765,6 +895,11 @@ __global__ __launch_bounds__(256) void k_join(Join first, Join second) {
 
 // ---------------------------------------------------------------- launches
 
+#define CTP_TRY(call)                                                 \
+    do {                                                              \
+        if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+    } while (0)
+
 constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
 constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 
@@ -802,7 +937,8 @@ bool direct(const Gemm& g) {
     const auto whole = [](const T* p, long ld, long batch, long n) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && batch % V == 0 && n % V == 0;
     };
-    return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m) && whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n);
+    return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m_read) &&
+           whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n_read);
 }
 
 #if CTP_DENSE_TYPE == 0
@@ -827,7 +963,7 @@ hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t 
     if constexpr (kParts == 1) {
         if (direct<AlongA, AlongB>(g)) {
             if (div_up(g.m, 256) * div_up(n, 256) * outer >= kFill * 3 / 8) return run_direct<AlongA, AlongB, 256, Pairs>(g, outer, epi, st);
-            if (div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
+            if (g.m > 64 && n > 64 && div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
         }
     }
 #if CTP_DENSE_TYPE == 0
@@ -855,26 +991,44 @@ hipError_t run_few(const Gemm& g, unsigned batches, const Epi& epi, hipStream_t 
     return hipGetLastError();
 }
 
-template <bool AlongA, bool AlongB, class Epi>
-hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
+// How many ways a product's k is cut: where its tiles leave the card empty and its sums are long.  64 rows of
+// 4096 -> 4096 bf16 take 17 us cut and 36 us whole.
+unsigned sum_cut(long m, long n, long k, long batches) {
+    // a part's terms, and the least of a sum that is cut: 256 x 1024 -> 1024 takes 11 us cut and 8 us whole in bf16, 14
+    // and 25 in floats
+    constexpr long kTerms = kParts == 1 ? 512 : 256, kLeast = kParts == 1 ? 2048 : 768;
+    const long tiles = div_up(m, 64) * div_up(n, 64) * batches;
+    if (k < kLeast) return 1;
+    return (unsigned)max(1L, min(kFill / max(1L, tiles), k / kTerms));
+}
+long sum_cut_bytes(long m, long n, long k, long batches) {
+    const long splits = sum_cut(m, n, k, batches);
+    return splits > 1 ? align256(splits * batches * m * n * 4) : 0;
+}
+
+template <bool AlongA, bool AlongB, bool Pairs, class Epi>
+hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, float* parts, hipStream_t st) {
     if (g.m == 0) return hipSuccess;
     g.splits = 1;
     g.k_split = div_up(g.k, kDepth) * kDepth;
     if constexpr (AlongB) {
-        if (g.m <= 16) return run_few<1, false>(g, batches, epi, st);
-        if (g.m <= 32) return run_few<2, false>(g, batches, epi, st);
+        if (g.m <= 16) return run_few<1, Pairs>(g, batches, epi, st);
+        if (g.m <= 32) return run_few<2, Pairs>(g, batches, epi, st);
     }
-    return run_tiles<AlongA, AlongB, false>(g, batches, epi, st);
+    const int n = g.n, width = Pairs ? 2 * n : n;
+    const unsigned splits = sum_cut(g.m, width, g.k, batches);
+    if (splits == 1) return run_tiles<AlongA, AlongB, Pairs>(g, batches, epi, st);
+    g.n = width;
+    g.k_split = div_up(div_up(g.k, splits), kDepth) * kDepth;
+    g.splits = (unsigned)div_up(g.k, g.k_split);
+    if (const hipError_t e = run_tiles<AlongA, AlongB, false>(g, batches * g.splits, EpiPart{parts, g.m * width, width}, st)) return e;
+    const long threads = batches * g.m * div_up(n, V);
+    k_finish<Pairs><<<dim3((unsigned)min(div_up(threads, 256), 4 * kFill)), 256, 0, st>>>(parts, g.splits, (int)g.m, n, batches, epi);
+    return hipGetLastError();
 }
-template <class Epi>
-hipError_t run_pairs(Gemm g, const Epi& epi, hipStream_t st) {
-    if (g.m == 0) return hipSuccess;
-    g.splits = 1;
-    g.k_split = div_up(g.k, kDepth) * kDepth;
-    if (g.m <= 16) return run_few<1, true>(g, 1, epi, st);
-    if (g.m <= 32) return run_few<2, true>(g, 1, epi, st);
-    return run_tiles<true, true, true>(g, 1, epi, st);
-}
+
+// Layers whose first gradients go through k_small_bwd.
+bool small_bwd(const LinearArgs& a) { return !a.gated && a.inner <= 128 && a.outer <= 128; }
 
 // How d_W[outer][inner] = sum over rows is cut: every component by itself, and its rows into `splits`.
 struct WeightCut {
@@ -885,10 +1039,11 @@ struct WeightCut {
 WeightCut weight_cut(const LinearArgs& a, bool twice) {
     const long comps = (long)(a.lmax + 1) * (a.lmax + 1), out = (long)a.outer * (a.gated ? 2 : 1);
     WeightCut c;
-    // large matrices fill the card by themselves
-    const bool wide = div_up(out, 128) * div_up(a.inner, 128) * comps >= kFill / 8 && a.inner > 64 && out > 64;
-    const long tile = wide ? 128 : 64, tiles = div_up(out, tile) * div_up(a.inner, tile) * comps;
-    long splits = max(1L, min(kFill / tiles, a.n_rows / (4 * kDepth)));
+    // tiles of 128 where they and the rows are enough for the card, else smaller ones in more parts
+    const long most = max(1L, a.n_rows / (4 * kDepth)), tiles128 = div_up(out, 128) * div_up(a.inner, 128) * comps;
+    const bool wide = tiles128 >= 32 && tiles128 * min(most, 16L) >= kFill / 2;
+    const long tiles = wide ? tiles128 : div_up(out, 64) * div_up(a.inner, 64) * comps;
+    long splits = max(1L, min((wide || small_bwd(a) ? kFill : 2 * kFill) / tiles, most));
     splits = max(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
     c.k_split = max(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
     c.splits = (unsigned)max(1L, div_up(a.n_rows, c.k_split));
@@ -915,81 +1070,151 @@ BiasCut bias_cut(long rows, int n) {
     return c;
 }
 
+// What of a layer is laid out anew for its products: 16-bit types in rows that are not whole 16-byte pieces, where the
+// products are large enough to win it back (measured in bf16: forward 8191 x 2047 -> 4099 188 us so and 249 without,
+// 5001 x 1003 -> 777 33 and 31; both gradients of the latter 85 and 125, of 20000 x 301 -> 301 58 and 57).
+struct Packs {
+    bool x, w, grad;        // grad: without an activation, where it is s itself
+    long inner, outer;      // a component's values then (outer: of s; a gated layer's two halves together)
+};
+Packs packs_of(const LinearArgs& a, bool bwd) {
+    const long out = (long)a.outer * (a.gated ? 2 : 1), comps = (long)(a.lmax + 1) * (a.lmax + 1);
+    Packs p{false, false, false, a.inner, out};
+    const double flops = 2.0 * a.n_rows * comps * a.inner * out;
+    if (kParts != 1 || a.n_rows <= 32 || flops < (bwd ? 6e9 : 2e10) || (bwd && (small_bwd(a) || (a.gated && out % V != 0)))) return p;
+    const bool inner = a.inner % V != 0, outer = bwd && out % V != 0, curved = a.act != kActNone || a.gated;
+    p.x = inner || a.x_stride % V != 0;
+    p.w = inner || outer;
+    p.grad = bwd && !curved && (outer || a.grad_stride % V != 0);
+    p.inner = div_up(a.inner, V) * V;
+    if (bwd) p.outer = div_up(out, V) * V;
+    return p;
+}
+
 struct Layout {
-    long s, g_z, sums, parts, bytes;
+    long x, w, s, g_z, sums, parts, bytes;
 };
 Layout layout_of(const LinearArgs& a, bool second) {
-    const long z_bytes = align256(a.n_rows * a.outer * (a.gated ? 2 : 1) * (long)sizeof(T));
-    const bool act = a.act != kActNone || a.gated;
     const long out = (long)a.outer * (a.gated ? 2 : 1), comps = (long)(a.lmax + 1) * (a.lmax + 1);
+    const Packs p = second ? Packs{false, false, false, a.inner, out} : packs_of(a, true);
+    const bool act = a.act != kActNone || a.gated;
+    const long s_bytes = act || p.grad ? align256(a.n_rows * comps * p.outer * (long)sizeof(T)) : 0;
     const WeightCut w = weight_cut(a, second && act);
     const BiasCut b = bias_cut(a.n_rows, a.outer);
     Layout y;
-    y.s = 0;
-    y.g_z = act ? z_bytes : 0;
-    y.sums = y.g_z + (act && second ? z_bytes : 0);
-    y.parts = y.sums + align256(b.chunks * out * 4);
-    y.bytes = y.parts + (w.direct ? 0 : align256(w.splits * comps * out * a.inner * 4 * (second && act ? 2 : 1)));
+    y.x = 0;
+    y.w = p.x ? align256(a.n_rows * comps * p.inner * (long)sizeof(T)) : 0;
+    y.s = y.w + (p.w ? align256((a.lmax + 1) * p.outer * p.inner * (long)sizeof(T)) : 0);
+    y.g_z = y.s + s_bytes;
+    y.sums = y.g_z + (second ? s_bytes : 0);
+    y.parts = y.sums + align256(max(b.chunks, w.splits) * out * 4);
+    // one product's parts at a time
+    const bool small = small_bwd(a) && !second;
+    long parts = w.direct && !small ? 0 : align256(w.splits * comps * out * a.inner * 4 * (second && act ? 2 : 1));
+    parts = max(parts, sum_cut_bytes(a.n_rows, a.inner, p.outer, comps));
+    if (second) parts = max(parts, sum_cut_bytes(a.n_rows, out, a.inner, comps));
+    y.bytes = y.parts + parts;
     return y;
 }
 
-Gemm forward_product(const LinearArgs& a, const T* x, long x_row) {
+Pack rows_pack(const T* from, long row, long n_rows, int comps, int width, long padded, T* to) {
+    return Pack{from, to, n_rows, row, width, comps, comps, width, (int)padded};
+}
+// [degrees][outer][inner] to [degrees][padded outer][padded inner]
+Pack weight_pack(const LinearArgs& a, long outer, long inner, T* to) {
+    const int out = a.outer * (a.gated ? 2 : 1);
+    return Pack{static_cast<const T*>(a.w), to, a.lmax + 1, (long)out * a.inner, a.inner, (int)outer, out, a.inner, (int)inner};
+}
+hipError_t pack(const Pack& a, const Pack& b, hipStream_t st) {
+    const auto groups = [](const Pack& p) { return p.to ? (unsigned)min(div_up(p.n_i * p.n_j * (p.padded / V), 256), 8 * kFill) : 0; };
+    if (groups(a) + groups(b) == 0) return hipSuccess;
+    k_pack<<<groups(a) + groups(b), 256, 0, st>>>(a, b, groups(a));
+    return hipGetLastError();
+}
+
+// A layer's operands as a product reads them: rows of components one after the other, matrices of the degrees.
+struct Operand {
+    const T* p;
+    long row, part;     // elements from row to row, from component to component (w: from degree to degree)
+    long width;         // values of a component that may be read, zeros past those that are there
+};
+Operand input_of(const LinearArgs& a, const void* x, long row) { return Operand{static_cast<const T*>(x), row, a.inner, a.inner}; }
+Operand weight_of(const LinearArgs& a) {
+    return Operand{static_cast<const T*>(a.w), a.inner, (long)a.outer * (a.gated ? 2 : 1) * a.inner, a.inner};
+}
+
+Gemm forward_product(const LinearArgs& a, const Operand& x, const Operand& w) {
     Gemm g{};
-    g.a = x;
-    g.a_ld = x_row;
-    g.a_batch = a.inner;
-    g.b = static_cast<const T*>(a.w);
-    g.b_ld = a.inner;
+    g.a = x.p;
+    g.a_ld = x.row;
+    g.a_batch = x.part;
+    g.b = w.p;
+    g.b_ld = w.row;
     g.b_degree = 1;
-    g.b_batch = (long)a.outer * a.inner;
-    g.m = a.n_rows;
-    g.n = a.outer;
-    g.k = a.inner;
+    g.b_batch = w.part;
+    g.m = g.m_read = a.n_rows;
+    g.n = g.n_read = a.outer;
+    g.k = x.width;
     g.pair = a.outer;
     return g;
 }
 
 // out[row][inner] = s W
-hipError_t input_gradient(const LinearArgs& a, const T* s, long s_row, void* out, hipStream_t st) {
-    const int comps = (a.lmax + 1) * (a.lmax + 1);
+Gemm input_product(const LinearArgs& a, const Operand& s, const Operand& w) {
     Gemm g{};
-    g.a = s;
-    g.a_ld = s_row;
-    g.a_batch = a.outer;
-    g.b = static_cast<const T*>(a.w);
-    g.b_ld = a.inner;
+    g.a = s.p;
+    g.a_ld = s.row;
+    g.a_batch = s.part;
+    g.b = w.p;
+    g.b_ld = w.row;
     g.b_degree = 1;
-    g.b_batch = (long)a.outer * a.inner;
-    g.m = a.n_rows;
+    g.b_batch = w.part;
+    g.m = g.m_read = a.n_rows;
     g.n = a.inner;
-    g.k = (long)a.outer * (a.gated ? 2 : 1);
-    return run_gemm<true, false>(g, comps, EpiPlain{static_cast<T*>(out), (long)comps * a.inner, a.inner, streams_out(a.n_rows * comps * a.inner * (long)sizeof(T))}, st);
+    g.n_read = (int)w.width;
+    g.k = s.width;
+    return g;
+}
+EpiPlain input_epilogue(const LinearArgs& a, void* out) {
+    const long row = (long)(a.lmax + 1) * (a.lmax + 1) * a.inner;
+    return EpiPlain{static_cast<T*>(out), row, a.inner, streams_out(a.n_rows * row * (long)sizeof(T))};
+}
+hipError_t input_gradient(const LinearArgs& a, const Operand& s, const Operand& w, void* out, float* parts, hipStream_t st) {
+    return run_gemm<true, false, false>(input_product(a, s, w), (a.lmax + 1) * (a.lmax + 1), input_epilogue(a, out), parts, st);
 }
 
-// The parts of s^T x over the rows (direct: d_w itself).
-hipError_t weight_gradient(const LinearArgs& a, const T* s, long s_row, const T* x, long x_row, const WeightCut& c,
-                           float* parts, T* d_w, hipStream_t st) {
-    const unsigned comps = (a.lmax + 1) * (a.lmax + 1);
-    const long out = (long)a.outer * (a.gated ? 2 : 1);
+// s^T x over the rows, in the parts of a cut.
+Gemm weight_product(const LinearArgs& a, const Operand& s, const Operand& x, const WeightCut& c) {
     Gemm g{};
-    g.a = s;
-    g.a_ld = s_row;
-    g.a_batch = a.outer;
-    g.b = x;
-    g.b_ld = x_row;
-    g.b_batch = a.inner;
-    g.m = out;
+    g.a = s.p;
+    g.a_ld = s.row;
+    g.a_batch = s.part;
+    g.b = x.p;
+    g.b_ld = x.row;
+    g.b_batch = x.part;
+    g.m = (long)a.outer * (a.gated ? 2 : 1);
+    g.m_read = s.width;
     g.n = a.inner;
+    g.n_read = (int)x.width;
     g.k = a.n_rows;
     g.splits = c.splits;
     g.k_split = c.k_split;
+    return g;
+}
+EpiPart weight_epilogue(const LinearArgs& a, float* parts) {
+    return EpiPart{parts, (long)a.outer * (a.gated ? 2 : 1) * a.inner, a.inner};
+}
+// The parts (direct: d_w itself).
+hipError_t weight_gradient(const LinearArgs& a, const Operand& s, const Operand& x, const WeightCut& c, float* parts, T* d_w,
+                           hipStream_t st) {
+    const Gemm g = weight_product(a, s, x, c);
     if (c.direct) return run_tiles<false, false, false>(g, 1, EpiPlain{d_w, a.inner, a.inner, false}, st);
-    return run_tiles<false, false, false>(g, comps * c.splits, EpiPart{parts, out * a.inner, a.inner}, st);
+    return run_tiles<false, false, false>(g, (a.lmax + 1) * (a.lmax + 1) * c.splits, weight_epilogue(a, parts), st);
 }
 
-hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, float* sums, bool gated, int n, const BiasCut& c,
-                   hipStream_t st) {
-    const ActBwd p{grad, static_cast<const T*>(a.z), s, sums, grad_row, a.n_rows, c.chunk, n, a.act, c.across};
+hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, long s_row, float* sums, bool gated, int n,
+                   const BiasCut& c, hipStream_t st) {
+    const ActBwd p{grad, static_cast<const T*>(a.z), s, sums, grad_row, a.n_rows, c.chunk, n, a.act, c.across, s_row};
     if (a.n_rows == 0 && sums == nullptr) return hipSuccess;
     const dim3 grid(c.groups, c.chunks);
     if (n % V == 0)
@@ -1000,7 +1225,7 @@ hipError_t act_bwd(const LinearArgs& a, const T* grad, long grad_row, T* s, floa
 }
 
 Join join_of(const float* parts, void* out, long size, int degrees, unsigned per_component) {
-    const int ways = per_component <= 4 ? 1 : per_component <= 64 ? 4 : 16;
+    const int ways = per_component <= 16 ? 1 : per_component <= 64 ? 4 : 16;
     return Join{parts, static_cast<T*>(out), size, degrees, per_component, ways, (unsigned)div_up(size, 256 / ways)};
 }
 hipError_t join(const Join& a, const Join& b, hipStream_t st) {
@@ -1010,22 +1235,74 @@ hipError_t join(const Join& a, const Join& b, hipStream_t st) {
     return hipGetLastError();
 }
 
-#define CTP_TRY(call)                                                 \
-    do {                                                              \
-        if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
-    } while (0)
+struct FwdLayout {
+    long x, w, parts, bytes;
+};
+FwdLayout fwd_layout(const LinearArgs& a) {
+    const long comps = (a.lmax + 1) * (a.lmax + 1), out = (long)a.outer * (a.gated ? 2 : 1);
+    const Packs p = packs_of(a, false);
+    FwdLayout l{};
+    if (a.n_rows <= 32) return l;       // k_few
+    l.w = p.x ? align256(a.n_rows * comps * p.inner * (long)sizeof(T)) : 0;
+    l.parts = l.w + (p.w ? align256((a.lmax + 1) * p.outer * p.inner * (long)sizeof(T)) : 0);
+    l.bytes = l.parts + sum_cut_bytes(a.n_rows, out, p.inner, comps);
+    return l;
+}
 
 hipError_t fwd(const LinearArgs& a, hipStream_t st) {
     const int comps = (a.lmax + 1) * (a.lmax + 1);
-    const Gemm g = forward_product(a, static_cast<const T*>(a.x), a.x_stride);
+    Operand x = input_of(a, a.x, a.x_stride), w = weight_of(a);
+    const Packs p = packs_of(a, false);
+    const FwdLayout l = fwd_layout(a);
+    char* ws = static_cast<char*>(a.workspace);
+    Pack px{}, pw{};
+    if (p.x) {
+        px = rows_pack(x.p, x.row, a.n_rows, comps, a.inner, p.inner, reinterpret_cast<T*>(ws + l.x));
+        x = Operand{px.to, comps * p.inner, p.inner, p.inner};
+    }
+    if (p.w) {
+        pw = weight_pack(a, p.outer, p.inner, reinterpret_cast<T*>(ws + l.w));
+        w = Operand{pw.to, p.inner, p.outer * p.inner, p.inner};
+    }
+    CTP_TRY(pack(px, pw, st));
+    const Gemm g = forward_product(a, x, w);
     T *y = static_cast<T*>(a.y), *z = static_cast<T*>(a.z_out);
     const T *bias = static_cast<const T*>(a.bias), *residual = static_cast<const T*>(a.residual);
+    float* parts = reinterpret_cast<float*>(ws + l.parts);
     const long row = (long)comps * a.outer;
     const bool stream = streams_out(a.n_rows * row * (long)sizeof(T) * (1 + (z ? a.gated ? 2 : 1 : 0)));
-    if (a.gated) return run_pairs(g, EpiGated{y, z, bias, a.outer, a.act, stream}, st);
-    // without anything to do the epilogue's questions cost a layer that writes much (83325 x 64 -> 4352: 408 instead of 340 us) a sixth of its time
-    if (!z && !bias && !residual && a.act == kActNone) return run_gemm<true, true>(g, comps, EpiPlain{y, row, a.outer, stream}, st);
-    return run_gemm<true, true>(g, comps, EpiLinear{y, z, bias, residual, row, a.residual_stride, a.outer, a.act, stream}, st);
+    if (a.gated) return run_gemm<true, true, true>(g, 1, EpiGated{y, z, bias, a.outer, a.act, stream}, parts, st);
+    // without anything to do the epilogue's questions cost a layer that writes much a sixth of its time
+    // (83325 x 64 -> 4352: 408 instead of 340 us)
+    if (!z && !bias && !residual && a.act == kActNone)
+        return run_gemm<true, true, false>(g, comps, EpiPlain{y, row, a.outer, stream}, parts, st);
+    return run_gemm<true, true, false>(g, comps, EpiLinear{y, z, bias, residual, row, a.residual_stride, a.outer, a.act, stream},
+                                       parts, st);
+}
+
+// k_small_bwd; the bias's sums are d_W's workgroups'.
+hipError_t both_small(const LinearArgs& a, const WeightCut& c, float* sums, float* parts, hipStream_t st) {
+    const unsigned comps = (a.lmax + 1) * (a.lmax + 1);
+    const T* grad = static_cast<const T*>(a.grad);
+    const Operand s{grad, a.grad_stride, a.outer, a.outer};
+    Gemm of_w = weight_product(a, s, input_of(a, a.x, a.x_stride), c);
+    Gemm of_x = input_product(a, s, weight_of(a));
+    of_x.splits = 1;
+    of_x.k_split = div_up(of_x.k, kDepth) * kDepth;
+    if (!set_tiles(of_w, 64, 64, comps * c.splits) || !set_tiles(of_x, 64, 64, comps)) return hipErrorInvalidValue;
+    if (!a.d_w && !a.d_bias) of_w.total = 0;
+    if (!a.d_x) of_x.total = 0;
+    const long total = (long)of_w.total + of_x.total;
+    if (total == 0) return hipSuccess;
+    if (total > max_groups(256)) return hipErrorInvalidValue;
+    const Curve curve{static_cast<const T*>(a.z), a.outer, a.act, sums};
+    const EpiPart to_w = weight_epilogue(a, parts);
+    const EpiPlain to_x = input_epilogue(a, a.d_x);
+    if (a.act != kActNone)
+        k_small_bwd<true><<<dim3((unsigned)total), 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
+    else
+        k_small_bwd<false><<<dim3((unsigned)total), 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
+    return hipGetLastError();
 }
 
 hipError_t bwd(const LinearArgs& a, hipStream_t st) {
@@ -1034,16 +1311,40 @@ hipError_t bwd(const LinearArgs& a, hipStream_t st) {
     const bool act = a.act != kActNone || a.gated;
     const long out = (long)a.outer * (a.gated ? 2 : 1);
     float *sums = a.d_bias ? reinterpret_cast<float*>(ws + y.sums) : nullptr, *parts = reinterpret_cast<float*>(ws + y.parts);
-    const BiasCut b = bias_cut(a.n_rows, a.outer);
-    const T* s = static_cast<const T*>(a.grad);
-    long s_row = a.grad_stride;
-    if (act || sums) { CTP_TRY(act_bwd(a, s, s_row, act ? reinterpret_cast<T*>(ws + y.s) : nullptr, sums, a.gated, a.outer, b, st)); }
-    if (act) s = reinterpret_cast<const T*>(ws + y.s), s_row = out;
-    if (a.d_x) CTP_TRY(input_gradient(a, s, s_row, a.d_x, st));
+    WeightCut c = weight_cut(a, false);
     Join of_w{}, of_b{};
+    if (small_bwd(a)) {
+        CTP_TRY(both_small(a, c, sums, parts, st));
+        if (a.d_w) of_w = join_of(parts, a.d_w, out * a.inner, a.lmax + 1, c.splits);
+        if (a.d_bias) of_b = join_of(sums, a.d_bias, out, 1, c.splits);
+        return join(of_w, of_b, st);
+    }
+    const BiasCut b = bias_cut(a.n_rows, a.outer);
+    const int comps = (a.lmax + 1) * (a.lmax + 1);
+    const Packs p = packs_of(a, true);
+    const T* grad = static_cast<const T*>(a.grad);
+    Operand s{grad, a.grad_stride, a.outer, a.outer}, x = input_of(a, a.x, a.x_stride), w = weight_of(a);
+    T* own_s = reinterpret_cast<T*>(ws + y.s);
+    Pack px{}, pw{}, ps{};
+    if (p.x && a.d_w) {
+        px = rows_pack(x.p, x.row, a.n_rows, comps, a.inner, p.inner, reinterpret_cast<T*>(ws + y.x));
+        x = Operand{px.to, comps * p.inner, p.inner, p.inner};
+    }
+    if (p.w && a.d_x) {
+        pw = weight_pack(a, p.outer, p.inner, reinterpret_cast<T*>(ws + y.w));
+        w = Operand{pw.to, p.inner, p.outer * p.inner, p.inner};
+    }
+    CTP_TRY(pack(px, pw, st));
+    if (act || sums) CTP_TRY(act_bwd(a, grad, a.grad_stride, act ? own_s : nullptr, p.outer, sums, a.gated, a.outer, b, st));
+    if (act) s = Operand{own_s, p.outer, p.outer, p.outer};
+    if (p.grad && (a.d_x || a.d_w)) {
+        ps = rows_pack(grad, a.grad_stride, a.n_rows, comps, a.outer, p.outer, own_s);
+        CTP_TRY(pack(ps, Pack{}, st));
+        s = Operand{own_s, comps * p.outer, p.outer, p.outer};
+    }
+    if (a.d_x) CTP_TRY(input_gradient(a, s, w, a.d_x, parts, st));
     if (a.d_w) {
-        const WeightCut c = weight_cut(a, false);
-        CTP_TRY(weight_gradient(a, s, s_row, static_cast<const T*>(a.x), a.x_stride, c, parts, static_cast<T*>(a.d_w), st));
+        CTP_TRY(weight_gradient(a, s, x, c, parts, static_cast<T*>(a.d_w), st));
         if (!c.direct) of_w = join_of(parts, a.d_w, out * a.inner, a.lmax + 1, c.splits);
     }
     if (a.d_bias) of_b = join_of(sums, a.d_bias, out, 1, b.chunks);
@@ -1059,26 +1360,29 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
     const T *u = static_cast<const T*>(a.a_d_x), *grad = static_cast<const T*>(a.grad), *z = static_cast<const T*>(a.z);
     T *s = reinterpret_cast<T*>(ws + y.s), *g_z = reinterpret_cast<T*>(ws + y.g_z);
     float *sums = reinterpret_cast<float*>(ws + y.sums), *parts = reinterpret_cast<float*>(ws + y.parts);
-    const Gemm v = forward_product(a, u, (long)comps * a.inner);
+    const Operand of_u = input_of(a, u, (long)comps * a.inner), of_x = input_of(a, a.x, a.x_stride), w = weight_of(a);
+    const Operand of_s{s, out, out, out}, of_z{g_z, out, out, out};
+    const Gemm v = forward_product(a, of_u, w);
     const WeightCut c = weight_cut(a, act);
     if (!act) {
-        if (a.g_grad) CTP_TRY((run_gemm<true, true>(v, comps, EpiPlain{static_cast<T*>(a.g_grad), (long)comps * a.outer, a.outer, false}, st)));
+        if (a.g_grad)
+            CTP_TRY((run_gemm<true, true, false>(v, comps, EpiPlain{static_cast<T*>(a.g_grad), (long)comps * a.outer, a.outer, false}, parts, st)));
         if (a.g_w == nullptr) return hipSuccess;
-        CTP_TRY(weight_gradient(a, grad, a.grad_stride, u, (long)comps * a.inner, c, parts, static_cast<T*>(a.g_w), st));
+        CTP_TRY(weight_gradient(a, Operand{grad, a.grad_stride, a.outer, a.outer}, of_u, c, parts, static_cast<T*>(a.g_w), st));
         return c.direct ? hipSuccess : join(join_of(parts, a.g_w, out * a.inner, a.lmax + 1, c.splits), Join{}, st);
     }
     const bool need_z = a.g_x || a.g_w || a.g_bias;
     if (a.gated)
-        CTP_TRY(run_pairs(v, EpiSecond<true>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr, a.g_w ? s : nullptr,
-                                             a.grad_stride, a.outer, a.act}, st));
+        CTP_TRY((run_gemm<true, true, true>(v, 1, EpiSecond<true>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
+                                                                  a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, parts, st)));
     else
-        CTP_TRY((run_gemm<true, true>(v, 1, EpiSecond<false>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
-                                                            a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, st)));
-    if (a.g_x) CTP_TRY(input_gradient(a, g_z, out, a.g_x, st));
+        CTP_TRY((run_gemm<true, true, false>(v, 1, EpiSecond<false>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
+                                                                    a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, parts, st)));
+    if (a.g_x) CTP_TRY(input_gradient(a, of_z, w, a.g_x, parts, st));
     Join of_w{}, of_b{};
     if (a.g_w) {
-        CTP_TRY(weight_gradient(a, g_z, out, static_cast<const T*>(a.x), a.x_stride, c, parts, nullptr, st));
-        CTP_TRY(weight_gradient(a, s, out, u, a.inner, c, parts + c.splits * out * a.inner, nullptr, st));
+        CTP_TRY(weight_gradient(a, of_z, of_x, c, parts, nullptr, st));
+        CTP_TRY(weight_gradient(a, of_s, of_u, c, parts + c.splits * out * a.inner, nullptr, st));
         of_w = join_of(parts, a.g_w, out * a.inner, 1, 2 * c.splits);
     }
     if (a.g_bias) {
@@ -1086,7 +1390,7 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
         const BiasCut b = bias_cut(a.n_rows, half);
         // the halves of a gated z as columns side by side: summed one half at a time
         for (int h = 0; h < (a.gated ? 2 : 1); ++h) {
-            CTP_TRY(act_bwd(a, g_z + (long)h * half, out, nullptr, sums + (long)h * b.chunks * half, false, half, b, st));
+            CTP_TRY(act_bwd(a, g_z + (long)h * half, out, nullptr, 0, sums + (long)h * b.chunks * half, false, half, b, st));
             const Join of = join_of(sums + (long)h * b.chunks * half, static_cast<T*>(a.g_bias) + (long)h * half, half, 1, b.chunks);
             if (h + 1 == (a.gated ? 2 : 1))
                 of_b = of;
@@ -1097,13 +1401,14 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
     return join(of_w, of_b, st);
 }
 
-long workspace(const LinearArgs& a, bool second) { return layout_of(a, second).bytes; }
+long fwd_workspace(const LinearArgs& a) { return fwd_layout(a).bytes; }
+long bwd_workspace(const LinearArgs& a, bool second) { return layout_of(a, second).bytes; }
 
 }  // namespace
 
 template <>
 const LinearOps& linear_ops<CTP_DENSE_TYPE>() {
-    static constexpr LinearOps ops{fwd, bwd, bwd_bwd, workspace};
+    static constexpr LinearOps ops{fwd, bwd, bwd_bwd, fwd_workspace, bwd_workspace};
     return ops;
 }
 

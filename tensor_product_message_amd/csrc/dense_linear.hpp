@@ -9,7 +9,8 @@ struct LinearOps {
     hipError_t (*fwd)(const LinearArgs&, hipStream_t);
     hipError_t (*bwd)(const LinearArgs&, hipStream_t);
     hipError_t (*bwd_bwd)(const LinearArgs&, hipStream_t);
-    long (*workspace)(const LinearArgs&, bool second);
+    long (*fwd_workspace)(const LinearArgs&);
+    long (*bwd_workspace)(const LinearArgs&, bool second);
 };
 
 template <int Code>

@@ -389,7 +389,7 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
     p.wide = tiles >= 256;
     // A's sums are cut where a long side would keep few workgroups busy for long
     for (int k = 0; k < p.n; ++k) terms += p.g[k].batch * triangle(div_up(p.g[k].s, p.wide ? 128 : 64)) * p.g[k].l;
-    const long cut = max((long)kLeastCut, div_up(terms, 768));
+    const long cut = max((long)kLeastCut, div_up(terms, 1024));
     for (int k = 0; k < p.n; ++k) {
         Group& g = p.g[k];
         g.splits = (unsigned)max(1L, g.l / cut);

@@ -220,6 +220,7 @@ def to(dev, *ts):
 SHAPES = [  # rows, inner, outer: single rows, odd sizes, tiles and their edges, sums longer than a tile
     (1, 1, 1), (1, 8, 5), (1, 333, 77), (3, 64, 64), (5, 7, 9), (16, 512, 40), (17, 520, 33), (31, 100, 130),
     (1, 4099, 37), (20, 3000, 50), (9, 2600, 1000),
+    (33, 600, 70), (64, 2048, 100), (200, 1030, 90), (90, 70, 1100), (2, 100, 2000), (5000, 64, 64), (3001, 100, 128), (900, 127, 3),
     (64, 16, 16), (65, 63, 129), (130, 65, 66), (257, 130, 257), (1503, 8, 64), (300, 1003, 77), (40, 2051, 24),
     (2000, 24, 3), (129, 192, 320), (513, 256, 264), (700, 264, 520),
 ]
@@ -254,6 +255,7 @@ def test_linear(ctp, dev, rows, inner, outer, dtype):
 WIDE = [  # enough tiles of 256 and of 128 for the card, in each direction's product; sums that end inside a tile
     (3400, 72, 3600, False), (1500, 80, 1400, False), (3400, 3600, 40, False), (2600, 2608, 40, False), (40, 3400, 3600, False),
     (72, 1400, 1504, False), (3400, 72, 1800, True), (1500, 136, 712, True), (40, 3400, 1800, True),
+    (1500, 1003, 777, False), (2000, 1000, 777, False), (2000, 1003, 776, False), (1300, 1003, 512, True), (1300, 1001, 511, True),
 ]
 
 
@@ -275,8 +277,34 @@ def test_wide(ctp, dev, rows, inner, outer, gated, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lmax,rows,inner,outer,gap", [(0, 1501, 1001, 779, 0), (0, 1501, 1000, 776, 3), (1, 700, 333, 1111, 0),
+                                                       (1, 700, 336, 1104, 5), (2, 300, 600, 645, 0), (0, 1501, 1000, 777, 0)])
+def test_wide_without_activation(ctp, dev, lmax, rows, inner, outer, gap, dtype):
+    """Odd rows and odd strides (gap values behind each row), sizes at which 16-bit rows are laid out anew."""
+    c = Case(rows, inner, outer, dtype, lmax=lmax)
+    tell("wide, no activation", lmax, rows, inner, outer, gap, dtype)
+    x, w, b, grad = to(dev, c.x, c.w, c.bias, c.grad)
+
+    def with_gap(t):
+        wide = torch.full((t.shape[0], t[0].numel() + gap), float("nan"), dtype=dtype, device=dev)
+        wide[:, :t[0].numel()] = t.view(t.shape[0], -1)
+        return wide[:, :t[0].numel()].unflatten(1, t.shape[1:])
+
+    x, grad = with_gap(x), with_gap(grad)
+    y, _ = ctp.linear_fwd(x, w, b, lmax=lmax)
+    _, _, y_ref, ey = c.forward()
+    close("y", y, y_ref, ey)
+    got = ctp.linear_bwd(grad, x, w, lmax=lmax)
+    for n, a, (ref, bound) in zip(("d_x", "d_w", "d_bias"), got, c.backward(None)):
+        close(n, a, ref, bound)
+    part = ctp.linear_bwd(grad, x, w, lmax=lmax, needs=(False, True, False))
+    assert part[0] is None and torch.equal(part[1], got[1])
+    assert torch.equal(ctp.linear_bwd(grad, x, w, lmax=lmax, needs=(True, False, False))[0], got[0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lmax,rows,inner,outer", [(1, 1, 16, 16), (1, 64, 16, 16), (2, 77, 33, 20), (3, 100, 128, 128),
-                                                   (3, 301, 9, 65), (2, 700, 64, 136)])
+                                                   (3, 301, 9, 65), (2, 700, 64, 136), (1, 50, 640, 40), (1, 40, 40, 700), (3, 1503, 24, 32)])
 def test_linear_degrees(ctp, dev, lmax, rows, inner, outer, dtype):
     c = Case(rows, inner, outer, dtype, lmax=lmax, residual=True)
     tell("linear degrees", lmax, rows, inner, outer, dtype)
@@ -296,7 +324,7 @@ def test_linear_degrees(ctp, dev, lmax, rows, inner, outer, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,inner,outer", [(1, 8, 1), (1, 257, 96), (2, 64, 33), (15, 100, 64), (64, 40, 31), (65, 129, 65),
-                                              (300, 72, 136), (1503, 129, 17), (513, 256, 264), (33, 1029, 8)])
+                                              (300, 72, 136), (1503, 129, 17), (513, 256, 264), (33, 1029, 8), (50, 2048, 48), (41, 1100, 33)])
 def test_gated(ctp, dev, rows, inner, outer, dtype):
     for k, bias in ((0, True), (3, False)):
         name = ACTS[(rows + outer + k) % 6]
