@@ -191,6 +191,8 @@ __device__ __forceinline__ ThreeParts take_apart(float x) {
 
 // A tile's way from memory: 16-byte reads into registers, then into LDS as parts.
 // n_rows: how many m (or n) there are, values past which are any; k_end: where k ends, zeros past it.
+enum How : int { kGuarded, kWhole, kClamped };
+
 template <class T, bool Along, int Rows, int Depth, int Threads>
 struct Staged {
     typedef typename Parts<T>::E E;
@@ -201,24 +203,40 @@ struct Staged {
     vec_t<T> v[kVecs];
 
     // The tile's k from k0 on, base being the tile's first row (Along) or column and k = 0.  row_of(r): where row r of
-    // the tile lies among the operand's rows (Along), which may be any permutation.  Whole: nothing of the tile lies
-    // past k_end or n_left, and the reads are straight-line code.
-    template <bool Whole, class F>
+    // the tile lies among the operand's rows (Along), which may be any permutation.  Three ways to read, of which a loop
+    // takes one, so that what it waits for is known when it is compiled:
+    //   kWhole    nothing of the tile lies past k_end or n_left;
+    //   kClamped  reads go to the last vector and row that are there, and fix() makes of them what was meant;
+    //             rows of no less than a vector (Along: k_end, Across: n_left);
+    //   kGuarded  any size.
+    template <int How, class F>
     __device__ __forceinline__ void load(const T* base, long ld, int n_left, int k0, int k_end, F&& row_of) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow;
             // a vector of the row `row` of `width` values, from value `at`
-            const long row = Along ? row_of(r) : k0 + r;
+            const long row = Along ? row_of(r) : How == kClamped ? min(k0 + r, k_end - 1) : k0 + r;
             const int at = (Along ? k0 : 0) + c * kVec<T>, width = Along ? k_end : n_left;
-            if (Whole || (at + kVec<T> <= width && (Along || row < k_end))) {
-                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + row * ld + at);
-            } else if (at < width && (Along || row < k_end)) {
-                v[i] = load_vec<T>(base + row * ld, at / kVec<T>, width);
-            } else {
+            if constexpr (How == kGuarded) {
                 v[i] = vec_t<T>{};
+                if (at < width && (Along || row < k_end)) v[i] = load_vec<T>(base + row * ld, at / kVec<T>, width);
+            } else {
+                const int from = How == kClamped ? min(at, width - kVec<T>) : at;
+                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + row * ld + from);
             }
+        }
+    }
+    // Zeros past k_end and n_left, the rest in its place, after a clamped load.
+    __device__ __forceinline__ void fix(int n_left, int k0, int k_end) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow;
+            const int over = (Along ? k0 : 0) + c * kVec<T> + kVec<T> - (Along ? k_end : n_left);
+            const bool in = over < kVec<T> && (Along || k0 + r < k_end);
+            const vec_t<T> x = __builtin_bit_cast(vec_t<T>, __builtin_bit_cast(unsigned __int128, v[i]) >> (over > 0 && in ? over * 8 * (int)sizeof(T) : 0));
+            v[i] = in ? x : vec_t<T>{};
         }
     }
 

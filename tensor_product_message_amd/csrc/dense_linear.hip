@@ -181,34 +181,48 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
             return (long)min(r, n_left - 1);
         };
         const bool whole_m = m_left == BM, whole_n = n_left >= (Pairs ? BN / 2 : BN);
-        SA sa, sz;
-        SB sb;
-        auto load = [&](int k) {
-            auto read = [&](auto whole) {
-                constexpr bool Whole = decltype(whole)::value != 0;
-                sa.template load<Whole>(a, g.a_ld, m_left, k, k_end, row_a);
-                if constexpr (Curved) sz.template load<Whole>(z, c.z_ld, m_left, k, k_end, row_a);
-                sb.template load<Whole>(b, g.b_ld, n_left, k, k_end, row_b);
-            };
-            if (k + kDepth <= k_end && (AlongA || whole_m) && (AlongB || whole_n))
-                read(Is<1>{});
-            else
-                read(Is<0>{});
-        };
         const bool sums = Summed && c.sums != nullptr && t.n == 0 && batch == 0;
         float sum[V] = {};
         f32x16 acc[NT][MT] = {};
-        load(0);
-        for (int k = 0; k < k_end; k += kDepth) {
-            if constexpr (Curved) sa.curve(sz, c.act);
-            if constexpr (Summed)
-                if (sums) sa.add_columns(sum);
-            lds_barrier();
-            sa.store(la);
-            sb.store(lb);
-            lds_barrier();
-            if (k + kDepth < k_end) load(k + kDepth);
-            multiply_step<typename SA::tile_t, typename SB::tile_t, kParts, MT, NT, kDepth>(acc, la, lb, wm, wn, lane);
+        // The tiles of k from step `first` to before `last`, the next one on its way while one is multiplied.  (Two on
+        // their way measured no faster: a step's own instructions are its time, not its reads.)
+        auto run = [&](auto how, int first, int last) {
+            constexpr int How = decltype(how)::value;
+            if (first >= last) return;
+            SA sa, sz;
+            SB sb;
+            auto load = [&](int step) {
+                const int k = step * kDepth;
+                sa.template load<How>(a, g.a_ld, m_left, k, k_end, row_a);
+                if constexpr (Curved) sz.template load<How>(z, c.z_ld, m_left, k, k_end, row_a);
+                sb.template load<How>(b, g.b_ld, n_left, k, k_end, row_b);
+            };
+            load(first);
+            for (int step = first; step < last; ++step) {
+                if constexpr (How == kClamped) {
+                    sa.fix(m_left, step * kDepth, k_end);
+                    if constexpr (Curved) sz.fix(m_left, step * kDepth, k_end);
+                    sb.fix(n_left, step * kDepth, k_end);
+                }
+                if constexpr (Curved) sa.curve(sz, c.act);
+                if constexpr (Summed)
+                    if (sums) sa.add_columns(sum);
+                lds_barrier();
+                sa.store(la);
+                sb.store(lb);
+                lds_barrier();
+                if (step + 1 < last) load(step + 1);
+                multiply_step<typename SA::tile_t, typename SB::tile_t, kParts, MT, NT, kDepth>(acc, la, lb, wm, wn, lane);
+            }
+        };
+        const int steps = (k_end + kDepth - 1) / kDepth, whole = k_end / kDepth;
+        if ((AlongA || whole_m) && (AlongB || whole_n)) {
+            run(Is<kWhole>{}, 0, whole);
+            run(Is<kGuarded>{}, whole, steps);
+        } else if ((AlongA ? k_end : m_left) >= V && (AlongB ? k_end : n_left) >= V) {
+            run(Is<kClamped>{}, 0, steps);
+        } else {
+            run(Is<kGuarded>{}, 0, steps);
         }
         lds_barrier();
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
@@ -552,9 +566,9 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
             return (long)min(r, n_left - 1);
         };
         if (k_end == kLong && n_left >= kCols)
-            sb.template load<true>(from, g.b_ld, n_left, 0, k_end, row_b);
+            sb.template load<kWhole>(from, g.b_ld, n_left, 0, k_end, row_b);
         else
-            sb.template load<false>(from, g.b_ld, n_left, 0, k_end, row_b);
+            sb.template load<kGuarded>(from, g.b_ld, n_left, 0, k_end, row_b);
     };
     load(n_first);
     for (int n0 = n_first; n0 < n_last; n0 += kCols) {
