@@ -1,20 +1,21 @@
 #!/usr/bin/env python3
 """A small message-passing potential, trained on the energies and forces of synthetic structures.
 
-    python examples/train_energy.py [--steps 40] [--atoms 400] [--channels 32] [--lmax 2]
+    python examples/train_energy.py [--steps 40] [--atoms 400] [--channels 32] [--lmax 2] [--orthogonal]
 
 One training step runs the package's operators as a model uses them:
 
+    distances -> linear (silu) -> linear   radial weights of every edge, for each block
     species -> embed                       node features [N, C]
     conv_tp  (scalars in, degrees out)     block 1
     norm_residual                          r1 = r0 + alpha gate N(h1), u1 = N(r1)
     conv_tp  (degrees in, degrees out)     block 2
     norm_residual                          r2, u2; the scalars of u2 give the energies
     forces = -dE/d(edge vectors), summed onto atoms (first gradients, kept for the loss)
-    backward of the energy and force loss, clip_grad_norm, one step of Adam
+    backward of the energy and force loss, clip_grad_norm, one step of Adam; with
+    --orthogonal the radial networks' matrices take orthogonalised steps instead
 
-The radial weights of every edge come from a small torch network on Bessel
-functions of the distance.  The targets are a number per species for every
+The radial networks see Bessel functions of the distance.  The targets are a number per species for every
 atom and a repulsion exp(-distance) between neighbours.
 """
 from __future__ import annotations
@@ -77,7 +78,8 @@ class Potential(torch.nn.Module):
         dist = vec.norm(dim=1, keepdim=True)
         k = torch.arange(1, 9, device=vec.device) * math.pi / CUTOFF
         bessel = torch.sin(k * dist) / dist * (1 + torch.cos(math.pi * dist / CUTOFF)) / 2
-        w = [net(bessel).view(-1, p, C) for net, p in zip(self.radial, self.paths)]
+        w = [ctp.linear(ctp.linear(bessel, net[0].weight, net[0].bias, act="silu"), net[2].weight, net[2].bias).view(-1, p, C)
+             for net, p in zip(self.radial, self.paths)]
         x = ctp.embed(self.table, species)                              # [N, C]
         r = torch.cat([x[:, None], x.new_zeros(n, (L + 1) ** 2 - 1, C)], 1)
         h = ctp.conv_tp(x[:, None], vec, w[0], graph, (0, L, L), ctp.VEC_GIVEN)
@@ -87,18 +89,22 @@ class Potential(torch.nn.Module):
         return u.new_zeros(n_structures).index_add(0, batch, u[:, 0] @ self.readout)
 
 
-def train(steps=40, atoms=400, channels=32, lmax=2, n_structures=8, max_norm=10.0, seed=0, device="cuda:0", log=print):
+def train(steps=40, atoms=400, channels=32, lmax=2, n_structures=8, max_norm=10.0, seed=0, device="cuda:0", log=print,
+          orthogonal=False):
     """(losses, gradient norms) of every step, as lists."""
     torch.manual_seed(seed)
     species, vec, (recv, send), graph, batch, energy, forces = structures(atoms, n_structures, torch.device(device), seed)
     vec.requires_grad_()
     model = Potential(channels, lmax, device)
     params = list(model.parameters())
-    adam = torch.optim.Adam(params, lr=1e-2)
+    matrices = [p for p in model.radial.parameters() if p.dim() == 2] if orthogonal else []
+    momenta = [torch.zeros_like(p) for p in matrices]
+    adam = torch.optim.Adam([p for p in params if not any(p is m for m in matrices)], lr=1e-2)
     losses, norms = [], []
     per_atom = atoms / n_structures
     for step in range(steps):
-        adam.zero_grad()
+        for p in params:
+            p.grad = None
         e = model(species, vec, graph, batch, n_structures)
         g, = torch.autograd.grad(e.sum(), vec, create_graph=True)
         f = torch.zeros_like(forces).index_add(0, send, g).index_add(0, recv, -g)
@@ -107,6 +113,12 @@ def train(steps=40, atoms=400, channels=32, lmax=2, n_structures=8, max_norm=10.
         grads = [p.grad for p in params]
         _, norm = ctp.clip_grad_norm(grads, max_norm, out=grads)
         adam.step()
+        if matrices:
+            for m, p in zip(momenta, matrices):
+                m.mul_(0.9).add_(p.grad)
+            with torch.no_grad():
+                for p, step_of in zip(matrices, ctp.orthogonalise(momenta)):
+                    p.sub_(step_of, alpha=2e-3 * max(p.shape) ** 0.5)
         losses.append(loss.detach())
         norms.append(norm)
         if log and step % 10 == 0:
@@ -118,6 +130,7 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, default in (("steps", 40), ("atoms", 400), ("channels", 32), ("lmax", 2)):
         ap.add_argument("--" + name, type=int, default=default)
+    ap.add_argument("--orthogonal", action="store_true")
     a = ap.parse_args()
-    losses, _ = train(a.steps, a.atoms, a.channels, a.lmax)
+    losses, _ = train(a.steps, a.atoms, a.channels, a.lmax, orthogonal=a.orthogonal)
     print(f"loss {losses[0]:.5f} -> {losses[-1]:.5f}")

@@ -7,7 +7,7 @@
 // with m or n contiguous ("across": what a gradient sums over are rows of
 // storage).  Operands of 16 bits go to the matrix cores as they are.  Floats are
 // taken apart into three bfloat16, x = h + m + l, each the rest rounded to
-// nearest: 24 bits, so h + m + l is x (what underflows, 2^-133 and less, aside).
+// nearest: 24 bits, so h + m + l is x (parts below 2^-126 aside).
 // Of the nine products of the parts those below 2^-23 of the whole (m l, l m,
 // l l) are left out; the other six are summed in fp32, which is a float
 // product's accuracy at 2.7 times the rate of the fp32 matrix instructions

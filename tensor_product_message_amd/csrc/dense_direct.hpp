@@ -16,7 +16,8 @@ __device__ __forceinline__ i32x4 buffer_at(const void* base, unsigned bytes) {
 }
 
 // 16 bytes from each lane's offset to LDS, lane after lane from `lds` (the same in every lane).  The compiler does not
-// know of the read (it would wait for all of them before any read of LDS): loads_arrived waits for it.
+// know of the read (it would wait for all of them before any read of LDS): loads_arrived waits for it.  m0 is a
+// register that it sets before each use of its own.
 __device__ __forceinline__ void load_lds(const i32x4& buffer, unsigned offset, unsigned lds) {
     asm volatile(
         "s_mov_b32 m0, %0\n\t"

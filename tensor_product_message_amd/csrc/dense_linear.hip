@@ -470,7 +470,7 @@ __global__ __launch_bounds__(256, 2) void k_small_bwd(Gemm of_w, EpiPart to_w, G
     if (blockIdx.x < of_w.total)
         staged_tiles<false, false, 64, 64, 2, false, Curved, true>(of_w, to_w, c, lds, blockIdx.x, of_w.total);
     else
-        staged_tiles<true, false, 64, 64, 2, false, Curved, false>(of_x, to_x, c, lds, blockIdx.x - of_w.total, of_x.total);
+        staged_tiles<true, false, 64, 64, 2, false, Curved, false>(of_x, to_x, c, lds, blockIdx.x - of_w.total, gridDim.x - of_w.total);
 }
 
 // ---------------------------------------------------------------- long sums, few tiles
@@ -637,8 +637,7 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
 // Up to 16 MB rows, where the weights' way from memory is all there is: no tile of x fills the matrix cores, and no
 // weight is used twice.  Each wave takes 32 rows of w (Pairs: 16 and their partners) and one of Waves shares of k,
 // straight from memory into the matrix instruction's registers, kAhead reads of each row under way at once; the
-// waves' sums meet in LDS, in the waves' order.  Within 4 lanes' reads a row of w is 128 bytes in one piece: which k
-// goes to which lane does not matter as long as w and x agree.
+// waves' sums meet in LDS, in the waves' order.  Which k goes to which lane does not matter as long as w and x agree.
 template <class U>
 struct Small;
 template <>
@@ -667,7 +666,7 @@ template <int MB, int Waves, bool Pairs, class Epi>
 __global__ __launch_bounds__(64 * Waves) void k_few(Gemm g, Epi epi) {
     constexpr int kStep = 8 * V, kAhead = 4 / MB, kRow = 36;
     __shared__ __attribute__((aligned(16))) float part[Waves][16 * MB][kRow];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, from = (lane >> 4) * 2 * V;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, from = (lane >> 4) * V;
     const unsigned batch = blockIdx.y;
     const int n0 = blockIdx.x * (Pairs ? 16 : 32), k_end = (int)g.k;
     const T *a[MB], *b[2];
@@ -687,7 +686,7 @@ __global__ __launch_bounds__(64 * Waves) void k_few(Gemm g, Epi epi) {
             for (int s = 0; s < kAhead; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int k = k0 + s * kStep + from + h * V;
+                    const int k = k0 + s * kStep + h * 4 * V + from;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) vb[s][h][j] = *reinterpret_cast<const typename Vec<T>::unaligned*>(b[j] + k);
 #pragma unroll
@@ -698,7 +697,7 @@ __global__ __launch_bounds__(64 * Waves) void k_few(Gemm g, Epi epi) {
             for (int s = 0; s < kAhead; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int k = k0 + s * kStep + from + h * V;
+                    const int k = k0 + s * kStep + h * 4 * V + from;
                     const bool in = k < k_end;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) vb[s][h][j] = in ? load_vec<T>(b[j], k / V, k_end) : vec_t<T>{};
@@ -879,31 +878,35 @@ struct Join {
 
 __global__ __launch_bounds__(256) void k_join(Join first, Join second) {
     __shared__ float part[256];
-    const bool is_first = blockIdx.x < first.groups * first.degrees;
-    const Join j = is_first ? first : second;
-    const unsigned id = is_first ? blockIdx.x : blockIdx.x - first.groups * first.degrees;
-    const int wide = 256 / j.ways, c = threadIdx.x % wide, q = threadIdx.x / wide;
-    const unsigned l = id / j.groups;
-    const long i = (long)(id % j.groups) * wide + c;
-    const unsigned p1 = (l + 1) * (l + 1) * j.per_component;
-    unsigned p = l * l * j.per_component + q;
-    float s = 0.0f;
-    if (i < j.size) {
-        // eight reads at once
-        for (; p + 7 * j.ways < p1; p += 8 * j.ways) {
-            float x[8];
+    const long of_first = (long)first.groups * first.degrees, total = of_first + (long)second.groups * second.degrees;
+    for (long block = blockIdx.x; block < total; block += gridDim.x) {
+        const bool is_first = block < of_first;
+        const Join j = is_first ? first : second;
+        const unsigned id = (unsigned)(is_first ? block : block - of_first);
+        const int wide = 256 / j.ways, c = threadIdx.x % wide, q = threadIdx.x / wide;
+        const unsigned l = id / j.groups;
+        const long i = (long)(id % j.groups) * wide + c;
+        const unsigned p1 = (l + 1) * (l + 1) * j.per_component;
+        unsigned p = l * l * j.per_component + q;
+        float s = 0.0f;
+        if (i < j.size) {
+            // eight reads at once
+            for (; p + 7 * j.ways < p1; p += 8 * j.ways) {
+                float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = j.parts[(p + e * j.ways) * j.size + i];
+                for (int e = 0; e < 8; ++e) x[e] = j.parts[(p + e * j.ways) * j.size + i];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[e];
+                for (int e = 0; e < 8; ++e) s += x[e];
+            }
+            for (; p < p1; p += j.ways) s += j.parts[p * j.size + i];
         }
-        for (; p < p1; p += j.ways) s += j.parts[p * j.size + i];
-    }
-    part[threadIdx.x] = s;
-    lds_barrier();
-    if (q == 0 && i < j.size) {
-        for (int r = 1; r < j.ways; ++r) s += part[r * wide + c];
-        j.out[l * j.size + i] = (T)s;
+        part[threadIdx.x] = s;
+        lds_barrier();
+        if (q == 0 && i < j.size) {
+            for (int r = 1; r < j.ways; ++r) s += part[r * wide + c];
+            j.out[l * j.size + i] = (T)s;
+        }
+        lds_barrier();
     }
 }
 
@@ -945,11 +948,12 @@ hipError_t run_direct(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Whether tiles may go to LDS directly: 16-byte pieces, whole in every row.
+// Whether tiles may go to LDS directly: 16-byte pieces, whole in every row, and rows so near each other that a tile's
+// offsets fit into 31 bits.
 template <bool AlongA, bool AlongB>
 bool direct(const Gemm& g) {
     const auto whole = [](const T* p, long ld, long batch, long n) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && batch % V == 0 && n % V == 0;
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && batch % V == 0 && n % V == 0 && ld <= 1L << 21;
     };
     return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m_read) &&
            whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n_read);
@@ -1041,9 +1045,6 @@ hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, float* parts, hipS
     return hipGetLastError();
 }
 
-// Layers whose first gradients go through k_small_bwd.
-bool small_bwd(const LinearArgs& a) { return !a.gated && a.inner <= 128 && a.outer <= 128; }
-
 // How d_W[outer][inner] = sum over rows is cut: every component by itself, and its rows into `splits`.
 struct WeightCut {
     unsigned splits;
@@ -1057,12 +1058,21 @@ WeightCut weight_cut(const LinearArgs& a, bool twice) {
     const long most = max(1L, a.n_rows / (4 * kDepth)), tiles128 = div_up(out, 128) * div_up(a.inner, 128) * comps;
     const bool wide = tiles128 >= 32 && tiles128 * min(most, 16L) >= kFill / 2;
     const long tiles = wide ? tiles128 : div_up(out, 64) * div_up(a.inner, 64) * comps;
-    long splits = max(1L, min((wide || small_bwd(a) ? kFill : 2 * kFill) / tiles, most));
+    long splits = max(1L, min(kFill / tiles, most));
     splits = max(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
     c.k_split = max(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
     c.splits = (unsigned)max(1L, div_up(a.n_rows, c.k_split));
     c.direct = c.splits == 1 && comps == 1 && !twice;
     return c;
+}
+
+// Layers whose first gradients go through k_small_bwd: few tiles wide, or few tiles at all and no long sum.
+bool small_bwd(const LinearArgs& a) {
+    if (a.gated) return false;
+    if (a.inner <= 128 && a.outer <= 128) return true;
+    const long comps = (long)(a.lmax + 1) * (a.lmax + 1);
+    const long tiles = comps * (div_up(a.n_rows, 64) * div_up(a.inner, 64) + div_up(a.outer, 64) * div_up(a.inner, 64));
+    return a.outer <= 512 && tiles <= kFill && sum_cut(a.n_rows, a.inner, a.outer, comps) == 1;
 }
 
 struct BiasCut {
@@ -1243,9 +1253,9 @@ Join join_of(const float* parts, void* out, long size, int degrees, unsigned per
     return Join{parts, static_cast<T*>(out), size, degrees, per_component, ways, (unsigned)div_up(size, 256 / ways)};
 }
 hipError_t join(const Join& a, const Join& b, hipStream_t st) {
-    const unsigned groups = a.groups * a.degrees + b.groups * b.degrees;
+    const long groups = (long)a.groups * a.degrees + (long)b.groups * b.degrees;
     if (groups == 0) return hipSuccess;
-    k_join<<<groups, 256, 0, st>>>(a, b);
+    k_join<<<dim3((unsigned)min(groups, max_groups(256))), 256, 0, st>>>(a, b);
     return hipGetLastError();
 }
 
@@ -1308,14 +1318,15 @@ hipError_t both_small(const LinearArgs& a, const WeightCut& c, float* sums, floa
     if (!a.d_x) of_x.total = 0;
     const long total = (long)of_w.total + of_x.total;
     if (total == 0) return hipSuccess;
-    if (total > max_groups(256)) return hipErrorInvalidValue;
+    if (of_w.total >= max_groups(256)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)min(total, max_groups(256)));
     const Curve curve{static_cast<const T*>(a.z), a.outer, a.act, sums};
     const EpiPart to_w = weight_epilogue(a, parts);
     const EpiPlain to_x = input_epilogue(a, a.d_x);
     if (a.act != kActNone)
-        k_small_bwd<true><<<dim3((unsigned)total), 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
+        k_small_bwd<true><<<grid, 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
     else
-        k_small_bwd<false><<<dim3((unsigned)total), 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
+        k_small_bwd<false><<<grid, 256, 0, st>>>(of_w, to_w, of_x, to_x, curve);
     return hipGetLastError();
 }
 

@@ -56,6 +56,8 @@ struct Groups {
     unsigned first[kMostGroups + 1];    // of this launch's workgroups, each group's first
 };
 
+static_assert(sizeof(Groups) <= 4000);      // with a launch's other argument
+
 __device__ __forceinline__ int group_of(const Groups& p, unsigned id) {
     int k = 0;
     while (k + 1 < p.n && id >= p.first[k + 1]) ++k;

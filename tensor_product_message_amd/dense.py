@@ -139,11 +139,15 @@ class LinearBackward(torch.autograd.Function):
 
 def linear(x, w, bias=None, residual=None, act: str = "none", lmax: int = 0):
     """Differentiable linear_fwd: act(x w^T + bias) + residual (twice in x, as a loss on forces needs it)."""
+    if not torch.is_grad_enabled():
+        return linear_fwd(x, w, bias, residual, act, int(lmax))[0]
     return LinearFunction.apply(x, w, bias, residual, act, int(lmax), False)
 
 
 def gated_linear(x, w, bias=None, act: str = "silu"):
     """Differentiable gated_linear_fwd: act(x w[0]^T + bias[0]) (x w[1]^T + bias[1]) (twice in x)."""
+    if not torch.is_grad_enabled():
+        return gated_linear_fwd(x, w, bias, act)[0]
     return LinearFunction.apply(x, w, bias, None, act, 0, True)
 
 

@@ -512,6 +512,44 @@ def test_block_run_together(ctp, dev):
         assert float((s.double().cpu() - ref).norm()) <= 1e-3 * float(ref.norm())
 
 
+def test_example_runs_with_orthogonalised_steps(dev):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import train_energy
+    losses, norms = train_energy.train(steps=6, atoms=120, channels=16, lmax=1, log=None, orthogonal=True)
+    assert len(losses) == 6 and all(math.isfinite(x) for x in losses + norms)
+
+
+def test_example_gradients(ctp, dev):
+    """The example's gradients through its radial networks: as with torch's own layers in them."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import train_energy
+    species, vec, _, graph, batch, energy, _ = train_energy.structures(60, 2, dev, 0)
+    torch.manual_seed(0)
+    model = train_energy.Potential(8, 1, dev)
+    vec.requires_grad_()
+    params = [p for p in model.parameters()]
+
+    def gradients():
+        e = model(species, vec, graph, batch, 2)
+        f, = torch.autograd.grad(e.sum(), vec, create_graph=True)
+        return torch.autograd.grad((e - energy).square().sum() + f.square().sum(), params)
+
+    got = gradients()
+    own, ctp.linear = ctp.linear, lambda x, w, b, act="none": (
+        torch.nn.functional.silu(torch.nn.functional.linear(x, w, b)) if act == "silu" else torch.nn.functional.linear(x, w, b))
+    try:
+        want = gradients()
+    finally:
+        ctp.linear = own
+    # fp32 on both sides: some hundred roundings of terms up to a hundred times the result
+    for a, b in zip(got, want):
+        assert float((a - b).abs().max()) <= 1e4 * EPS32 * float(b.abs().max()) + 1e-6
+
+
 # ---------------------------------------------------------------- orthogonalising
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -647,6 +685,39 @@ def test_streams_and_graphs(ctp, dev):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b2) for a, b2 in zip(out, step())), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_far_apart(ctp, dev, dtype):
+    """Row strides at which a tile's offsets pass 32 bits."""
+    rows, inner, outer, stride = 260, 64, 8320, 9_000_000
+    base = torch.empty(rows * stride, dtype=dtype, device=dev)
+    far = base.as_strided((rows, inner), (stride, 1))
+    g = torch.Generator().manual_seed(8)
+    x = normal(g, (rows, inner), dtype).to(dev)
+    far.copy_(x)
+    w = normal(g, (outer, inner), dtype, 0.1).to(dev)
+    assert torch.equal(ctp.linear_fwd(far, w)[0], ctp.linear_fwd(x, w)[0])
+    grad = normal(g, (rows, outer), dtype).to(dev)
+    for a, b in zip(ctp.linear_bwd(grad, far, w), ctp.linear_bwd(grad, x, w)):
+        assert float((a - b).abs().max()) <= 8 * U[dtype] * float(b.abs().max())
+    del far, base
+    torch.cuda.empty_cache()
+
+
+def test_no_grad_and_frozen(ctp, dev):
+    x, w, b = torch.randn(5, 8, device=dev), torch.randn(6, 8, device=dev), torch.randn(6, device=dev)
+    want = torch.nn.functional.silu(x @ w.T + b)
+    for req in (False, True):
+        w.requires_grad_(req)
+        with torch.no_grad():
+            y = ctp.linear(x, w, b, act="silu")
+        assert not y.requires_grad and float((y - want).abs().max()) <= 1e-5
+    y = ctp.linear(x, w, b, act="silu")
+    y.sum().backward()
+    assert x.grad is None and b.grad is None and w.grad.shape == w.shape
+    with torch.inference_mode():
+        assert float((ctp.gated_linear(x, w.detach().view(2, 3, 8)) - torch.nn.functional.silu(x @ w[:3].T) * (x @ w[3:].T)).abs().max()) <= 1e-4
 
 
 def test_refusals(ctp, dev):
