@@ -94,7 +94,8 @@ int32_t conv_tp_linear_bwd_bwd_workspace(const conv_tp_linear_problem *prob, int
  * pointers), batch, rows, cols, dtype: host arrays of n_tensors entries, read
  * before the call returns.  out[k] has in[k]'s type and may be in[k]; other
  * overlaps are not allowed.  X and A are held in 32 bits whatever the type.  A
- * matrix of zeros gives zeros, one with a value that is not finite gives NaN. */
+ * matrix of zeros gives zeros (eps > 0), one with a value that is not finite
+ * gives NaN. */
 int32_t conv_tp_orthogonalise(int32_t n_tensors, const void *const *in, void *const *out, const int64_t *batch,
                               const int32_t *rows, const int32_t *cols, const int32_t *dtype, int32_t steps, float eps,
                               float scale, void *workspace, int64_t workspace_bytes, void *stream);
