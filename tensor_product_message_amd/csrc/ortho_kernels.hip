@@ -25,7 +25,10 @@ namespace {
 typedef _Float16 E;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScale = 4096.0f;
-constexpr int kPad = 64, kDepth = 32;
+constexpr int kPad = 64;
+// of k a tile: 64 where tiles are small and a product's few steps are its time, 32 where two workgroups share a CU's LDS
+template <int Side>
+constexpr int kDepthOf = Side == 64 ? 64 : 32;
 constexpr int kMostGroups = 32;     // tensors of one launch
 constexpr int kMostSums = 512;      // shares of a matrix's sum of squares
 constexpr int kLeastCut = 256;      // of the long side, a share of A
@@ -58,10 +61,13 @@ struct Groups {
 
 static_assert(sizeof(Groups) <= 4000);      // with a launch's other argument
 
+// The group of a workgroup: a lane compares each group's first with it (a search would read one after the other, and
+// these kernels are short).
 __device__ __forceinline__ int group_of(const Groups& p, unsigned id) {
-    int k = 0;
-    while (k + 1 < p.n && id >= p.first[k + 1]) ++k;
-    return k;
+    static_assert(kMostGroups < 64);
+    const int lane = threadIdx.x & 63;
+    const bool behind = lane + 1 < p.n && id >= p.first[lane + 1];
+    return __builtin_amdgcn_readfirstlane(__popcll(__ballot(behind)));
 }
 
 // Calls f(T{}) for an element type's code.
@@ -210,7 +216,7 @@ __device__ __forceinline__ TileAt triangle_at(unsigned id) {
 // symmetric: the tiles on and below the diagonal are computed and written twice.
 template <int K, int Side>
 __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
-    constexpr int MT = Side / 64;       // 32 x 32 tiles of a wave, in each direction
+    constexpr int MT = Side / 64, kDepth = kDepthOf<Side>;      // MT: 32 x 32 tiles of a wave, in each direction
     constexpr bool kSymmetric = K == kGram || K == kPoly, kAlong = kSymmetric;      // kAlong: the second operand
     typedef Tile<E, 2, true, Side, kDepth> TA;
     typedef Tile<E, 2, kAlong, Side, kDepth> TB;
