@@ -93,6 +93,7 @@ __global__ __launch_bounds__(256) void k_squares(Groups p) {
     of_type(g.dtype, [&](auto type) {
         typedef decltype(type) T;
         const T* x = static_cast<const T*>(g.in) + from;
+#pragma unroll 4
         for (long i = first + (long)threadIdx.x * kVec<T>; i < last; i += 256 * kVec<T>) {
             if (i + kVec<T> <= last) {
                 const vec_t<T> v = *reinterpret_cast<const typename Vec<T>::unaligned*>(x + i);
@@ -383,7 +384,7 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
         g.l = (int)div_up(max(rows[k], cols[k]), kPad) * kPad;
         if (rows[k] == 0 || cols[k] == 0) g.batch = 0;
         const long size = (long)rows[k] * cols[k];
-        g.chunks = (unsigned)max(1L, min((long)kMostSums, size / 16384));
+        g.chunks = (unsigned)max(1L, min((long)kMostSums, size / 4096));
         for (long* q : {&g.x[0], &g.x[1], &g.a, &g.b}) {
             *q = at;
             at += 2 * g.batch * (long)g.s * (q < &g.a ? g.l : g.s);

@@ -40,7 +40,7 @@ def _code(act: str) -> int:
 
 def linear_fwd(x, w, bias=None, residual=None, act: str = "none", lmax: int = 0, keep_z: bool = False, out=None):
     """(y, z) with z = x w^T + bias and y = act(z) + residual; z is None unless keep_z (a backward pass through an
-    activation takes it).  out: y to write into, which may be residual."""
+    activation takes it).  out: y to write into, which may be residual, but must not overlap x or w."""
     return dense_native().linear_fwd(x, w, bias, residual, _code(act), lmax, False, keep_z, out)
 
 

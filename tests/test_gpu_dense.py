@@ -401,6 +401,32 @@ def test_strides_shapes_outputs_and_empty(ctp, dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer", [(7, 64, 40), (200, 64, 64), (300, 512, 512), (1600, 1000, 1000), (30000, 64, 320)])
+def test_storage_at_any_element(ctp, dev, rows, inner, outer, dtype):
+    """Every array one element behind a 16-byte place: the results of arrays at such places."""
+    c = Case(rows, inner, outer, dtype, "silu", residual=True)
+    tell("odd places", rows, inner, outer, dtype)
+    even = to(dev, c.x, c.w, c.bias, c.residual, c.grad, c.u)
+
+    def odd(t):
+        s = torch.empty(t.numel() + 1, dtype=dtype, device=dev)[1:].view(t.shape)
+        return s.copy_(t)
+
+    results = []
+    for place in (lambda t: t, odd):
+        x, w, b, r, grad, u = (place(t) for t in even)
+        out = place(torch.zeros(rows, outer, dtype=dtype, device=dev))
+        y, z = ctp.linear_fwd(x, w, b, r, act="silu", keep_z=True, out=out)
+        assert y is out or y.data_ptr() == out.data_ptr()
+        z = place(z)
+        results.append([y, z, *ctp.linear_bwd(grad, x, w, z, act="silu"), *ctp.linear_bwd_bwd(u, grad, x, w, z, act="silu")])
+    k = max(inner, outer, rows)
+    for a, b in zip(*results):
+        # other tiles may sum in another order
+        assert float((a - b).abs().max()) <= (2 * U[dtype] + 12 * k ** 0.5 * EPS32) * float(b.abs().max()) * 2
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("gated", [False, True])
 def test_extreme_values(ctp, dev, dtype, gated):
     """Values outside one row do not reach another; derivatives far out are 0 or 1."""
