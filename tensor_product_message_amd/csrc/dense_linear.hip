@@ -980,7 +980,7 @@ hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t 
     const long n = Pairs ? 2L * g.n : g.n;
     if constexpr (kParts == 1) {
         if (direct<AlongA, AlongB>(g)) {
-            if (div_up(g.m, 256) * div_up(n, 256) * outer >= kFill * 3 / 8) return run_direct<AlongA, AlongB, 256, Pairs>(g, outer, epi, st);
+            if (g.m > 128 && n > 128 && div_up(g.m, 256) * div_up(n, 256) * outer >= kFill * 3 / 8) return run_direct<AlongA, AlongB, 256, Pairs>(g, outer, epi, st);
             if (g.m > 64 && n > 64 && div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
         }
     }
