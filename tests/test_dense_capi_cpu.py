@@ -115,6 +115,15 @@ def test_workspaces_at_the_limits_are_counted_in_64_bits(capi, L):
             assert n.value >= (2 ** 31 - 1) * 2 ** 20 * 4 * (1 + gated)
 
 
+def test_workspaces_without_rows(capi, L):
+    n = ctypes.c_int64()
+    for kw in (dict(), dict(gated=1), dict(act=0), dict(act=0, lmax=2)):
+        for dtype in (0, 1, 2):
+            p = linear(capi, n_rows=0, inner=2049, outer=4096, x_stride=2 ** 16, grad_stride=2 ** 16, dtype=dtype, **kw)
+            for size in (L.conv_tp_linear_fwd_workspace, L.conv_tp_linear_bwd_workspace, L.conv_tp_linear_bwd_bwd_workspace):
+                assert size(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK and n.value >= 0
+
+
 def ortho(L, ins=(A, B), outs=(C, D), batch=(1, 2), rows=(4, 5), cols=(6, 7), dtype=(0, 1), steps=5, eps=1e-7, scale=1.0,
           ws=B, nbytes=BIG, n=None):
     k = len(batch) if batch else 2
