@@ -86,9 +86,11 @@ ctp::LinearArgs linear_args(const conv_tp_linear_problem* p) {
     a.dtype = p->dtype;
     a.act = p->act;
     a.gated = p->gated != 0;
-    a.x_stride = p->x_stride;
-    a.residual_stride = p->residual_stride;
-    a.grad_stride = p->grad_stride;
+    // one row has no next one: a stride that nothing reads, but tiles count with it
+    const bool one = p->n_rows <= 1;
+    a.x_stride = one ? comps_of(p) * p->inner : p->x_stride;
+    a.residual_stride = one ? comps_of(p) * p->outer : p->residual_stride;
+    a.grad_stride = one ? comps_of(p) * p->outer : p->grad_stride;
     return a;
 }
 

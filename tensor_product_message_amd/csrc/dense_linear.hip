@@ -338,12 +338,12 @@ struct EpiLinear {
     }
 };
 
-// h = act(x + bias[0]) (y + bias[1]), z the two sums
+// h = act(x + bias[0]) (y + bias[1]), z the two sums.  (Not marked as streams: a wave's rows are 64 bytes of 16-bit
+// values here, and half lines written around the cache are written twice, 451 MB for 403.)
 struct EpiGated {
     T *h, *z;
     const T* bias;
     int n, act;
-    bool stream;
     template <bool Whole, int R>
     __device__ __forceinline__ void run(const Place& p, float (&x)[R][V], float (&y)[R][V]) const {
         const Rows<Whole, R> rows{p.some, p.at, n};
@@ -352,8 +352,8 @@ struct EpiGated {
             rows.add(bias + n, y);
         }
         if (z != nullptr) {
-            rows.write(z + p.m * 2 * n, p.step * 2L * n, x, stream);
-            rows.write(z + p.m * 2 * n + n, p.step * 2L * n, y, stream);
+            rows.write(z + p.m * 2 * n, p.step * 2L * n, x, false);
+            rows.write(z + p.m * 2 * n + n, p.step * 2L * n, y, false);
         }
         with_act(act, [&](auto is) {
             float d1, d2;
@@ -365,7 +365,7 @@ struct EpiGated {
                     x[i][q] *= y[i][q];
                 }
         });
-        rows.write(h + p.m * n, (long)p.step * n, x, stream);
+        rows.write(h + p.m * n, (long)p.step * n, x, false);
     }
 };
 
@@ -1294,8 +1294,8 @@ hipError_t fwd(const LinearArgs& a, hipStream_t st) {
     const T *bias = static_cast<const T*>(a.bias), *residual = static_cast<const T*>(a.residual);
     float* parts = reinterpret_cast<float*>(ws + l.parts);
     const long row = (long)comps * a.outer;
-    const bool stream = streams_out(a.n_rows * row * (long)sizeof(T) * (1 + (z ? a.gated ? 2 : 1 : 0)));
-    if (a.gated) return run_gemm<true, true, true>(g, 1, EpiGated{y, z, bias, a.outer, a.act, stream}, parts, st);
+    if (a.gated) return run_gemm<true, true, true>(g, 1, EpiGated{y, z, bias, a.outer, a.act}, parts, st);
+    const bool stream = streams_out(a.n_rows * row * (long)sizeof(T) * (z ? 2 : 1));
     // without anything to do the epilogue's questions cost a layer that writes much a sixth of its time
     // (83325 x 64 -> 4352: 408 instead of 340 us)
     if (!z && !bias && !residual && a.act == kActNone)

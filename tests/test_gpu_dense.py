@@ -731,6 +731,29 @@ def test_rows_far_apart(ctp, dev, dtype):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_stride_of_a_single_row_is_not_looked_at(ctp, dev, dtype):
+    """Through the C ABI, where the stride of one row may be anything."""
+    import ctypes
+
+    from tensor_product_message_amd import _capi
+    L = _capi.dense_lib()
+    c = Case(1, 1024, 2048, dtype, "silu")
+    x, w, grad = to(dev, c.x, c.w, c.grad)
+    z = torch.zeros(1, 2048, dtype=dtype, device=dev)
+    want = ctp.linear_bwd(grad, x, w, z, act="silu")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for stride in (0, 8, -64):
+        prob = _capi.LinearProblem(1, stride, stride, stride, 0, 1024, 2048, DTYPES.index(dtype), 2, 0)
+        n = ctypes.c_int64()
+        assert L.conv_tp_linear_bwd_workspace(ctypes.byref(prob), ctypes.byref(n)) == 0
+        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        got = [torch.empty_like(t) for t in want]
+        st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert L.conv_tp_linear_bwd(ctypes.byref(prob), p(grad), p(x), p(w), p(z), *map(p, got), p(ws), n.value, st) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), stride
+
+
 def test_no_grad_and_frozen(ctp, dev):
     x, w, b = torch.randn(5, 8, device=dev), torch.randn(6, 8, device=dev), torch.randn(6, device=dev)
     want = torch.nn.functional.silu(x @ w.T + b)
