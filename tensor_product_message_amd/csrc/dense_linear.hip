@@ -1013,10 +1013,10 @@ hipError_t run_few(const Gemm& g, unsigned batches, const Epi& epi, hipStream_t 
 // 4096 -> 4096 bf16 take 17 us cut and 36 us whole.
 unsigned sum_cut(long m, long n, long k, long batches) {
     // a part's terms, and the least of a sum that is cut: 256 x 1024 -> 1024 takes 11 us cut and 8 us whole in bf16, 14
-    // and 25 in floats
-    constexpr long kTerms = kParts == 1 ? 512 : 256, kLeast = kParts == 1 ? 2048 : 768;
-    const long tiles = div_up(m, 64) * div_up(n, 64) * batches;
-    if (k < kLeast) return 1;
+    // and 25 in floats; of few tiles shorter sums too (108 x 684 -> 29 floats 16 and 23, 1503 x 512 -> 512 17 and 14)
+    constexpr long kTerms = kParts == 1 ? 512 : 256;
+    const long tiles = div_up(m, 64) * div_up(n, 64) * batches, least = kParts == 1 ? 2048 : tiles <= 64 ? 512 : 768;
+    if (k < least) return 1;
     return (unsigned)max(1L, min(kFill / max(1L, tiles), k / kTerms));
 }
 long sum_cut_bytes(long m, long n, long k, long batches) {
