@@ -1017,7 +1017,8 @@ unsigned sum_cut(long m, long n, long k, long batches) {
     constexpr long kTerms = kParts == 1 ? 512 : 256;
     const long tiles = div_up(m, 64) * div_up(n, 64) * batches, least = kParts == 1 ? 2048 : tiles <= 64 ? 512 : 768;
     if (k < least) return 1;
-    return (unsigned)max(1L, min(kFill / max(1L, tiles), k / kTerms));
+    // a CU holds three workgroups of the float tiles
+    return (unsigned)max(1L, min((kParts == 1 ? kFill : 3 * kFill / 2) / max(1L, tiles), k / kTerms));
 }
 long sum_cut_bytes(long m, long n, long k, long batches) {
     const long splits = sum_cut(m, n, k, batches);
