@@ -61,10 +61,10 @@ struct Tile {
     static constexpr int kBytes = Parts_ * kPlane * 2;
     typedef typename Frag<E>::type frag_t;
 
-    static __device__ __forceinline__ int chunk_of(int row, int c) {
+    static __host__ __device__ __forceinline__ int chunk_of(int row, int c) {
         return Depth == 128 ? c ^ (row & 15) : Depth == 64 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
     }
-    static __device__ __forceinline__ int unit_of(int k, int u) { return u ^ (Rows >= 128 ? (k & 3) << 1 : k & 2); }
+    static __host__ __device__ __forceinline__ int unit_of(int k, int u) { return u ^ (Rows >= 128 ? (k & 3) << 1 : k & 2); }
     // element offset of value (row, k)
     static __device__ __forceinline__ int at(int row, int k) {
         if constexpr (Along) return row * Depth + chunk_of(row, k >> 3) * 8 + (k & 7);
@@ -364,6 +364,13 @@ __device__ __forceinline__ void by_rows(const f32x16 (&acc)[NT][MT], float* slab
             f(32 * decltype(i)::value + r0 * kRows + lane / kLanes, kRows, n, x, y);
         }
     });
+}
+
+// Row r of a tile of pairs among B's rows: 32 of them, their partners `pair` rows on, the next 32, and so on.  Rows past
+// the last of `left` are the last one.
+__host__ __device__ __forceinline__ long pair_row(int r, int left, long pair) {
+    const int at = (r >> 6 << 5) + (r & 31);
+    return (at < left ? at : left - 1) + (r >> 5 & 1) * pair;
 }
 
 // Where workgroup `id` of `total` works: the workgroups of one of the 8 XCDs, which get every eighth, take

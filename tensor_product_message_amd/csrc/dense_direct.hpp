@@ -40,6 +40,16 @@ __device__ __forceinline__ unsigned lds_address(const void* p) {
     return (unsigned)reinterpret_cast<unsigned long>((const __attribute__((address_space(3))) void*)p);
 }
 
+// Bytes of the buffers that tiles are read from; places in them are held in 32 bits.
+constexpr long kBufferBytes = 0x7ffffff0;
+
+// Whether an operand's tiles may go this way: 16-byte pieces, whole in every row of n values, and rows so near each
+// other that all places of a tile of 256 of them, and of their partners `pair` rows on, lie in a buffer.
+inline bool comes_directly(const void* p, long ld, long batch, long n, long pair) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && batch % 8 == 0 && n % 8 == 0 && ld <= 1L << 21 &&
+           (pair + 256) * ld * 2 <= kBufferBytes;
+}
+
 // The way of a Tile<E, NParts, Along, Rows, Depth>: each wave brings kLoads 1-KB pieces of each plane.  A lane's place in
 // LDS is given, so the order of the chunks in a row (see Tile) is made by where in memory the lane reads.
 template <bool Along, int Rows, int Depth, int Waves>
@@ -48,25 +58,30 @@ struct Direct {
     static_assert(kLoads * Waves * 64 * 8 == Rows * Depth);
     typedef Tile<_Float16, 1, Along, Rows, Depth> tile_t;       // (the places are the same for any 16-bit type)
     static constexpr unsigned kNowhere = 0xfffffff0u;       // past the end of any buffer
+    static constexpr int kInRow = (Along ? Depth : Rows) / 8;
     unsigned at[kLoads];        // byte offsets from the tile's first value
     int k[kLoads];              // Along: the chunk's first k
 
-    // row_of(r): where row r of the tile lies among the operand's rows (Along).
+    // Along: the first k of a chunk.
+    static __host__ __device__ __forceinline__ int first_k(int chunk) { return 8 * tile_t::chunk_of(chunk / kInRow, chunk % kInRow); }
+    // Bytes from the tile's first value to a chunk's.  row_of(r): where row r of the tile lies among the operand's rows
+    // (Along).
+    template <class F>
+    static __host__ __device__ __forceinline__ long place(int chunk, long ld, F&& row_of) {
+        const int r = chunk / kInRow, c = chunk % kInRow;
+        if constexpr (Along) return (row_of(r) * ld + first_k(chunk)) * 2;
+        return (r * ld + 16 * tile_t::unit_of(r, c >> 1) + 8 * (c & 1)) * 2;
+    }
+
+    // The operand is one that comes_directly.
     template <class F>
     __device__ __forceinline__ void init(long ld, F&& row_of) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int chunk = (wave * kLoads + j) * 64 + lane;
-            if constexpr (Along) {
-                const int row = chunk / (Depth / 8), c = chunk % (Depth / 8);
-                k[j] = 8 * tile_t::chunk_of(row, c);
-                at[j] = (unsigned)((row_of(row) * ld + k[j]) * 2);
-            } else {
-                const int kr = chunk / (Rows / 8), c = chunk % (Rows / 8);
-                at[j] = (unsigned)((kr * ld + 16 * tile_t::unit_of(kr, c >> 1) + 8 * (c & 1)) * 2);
-                k[j] = 0;
-            }
+            at[j] = (unsigned)place(chunk, ld, row_of);
+            k[j] = Along ? first_k(chunk) : 0;
         }
     }
     // left: k that are there from the tile's first on (Along; Across leaves it to the buffer's end)

@@ -41,7 +41,7 @@ struct Gemm {
     int n;                      // Pairs: columns of one half
     long m_read;                // Across: values of a row of A, of B, that may be read, at least m, n
     int n_read;
-    long pair;                  // Pairs: elements of B from a column to its partner
+    long pair;                  // Pairs: rows of B from a column's to its partner's
     long k_split;               // k of a split, a multiple of kDepth
     unsigned splits, tiles_m, tiles_n, total;
 };
@@ -177,7 +177,7 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
         // rows past the last give results that nobody stores
         auto row_a = [&](int r) { return (long)min(r, m_left - 1); };
         auto row_b = [&](int r) {
-            if constexpr (Pairs) return (long)min((r >> 6 << 5) + (r & 31), n_left - 1) + (r >> 5 & 1) * g.pair;
+            if constexpr (Pairs) return pair_row(r, n_left, g.pair);
             return (long)min(r, n_left - 1);
         };
         const bool whole_m = m_left == BM, whole_n = n_left >= (Pairs ? BN / 2 : BN);
@@ -283,17 +283,17 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
         // rows past the last give results that nobody stores
         da.init(g.a_ld, [&](int r) { return (long)min(r, m_left - 1); });
         db.init(g.b_ld, [&](int r) {
-            if constexpr (Pairs) return (long)min((r >> 6 << 5) + (r & 31), n_left - 1) + (r >> 5 & 1) * g.pair;
+            if constexpr (Pairs) return pair_row(r, n_left, g.pair);
             return (long)min(r, n_left - 1);
         });
         auto issue = [&](int step, int buffer) {
             const int k = step * kDepth;
             // Across: what lies past the last k is the buffer's end
             const long rows = min(k_end - k, kDepth) - 1;
-            const long a_left = AlongA ? 0x7ffffff0L : 2 * (rows * g.a_ld + min((long)Side, g.m_read - m0));
-            const long b_left = AlongB ? 0x7ffffff0L : 2 * (rows * g.b_ld + min(Side, g.n_read - n0));
-            da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), (unsigned)min(a_left, 0x7ffffff0L)), base + buffer * kBuffer, k_end - k);
-            db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), (unsigned)min(b_left, 0x7ffffff0L)),
+            const long a_left = AlongA ? kBufferBytes : 2 * (rows * g.a_ld + min((long)Side, g.m_read - m0));
+            const long b_left = AlongB ? kBufferBytes : 2 * (rows * g.b_ld + min(Side, g.n_read - n0));
+            da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), (unsigned)min(a_left, kBufferBytes)), base + buffer * kBuffer, k_end - k);
+            db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), (unsigned)min(b_left, kBufferBytes)),
                      base + buffer * kBuffer + TA::kBytes, k_end - k);
         };
         f32x16 acc[NT][MT] = {};
@@ -948,15 +948,11 @@ hipError_t run_direct(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Whether tiles may go to LDS directly: 16-byte pieces, whole in every row, and rows so near each other that a tile's
-// offsets fit into 31 bits.
-template <bool AlongA, bool AlongB>
+// Whether tiles may go to LDS directly (a gated layer's of 2^30 values or more a matrix do not: staged tiles).
+template <bool AlongA, bool AlongB, bool Pairs>
 bool direct(const Gemm& g) {
-    const auto whole = [](const T* p, long ld, long batch, long n) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % V == 0 && batch % V == 0 && n % V == 0 && ld <= 1L << 21;
-    };
-    return kParts == 1 && whole(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m_read) &&
-           whole(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n_read);
+    return kParts == 1 && comes_directly(g.a, g.a_ld, g.a_batch, AlongA ? g.k : g.m_read, 0) &&
+           comes_directly(g.b, g.b_ld, g.b_batch, AlongB ? g.k : (long)g.n_read, Pairs ? g.pair : 0);
 }
 
 #if CTP_DENSE_TYPE == 0
@@ -979,7 +975,7 @@ template <bool AlongA, bool AlongB, bool Pairs, class Epi>
 hipError_t run_tiles(const Gemm& g, unsigned outer, const Epi& epi, hipStream_t st) {
     const long n = Pairs ? 2L * g.n : g.n;
     if constexpr (kParts == 1) {
-        if (direct<AlongA, AlongB>(g)) {
+        if (direct<AlongA, AlongB, Pairs>(g)) {
             if (g.m > 128 && n > 128 && div_up(g.m, 256) * div_up(n, 256) * outer >= kFill * 3 / 8) return run_direct<AlongA, AlongB, 256, Pairs>(g, outer, epi, st);
             if (g.m > 64 && n > 64 && div_up(g.m, 128) * div_up(n, 128) * outer >= kFill / 4) return run_direct<AlongA, AlongB, 128, Pairs>(g, outer, epi, st);
         }

@@ -261,11 +261,11 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
         const unsigned to = base + buffer * kBuffer;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            da.issue(buffer_at(pa + q * a_step + k0, 0x7ffffff0u), to + q * TA::kPlane * 2, kDepth);
+            da.issue(buffer_at(pa + q * a_step + k0, (unsigned)kBufferBytes), to + q * TA::kPlane * 2, kDepth);
             // Across: past the last column of a row lies the next row, past the last row's the buffer's end
             const E* from_b = pb + q * b_step + (kAlong ? k0 : (long)k0 * b_ld + n0);
-            const long left = kAlong ? 0x7ffffff0L : 2 * ((long)(g.s - k0) * b_ld - n0);
-            db.issue(buffer_at(from_b, (unsigned)min(left, 0x7ffffff0L)), to + TA::kBytes + q * TB::kPlane * 2, kDepth);
+            const long left = kAlong ? kBufferBytes : 2 * ((long)(g.s - k0) * b_ld - n0);
+            db.issue(buffer_at(from_b, (unsigned)min(left, kBufferBytes)), to + TA::kBytes + q * TB::kPlane * 2, kDepth);
         }
     };
     f32x16 acc[MT][MT] = {};

@@ -1,0 +1,52 @@
+"""The dense operators on the GPU at sizes and values of which the documentation says something; forms and tolerances
+as in test_gpu_dense.py."""
+import pytest
+import torch
+
+from tests.test_gpu_dense import EPS32, act, close, normal, sum_error, tell
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def ctp(dev):
+    import tensor_product_message_amd as t
+    return t
+
+
+@pytest.mark.parametrize("dtype,rows,inner,outer", [(torch.bfloat16, 70, 16384, 65536), (torch.float16, 200, 32768, 32768)])
+def test_gated_matrices_of_2_30_values(ctp, dev, dtype, rows, inner, outer):
+    """A column's partner lies 2^31 bytes on: columns of both halves, in the forward and the second backward pass."""
+    tell("large gated", dtype, rows, inner, outer)
+    g = torch.Generator().manual_seed(1)
+    x, u, grad = (normal(g, (rows, n), dtype) for n in (inner, inner, outer))
+    bias = normal(g, (2, outer), dtype, 0.5)
+    w = torch.empty(2, outer, inner, dtype=dtype, device=dev).normal_(0, inner ** -0.5, generator=torch.Generator(dev).manual_seed(2))
+    cols = torch.tensor([0, 1, 31, 32, 63, 64, 127, 128, outer // 2 + 5, outer - 64, outer - 33, outer - 1])
+    W = w[:, cols.to(dev)].double().cpu()
+    h, z = ctp.gated_linear_fwd(x.to(dev), w, bias.to(dev), keep_z=True)
+    e = sum_error(dtype, inner)
+    Z = [x.double() @ W[k].T + bias[k, cols].double() for k in (0, 1)]
+    ez = [e * (x.double().abs() @ W[k].abs().T + bias[k, cols].double().abs()) for k in (0, 1)]
+    f = act("silu", Z[0])[0]
+    ef = 1.13 * ez[0] + 16 * EPS32 * (1 + Z[0].abs())
+    for k in (0, 1):
+        close(f"z[{k}]", z[:, k][:, cols.to(dev)], Z[k], ez[k])
+    close("h", h[:, cols.to(dev)], f * Z[1], ef * Z[1].abs() + f.abs() * ez[1] + ef * ez[1] + 4 * EPS32 * (f * Z[1]).abs())
+    g_grad = ctp.gated_linear_bwd_bwd(u.to(dev), grad.to(dev), x.to(dev), w, z, needs=(True, False, False, False))[0]
+    a, b = (z[:, k][:, cols.to(dev)].double().cpu() for k in (0, 1))
+    f, d1, _ = act("silu", a)
+    va, vb = (u.double() @ W[k].T for k in (0, 1))
+    ea, eb = (e * (u.double().abs() @ W[k].abs().T) for k in (0, 1))
+    one = 32 * EPS32 * (1 + a.abs()) ** 2
+    close("g_grad", g_grad[:, cols.to(dev)], va * b * d1 + vb * f,
+          ea * (b * d1).abs() + eb * f.abs() + one * (va.abs() + ea) * b.abs() + one * (vb.abs() + eb))
+    del w, h, z, g_grad
+    torch.cuda.empty_cache()
