@@ -14,6 +14,7 @@
 #include "dense_direct.hpp"
 #include "dense_linear.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace ctp {
@@ -917,6 +918,7 @@ __global__ __launch_bounds__(256) void k_join(Join first, Join second) {
         if (const hipError_t e_ = (call); e_ != hipSuccess) return e_; \
     } while (0)
 
+// (Sizes here are compared by std::min and max<long>: those without std are int's on the host.)
 constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
 constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 
@@ -936,7 +938,7 @@ template <bool AlongA, bool AlongB, int BM, int BN, int WM, bool Pairs, class Ep
 hipError_t run_staged(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
     if (!set_tiles(g, BM, Pairs ? BN / 2 : BN, outer)) return hipErrorInvalidValue;
     if (g.total == 0) return hipSuccess;
-    k_gemm<AlongA, AlongB, BM, BN, WM, Pairs><<<dim3((unsigned)min((long)g.total, max_groups(256))), 256, 0, st>>>(g, epi);
+    k_gemm<AlongA, AlongB, BM, BN, WM, Pairs><<<dim3((unsigned)std::min<long>(g.total, max_groups(256))), 256, 0, st>>>(g, epi);
     return hipGetLastError();
 }
 template <bool AlongA, bool AlongB, int Side, bool Pairs, class Epi>
@@ -944,7 +946,7 @@ hipError_t run_direct(Gemm g, unsigned outer, const Epi& epi, hipStream_t st) {
     if (!set_tiles(g, Side, Pairs ? Side / 2 : Side, outer)) return hipErrorInvalidValue;
     if (g.total == 0) return hipSuccess;
     k_gemm_direct<AlongA, AlongB, Side, Pairs>
-        <<<dim3((unsigned)min((long)g.total, max_groups(2 * Side))), 2 * Side, 0, st>>>(g, epi);
+        <<<dim3((unsigned)std::min<long>(g.total, max_groups(2 * Side))), 2 * Side, 0, st>>>(g, epi);
     return hipGetLastError();
 }
 
@@ -960,7 +962,7 @@ template <int Blocks, bool AlongB, bool Pairs, class Epi>
 hipError_t run_rows(Gemm g, unsigned batches, const Epi& epi, hipStream_t st) {
     // columns are cut into groups where the rows alone would leave the card empty
     const long cols = Pairs ? 32 : 64, tiles = div_up(g.n, cols), rows = div_up(g.m, 128) * batches;
-    const long groups = max(1L, min(tiles, div_up(4 * kFill, rows)));
+    const long groups = std::max<long>(1L, std::min<long>(tiles, div_up(4 * kFill, rows)));
     const long per = div_up(tiles, groups);
     if (!set_tiles(g, 128, per * cols, batches)) return hipErrorInvalidValue;
     if (g.total > max_groups(256)) return hipErrorInvalidValue;
@@ -1014,7 +1016,7 @@ unsigned sum_cut(long m, long n, long k, long batches) {
     const long tiles = div_up(m, 64) * div_up(n, 64) * batches, least = kParts == 1 ? 2048 : tiles <= 64 ? 512 : 768;
     if (k < least) return 1;
     // a CU holds three workgroups of the float tiles
-    return (unsigned)max(1L, min((kParts == 1 ? kFill : 3 * kFill / 2) / max(1L, tiles), k / kTerms));
+    return (unsigned)std::max<long>(1L, std::min<long>((kParts == 1 ? kFill : 3 * kFill / 2) / std::max<long>(1L, tiles), k / kTerms));
 }
 long sum_cut_bytes(long m, long n, long k, long batches) {
     const long splits = sum_cut(m, n, k, batches);
@@ -1038,7 +1040,7 @@ hipError_t run_gemm(Gemm g, unsigned batches, const Epi& epi, float* parts, hipS
     g.splits = (unsigned)div_up(g.k, g.k_split);
     if (const hipError_t e = run_tiles<AlongA, AlongB, false>(g, batches * g.splits, EpiPart{parts, g.m * width, width}, st)) return e;
     const long threads = batches * g.m * div_up(n, V);
-    k_finish<Pairs><<<dim3((unsigned)min(div_up(threads, 256), 4 * kFill)), 256, 0, st>>>(parts, g.splits, (int)g.m, n, batches, epi);
+    k_finish<Pairs><<<dim3((unsigned)std::min<long>(div_up(threads, 256), 4 * kFill)), 256, 0, st>>>(parts, g.splits, (int)g.m, n, batches, epi);
     return hipGetLastError();
 }
 
@@ -1052,13 +1054,13 @@ WeightCut weight_cut(const LinearArgs& a, bool twice) {
     const long comps = (long)(a.lmax + 1) * (a.lmax + 1), out = (long)a.outer * (a.gated ? 2 : 1);
     WeightCut c;
     // tiles of 128 where they and the rows are enough for the card, else smaller ones in more parts
-    const long most = max(1L, a.n_rows / (4 * kDepth)), tiles128 = div_up(out, 128) * div_up(a.inner, 128) * comps;
-    const bool wide = tiles128 >= 32 && tiles128 * min(most, 16L) >= kFill / 2;
+    const long most = std::max<long>(1L, a.n_rows / (4 * kDepth)), tiles128 = div_up(out, 128) * div_up(a.inner, 128) * comps;
+    const bool wide = tiles128 >= 32 && tiles128 * std::min<long>(most, 16L) >= kFill / 2;
     const long tiles = wide ? tiles128 : div_up(out, 64) * div_up(a.inner, 64) * comps;
-    long splits = max(1L, min(kFill / tiles, most));
-    splits = max(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
-    c.k_split = max(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
-    c.splits = (unsigned)max(1L, div_up(a.n_rows, c.k_split));
+    long splits = std::max<long>(1L, std::min<long>(kFill / tiles, most));
+    splits = std::max<long>(splits, div_up(a.n_rows, 1L << 30));       // a split's k is counted in 32 bits
+    c.k_split = std::max<long>(1L, div_up(div_up(a.n_rows, splits), kDepth)) * kDepth;
+    c.splits = (unsigned)std::max<long>(1L, div_up(a.n_rows, c.k_split));
     c.direct = c.splits == 1 && comps == 1 && !twice;
     return c;
 }
@@ -1085,9 +1087,9 @@ BiasCut bias_cut(long rows, int n) {
     c.groups = (unsigned)div_up(n, (long)c.across * V);
     const long high = 256 / c.across;
     // enough workgroups for the card, at most 512 chunks, which are joined afterwards; a lane reads 4 rows at once
-    const long most = max(1L, min(512L, div_up(4 * kFill, c.groups)));
-    c.chunk = max(1L, div_up(div_up(rows, most), 4 * high)) * 4 * high;
-    c.chunks = (unsigned)max(1L, div_up(rows, c.chunk));
+    const long most = std::max<long>(1L, std::min<long>(512L, div_up(4 * kFill, c.groups)));
+    c.chunk = std::max<long>(1L, div_up(div_up(rows, most), 4 * high)) * 4 * high;
+    c.chunks = (unsigned)std::max<long>(1L, div_up(rows, c.chunk));
     return c;
 }
 
@@ -1128,12 +1130,12 @@ Layout layout_of(const LinearArgs& a, bool second) {
     y.s = y.w + (p.w ? align256((a.lmax + 1) * p.outer * p.inner * (long)sizeof(T)) : 0);
     y.g_z = y.s + s_bytes;
     y.sums = y.g_z + (second ? s_bytes : 0);
-    y.parts = y.sums + align256(max(b.chunks, w.splits) * out * 4);
+    y.parts = y.sums + align256(std::max<long>(b.chunks, w.splits) * out * 4);
     // one product's parts at a time
     const bool small = small_bwd(a) && !second;
     long parts = w.direct && !small ? 0 : align256(w.splits * comps * out * a.inner * 4 * (second && act ? 2 : 1));
-    parts = max(parts, sum_cut_bytes(a.n_rows, a.inner, p.outer, comps));
-    if (second) parts = max(parts, sum_cut_bytes(a.n_rows, out, a.inner, comps));
+    parts = std::max<long>(parts, sum_cut_bytes(a.n_rows, a.inner, p.outer, comps));
+    if (second) parts = std::max<long>(parts, sum_cut_bytes(a.n_rows, out, a.inner, comps));
     y.bytes = y.parts + parts;
     return y;
 }
@@ -1147,7 +1149,7 @@ Pack weight_pack(const LinearArgs& a, long outer, long inner, T* to) {
     return Pack{static_cast<const T*>(a.w), to, a.lmax + 1, (long)out * a.inner, a.inner, (int)outer, out, a.inner, (int)inner};
 }
 hipError_t pack(const Pack& a, const Pack& b, hipStream_t st) {
-    const auto groups = [](const Pack& p) { return p.to ? (unsigned)min(div_up(p.n_i * p.n_j * (p.padded / V), 256), 8 * kFill) : 0; };
+    const auto groups = [](const Pack& p) { return p.to ? (unsigned)std::min<long>(div_up(p.n_i * p.n_j * (p.padded / V), 256), 8 * kFill) : 0; };
     if (groups(a) + groups(b) == 0) return hipSuccess;
     k_pack<<<groups(a) + groups(b), 256, 0, st>>>(a, b, groups(a));
     return hipGetLastError();
@@ -1252,7 +1254,7 @@ Join join_of(const float* parts, void* out, long size, int degrees, unsigned per
 hipError_t join(const Join& a, const Join& b, hipStream_t st) {
     const long groups = (long)a.groups * a.degrees + (long)b.groups * b.degrees;
     if (groups == 0) return hipSuccess;
-    k_join<<<dim3((unsigned)min(groups, max_groups(256))), 256, 0, st>>>(a, b);
+    k_join<<<dim3((unsigned)std::min<long>(groups, max_groups(256))), 256, 0, st>>>(a, b);
     return hipGetLastError();
 }
 
@@ -1316,7 +1318,7 @@ hipError_t both_small(const LinearArgs& a, const WeightCut& c, float* sums, floa
     const long total = (long)of_w.total + of_x.total;
     if (total == 0) return hipSuccess;
     if (of_w.total >= max_groups(256)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)min(total, max_groups(256)));
+    const dim3 grid((unsigned)std::min<long>(total, max_groups(256)));
     const Curve curve{static_cast<const T*>(a.z), a.outer, a.act, sums};
     const EpiPart to_w = weight_epilogue(a, parts);
     const EpiPlain to_x = input_epilogue(a, a.d_x);

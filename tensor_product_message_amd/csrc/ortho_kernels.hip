@@ -19,6 +19,8 @@
 // All matrices of a call go through the same launches, three a step.
 #include "dense_direct.hpp"
 
+#include <algorithm>
+
 namespace ctp {
 namespace {
 
@@ -368,6 +370,7 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
 constexpr long align256(long bytes) { return (bytes + 255) & ~255L; }
 constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 
+// (As in dense_linear.hip: min and max without std are int's on the host.)
 long triangle(long tiles) { return tiles * (tiles + 1) / 2; }
 
 // Places of the tensors from `first` on (at most kMostGroups) and the bytes they take.
@@ -380,11 +383,11 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
         g.rows = rows[k], g.cols = cols[k];
         g.batch = (unsigned)batch[k];
         g.tall = rows[k] > cols[k];
-        g.s = (int)div_up(min(rows[k], cols[k]), kPad) * kPad;
-        g.l = (int)div_up(max(rows[k], cols[k]), kPad) * kPad;
+        g.s = (int)div_up(std::min<long>(rows[k], cols[k]), kPad) * kPad;
+        g.l = (int)div_up(std::max<long>(rows[k], cols[k]), kPad) * kPad;
         if (rows[k] == 0 || cols[k] == 0) g.batch = 0;
         const long size = (long)rows[k] * cols[k];
-        g.chunks = (unsigned)max(1L, min((long)kMostSums, size / 4096));
+        g.chunks = (unsigned)std::max<long>(1L, std::min<long>(kMostSums, size / 4096));
         for (long* q : {&g.x[0], &g.x[1], &g.a, &g.b}) {
             *q = at;
             at += 2 * g.batch * (long)g.s * (q < &g.a ? g.l : g.s);
@@ -398,12 +401,12 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
     p.wide = tiles >= 256;
     // A's sums are cut where a long side would keep few workgroups busy for long
     for (int k = 0; k < p.n; ++k) terms += p.g[k].batch * triangle(div_up(p.g[k].s, p.wide ? 128 : 64)) * p.g[k].l;
-    const long cut = max((long)kLeastCut, div_up(terms, 1024));
+    const long cut = std::max<long>(kLeastCut, div_up(terms, 1024));
     for (int k = 0; k < p.n; ++k) {
         Group& g = p.g[k];
-        g.splits = (unsigned)max(1L, g.l / cut);
+        g.splits = (unsigned)std::max<long>(1L, g.l / cut);
         g.cut = (int)div_up(div_up(g.l, g.splits), kPad) * kPad;
-        g.splits = (unsigned)max(1L, div_up(g.l, g.cut));
+        g.splits = (unsigned)std::max<long>(1L, div_up(g.l, g.cut));
         g.parts = at / 2;       // a float for two E; at is a multiple of the padding's square
         if (g.splits > 1) at += 2 * g.batch * g.splits * (long)g.s * g.s;
     }
@@ -480,7 +483,7 @@ hipError_t run(Groups& p, int steps, hipStream_t st) {
 long ortho_workspace(int n_tensors, const long* batch, const int* rows, const int* cols) {
     Groups p;
     long most = 0;
-    for (int k = 0; k < n_tensors; k += kMostGroups) most = max(most, lay_out(p, k, n_tensors, batch, rows, cols));
+    for (int k = 0; k < n_tensors; k += kMostGroups) most = std::max<long>(most, lay_out(p, k, n_tensors, batch, rows, cols));
     return most;
 }
 

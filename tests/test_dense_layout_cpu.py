@@ -1,0 +1,52 @@
+"""How the dense operators lay out their workspaces, without a GPU."""
+import ctypes
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def capi():
+    from tensor_product_message_amd import _capi
+    if not os.path.exists(_capi.LIB_PATH):
+        from tensor_product_message_amd.build import build
+        build(verbose=False)
+    return _capi
+
+
+def ortho_workspace(capi, shapes):
+    n, arr = ctypes.c_int64(-1), lambda t, k: (t * len(shapes))(*(s[k] for s in shapes))  # noqa: E731
+    status = capi.dense_lib().conv_tp_orthogonalise_workspace(len(shapes), arr(ctypes.c_int64, 0), arr(ctypes.c_int32, 1),
+                                                              arr(ctypes.c_int32, 2), ctypes.byref(n))
+    assert status == capi.CTP_OK
+    return n.value
+
+
+@pytest.mark.parametrize("shapes", [[(65536, 3, 2)], [(1024, 1024, 1024)], [(60000, 3, 2)], [(1, 131072, 4096)], [(1, 131072, 131072)],
+                                    [(1, 16384, 8192)] * 7, [(4, 2048, 8192)] * 20, [(1, 64, 64)] * 31 + [(200, 1000, 1500)] * 5])
+def test_workspace_of_many_matrices_is_counted_in_64_bits(capi, shapes):
+    pad = lambda n: (n + 63) // 64 * 64  # noqa: E731
+    least = 0
+    for first in range(0, len(shapes), 32):     # a launch's tensors
+        # X, the next X, A and b A + c A A of every matrix, 32 bits a value
+        least = max(least, sum(8 * b * (pad(r) * pad(c) + pad(min(r, c)) ** 2) for b, r, c in shapes[first:first + 32]))
+    n = ortho_workspace(capi, shapes)
+    assert least <= n <= 40 * least
+    assert least > 2 ** 31 or shapes[0] == (1, 131072, 4096)
+
+
+@pytest.mark.parametrize("rows,lmax,act,inner,outer", [(5, 1, 0, 16384, 16384), (300, 3, 0, 65536, 2048), (64, 1, 0, 131072, 131072),
+                                                       (40, 0, 2, 16384, 16384), (7, 0, 1, 2 ** 20, 1024), (65, 0, 4, 65536, 65536)])
+@pytest.mark.parametrize("gated", [0, 1])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_workspace_of_large_matrices_is_counted_in_64_bits(capi, rows, lmax, act, inner, outer, gated, dtype):
+    """The parts of d_w: one a component, of the second pass one of each of its two products, in fp32."""
+    if gated and lmax:
+        return
+    L, n, comps = capi.dense_lib(), ctypes.c_int64(), (lmax + 1) ** 2
+    p = capi.LinearProblem(rows, comps * inner, comps * outer, comps * outer, lmax, inner, outer, dtype, act, gated)
+    matrix = 4 * inner * outer * (1 + gated)
+    assert L.conv_tp_linear_bwd_workspace(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK
+    assert n.value >= (comps * matrix if lmax else 0)
+    assert L.conv_tp_linear_bwd_bwd_workspace(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK
+    assert n.value >= (comps if lmax else 2) * matrix >= 2 ** 31

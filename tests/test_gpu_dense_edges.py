@@ -3,7 +3,7 @@ as in test_gpu_dense.py."""
 import pytest
 import torch
 
-from tests.test_gpu_dense import EPS32, act, close, normal, sum_error, tell
+from tests.test_gpu_dense import EPS32, act, close, newton_schulz, normal, sum_error, tell
 
 pytestmark = pytest.mark.gpu
 
@@ -49,4 +49,47 @@ def test_gated_matrices_of_2_30_values(ctp, dev, dtype, rows, inner, outer):
     close("g_grad", g_grad[:, cols.to(dev)], va * b * d1 + vb * f,
           ea * (b * d1).abs() + eb * f.abs() + one * (va.abs() + ea) * b.abs() + one * (vb.abs() + eb))
     del w, h, z, g_grad
+    torch.cuda.empty_cache()
+
+
+def test_gradients_of_matrices_beyond_2_gib(ctp, dev):
+    """d_w's parts, one a component, of 4 GiB; the second pass's, one of each of its products, of 2 GiB each."""
+    tell("large parts")
+    g = torch.Generator().manual_seed(3)
+    inner = outer = 16384
+    rows, dtype = 20, torch.bfloat16
+    cols = torch.tensor([0, 1, 63, 64, 8191, 16383])
+    x, grad = normal(g, (rows, 4, inner), dtype), normal(g, (rows, 4, outer), dtype)
+    w = torch.empty(2, outer, inner, dtype=dtype, device=dev).normal_(0, inner ** -0.5, generator=torch.Generator(dev).manual_seed(4))
+    d_w = ctp.linear_bwd(grad.to(dev), x.to(dev), w, lmax=1, needs=(False, True, False))[1]
+    for degree, comps in ((0, slice(0, 1)), (1, slice(1, 4))):
+        X, G = x[:, comps].double().reshape(-1, inner), grad[:, comps][..., cols].double().reshape(-1, len(cols))
+        close(f"d_w[{degree}]", d_w[degree][cols.to(dev)], G.T @ X, sum_error(dtype, 3 * rows * 7) * (G.abs().T @ X.abs()))
+    del d_w
+    x, u, grad, z = (normal(g, (rows, n), dtype) for n in (inner, inner, outer, outer))
+    g_w = ctp.linear_bwd_bwd(u.to(dev), grad.to(dev), x.to(dev), w[0], z.to(dev), act="silu", needs=(False, False, True, False))[2]
+    W, X, V, G, Z = (t.double() for t in (w[0][cols.to(dev)].cpu(), x, u, grad[:, cols], z[:, cols]))
+    _, d1, d2 = act("silu", Z)
+    v, ev = V @ W.T, sum_error(dtype, inner) * (V.abs() @ W.abs().T)
+    one, half = 32 * EPS32 * (1 + Z.abs()) ** 2, 2.0 ** -8
+    gz, s = v * G * d2, G * d1
+    ez = ev * (G * d2).abs() + one * (v.abs() + ev) * G.abs()
+    ez, es = ez + half * (gz.abs() + ez), half * s.abs() + one * G.abs()
+    e = sum_error(dtype, 2 * rows * 7)
+    close("g_w", g_w[cols.to(dev)], gz.T @ X + s.T @ V,
+          (ez + e * (gz.abs() + ez)).T @ X.abs() + (es + e * (s.abs() + es)).T @ V.abs())
+    del w, g_w
+    torch.cuda.empty_cache()
+
+
+def test_orthogonalise_beyond_2_gib(ctp, dev):
+    """A workspace of more than 2^31 bytes; the bound is test_gpu_dense.py's."""
+    tell("large list")
+    m = torch.randn(150, 1024, 1024, device=dev, generator=torch.Generator(dev).manual_seed(5))
+    out, = ctp.orthogonalise([m])
+    for k in (0, 149):
+        ref, e = newton_schulz(m[k].cpu())
+        assert float((out[k].double().cpu() - ref).norm()) <= e + EPS32 * float(ref.norm()), k
+    assert torch.isfinite(out).all()
+    del m, out
     torch.cuda.empty_cache()
