@@ -385,7 +385,7 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
         g.tall = rows[k] > cols[k];
         g.s = (int)div_up(std::min<long>(rows[k], cols[k]), kPad) * kPad;
         g.l = (int)div_up(std::max<long>(rows[k], cols[k]), kPad) * kPad;
-        if (rows[k] == 0 || cols[k] == 0) g.batch = 0;
+        if (rows[k] == 0 || cols[k] == 0) g.batch = 0, g.s = g.l = kPad;      // nothing to do for it
         const long size = (long)rows[k] * cols[k];
         g.chunks = (unsigned)std::max<long>(1L, std::min<long>(kMostSums, size / 4096));
         for (long* q : {&g.x[0], &g.x[1], &g.a, &g.b}) {

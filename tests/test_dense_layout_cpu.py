@@ -1,8 +1,11 @@
-"""How the dense operators lay out their workspaces, without a GPU."""
+"""How the dense operators lay out their workspaces, without a GPU: through the C ABI, and on the host under
+AddressSanitizer and UndefinedBehaviorSanitizer (tests/sanitize/ortho_layout.hip)."""
 import ctypes
 import os
 
 import pytest
+
+from tests.test_sanitizers_cpu import HIPCC, ROOT, SAN_ENV, _run
 
 
 @pytest.fixture(scope="module")
@@ -50,3 +53,21 @@ def test_workspace_of_large_matrices_is_counted_in_64_bits(capi, rows, lmax, act
     assert n.value >= (comps * matrix if lmax else 0)
     assert L.conv_tp_linear_bwd_bwd_workspace(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK
     assert n.value >= (comps if lmax else 2) * matrix >= 2 ** 31
+
+
+def test_layout_of_orthogonalised_matrices_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "ortho_layout")
+    _run([HIPCC, "-O1", "-g", "-std=c++20", "--offload-arch=gfx950", "-ffp-contract=off", "-Wno-undefined-inline",
+          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Xarch_host", "-fsanitize=address",
+          "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fsanitize=integer-divide-by-zero",
+          "-Xarch_host", "-fno-sanitize-recover=all", os.path.join(ROOT, "tests", "sanitize", "ortho_layout.hip"), "-o", exe])
+    r = _run([exe], env=dict(os.environ, **SAN_ENV))
+    assert r.stdout.startswith("checked ") and "runtime error" not in r.stderr
+
+
+@pytest.mark.parametrize("shape", [(1, 0, 0), (1, 0, 5), (1, 5, 0), (2, 0, 0), (0, 5, 5), (0, 0, 0)])
+def test_empty_matrices(capi, shape):
+    assert ortho_workspace(capi, [shape]) == 0 and ortho_workspace(capi, [shape, (1, 3, 4), shape]) == ortho_workspace(capi, [(1, 3, 4)])
+    one, none = lambda t, x: (t * 1)(x), (ctypes.c_void_p * 1)(None)  # noqa: E731
+    sizes = one(ctypes.c_int64, shape[0]), one(ctypes.c_int32, shape[1]), one(ctypes.c_int32, shape[2])
+    assert capi.dense_lib().conv_tp_orthogonalise(1, none, none, *sizes, one(ctypes.c_int32, 0), 5, 1e-7, 1.0, None, 0, None) == capi.CTP_OK

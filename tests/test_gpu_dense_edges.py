@@ -93,3 +93,15 @@ def test_orthogonalise_beyond_2_gib(ctp, dev):
     assert torch.isfinite(out).all()
     del m, out
     torch.cuda.empty_cache()
+
+
+def test_orthogonalise_empty_matrices(ctp, dev):
+    """Matrices without rows, without columns or without either, by themselves and beside others."""
+    shapes = [(0, 0), (0, 5), (5, 0), (2, 0, 0), (0, 5, 5), (3, 0, 7)]
+    empty = [torch.empty(s, device=dev) for s in shapes]
+    for one, s in zip(empty, shapes):
+        assert ctp.orthogonalise([one])[0].shape == s
+    m = torch.randn(40, 70, device=dev)
+    want, = ctp.orthogonalise([m])
+    outs = ctp.orthogonalise([*empty, m, *empty])
+    assert torch.equal(outs[len(empty)], want) and [tuple(o.shape) for o in outs] == [*shapes, (40, 70), *shapes]
