@@ -22,6 +22,7 @@ Gated: w [2, outer, inner], bias [2, outer], z [..., 2, outer].
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from ._capi import dense_native
 
@@ -137,16 +138,24 @@ class LinearBackward(torch.autograd.Function):
                 None, None, None, None, None)
 
 
+def _no_derivatives() -> bool:
+    """Whether no derivative can be asked of a call, so that it may go past autograd: a level of forward mode works
+    without grad mode too (autograd refuses it: there is no forward-mode formula)."""
+    return not torch.is_grad_enabled() and getattr(forward_ad, "_current_level", 0) < 0
+
+
 def linear(x, w, bias=None, residual=None, act: str = "none", lmax: int = 0):
-    """Differentiable linear_fwd: act(x w^T + bias) + residual (twice in x, as a loss on forces needs it)."""
-    if not torch.is_grad_enabled():
+    """Differentiable linear_fwd: act(x w^T + bias) + residual (twice in x, as a loss on forces needs it; not in
+    forward mode)."""
+    if _no_derivatives():
         return linear_fwd(x, w, bias, residual, act, int(lmax))[0]
     return LinearFunction.apply(x, w, bias, residual, act, int(lmax), False)
 
 
 def gated_linear(x, w, bias=None, act: str = "silu"):
-    """Differentiable gated_linear_fwd: act(x w[0]^T + bias[0]) (x w[1]^T + bias[1]) (twice in x)."""
-    if not torch.is_grad_enabled():
+    """Differentiable gated_linear_fwd: act(x w[0]^T + bias[0]) (x w[1]^T + bias[1]) (twice in x;
+    not in forward mode)."""
+    if _no_derivatives():
         return gated_linear_fwd(x, w, bias, act)[0]
     return LinearFunction.apply(x, w, bias, None, act, 0, True)
 
