@@ -240,8 +240,11 @@ struct Staged {
         }
     }
 
-    // Every value times act'(z).
-    __device__ __forceinline__ void curve(const Staged& z, int act) {
+    // Every value times act'(z).  Summed (Across): what that is before its rounding is added to the sums of the thread's
+    // columns, which are the same for all of its vectors.
+    template <bool Summed>
+    __device__ __forceinline__ void curve(const Staged& z, int act, float (&sum)[kVec<T>]) {
+        static_assert(!Summed || (!Along && Threads % kPerRow == 0));
         with_act(act, [&](auto is) {
             float f, d1, d2;
 #pragma unroll
@@ -249,11 +252,13 @@ struct Staged {
 #pragma unroll
                 for (int q = 0; q < kVec<T>; ++q) {
                     activation<decltype(is)::value>((float)z.v[i][q], f, d1, d2);
-                    v[i][q] = (T)((float)v[i][q] * d1);
+                    const float s = (float)v[i][q] * d1;
+                    if constexpr (Summed) sum[q] += s;
+                    v[i][q] = (T)s;
                 }
         });
     }
-    // Across: adds to the sums of the thread's columns, which are the same for all of its vectors.
+    // Across: the values as they are, added to those sums.
     __device__ __forceinline__ void add_columns(float (&sum)[kVec<T>]) const {
         static_assert(Along || Threads % kPerRow == 0);
 #pragma unroll

@@ -205,8 +205,9 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
                     if constexpr (Curved) sz.fix(m_left, step * kDepth, k_end);
                     sb.fix(n_left, step * kDepth, k_end);
                 }
-                if constexpr (Curved) sa.curve(sz, c.act);
-                if constexpr (Summed)
+                if constexpr (Curved)
+                    sa.template curve<Summed>(sz, c.act, sum);
+                else if constexpr (Summed)
                     if (sums) sa.add_columns(sum);
                 lds_barrier();
                 sa.store(la);

@@ -105,3 +105,25 @@ def test_orthogonalise_empty_matrices(ctp, dev):
     want, = ctp.orthogonalise([m])
     outs = ctp.orthogonalise([*empty, m, *empty])
     assert torch.equal(outs[len(empty)], want) and [tuple(o.shape) for o in outs] == [*shapes, (40, 70), *shapes]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,inner,outer", [(3000, 64, 64), (81, 100, 128), (600, 24, 7), (3000, 200, 300), (900, 1003, 1000)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_bias_sums_before_any_rounding(ctp, dev, dtype, rows, inner, outer, gated):
+    """Terms that cancel: what they are rounded to would not (each up to half a step of some 20, thousands of them)."""
+    tell("bias", dtype, rows, inner, outer, gated)
+    g = torch.Generator().manual_seed(6)
+    a, b = (torch.randint(-60, 61, (rows // 3, outer), generator=g).double() for _ in range(2))
+    grad = torch.cat([a, b, -(a + b)])[torch.randperm(rows, generator=g)].to(dtype)     # whole numbers below 128
+    z = normal(g, (2, outer) if gated else (outer,), dtype)
+    zs = z.expand(rows, *z.shape).contiguous()
+    x, w = normal(g, (rows, inner), dtype), normal(g, (2, outer, inner) if gated else (outer, inner), dtype, inner ** -0.5)
+    for name in ("silu", "gelu", "tanh"):
+        back = ctp.gated_linear_bwd if gated else ctp.linear_bwd
+        d_bias = back(grad.to(dev), x.to(dev), w.to(dev), zs.to(dev), act=name, needs=(True, True, True))[2]
+        Z, S = z.double(), grad.double().abs().sum(0)
+        f, d1, _ = act(name, Z[0] if gated else Z)
+        # a row's derivative is the same number in all rows, a term one rounding (gated: two) and the additions follow
+        slope = torch.stack([(Z[1] * d1).abs(), f.abs()]) if gated else d1.abs()
+        close(name, d_bias, torch.zeros_like(slope), (rows + 8) * EPS32 * S * slope * (1 + 2.0 ** -10))
