@@ -411,8 +411,20 @@ template <bool Gated>
 struct EpiSecond {
     const T *grad, *z;
     T *g_grad, *g_z, *s;
+    float* exact;       // g_z before its rounding, for the bias's sums; null: not wanted
     long grad_row;
     int n, act;
+    template <bool Whole>
+    __device__ __forceinline__ void write_exact(float* row, int at, const float (&x)[V]) const {
+#pragma unroll
+        for (int q = 0; q < V; q += 4) {
+            const vec_t<float> v{x[q], x[q + 1], x[q + 2], x[q + 3]};
+            if constexpr (Whole)
+                *reinterpret_cast<Vec<float>::unaligned*>(row + at + q) = v;
+            else if (at + q < n)
+                store_left<float>(row + at + q, n - at - q, v);
+        }
+    }
     template <bool Whole, int R>
     __device__ __forceinline__ void run(const Place& place, float (&x)[R][V], float (&y)[R][V]) const {
         // a row at a time: its many values would not all find registers
@@ -446,6 +458,10 @@ struct EpiSecond {
                 }
             });
             if (g_grad != nullptr) row.write(g_grad + m * n, 0, o, false);
+            if (exact != nullptr) {
+                write_exact<Whole>(exact + zr, place.at, p[0]);
+                if constexpr (Gated) write_exact<Whole>(exact + zr + n, place.at, pb[0]);
+            }
             if (g_z != nullptr) {
                 row.write(g_z + zr, 0, p, false);
                 if constexpr (Gated) row.write(g_z + zr + n, 0, pb, false);
@@ -777,6 +793,25 @@ __device__ __forceinline__ void write_rows(const Rows<Whole, R>& rows, T* to, lo
         if (r < rows.some) Rows<Whole, 1>{1, rows.at, rows.width}.write(to + r * step, 0, reinterpret_cast<const float(&)[1][V]>(x[r]), false);
 }
 
+// The lanes' sums of N columns of H halves of n, `across` lanes beside each other, added over the workgroup's rows in
+// their order.  part: 256 H N floats.
+template <int H, int N>
+__device__ __forceinline__ void put_sums(const float (&sum)[H][N], float* part, int across, int n, float* to) {
+    const int tx = threadIdx.x % across, ty = threadIdx.x / across, high = 256 / across;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int q = 0; q < N; ++q) part[((h * high + ty) * N + q) * across + tx] = sum[h][q];
+    lds_barrier();
+    for (int i = threadIdx.x; i < H * N * across; i += 256) {
+        const int h = i / (N * across), c = i % (N * across), col = blockIdx.x * across * N + c;
+        if (col >= n) continue;
+        float s = 0.0f;
+        for (int r = 0; r < high; ++r) s += part[((h * high + r) * N + c % N) * across + c / N];
+        to[h * n + col] = s;
+    }
+}
+
 // Whole: n is whole vectors.
 template <bool Gated, bool Whole>
 __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
@@ -826,20 +861,37 @@ __global__ __launch_bounds__(256) void k_act_bwd(ActBwd p) {
                 if constexpr (Gated) sum[1][q] += u[i][q];
             }
     }
-    if (p.sums == nullptr) return;
+    if (p.sums != nullptr) put_sums(sum, part, p.across, p.n, p.sums + (long)blockIdx.y * p.n * H);
+}
+
+// Sums of the columns of dense rows of floats, a part for each chunk of rows; workgroups as k_act_bwd's.
+struct ColumnSums {
+    const float* from;
+    float* sums;
+    long rows, chunk;
+    int n, across;
+};
+
+__global__ __launch_bounds__(256) void k_sums(ColumnSums p) {
+    constexpr int N = kVec<float>, R = 4;
+    __shared__ float part[256 * N];
+    const int tx = threadIdx.x % p.across, ty = threadIdx.x / p.across, high = 256 / p.across;
+    const int at = (blockIdx.x * p.across + tx) * N;
+    const long first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.rows);
+    float sum[1][N] = {};
+    for (long m = at < p.n ? first + ty : last; m < last; m += R * high) {
+        vec_t<float> v[R];
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+        for (int i = 0; i < R; ++i) {
+            v[i] = vec_t<float>{};
+            if (m + i * high < last) v[i] = load_vec<float>(p.from + (m + i * high) * p.n, at / N, p.n);
+        }
 #pragma unroll
-        for (int q = 0; q < V; ++q) part[((h * high + ty) * V + q) * p.across + tx] = sum[h][q];
-    lds_barrier();
-    // value i of the workgroup's across * V columns, summed over its rows in order
-    for (int i = threadIdx.x; i < H * V * p.across; i += 256) {
-        const int h = i / (V * p.across), c = i % (V * p.across), col = blockIdx.x * p.across * V + c;
-        if (col >= p.n) continue;
-        float s = 0.0f;
-        for (int r = 0; r < high; ++r) s += part[((h * high + r) * V + c % V) * p.across + c / V];
-        p.sums[(long)blockIdx.y * p.n * H + h * p.n + col] = s;
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int q = 0; q < N; ++q) sum[0][q] += v[i][q];
     }
+    put_sums(sum, part, p.across, p.n, p.sums + (long)blockIdx.y * p.n);
 }
 
 // Rows laid out for 16-byte pieces: to[i][j][0 .. padded) = from[i][j][0 .. width), zeros past the width and for
@@ -1081,11 +1133,12 @@ struct BiasCut {
     int across;
     unsigned groups;
 };
-BiasCut bias_cut(long rows, int n) {
+// vec: values of a lane's reads
+BiasCut bias_cut(long rows, int n, int vec) {
     BiasCut c;
     c.across = 1;
-    while (c.across < 64 && c.across * V < n) c.across *= 2;
-    c.groups = (unsigned)div_up(n, (long)c.across * V);
+    while (c.across < 64 && c.across * vec < n) c.across *= 2;
+    c.groups = (unsigned)div_up(n, (long)c.across * vec);
     const long high = 256 / c.across;
     // enough workgroups for the card, at most 512 chunks, which are joined afterwards; a lane reads 4 rows at once
     const long most = std::max<long>(1L, std::min<long>(512L, div_up(4 * kFill, c.groups)));
@@ -1116,7 +1169,7 @@ Packs packs_of(const LinearArgs& a, bool bwd) {
 }
 
 struct Layout {
-    long x, w, s, g_z, sums, parts, bytes;
+    long x, w, s, g_z, exact, sums, parts, bytes;
 };
 Layout layout_of(const LinearArgs& a, bool second) {
     const long out = (long)a.outer * (a.gated ? 2 : 1), comps = (long)(a.lmax + 1) * (a.lmax + 1);
@@ -1124,13 +1177,14 @@ Layout layout_of(const LinearArgs& a, bool second) {
     const bool act = a.act != kActNone || a.gated;
     const long s_bytes = act || p.grad ? align256(a.n_rows * comps * p.outer * (long)sizeof(T)) : 0;
     const WeightCut w = weight_cut(a, second && act);
-    const BiasCut b = bias_cut(a.n_rows, a.outer);
+    const BiasCut b = second ? bias_cut(a.n_rows, (int)out, kVec<float>) : bias_cut(a.n_rows, a.outer, V);
     Layout y;
     y.x = 0;
     y.w = p.x ? align256(a.n_rows * comps * p.inner * (long)sizeof(T)) : 0;
     y.s = y.w + (p.w ? align256((a.lmax + 1) * p.outer * p.inner * (long)sizeof(T)) : 0);
     y.g_z = y.s + s_bytes;
-    y.sums = y.g_z + (second ? s_bytes : 0);
+    y.exact = y.g_z + (second ? s_bytes : 0);
+    y.sums = y.exact + (second && act && kParts == 1 ? align256(a.n_rows * out * 4) : 0);
     y.parts = y.sums + align256(std::max<long>(b.chunks, w.splits) * out * 4);
     // one product's parts at a time
     const bool small = small_bwd(a) && !second;
@@ -1344,7 +1398,7 @@ hipError_t bwd(const LinearArgs& a, hipStream_t st) {
         if (a.d_bias) of_b = join_of(sums, a.d_bias, out, 1, c.splits);
         return join(of_w, of_b, st);
     }
-    const BiasCut b = bias_cut(a.n_rows, a.outer);
+    const BiasCut b = bias_cut(a.n_rows, a.outer, V);
     const int comps = (a.lmax + 1) * (a.lmax + 1);
     const Packs p = packs_of(a, true);
     const T* grad = static_cast<const T*>(a.grad);
@@ -1396,13 +1450,16 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
         CTP_TRY(weight_gradient(a, Operand{grad, a.grad_stride, a.outer, a.outer}, of_u, c, parts, static_cast<T*>(a.g_w), st));
         return c.direct ? hipSuccess : join(join_of(parts, a.g_w, out * a.inner, a.lmax + 1, c.splits), Join{}, st);
     }
-    const bool need_z = a.g_x || a.g_w || a.g_bias;
+    // the bias sums what g_z is before its rounding: 16-bit types keep that beside it
+    float* exact = a.g_bias ? reinterpret_cast<float*>(kParts == 1 ? ws + y.exact : ws + y.g_z) : nullptr;
+    const bool need_z = a.g_x || a.g_w || (a.g_bias && kParts != 1);
+    float* to_exact = kParts == 1 ? exact : nullptr;
     if (a.gated)
         CTP_TRY((run_gemm<true, true, true>(v, 1, EpiSecond<true>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
-                                                                  a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, parts, st)));
+                                                                  a.g_w ? s : nullptr, to_exact, a.grad_stride, a.outer, a.act}, parts, st)));
     else
         CTP_TRY((run_gemm<true, true, false>(v, 1, EpiSecond<false>{grad, z, static_cast<T*>(a.g_grad), need_z ? g_z : nullptr,
-                                                                    a.g_w ? s : nullptr, a.grad_stride, a.outer, a.act}, parts, st)));
+                                                                    a.g_w ? s : nullptr, to_exact, a.grad_stride, a.outer, a.act}, parts, st)));
     if (a.g_x) CTP_TRY(input_gradient(a, of_z, w, a.g_x, parts, st));
     Join of_w{}, of_b{};
     if (a.g_w) {
@@ -1411,17 +1468,10 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
         of_w = join_of(parts, a.g_w, out * a.inner, 1, 2 * c.splits);
     }
     if (a.g_bias) {
-        const int half = a.outer;
-        const BiasCut b = bias_cut(a.n_rows, half);
-        // the halves of a gated z as columns side by side: summed one half at a time
-        for (int h = 0; h < (a.gated ? 2 : 1); ++h) {
-            CTP_TRY(act_bwd(a, g_z + (long)h * half, out, nullptr, 0, sums + (long)h * b.chunks * half, false, half, b, st));
-            const Join of = join_of(sums + (long)h * b.chunks * half, static_cast<T*>(a.g_bias) + (long)h * half, half, 1, b.chunks);
-            if (h + 1 == (a.gated ? 2 : 1))
-                of_b = of;
-            else
-                CTP_TRY(join(of, Join{}, st));
-        }
+        const BiasCut b = bias_cut(a.n_rows, (int)out, kVec<float>);
+        k_sums<<<dim3(b.groups, b.chunks), 256, 0, st>>>(ColumnSums{exact, sums, a.n_rows, b.chunk, (int)out, b.across});
+        CTP_TRY(hipGetLastError());
+        of_b = join_of(sums, a.g_bias, out, 1, b.chunks);
     }
     return join(of_w, of_b, st);
 }

@@ -127,3 +127,30 @@ def test_bias_sums_before_any_rounding(ctp, dev, dtype, rows, inner, outer, gate
         # a row's derivative is the same number in all rows, a term one rounding (gated: two) and the additions follow
         slope = torch.stack([(Z[1] * d1).abs(), f.abs()]) if gated else d1.abs()
         close(name, d_bias, torch.zeros_like(slope), (rows + 8) * EPS32 * S * slope * (1 + 2.0 ** -10))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,inner,outer", [(24, 64, 40), (81, 100, 128), (600, 24, 7), (90, 2100, 33), (900, 512, 500)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_second_bias_sums_before_any_rounding(ctp, dev, dtype, rows, inner, outer, gated):
+    """As above for the second pass: every row has the same cotangent and z, so only grad's values differ, and cancel."""
+    tell("second bias", dtype, rows, inner, outer, gated)
+    g = torch.Generator().manual_seed(7)
+    a, b = (torch.randint(-60, 61, (rows // 3, outer), generator=g).double() for _ in range(2))
+    grad = torch.cat([a, b, -(a + b)])[torch.randperm(rows, generator=g)].to(dtype)
+    z = normal(g, (2, outer) if gated else (outer,), dtype)
+    u, w = normal(g, (inner,), dtype), normal(g, (2, outer, inner) if gated else (outer, inner), dtype, inner ** -0.5)
+    x = normal(g, (rows, inner), dtype)
+    args = [t.to(dev) for t in (u.expand(rows, inner).contiguous(), grad, x, w, z.expand(rows, *z.shape).contiguous())]
+    second = ctp.gated_linear_bwd_bwd if gated else ctp.linear_bwd_bwd
+    for name in ("silu", "gelu", "tanh"):
+        g_bias = second(*args, act=name)[3]
+        Z, V, S = z.double(), w.double() @ u.double(), grad.double().abs().sum(0)
+        f, d1, d2 = act(name, Z[0] if gated else Z)
+        # v, its error in it, is the same in all rows
+        V = V.abs() + sum_error(dtype, inner) * (w.double().abs() @ u.double().abs())
+        slope = (torch.stack([V[0] * (Z[1] * d2).abs() + V[1] * d1.abs(), V[0] * d1.abs()]) if gated else V * d2.abs())
+        # act' and act'' off by some roundings of 1 + |z|
+        slope = slope + 32 * EPS32 * (1 + Z.abs()) ** 2 * (V.sum(0) * (1 + Z[1].abs()) if gated else V)
+        close(name, g_bias, torch.zeros_like(slope), (rows + 8) * EPS32 * S * slope * (1 + 2.0 ** -10))
+        assert torch.equal(second(*args, act=name, needs=(False, False, False, True))[3], g_bias)
