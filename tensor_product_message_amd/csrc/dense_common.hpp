@@ -140,7 +140,8 @@ __device__ __forceinline__ void activation(float z, float& f, float& d1, float& 
         // Phi(-|z|) = exp(-z^2 / 2) times a function that a polynomial in t = 1 / (1 + 0.4 |z| / sqrt(2)) follows to
         // 1.3 2^-23 of it (least squares at Chebyshev points, reweighted to even out the error), 4.4e-7 with the
         // evaluation's roundings; erfcf is four times the instructions.  Past 42 the exponential is zero anyway.
-        const float g = exp_falling(-0.5f * z * z), t = one_over(__builtin_fmaf(0.28284271f, fminf(fabsf(z), 42.0f), 1.0f));
+        const float near = fminf(fabsf(z), 42.0f);
+        const float g = exp_falling(-0.5f * z * z), t = one_over(__builtin_fmaf(0.28284271f, near, 1.0f));
         constexpr float kPoly[9] = {0.22567586600780487f, 0.22566959261894226f, 0.20784272253513336f, 0.1685418039560318f,
                                     0.14143219590187073f, -0.005609337240457535f, 0.169087752699852f, -0.1829030066728592f,
                                     0.050262536853551865f};
@@ -149,7 +150,8 @@ __device__ __forceinline__ void activation(float z, float& f, float& d1, float& 
         for (int k = 7; k >= 0; --k) q = __builtin_fmaf(q, t, kPoly[k]);
         q *= 0.5f * t * g;
         const float c = z < 0.0f ? q : 1.0f - q, p = 0.39894228040143268f * g;
-        f = z * c, d1 = __builtin_fmaf(z, p, c), d2 = p * __builtin_fmaf(-z, z, 2.0f);
+        f = z * c, d1 = __builtin_fmaf(z, p, c);
+        d2 = p * __builtin_fmaf(-near, near, 2.0f);     // z^2 may overflow where p is zero
     } else if constexpr (Act_ == kActTanh) {
         const float e = exp_falling(-2.0f * fabsf(z)), r = one_over(1.0f + e);
         f = tanhf(z);

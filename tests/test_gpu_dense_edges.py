@@ -154,3 +154,28 @@ def test_second_bias_sums_before_any_rounding(ctp, dev, dtype, rows, inner, oute
         slope = slope + 32 * EPS32 * (1 + Z.abs()) ** 2 * (V.sum(0) * (1 + Z[1].abs()) if gated else V)
         close(name, g_bias, torch.zeros_like(slope), (rows + 8) * EPS32 * S * slope * (1 + 2.0 ** -10))
         assert torch.equal(second(*args, act=name, needs=(False, False, False, True))[3], g_bias)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_activations_far_out(ctp, dev, dtype):
+    """z whose square is beyond float's range: slopes 0 or 1, curvature 0, and what a row gets from it."""
+    z = torch.tensor([-3e38, -1e25, -1e20, -2e19, -1.8e19, 0.0, 1.8e19, 2e19, 1e20, 1e25, 3e38]).to(dtype)[:, None]
+    one = torch.ones(len(z), 1, dtype=dtype, device=dev)
+    far = (z != 0).double()
+    for name in ("relu", "silu", "gelu", "sigmoid", "tanh"):
+        d_x, d_w, d_bias = ctp.linear_bwd(one, one, one[:1], z.to(dev), act=name)
+        slope = act(name, z.double())[1]
+        close(name, d_x, slope, 64 * EPS32 * (1 + slope.abs()))
+        assert torch.isfinite(d_w).all() and torch.isfinite(d_bias).all()
+        curve = act(name, z.double().clamp(-1e3, 1e3))[2]       # (beyond, the formula's own terms overflow)
+        g_grad, g_x, g_w, g_bias = ctp.linear_bwd_bwd(one, one, one, one[:1], z.to(dev), act=name)
+        assert not (curve * far).any()
+        close(name, g_x, curve, 256 * EPS32 * (1 + curve.abs()))
+        assert all(torch.isfinite(t).all() for t in (g_grad, g_w, g_bias))
+        y, _ = ctp.linear_fwd(z.to(dev), one[:1], act=name)
+        ref = act(name, z.double())[0]
+        close(name, y, ref, 16 * EPS32 * (1 + ref.abs()))
+        zz = torch.stack([z, torch.ones_like(z)], 1).to(dev)
+        got = [*ctp.gated_linear_bwd(one, one, one[:2, None], zz, act=name), *ctp.gated_linear_bwd_bwd(one, one, one, one[:2, None], zz, act=name)]
+        # act(z) itself is a slope of these, and sums of it pass the type's range: no NaN
+        assert not any(torch.isnan(t).any() for t in got)
