@@ -58,7 +58,7 @@ typedef struct conv_tp_linear_problem {
 } conv_tp_linear_problem;
 
 /* workspace here and below: 16-byte aligned, at least the bytes that the call of the same name with _workspace gives
- * (0: may be NULL); contents undefined afterwards. */
+ * for the same problem, its strides included (0: may be NULL); contents undefined afterwards. */
 int32_t conv_tp_linear_fwd(const conv_tp_linear_problem *prob, const void *x, const void *w, const void *bias,
                            const void *residual, void *y, void *z, void *workspace, int64_t workspace_bytes,
                            void *stream);

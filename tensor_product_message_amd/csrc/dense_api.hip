@@ -94,6 +94,12 @@ ctp::LinearArgs linear_args(const conv_tp_linear_problem* p) {
     return a;
 }
 
+// What a workspace's size depends on, as the call itself checks it; it is the call's own strides that count.
+int check_strides(const conv_tp_linear_problem* p, bool grad) {
+    if (int r = check_stride(p->x_stride, comps_of(p) * p->inner, p->n_rows, "x_stride")) return r;
+    return grad ? check_stride(p->grad_stride, comps_of(p) * p->outer, p->n_rows, "grad_stride") : CTP_OK;
+}
+
 int check_workspace(const void* ws, int64_t bytes, int64_t wants) {
     if (bytes < wants) return fail(CTP_EINVAL, "workspace of %lld bytes, %lld are needed", (long long)bytes, (long long)wants);
     return need(ws, wants, 16, "workspace");
@@ -135,6 +141,7 @@ extern "C" {
 
 int32_t conv_tp_linear_fwd_workspace(const conv_tp_linear_problem* prob, int64_t* bytes) {
     if (int r = check_linear(prob)) return r;
+    if (int r = check_strides(prob, false)) return r;
     if (bytes == nullptr) return fail(CTP_EINVAL, "bytes is null");
     *bytes = ctp::linear_fwd_workspace(linear_args(prob));
     return ok();
@@ -168,6 +175,7 @@ int32_t conv_tp_linear_fwd(const conv_tp_linear_problem* prob, const void* x, co
 
 int32_t conv_tp_linear_bwd_workspace(const conv_tp_linear_problem* prob, int64_t* bytes) {
     if (int r = check_linear(prob)) return r;
+    if (int r = check_strides(prob, true)) return r;
     if (bytes == nullptr) return fail(CTP_EINVAL, "bytes is null");
     *bytes = ctp::linear_bwd_workspace(linear_args(prob));
     return ok();
@@ -198,6 +206,7 @@ int32_t conv_tp_linear_bwd(const conv_tp_linear_problem* prob, const void* grad,
 
 int32_t conv_tp_linear_bwd_bwd_workspace(const conv_tp_linear_problem* prob, int64_t* bytes) {
     if (int r = check_linear(prob)) return r;
+    if (int r = check_strides(prob, true)) return r;
     if (bytes == nullptr) return fail(CTP_EINVAL, "bytes is null");
     *bytes = ctp::linear_bwd_bwd_workspace(linear_args(prob));
     return ok();

@@ -71,3 +71,30 @@ def test_empty_matrices(capi, shape):
     one, none = lambda t, x: (t * 1)(x), (ctypes.c_void_p * 1)(None)  # noqa: E731
     sizes = one(ctypes.c_int64, shape[0]), one(ctypes.c_int32, shape[1]), one(ctypes.c_int32, shape[2])
     assert capi.dense_lib().conv_tp_orthogonalise(1, none, none, *sizes, one(ctypes.c_int32, 0), 5, 1e-7, 1.0, None, 0, None) == capi.CTP_OK
+
+
+def test_workspaces_go_by_the_strides(capi):
+    """16-bit rows that do not begin on 16 bytes are laid out anew, which takes room: a query's strides are its call's."""
+    L, n = capi.dense_lib(), ctypes.c_int64()
+    sizes = {}
+    for x_stride in (1000, 1001, 1008):
+        for grad_stride in (1000, 1001, 1008):
+            p = capi.LinearProblem(5000, x_stride, 1000, grad_stride, 0, 1000, 1000, 1, 0, 0)
+            assert L.conv_tp_linear_bwd_workspace(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK
+            sizes[x_stride % 8, grad_stride % 8] = n.value
+    rows = 5000 * 1000 * 2
+    assert sizes[1, 0] >= sizes[0, 0] + rows and sizes[0, 1] >= sizes[0, 0] + rows and sizes[1, 1] >= sizes[0, 0] + 2 * rows
+
+
+@pytest.mark.parametrize("lmax,x_stride,grad_stride", [(0, 7, 6), (0, 0, 6), (0, 2 ** 41, 6), (0, -8, 6), (1, 31, 24), (0, 8, 5), (0, 8, 0), (2, 72, 53)])
+def test_workspace_queries_refuse_the_strides_that_calls_refuse(capi, lmax, x_stride, grad_stride):
+    L, n = capi.dense_lib(), ctypes.c_int64()
+    p = capi.LinearProblem(4, x_stride, 0, grad_stride, lmax, 8, 6, 0, 0, 0)
+    bad_x = x_stride < 8 * (lmax + 1) ** 2 or x_stride > 2 ** 40
+    assert L.conv_tp_linear_fwd_workspace(ctypes.byref(p), ctypes.byref(n)) == (capi.CTP_EINVAL if bad_x else capi.CTP_OK)
+    for size in (L.conv_tp_linear_bwd_workspace, L.conv_tp_linear_bwd_bwd_workspace):
+        assert size(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_EINVAL
+        assert b"stride" in L.conv_tp_dense_last_error()
+    for rows in (0, 1):         # strides of no next row
+        p.n_rows = rows
+        assert L.conv_tp_linear_bwd_workspace(ctypes.byref(p), ctypes.byref(n)) == capi.CTP_OK
