@@ -15,9 +15,17 @@
  *
  * Products are summed in fp32.  Operands of 16 bits enter the matrix cores as
  * they are; floats enter as three bfloat16 parts, which gives a float product's
- * accuracy (a float operand that is not finite may give NaN where a float
- * product gives an infinity).  What a gradient multiplies - grad act'(z), and
- * the second pass's factors - is rounded to the features' type first.
+ * accuracy.  A float operand that is not finite, or a product of two of them
+ * beyond or within 1% of float's range, may give NaN where a float product gives
+ * an infinity or a value near it; up to 32 rows forward products do not go
+ * through parts and give what a float product gives.
+ *
+ * What a gradient multiplies - grad act'(z), and the second pass's factors - is
+ * rounded to the features' type first, as a stored z is.  In float16 that has
+ * float16's range: grad act'(z), in the gated form grad z[1] act'(z[0]) and
+ * grad act(z[0]), beyond 65504 is an infinity although the gradient itself may
+ * be finite, and below 2^-24 it is zero.  Scale the loss to suit.  The biases'
+ * gradients sum these values in fp32 before that rounding.
  */
 #ifndef CONVTP_DENSE_H
 #define CONVTP_DENSE_H
@@ -87,15 +95,21 @@ int32_t conv_tp_linear_bwd_bwd_workspace(const conv_tp_linear_problem *prob, int
  * squares, then `steps` times X <- a X + (b A + c A A) X, A = X X^T, with
  * a, b, c = 3.4445, -4.7750, 2.0315 (for tall matrices the same of M^T), and
  * out = scale X: singular values between some 0.003 and 1 of |M| come out
- * between 0.7 and 1.2 times scale, the singular vectors stay.
+ * between 0.7 and 1.2 times scale, the singular vectors stay.  (The
+ * coefficients are the ones published with the Muon optimiser, K. Jordan 2024.)
  *
  * Tensor k holds batch[k] dense matrices [rows[k]][cols[k]], one after the
  * other, each orthogonalised by itself.  in, out (host arrays of device
  * pointers), batch, rows, cols, dtype: host arrays of n_tensors entries, read
  * before the call returns.  out[k] has in[k]'s type and may be in[k]; other
- * overlaps are not allowed.  X and A are held in 32 bits whatever the type.  A
+ * overlaps are not allowed.  X, A and b A + c A A are held in 32 bits whatever
+ * the type (two float16, 22 significant bits), their products summed in fp32.  A
  * matrix of zeros gives zeros (eps > 0), one with a value that is not finite
- * gives NaN. */
+ * gives NaN.
+ *
+ * The same call gives the same bits.  How A's sums are cut goes by the sizes
+ * of all matrices of a call, so a matrix's last bits may differ from those it
+ * gets in another company or alone. */
 int32_t conv_tp_orthogonalise(int32_t n_tensors, const void *const *in, void *const *out, const int64_t *batch,
                               const int32_t *rows, const int32_t *cols, const int32_t *dtype, int32_t steps, float eps,
                               float scale, void *workspace, int64_t workspace_bytes, void *stream);

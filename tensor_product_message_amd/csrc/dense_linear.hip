@@ -9,7 +9,8 @@
 //
 // s, g_z (and the gated form's pairs of them) are rounded to the features' type
 // before they enter a product, as the stored z is: they are operands of the
-// matrix cores.  What is summed is in fp32.
+// matrix cores.  What is summed is in fp32, the biases' sums of s and g_z
+// before that rounding.
 #include "dense_common.hpp"
 #include "dense_direct.hpp"
 #include "dense_linear.hpp"

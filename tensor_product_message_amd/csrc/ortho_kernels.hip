@@ -4,7 +4,8 @@
 //   A = X X^T,  X <- a X + (b A + c A A) X      `steps` times
 //
 // which takes every singular value s of X to a s + b s^3 + c s^5 and leaves the
-// singular vectors.  With a, b, c = 3.4445, -4.7750, 2.0315 the values between
+// singular vectors.  With a, b, c = 3.4445, -4.7750, 2.0315 (the coefficients
+// published with the Muon optimiser, K. Jordan 2024) the values between
 // some 0.003 and 1 are between 0.7 and 1.2 after five steps.
 //
 // X lies with its short side S first, [S][L]: a tall matrix is turned on its way

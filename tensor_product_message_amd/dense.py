@@ -7,7 +7,10 @@ library on the current HIP stream.
 
 Types: float32, bfloat16, float16, the same for all tensors of a call; products
 are summed in 32 bits and every output rounded once.  What a backward pass
-multiplies, grad act'(z), is rounded to that type first.  Rows of x, residual
+multiplies, grad act'(z), is rounded to that type first (in float16 it has
+float16's range: beyond 65504 an infinity); the biases' gradients sum it before
+that.  A float operand that is not finite may give NaN where a product gives an
+infinity (from 33 rows on; up to 32 the infinity).  Rows of x, residual
 and grad may lie any stride apart; w, bias and z are contiguous.
 
 Activations: "none", "relu", "silu", "gelu" (z Phi(z)), "sigmoid", "tanh".
@@ -166,7 +169,9 @@ def gated_linear(x, w, bias=None, act: str = "silu"):
 def orthogonalise(tensors, steps: int = 5, eps: float = 1e-7, scale: float = 1.0, out=None, workspace=None):
     """Every matrix [..., rows, cols] of `tensors` with its singular values brought near 1 (0.7 .. 1.2) by `steps`
     Newton-Schulz steps, times scale: X = M / (|M| + eps), X <- a X + (b A + c A A) X with A = X X^T.  out: the tensors
-    to write, shapes and types like `tensors`; `tensors` itself works in place; new ones if None.  Returns out."""
+    to write, shapes and types like `tensors`; `tensors` itself works in place; new ones if None.  Returns out.  Not
+    differentiable.  The same call gives the same bits; in another list a matrix's last bits may differ (22 are held, and
+    how sums are cut goes by the whole list)."""
     tensors = list(tensors)
     out = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in tensors] if out is None else list(out)
     dense_native().orthogonalise(tensors, out, steps, eps, scale, workspace)
