@@ -195,6 +195,13 @@ __device__ __forceinline__ ThreeParts take_apart(float x) {
 // n_rows: how many m (or n) there are, values past which are any; k_end: where k ends, zeros past it.
 enum How : int { kGuarded, kWhole, kClamped };
 
+// How a tile's edges are read: kWhole: whole steps of k, and guarded what is left; else all of it one way.
+template <class T, bool AlongA, bool AlongB>
+__host__ __device__ __forceinline__ How edges_of(bool whole_m, bool whole_n, int m_left, int n_left, int k_end) {
+    if ((AlongA || whole_m) && (AlongB || whole_n)) return kWhole;
+    return (AlongA ? k_end : m_left) >= kVec<T> && (AlongB ? k_end : n_left) >= kVec<T> ? kClamped : kGuarded;
+}
+
 template <class T, bool Along, int Rows, int Depth, int Threads>
 struct Staged {
     typedef typename Parts<T>::E E;
@@ -211,21 +218,31 @@ struct Staged {
     //   kClamped  reads go to the last vector and row that are there, and fix() makes of them what was meant;
     //             rows of no less than a vector (Along: k_end, Across: n_left);
     //   kGuarded  any size.
+    struct From {
+        long row;       // of the operand's
+        int at;         // first value
+        bool on;        // whether it is read at all
+    };
+    template <int How, class F>
+    static __host__ __device__ __forceinline__ From from(int id, int n_left, int k0, int k_end, F&& row_of) {
+        const int r = id / kPerRow, c = id % kPerRow;
+        // a vector of the row `row` of `width` values, from value `at`
+        const long row = Along ? row_of(r) : How == kClamped ? min(k0 + r, k_end - 1) : k0 + r;
+        const int at = (Along ? k0 : 0) + c * kVec<T>, width = Along ? k_end : n_left;
+        if constexpr (How == kGuarded) return From{row, at, at < width && (Along || row < k_end)};
+        return From{row, How == kClamped ? min(at, width - kVec<T>) : at, true};
+    }
     template <int How, class F>
     __device__ __forceinline__ void load(const T* base, long ld, int n_left, int k0, int k_end, F&& row_of) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow;
-            // a vector of the row `row` of `width` values, from value `at`
-            const long row = Along ? row_of(r) : How == kClamped ? min(k0 + r, k_end - 1) : k0 + r;
-            const int at = (Along ? k0 : 0) + c * kVec<T>, width = Along ? k_end : n_left;
+            const From f = from<How>(tid + i * Threads, n_left, k0, k_end, row_of);
             if constexpr (How == kGuarded) {
                 v[i] = vec_t<T>{};
-                if (at < width && (Along || row < k_end)) v[i] = load_vec<T>(base + row * ld, at / kVec<T>, width);
+                if (f.on) v[i] = load_vec<T>(base + f.row * ld, f.at / kVec<T>, Along ? k_end : n_left);
             } else {
-                const int from = How == kClamped ? min(at, width - kVec<T>) : at;
-                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + row * ld + from);
+                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + f.row * ld + f.at);
             }
         }
     }

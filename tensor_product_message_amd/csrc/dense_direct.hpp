@@ -43,6 +43,12 @@ __device__ __forceinline__ unsigned lds_address(const void* p) {
 // Bytes of the buffers that tiles are read from; places in them are held in 32 bits.
 constexpr long kBufferBytes = 0x7ffffff0;
 
+// Across: the buffer of `rows` rows of k, ld values apart, ends with the last one's `width` values.
+__host__ __device__ __forceinline__ unsigned buffer_bytes(long rows, long ld, long width) {
+    const long bytes = 2 * ((rows - 1) * ld + width);
+    return (unsigned)(bytes < kBufferBytes ? bytes : kBufferBytes);
+}
+
 // Whether an operand's tiles may go this way: 16-byte pieces, whole in every row of n values, and rows so near each
 // other that all places of a tile of 256 of them, and of their partners `pair` rows on, lie in a buffer.
 inline bool comes_directly(const void* p, long ld, long batch, long n, long pair) {

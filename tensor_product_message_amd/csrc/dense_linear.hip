@@ -219,10 +219,11 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
             }
         };
         const int steps = (k_end + kDepth - 1) / kDepth, whole = k_end / kDepth;
-        if ((AlongA || whole_m) && (AlongB || whole_n)) {
+        const How edges = edges_of<T, AlongA, AlongB>(whole_m, whole_n, m_left, n_left, k_end);
+        if (edges == kWhole) {
             run(Is<kWhole>{}, 0, whole);
             run(Is<kGuarded>{}, whole, steps);
-        } else if ((AlongA ? k_end : m_left) >= V && (AlongB ? k_end : n_left) >= V) {
+        } else if (edges == kClamped) {
             run(Is<kClamped>{}, 0, steps);
         } else {
             run(Is<kGuarded>{}, 0, steps);
@@ -292,12 +293,11 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
         auto issue = [&](int step, int buffer) {
             const int k = step * kDepth;
             // Across: what lies past the last k is the buffer's end
-            const long rows = min(k_end - k, kDepth) - 1;
-            const long a_left = AlongA ? kBufferBytes : 2 * (rows * g.a_ld + min((long)Side, g.m_read - m0));
-            const long b_left = AlongB ? kBufferBytes : 2 * (rows * g.b_ld + min(Side, g.n_read - n0));
-            da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), (unsigned)min(a_left, kBufferBytes)), base + buffer * kBuffer, k_end - k);
-            db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), (unsigned)min(b_left, kBufferBytes)),
-                     base + buffer * kBuffer + TA::kBytes, k_end - k);
+            const long rows = min(k_end - k, kDepth);
+            const unsigned a_bytes = AlongA ? (unsigned)kBufferBytes : buffer_bytes(rows, g.a_ld, min((long)Side, g.m_read - m0));
+            const unsigned b_bytes = AlongB ? (unsigned)kBufferBytes : buffer_bytes(rows, g.b_ld, min(Side, g.n_read - n0));
+            da.issue(buffer_at(a + (AlongA ? k : k * g.a_ld), a_bytes), base + buffer * kBuffer, k_end - k);
+            db.issue(buffer_at(b + (AlongB ? k : k * g.b_ld), b_bytes), base + buffer * kBuffer + TA::kBytes, k_end - k);
         };
         f32x16 acc[NT][MT] = {};
         if (k_end > 0)

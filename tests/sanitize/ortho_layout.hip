@@ -1,6 +1,7 @@
 // Host program under AddressSanitizer and UndefinedBehaviorSanitizer: how the
 // workspace of orthogonalised matrices is laid out and their work is divided
-// (lay_out and place in csrc/ortho_kernels.hip), empty matrices among them.
+// (lay_out and place in csrc/ortho_kernels.hip), empty matrices among them, and
+// that what the products' tiles read lies inside the planes.
 // Prints the number of lists checked.
 #include <cstdio>
 #include <random>
@@ -16,6 +17,43 @@ struct Shape {
     long batch;
     int rows, cols;
 };
+
+// Whether what the tiles of Side read of a product's operand (rows `count`, ld apart, from element `first` on; Along: its
+// k from `k` on, else k are the rows) lies before element `end`.
+template <bool Along, int Side>
+bool operand_inside(long first, int ld, int rows, int at, int k, long end) {
+    constexpr int depth = kDepthOf<Side>;
+    typedef Direct<Along, Side, depth, 4> D;
+    const long base = first + (Along ? (long)at * ld + k : (long)k * ld + at);
+    const long bytes = Along ? kBufferBytes : std::min<long>(2 * ((long)(rows - k) * ld - at), kBufferBytes);
+    for (int chunk = 0; chunk < D::kLoads * 4 * 64; ++chunk) {
+        const long place = D::place(chunk, ld, [&](int r) { return (long)std::min(r, rows - 1 - at); });
+        if (place < 0 || place > (long)D::kNowhere) return false;
+        if (place >= bytes) continue;       // gives zeros
+        if (place + 16 > bytes || base + place / 2 + 8 > end) return false;
+    }
+    return true;
+}
+
+// The last matrix's planes, in the places where tiles reach furthest.
+template <int Side>
+bool reads_inside(const Group& g) {
+    const long x = g.x[1] + (g.batch - 1L) * 2 * g.s * g.l, a = g.a + (g.batch - 1L) * 2 * g.s * g.s;
+    const long x_plane = (long)g.s * g.l, a_plane = (long)g.s * g.s;
+    const int depth = kDepthOf<Side>, last_m = (g.s - 1) / Side * Side, last_n = (g.l - 1) / Side * Side;
+    for (int q = 0; q < 2; ++q)
+        for (int m : {0, last_m}) {
+            const long x_end = x + (q + 1) * x_plane, a_end = a + (q + 1) * a_plane;
+            for (int k : {0, g.l - depth})
+                if (!operand_inside<true, Side>(x + q * x_plane, g.l, g.s, m, k, x_end)) return false;
+            for (int k : {0, g.s - depth}) {
+                if (!operand_inside<true, Side>(a + q * a_plane, g.s, g.s, m, k, a_end)) return false;
+                for (int n : {0, last_n})
+                    if (!operand_inside<false, Side>(x + q * x_plane, g.l, g.s, n, k, x_end)) return false;
+            }
+        }
+    return true;
+}
 
 // Null, or what is wrong with a list's layout.
 const char* check(const std::vector<Shape>& shapes) {
@@ -53,6 +91,8 @@ const char* check(const std::vector<Shape>& shapes) {
                 at += 2L * p.g[k].batch * p.g[k].splits * p.g[k].s * p.g[k].s;
             }
         if (p.sums_at < 2 * at || p.sums_at + 8 * sums > size) return "end";
+        for (int k = 0; k < p.n; ++k)
+            if (p.g[k].batch && !(reads_inside<64>(p.g[k]) && reads_inside<128>(p.g[k]))) return "reads";
         const unsigned total = place(p, [](const Group& g) { return (long)g.chunks; });
         if ((total == 0) != (work == 0) || total != sums) return "workgroups";
     }

@@ -1,5 +1,5 @@
 """How the dense operators lay out their workspaces, without a GPU: through the C ABI, and on the host under
-AddressSanitizer and UndefinedBehaviorSanitizer (tests/sanitize/ortho_layout.hip)."""
+AddressSanitizer and UndefinedBehaviorSanitizer (tests/sanitize/ortho_layout.hip, dense_access.hip)."""
 import ctypes
 import os
 
@@ -55,14 +55,25 @@ def test_workspace_of_large_matrices_is_counted_in_64_bits(capi, rows, lmax, act
     assert n.value >= (comps if lmax else 2) * matrix >= 2 ** 31
 
 
-def test_layout_of_orthogonalised_matrices_under_sanitizers(tmp_path):
-    exe = str(tmp_path / "ortho_layout")
-    _run([HIPCC, "-O1", "-g", "-std=c++20", "--offload-arch=gfx950", "-ffp-contract=off", "-Wno-undefined-inline",
-          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Xarch_host", "-fsanitize=address",
-          "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fsanitize=integer-divide-by-zero",
-          "-Xarch_host", "-fno-sanitize-recover=all", os.path.join(ROOT, "tests", "sanitize", "ortho_layout.hip"), "-o", exe])
+HOST = [HIPCC, "-O2", "-g", "-std=c++20", "--offload-arch=gfx950", "--offload-host-only", "-ffp-contract=off", "-Wno-undefined-inline",
+        # no kernel is launched, and none is there
+        "-Wl,--unresolved-symbols=ignore-all", "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fno-sanitize-recover=all"]
+
+
+def run_on_host(tmp_path, source, *flags):
+    exe = str(tmp_path / "program")
+    _run([*HOST, *flags, os.path.join(ROOT, "tests", "sanitize", source), "-o", exe])
     r = _run([exe], env=dict(os.environ, **SAN_ENV))
     assert r.stdout.startswith("checked ") and "runtime error" not in r.stderr
+
+
+def test_layout_of_orthogonalised_matrices_under_sanitizers(tmp_path):
+    run_on_host(tmp_path, "ortho_layout.hip", "-Xarch_host", "-fsanitize=address")
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_reads_and_regions_of_linear_layers_under_ubsan(tmp_path, dtype):
+    run_on_host(tmp_path, "dense_access.hip", f"-DCTP_DENSE_TYPE={dtype}")
 
 
 @pytest.mark.parametrize("shape", [(1, 0, 0), (1, 0, 5), (1, 5, 0), (2, 0, 0), (0, 5, 5), (0, 0, 0)])
