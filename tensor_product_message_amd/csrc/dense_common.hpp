@@ -195,11 +195,14 @@ __device__ __forceinline__ ThreeParts take_apart(float x) {
 // n_rows: how many m (or n) there are, values past which are any; k_end: where k ends, zeros past it.
 enum How : int { kGuarded, kWhole, kClamped };
 
-// How a tile's edges are read: kWhole: whole steps of k, and guarded what is left; else all of it one way.
+// Whether a tile's whole steps of k may be read whole (and guarded what is left), and if not, whether clamped.
+template <bool AlongA, bool AlongB>
+__host__ __device__ __forceinline__ bool read_whole(bool whole_m, bool whole_n) {
+    return (AlongA || whole_m) && (AlongB || whole_n);
+}
 template <class T, bool AlongA, bool AlongB>
-__host__ __device__ __forceinline__ How edges_of(bool whole_m, bool whole_n, int m_left, int n_left, int k_end) {
-    if ((AlongA || whole_m) && (AlongB || whole_n)) return kWhole;
-    return (AlongA ? k_end : m_left) >= kVec<T> && (AlongB ? k_end : n_left) >= kVec<T> ? kClamped : kGuarded;
+__host__ __device__ __forceinline__ bool read_clamped(int m_left, int n_left, int k_end) {
+    return (AlongA ? k_end : m_left) >= kVec<T> && (AlongB ? k_end : n_left) >= kVec<T>;
 }
 
 template <class T, bool Along, int Rows, int Depth, int Threads>
@@ -218,31 +221,29 @@ struct Staged {
     //   kClamped  reads go to the last vector and row that are there, and fix() makes of them what was meant;
     //             rows of no less than a vector (Along: k_end, Across: n_left);
     //   kGuarded  any size.
-    struct From {
-        long row;       // of the operand's
-        int at;         // first value
-        bool on;        // whether it is read at all
-    };
+    // Row r of the tile among the operand's, and the first value that is read for the vector c of a row of `width`.
     template <int How, class F>
-    static __host__ __device__ __forceinline__ From from(int id, int n_left, int k0, int k_end, F&& row_of) {
-        const int r = id / kPerRow, c = id % kPerRow;
-        // a vector of the row `row` of `width` values, from value `at`
-        const long row = Along ? row_of(r) : How == kClamped ? min(k0 + r, k_end - 1) : k0 + r;
-        const int at = (Along ? k0 : 0) + c * kVec<T>, width = Along ? k_end : n_left;
-        if constexpr (How == kGuarded) return From{row, at, at < width && (Along || row < k_end)};
-        return From{row, How == kClamped ? min(at, width - kVec<T>) : at, true};
+    static __host__ __device__ __forceinline__ long row(int r, int k0, int k_end, F&& row_of) {
+        return Along ? row_of(r) : How == kClamped ? min(k0 + r, k_end - 1) : k0 + r;
+    }
+    template <int How>
+    static __host__ __device__ __forceinline__ int value(int c, int k0, int width) {
+        const int at = (Along ? k0 : 0) + c * kVec<T>;
+        return How == kClamped ? min(at, width - kVec<T>) : at;
     }
     template <int How, class F>
     __device__ __forceinline__ void load(const T* base, long ld, int n_left, int k0, int k_end, F&& row_of) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const From f = from<How>(tid + i * Threads, n_left, k0, k_end, row_of);
+            const int id = tid + i * Threads, r = id / kPerRow, c = id % kPerRow, width = Along ? k_end : n_left;
+            const long from = row<How>(r, k0, k_end, row_of);
+            const int at = value<How>(c, k0, width);
             if constexpr (How == kGuarded) {
                 v[i] = vec_t<T>{};
-                if (f.on) v[i] = load_vec<T>(base + f.row * ld, f.at / kVec<T>, Along ? k_end : n_left);
+                if (at < width && (Along || from < k_end)) v[i] = load_vec<T>(base + from * ld, at / kVec<T>, width);
             } else {
-                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + f.row * ld + f.at);
+                v[i] = *reinterpret_cast<const typename Vec<T>::unaligned*>(base + from * ld + at);
             }
         }
     }

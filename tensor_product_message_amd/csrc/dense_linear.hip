@@ -219,11 +219,10 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
             }
         };
         const int steps = (k_end + kDepth - 1) / kDepth, whole = k_end / kDepth;
-        const How edges = edges_of<T, AlongA, AlongB>(whole_m, whole_n, m_left, n_left, k_end);
-        if (edges == kWhole) {
+        if (read_whole<AlongA, AlongB>(whole_m, whole_n)) {
             run(Is<kWhole>{}, 0, whole);
             run(Is<kGuarded>{}, whole, steps);
-        } else if (edges == kClamped) {
+        } else if (read_clamped<T, AlongA, AlongB>(m_left, n_left, k_end)) {
             run(Is<kClamped>{}, 0, steps);
         } else {
             run(Is<kGuarded>{}, 0, steps);

@@ -32,15 +32,14 @@ template <bool Along, int Rows, class F>
 bool staged_operand(How how, long base, long ld, int n_left, int k0, int k_end, long size, F&& row_of) {
     typedef Staged<T, Along, Rows, kDepth, 256> S;
     for (int id = 0; id < Rows * kDepth / V; ++id) {
-        const auto f = how == kWhole     ? S::template from<kWhole>(id, n_left, k0, k_end, row_of)
-                       : how == kClamped ? S::template from<kClamped>(id, n_left, k0, k_end, row_of)
-                                         : S::template from<kGuarded>(id, n_left, k0, k_end, row_of);
-        if (!f.on) continue;
-        long at = base + f.row * ld + f.at, count = V;
+        const int r = id / S::kPerRow, c = id % S::kPerRow, width = Along ? k_end : n_left;
+        const long row = how == kClamped ? S::template row<kClamped>(r, k0, k_end, row_of) : S::template row<kWhole>(r, k0, k_end, row_of);
+        const int value = how == kClamped ? S::template value<kClamped>(c, k0, width) : S::template value<kWhole>(c, k0, width);
+        if (how == kGuarded && !(value < width && (Along || row < k_end))) continue;
+        long at = base + row * ld + value, count = V;
         if (how == kGuarded) {          // load_vec
-            const int width = Along ? k_end : n_left;
-            const Span s = span_of<T>(f.at / V, width);
-            at = base + f.row * ld + s.at, count = width < V ? s.few : V;
+            const Span s = span_of<T>(value / V, width);
+            at = base + row * ld + s.at, count = width < V ? s.few : V;
         }
         if (!inside(at, count, size)) return false;
     }
@@ -86,7 +85,9 @@ bool tiles(const Job& j, std::mt19937& rng) {
                     const auto row_a = [&](int r) { return (long)std::min(r, m_left - 1); };
                     const auto row_b = [&](int r) { return Pairs ? pair_row(r, n_left, g.pair) : (long)std::min(r, n_left - 1); };
                     const int steps = (k_end + kDepth - 1) / kDepth, whole = k_end / kDepth;
-                    const How edges = edges_of<T, AlongA, AlongB>(m_left == BM, n_left >= kCols, m_left, n_left, k_end);
+                    const How edges = read_whole<AlongA, AlongB>(m_left == BM, n_left >= kCols)           ? kWhole
+                                      : read_clamped<T, AlongA, AlongB>(m_left, n_left, k_end) ? kClamped
+                                                                                              : kGuarded;
                     for (const long step : some(rng, steps, 5)) {
                         const int k = (int)step * kDepth;
                         if constexpr (Direct_) {
