@@ -15,10 +15,9 @@
  *
  * Products are summed in fp32.  Operands of 16 bits enter the matrix cores as
  * they are; floats enter as three bfloat16 parts, which gives a float product's
- * accuracy.  A float operand that is not finite, or a product of two of them
- * beyond or within 1% of float's range, may give NaN where a float product gives
- * an infinity or a value near it; up to 32 rows forward products do not go
- * through parts and give what a float product gives.
+ * accuracy; results that come out not finite are formed once more of the floats
+ * themselves, so infinities, NaN and what passes float's range are a float
+ * product's.
  *
  * What a gradient multiplies - grad act'(z), and the second pass's factors - is
  * rounded to the features' type first, as a stored z is.  In float16 that has

@@ -11,7 +11,8 @@
 // Of the nine products of the parts those below 2^-23 of the whole (m l, l m,
 // l l) are left out; the other six are summed in fp32, which is a float
 // product's accuracy at 2.7 times the rate of the fp32 matrix instructions
-// (2.5 PFLOP/s over six against 157 TFLOP/s).
+// (2.5 PFLOP/s over six against 157 TFLOP/s).  What comes out not finite is
+// formed once more of the floats (again_where_beyond).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -364,6 +365,57 @@ __device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i
             *reinterpret_cast<f32x4*>(slab + (lane & 31) * kSlab<NT> + 32 * j + 8 * g + 4 * (lane >> 5)) = x;
         }
     wave_lds_fence();
+}
+
+// Products of floats in parts give NaN where an operand is infinite (its parts are infinities of both signs) or where
+// one part's product passes the range and another's does not.  Results that are not finite are formed once more, of the
+// floats themselves, term by term.  (To see that there are none costs the hidden layer of 83325 x 64 -> 64 1% of its 16
+// us.  83325 x 64 -> 4352 with an infinity in every row takes 44 ms, all of it NaN 1.0 ms, 0.33 ms otherwise.)
+// there(m, n): whether row m and column n of the wave's tile belong to the output;
+// term(m, n, k, a, b): the factors of its term k.
+template <int MT, int NT, class There, class Term>
+__device__ __forceinline__ void again_where_beyond(f32x16 (&acc)[NT][MT], float* slab, int lane, int k_end, There&& there, Term&& term) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) t = __builtin_fmaf(acc[j][i][e], 0.0f, t);
+    if (__ballot(t != t) == 0) [[likely]] return;
+    forget(lane);       // what is derived from it is derived here, not before the products
+    each<MT>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        each<NT>([&](auto j) {
+            constexpr int J = decltype(j)::value;
+            float* own = slab + (lane & 31) * kSlab<1> + 4 * (lane >> 5);
+            wave_lds_fence();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) own[8 * g + q] = acc[J][I][4 * g + q];
+            wave_lds_fence();
+#pragma unroll 1
+            for (int id = lane; id < 32 * 32; id += 64) {
+                float* v = slab + id / 32 * kSlab<1> + id % 32;
+                const int m = 32 * I + id / 32, n = 32 * J + id % 32;
+                if (fabsf(*v) <= 3.4028235e38f || !there(m, n)) continue;
+                float sum = 0.0f;
+#pragma unroll 1
+                for (int k = 0; k < k_end && sum == sum; ++k) {
+                    float a, b;
+                    term(m, n, k, a, b);
+                    sum = __builtin_fmaf(a, b, sum);
+                }
+                *v = sum;
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[J][I][4 * g + q] = own[8 * g + q];
+        });
+    });
 }
 
 template <int V, bool Pairs, int MT, int NT, class F>

@@ -229,6 +229,23 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
         }
         lds_barrier();
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
+        if constexpr (kParts > 1)
+            again_where_beyond(
+                acc, slab, lane, k_end,
+                [&](int m, int n) { return wm + m < m_left && (Pairs ? ((wn + n) >> 6 << 5) + ((wn + n) & 31) : wn + n) < n_left; },
+                [&](int m, int n, int k, float& x, float& y) {
+                    m += wm, n += wn;
+                    x = (float)(AlongA ? a[m * g.a_ld + k] : a[k * g.a_ld + m]);
+                    if constexpr (Curved) {
+                        const float at = (float)(AlongA ? z[m * c.z_ld + k] : z[k * c.z_ld + m]);
+                        with_act(c.act, [&](auto is) {
+                            float f, d1, d2;
+                            activation<decltype(is)::value>(at, f, d1, d2);
+                            x *= d1;
+                        });
+                    }
+                    y = (float)(AlongB ? b[row_b(n) * g.b_ld + k] : b[k * g.b_ld + n]);
+                });
         write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left, whole_m && whole_n, epi, t.outer, batch, m0, n0);
         lds_barrier();
         if constexpr (Summed) {
@@ -594,7 +611,7 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
         sb.store(lb);
         lds_barrier();
         if (n0 + kCols < n_last) load(n0 + kCols);
-        f32x16 acc[2] = {};
+        f32x16 acc[2][1] = {};
 #pragma unroll
         for (int k = 0; k < kLong; k += 16) {
             frag_t f[2][kParts];
@@ -609,10 +626,17 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
 #pragma unroll
                 for (int p = 0; p <= s; ++p)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j] = mfma(f[j][s - p], a[k / 16][p], acc[j]);
+                    for (int j = 0; j < 2; ++j) acc[j][0] = mfma(f[j][s - p], a[k / 16][p], acc[j][0]);
         }
-        // 32 columns at a time: a row of them is 128 bytes
         const long m0 = (long)t.m * 128 + wave * 32;
+        const auto col = [&](int n) { return n0 + (Pairs ? n & 31 : n); };
+        again_where_beyond(
+            acc, slab, lane, k_end, [&](int m, int n) { return m0 + m < g.m && col(n) < g.n; },
+            [&](int m, int n, int k, float& x, float& y) {
+                x = (g.a + batch * g.a_batch)[(m0 + m) * g.a_ld + k];
+                y = AlongB ? b[(col(n) + (Pairs ? (n >> 5) * g.pair : 0L)) * g.b_ld + k] : b[(long)k * g.b_ld + col(n)];
+            });
+        // 32 columns at a time: a row of them is 128 bytes
         auto write = [&](auto whole) {
             constexpr bool Whole = decltype(whole)::value != 0;
             constexpr int B = kIsPlain<Epi> ? 4 : 1;       // rows of a lane at once
@@ -623,7 +647,7 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<f32x4*>(slab + (lane & 31) * kWide + (Pairs ? 32 * j : 0) + 8 * q + 4 * (lane >> 5)) =
-                        f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+                        f32x4{acc[j][0][4 * q], acc[j][0][4 * q + 1], acc[j][0][4 * q + 2], acc[j][0][4 * q + 3]};
                 if (Pairs && j == 0) continue;
                 wave_lds_fence();
                 const int n = n0 + nc + (Pairs ? 0 : 32 * j);

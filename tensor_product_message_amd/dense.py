@@ -9,9 +9,8 @@ Types: float32, bfloat16, float16, the same for all tensors of a call; products
 are summed in 32 bits and every output rounded once.  What a backward pass
 multiplies, grad act'(z), is rounded to that type first (in float16 it has
 float16's range: beyond 65504 an infinity); the biases' gradients sum it before
-that.  A float operand that is not finite may give NaN where a product gives an
-infinity (from 33 rows on; up to 32 the infinity).  Rows of x, residual
-and grad may lie any stride apart; w, bias and z are contiguous.
+that.  Rows of x, residual and grad may lie any stride apart; w, bias and z are
+contiguous.
 
 Activations: "none", "relu", "silu", "gelu" (z Phi(z)), "sigmoid", "tanh".
 

@@ -179,3 +179,76 @@ def test_activations_far_out(ctp, dev, dtype):
         got = [*ctp.gated_linear_bwd(one, one, one[:2, None], zz, act=name), *ctp.gated_linear_bwd_bwd(one, one, one, one[:2, None], zz, act=name)]
         # act(z) itself is a slope of these, and sums of it pass the type's range: no NaN
         assert not any(torch.isnan(t).any() for t in got)
+
+
+LAYERS = [  # few rows; tiles of 64 and of 128; rows in registers, plain and with an epilogue; cut sums; odd sizes
+    (20, 64, 40, {}), (100, 64, 64, dict(bias=True)), (1500, 600, 1400, {}), (5000, 64, 1024, {}), (5000, 100, 1040, dict(act="relu", bias=True)),
+    (200, 2100, 90, {}), (77, 33, 129, dict(residual=True)), (300, 2, 5, {}), (3000, 40, 520, dict(gated=True)), (90, 70, 33, dict(gated=True)),
+    (64, 1500, 200, dict(gated=True)),
+]
+
+
+@pytest.mark.parametrize("rows,inner,outer,how", LAYERS)
+def test_infinities_of_floats(ctp, dev, rows, inner, outer, how):
+    """What is not finite in a float layer comes out as the formula has it, whatever kernel forms it: infinities of either
+    sign, NaN, products beyond the range; the other results are not touched."""
+    tell("infinities", rows, inner, outer, how)
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator().manual_seed(9)
+    gated, name = how.get("gated", False), how.get("act", "none")
+    x = torch.randn(rows, inner, generator=g)
+    w = torch.randn(2, outer, inner, generator=g) if gated else torch.randn(outer, inner, generator=g)
+    w = torch.where(w.abs() < 0.05, 0.5, w)
+    bias = torch.randn(w.shape[:-1], generator=g) if how.get("bias") else None
+    residual = torch.randn(rows, outer, generator=g) if how.get("residual") else None
+    clean, _ = ctp.gated_linear_fwd(*(to_dev(dev, x, w, bias)), act=name) if gated else ctp.linear_fwd(*to_dev(dev, x, w, bias, residual), act=name)
+    odd = {1: (0, inf), 7: (inner - 1, -inf), rows - 1: (inner // 2, nan)}
+    if inner > 3:
+        odd[rows - 3] = (1, 3e38)
+    for r, (k, v) in odd.items():
+        x[r, k] = v
+    x[5, 0], x[5, inner // 2] = inf, inf
+    w.view(-1, inner)[3, 1] = 4.0                                   # times 3e38: beyond the range, without infinities beside it
+    w.view(-1, inner)[-1, 0] = -inf
+    w.view(-1, inner)[2, inner // 2] = 0.0
+    X, W = x.double(), w.double()
+
+    def product(x, w):      # one term of a sum at most is beyond float's range: its sum is
+        return (x[:, None, :] * w[None]).sum(-1)
+
+    Z = [torch.cat([product(X[i:i + 50], m) for i in range(0, rows, 50)]) for m in (W if gated else W[None])]
+    if bias is not None:
+        Z = [z + b.double() for z, b in zip(Z, bias.view(len(Z), -1))]
+    f = act(name, Z[0])[0]
+    want = f * Z[1] if gated else f
+    if residual is not None:
+        want = want + residual.double()
+    y, _ = ctp.gated_linear_fwd(*to_dev(dev, x, w, bias), act=name) if gated else ctp.linear_fwd(*to_dev(dev, x, w, bias, residual), act=name)
+    y = y.double().cpu()
+    want = want.float().double()        # beyond the range: infinities
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    beyond = torch.isinf(want)
+    assert torch.equal(y[beyond], want[beyond]) and not torch.isinf(y[~beyond]).any()
+    # rows and columns without any of it: the same bits
+    rest, cols = torch.ones(rows, dtype=torch.bool), torch.ones(outer, dtype=torch.bool)
+    rest[[*odd, 5, rows - 3]] = False
+    cols[[2, 3, outer - 1]] = False
+    assert torch.equal(y[rest][:, cols], clean.double().cpu()[rest][:, cols])
+    if gated:
+        return
+    # the gradients, of which d_w sums over the rows
+    grad = torch.randn(rows, outer, generator=g)
+    grad[2, 1], grad[9, 0] = inf, -inf
+    grad[rows - 3, :2] = 0
+    z = torch.randn(rows, outer, generator=g)
+    d_x, d_w, _ = ctp.linear_bwd(*to_dev(dev, grad, x, w), to_dev(dev, z)[0] if name != "none" else None, act=name)
+    s = (grad * act(name, z.double())[1].float()).double()
+    for got, a, b in ((d_x, s, W.T), (d_w, s.T, X.T)):
+        ref = torch.cat([product(a[i:i + 50], b) for i in range(0, len(a), 50)]).float()
+        assert torch.equal(torch.isnan(got.cpu()), torch.isnan(ref))
+        beyond = torch.isinf(ref)
+        assert torch.equal(got.cpu()[beyond], ref[beyond]) and not torch.isinf(got.cpu()[~beyond]).any()
+
+
+def to_dev(dev, *ts):
+    return [None if t is None else t.to(dev) for t in ts]
