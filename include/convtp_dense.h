@@ -104,11 +104,8 @@ int32_t conv_tp_linear_bwd_bwd_workspace(const conv_tp_linear_problem *prob, int
  * overlaps are not allowed.  X, A and b A + c A A are held in 32 bits whatever
  * the type (two float16, 22 significant bits), their products summed in fp32.  A
  * matrix of zeros gives zeros (eps > 0), one with a value that is not finite
- * gives NaN.
- *
- * The same call gives the same bits.  How A's sums are cut goes by the sizes
- * of all matrices of a call, so a matrix's last bits may differ from those it
- * gets in another company or alone. */
+ * gives NaN.  A matrix's result does not depend on the matrices beside it, to
+ * the last bit. */
 int32_t conv_tp_orthogonalise(int32_t n_tensors, const void *const *in, void *const *out, const int64_t *batch,
                               const int32_t *rows, const int32_t *cols, const int32_t *dtype, int32_t steps, float eps,
                               float scale, void *workspace, int64_t workspace_bytes, void *stream);

@@ -103,8 +103,10 @@ struct Direct {
 // buffers in LDS.  The fragments of the next 16 k are read while the matrix cores work on these, and across the end of a
 // tile too: its barrier stands before its last 16 k are multiplied, so that the cores have work while the first
 // fragments of the next tile come.  Without that they would wait for those at each barrier, all waves at once.
-template <class TA, class TB, int NParts, int MT, int NT, int Depth, class E, class Issue>
-__device__ __forceinline__ void multiply_tiles(f32x16 (&acc)[NT][MT], const E* lds, int steps, int wm, int wn, int lane, Issue&& issue) {
+// after(steps done): what is done with acc between two tiles.
+template <class TA, class TB, int NParts, int MT, int NT, int Depth, class E, class Issue, class After>
+__device__ __forceinline__ void multiply_tiles(f32x16 (&acc)[NT][MT], const E* lds, int steps, int wm, int wn, int lane, Issue&& issue,
+                                               After&& after) {
     typedef typename Frag<E>::type frag_t;
     constexpr int kBuffer = (TA::kBytes + TB::kBytes) / 2, kParts16 = Depth / 16;       // elements; even
     frag_t fa[2][MT][NParts], fb[2][NT][NParts];
@@ -153,6 +155,7 @@ __device__ __forceinline__ void multiply_tiles(f32x16 (&acc)[NT][MT], const E* l
         }
         multiply((kParts16 - 1) & 1);
         __builtin_amdgcn_sched_barrier(0);
+        after(step + 1);
     }
 }
 

@@ -317,7 +317,8 @@ __global__ __launch_bounds__(2 * Side, 2) void k_gemm_direct(Gemm g, Epi epi) {
         };
         f32x16 acc[NT][MT] = {};
         if (k_end > 0)
-            multiply_tiles<TA, TB, 1, MT, NT, kDepth>(acc, reinterpret_cast<const E*>(lds), (k_end + kDepth - 1) / kDepth, wm, wn, lane, issue);
+            multiply_tiles<TA, TB, 1, MT, NT, kDepth>(acc, reinterpret_cast<const E*>(lds), (k_end + kDepth - 1) / kDepth, wm, wn, lane, issue,
+                                                      [](int) {});
         tile_barrier();
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
         write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left,

@@ -34,7 +34,11 @@ template <int Side>
 constexpr int kDepthOf = Side == 64 ? 64 : 32;
 constexpr int kMostGroups = 32;     // tensors of one launch
 constexpr int kMostSums = 512;      // shares of a matrix's sum of squares
-constexpr int kLeastCut = 256;      // of the long side, a share of A
+// Of the long side, a share of A's sums: as much as the short side is, at least kLeastCut, and kMostCut for short sides
+// from kWideSide on (two of 8192 x 2048 and 2048 x 2048 take 4.3 ms so, which makes three shares of 8192, and 4.4 in four).
+constexpr int kLeastCut = 256, kMostCut = 2688, kWideSide = 2048;
+// Of one matrix no more shares than fill the card, or these: they are written and read.
+constexpr int kFill = 512, kLeastShares = 16;
 
 // One tensor: `batch` matrices.  Places are elements from the workspace's start; each matrix has two planes.
 struct Group {
@@ -47,7 +51,9 @@ struct Group {
     int s, l;               // padded sides
     unsigned batch;
     unsigned chunks;        // shares of the sum of squares
-    unsigned splits;        // of A's sums, each over `cut` of the long side
+    // A's sums are added up in shares of `cut` of the long side, in their order.  The cut goes by the matrix's sides alone,
+    // so its bits do not depend on the matrices beside it.  splits: the workgroups that have the shares, one or as many.
+    unsigned splits;
     int cut;
     bool tall;
 };
@@ -197,7 +203,8 @@ __global__ __launch_bounds__(256) void k_join_gram(Groups p) {
     write_parts(p.base + g.a + matrix * 2 * plane + at, plane, y);
 }
 
-enum Kind : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
+// kGramAll: kGram where a workgroup may have all shares of a sum.
+enum Kind : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3, kGramAll = 4 };
 
 __device__ __forceinline__ void write_out(void* p, int dtype, long i, float v) {
     if (dtype == kF32)
@@ -217,9 +224,11 @@ __device__ __forceinline__ TileAt triangle_at(unsigned id) {
 }
 
 // A tile of Side x Side of one of the products by 4 waves; from: which of the X buffers is X.  A and b A + c A A are
-// symmetric: the tiles on and below the diagonal are computed and written twice.
-template <int K, int Side>
+// symmetric: the tiles on and below the diagonal are computed, and blocks of 64 below it written twice (of 64 whatever the
+// tile: a product's two orders of h l + l h are not the same bits).
+template <int Kind_, int Side>
 __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
+    constexpr int K = Kind_ == kGramAll ? kGram : Kind_;
     constexpr int MT = Side / 64, kDepth = kDepthOf<Side>;      // MT: 32 x 32 tiles of a wave, in each direction
     constexpr bool kSymmetric = K == kGram || K == kPoly, kAlong = kSymmetric;      // kAlong: the second operand
     typedef Tile<E, 2, true, Side, kDepth> TA;
@@ -250,7 +259,8 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
     const int m0 = t.m * Side, n0 = t.n * Side;
     // the operands; rows of a tile past the matrix's last are read where the matrix's last is, and their results dropped
     const int a_ld = K == kGram ? g.l : g.s, b_ld = K == kPoly ? g.s : g.l;
-    const int first = K == kGram ? split * g.cut : 0, depth = K == kGram ? min(g.cut, g.l - first) : g.s;
+    const bool all = Kind_ == kGramAll && g.splits == 1;
+    const int first = K == kGram ? split * g.cut : 0, depth = K == kGram ? (all ? g.l : min(g.cut, g.l - first)) : g.s;
     const E* pa = (K == kGram ? x : K == kPoly ? a : b) + (long)m0 * a_ld + first;
     const E* pb = (K == kPoly ? a : x) + (kAlong ? (long)n0 * b_ld + first : 0);
     const long a_step = K == kGram ? x_plane : a_plane, b_step = K == kPoly ? a_plane : x_plane;
@@ -272,7 +282,27 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
         }
     };
     f32x16 acc[MT][MT] = {};
-    multiply_tiles<TA, TB, 2, MT, MT, kDepth>(acc, reinterpret_cast<const E*>(lds), depth / kDepth, wm, wn, lane, issue);
+    if (Kind_ == kGramAll && all) {
+        f32x16 sum[MT][MT] = {};
+        const int per = g.cut / kDepth;
+        int left = per;
+        auto add = [&] {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) sum[j][i] += acc[j][i], acc[j][i] = f32x16{};
+        };
+        multiply_tiles<TA, TB, 2, MT, MT, kDepth>(acc, reinterpret_cast<const E*>(lds), depth / kDepth, wm, wn, lane, issue, [&](int) {
+            if (--left == 0) add(), left = per;
+        });
+        add();      // a last share of fewer tiles, or zeros
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[j][i] = sum[j][i];
+    } else {
+        multiply_tiles<TA, TB, 2, MT, MT, kDepth>(acc, reinterpret_cast<const E*>(lds), depth / kDepth, wm, wn, lane, issue, [](int) {});
+    }
     tile_barrier();
     float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<MT>;
     // 8 values of row m of the output, from column n on
@@ -317,6 +347,8 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
         }
     };
     const bool turned = K == kLast && g.tall;       // the output's rows are the columns here
+    const int block_m = (m0 + wm) / 64, block_n = (n0 + wn) / 64;
+    const bool written = !kSymmetric || block_m >= block_n, twice = kSymmetric && block_m > block_n;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         by_rows_block(acc, i, slab, lane);
@@ -328,7 +360,7 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
             Eight y;
 #pragma unroll
             for (int q = 0; q < 8; ++q) y.v[q] = v[q];
-            if (m >= g.s || n >= width) continue;
+            if (m >= g.s || n >= width || !written) continue;
             if (turned) {
                 const Eight z = read_parts(x + (long)m * g.l + n, x_plane);
 #pragma unroll
@@ -338,7 +370,7 @@ __global__ __launch_bounds__(256, 2) void k_product(Groups p, int from) {
             }
         }
         wave_lds_fence();
-        if (turned || (kSymmetric && t.m != t.n)) {
+        if (turned || twice) {
             // columns of the tile: 4 lanes have 32 rows of one
 #pragma unroll
             for (int r = 0; r < 32 * MT; r += 16) {
@@ -374,6 +406,8 @@ constexpr long div_up(long a, long b) { return (a + b - 1) / b; }
 // (As in dense_linear.hip: min and max without std are int's on the host.)
 long triangle(long tiles) { return tiles * (tiles + 1) / 2; }
 
+long shares_of(const Group& g) { return div_up(g.l, g.cut); }
+
 // Places of the tensors from `first` on (at most kMostGroups) and the bytes they take.
 long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* rows, const int* cols) {
     long at = 0, sums = 0;
@@ -400,14 +434,15 @@ long lay_out(Groups& p, int first, int n_tensors, const long* batch, const int* 
     long tiles = 0, terms = 0;
     for (int k = 0; k < p.n; ++k) tiles += p.g[k].batch * triangle(div_up(p.g[k].s, 128));
     p.wide = tiles >= 256;
-    // A's sums are cut where a long side would keep few workgroups busy for long
+    // shares go to workgroups of their own where a long side would keep few workgroups busy for long
     for (int k = 0; k < p.n; ++k) terms += p.g[k].batch * triangle(div_up(p.g[k].s, p.wide ? 128 : 64)) * p.g[k].l;
-    const long cut = std::max<long>(kLeastCut, div_up(terms, 1024));
+    const long most = std::max<long>(kLeastCut, div_up(terms, 1024));
     for (int k = 0; k < p.n; ++k) {
         Group& g = p.g[k];
-        g.splits = (unsigned)std::max<long>(1L, g.l / cut);
-        g.cut = (int)div_up(div_up(g.l, g.splits), kPad) * kPad;
-        g.splits = (unsigned)std::max<long>(1L, div_up(g.l, g.cut));
+        const long shares = std::max<long>(kFill / triangle(g.s / 64), kLeastShares);
+        const long cut = std::max<long>(g.s < kWideSide ? std::max<long>(g.s, kLeastCut) : kMostCut, div_up(g.l, shares));
+        g.cut = (int)div_up(div_up(g.l, std::max<long>(1, g.l / cut)), kPad) * kPad;
+        g.splits = g.l / most >= 2 ? (unsigned)shares_of(g) : 1;
         g.parts = at / 2;       // a float for two E; at is a multiple of the padding's square
         if (g.splits > 1) at += 2 * g.batch * g.splits * (long)g.s * g.s;
     }
@@ -436,7 +471,7 @@ template <int K, int Side>
 hipError_t product(Groups& p, int from, hipStream_t st) {
     const unsigned total = place(p, [](const Group& g) {
         if (K == kStep || K == kLast) return div_up(g.s, Side) * div_up(g.l, Side);
-        return triangle(div_up(g.s, Side)) * (K == kGram ? (long)g.splits : 1);
+        return triangle(div_up(g.s, Side)) * (K == kGram || K == kGramAll ? (long)g.splits : 1);
     });
     k_product<K, Side><<<total, 256, 0, st>>>(p, from);
     return hipGetLastError();
@@ -459,10 +494,11 @@ hipError_t run(Groups& p, int steps, hipStream_t st) {
     total = place(p, [](const Group& g) { return (long)(g.s / 64) * (g.l / 64); });
     k_begin<<<total, 256, 0, st>>>(p);
     CTP_TRY(hipGetLastError());
-    bool cut = false;
-    for (int k = 0; k < p.n; ++k) cut |= p.g[k].batch && p.g[k].splits > 1;
+    bool cut = false, all = false;
+    for (int k = 0; k < p.n; ++k) cut |= p.g[k].batch && p.g[k].splits > 1, all |= p.g[k].batch && p.g[k].splits < shares_of(p.g[k]);
     for (int s = 0; s < steps; ++s) {
-        CTP_TRY(product<kGram>(p, s & 1, st));
+        // (a workgroup that adds shares up takes 205 registers a lane for 142)
+        CTP_TRY(all ? product<kGramAll>(p, s & 1, st) : product<kGram>(p, s & 1, st));
         if (cut) {
             total = place_groups(p, [](const Group& g) {
                 return g.splits > 1 ? div_up(g.batch * (long)g.s * g.s, 256 * 8) : 0L;

@@ -169,8 +169,7 @@ def orthogonalise(tensors, steps: int = 5, eps: float = 1e-7, scale: float = 1.0
     """Every matrix [..., rows, cols] of `tensors` with its singular values brought near 1 (0.7 .. 1.2) by `steps`
     Newton-Schulz steps, times scale: X = M / (|M| + eps), X <- a X + (b A + c A A) X with A = X X^T.  out: the tensors
     to write, shapes and types like `tensors`; `tensors` itself works in place; new ones if None.  Returns out.  Not
-    differentiable.  The same call gives the same bits; in another list a matrix's last bits may differ (22 are held, and
-    how sums are cut goes by the whole list)."""
+    differentiable.  A matrix's result does not depend on the others of the list, to the last bit."""
     tensors = list(tensors)
     out = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in tensors] if out is None else list(out)
     dense_native().orthogonalise(tensors, out, steps, eps, scale, workspace)

@@ -74,8 +74,13 @@ const char* check(const std::vector<Shape>& shapes) {
             if (g.batch != (empty ? 0 : s.batch)) return "batch";
             if (g.s < kPad || g.l < g.s || g.s % kPad || g.l % kPad) return "padding";
             if (!empty && (g.s < std::min(s.rows, s.cols) || g.l < std::max(s.rows, s.cols))) return "sides";
-            // a share of A is whole tiles of k, and the shares are the long side
-            if (g.cut < kPad || g.cut % kPad || (long)g.splits * g.cut < g.l || (long)(g.splits - 1) * g.cut >= g.l || g.chunks < 1) return "shares";
+            // a share of A is whole tiles of k, and the shares are the long side; they are one workgroup's or one's each
+            if (g.cut < kPad || g.cut % kPad || g.cut > g.l || g.chunks < 1) return "shares";
+            if (g.splits != 1 && g.splits != shares_of(g)) return "splits";
+            // and go by the matrix alone
+            Groups one{};
+            lay_out(one, 0, 1, &batch[first + k], &rows[first + k], &cols[first + k]);
+            if (one.g[0].cut != g.cut || one.g[0].chunks != g.chunks) return "company";
             const long planes[4] = {g.x[0], g.x[1], g.a, g.b}, each[4] = {2L * g.s * g.l, 2L * g.s * g.l, 2L * g.s * g.s, 2L * g.s * g.s};
             for (int q = 0; q < 4; ++q) {
                 if (planes[q] != at) return "planes";

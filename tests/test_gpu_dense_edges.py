@@ -252,3 +252,23 @@ def test_infinities_of_floats(ctp, dev, rows, inner, outer, how):
 
 def to_dev(dev, *ts):
     return [None if t is None else t.to(dev) for t in ts]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_orthogonalise_same_bits_in_any_list(ctp, dev, dtype):
+    """A matrix alone, in lists that are computed in tiles of 128 or of 64 and whose sums are cut or not: the same bits."""
+    g = torch.Generator().manual_seed(10)
+    shapes = [(2048, 2048), (520, 3000), (3, 300, 1100), (64, 5000), (1100, 130), (130, 130), (1, 700, 700), (257, 1030)]
+    ms = [normal(g, s, dtype).to(dev) for s in shapes]
+    alone = [ctp.orthogonalise([m])[0] for m in ms]
+    wide = torch.randn(40, 400, 900, generator=g).to(dev)       # enough tiles of 128 for the card
+    for k, company in enumerate(([wide], [ms[5]], [wide, wide, wide[:, :, :130].contiguous()], [])):
+        tell("company", k)
+        for m, o, a in zip(ms, ctp.orthogonalise([*ms, *company]), alone):
+            assert torch.equal(o, a), (k, tuple(m.shape))
+        for m, a in zip(ms, alone):
+            assert torch.equal(ctp.orthogonalise([*company, m])[-1], a), (k, tuple(m.shape))
+    # one matrix of a batch, and by itself
+    out, = ctp.orthogonalise([wide])
+    for k in (0, 17, 39):
+        assert torch.equal(out[k], ctp.orthogonalise([wide[k]])[0]), k
