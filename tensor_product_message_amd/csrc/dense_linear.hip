@@ -897,6 +897,8 @@ struct ColumnSums {
     int n, across;
 };
 
+// Whole: n is whole vectors.
+template <bool Whole>
 __global__ __launch_bounds__(256) void k_sums(ColumnSums p) {
     constexpr int N = kVec<float>, R = 4;
     __shared__ float part[256 * N];
@@ -909,7 +911,8 @@ __global__ __launch_bounds__(256) void k_sums(ColumnSums p) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             v[i] = vec_t<float>{};
-            if (m + i * high < last) v[i] = load_vec<float>(p.from + (m + i * high) * p.n, at / N, p.n);
+            const float* row = p.from + (m + i * high) * p.n;
+            if (m + i * high < last) v[i] = Whole ? *reinterpret_cast<const Vec<float>::unaligned*>(row + at) : load_vec<float>(row, at / N, p.n);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -1494,7 +1497,9 @@ hipError_t bwd_bwd(const LinearArgs& a, hipStream_t st) {
     }
     if (a.g_bias) {
         const BiasCut b = bias_cut(a.n_rows, (int)out, kVec<float>);
-        k_sums<<<dim3(b.groups, b.chunks), 256, 0, st>>>(ColumnSums{exact, sums, a.n_rows, b.chunk, (int)out, b.across});
+        const ColumnSums of{exact, sums, a.n_rows, b.chunk, (int)out, b.across};
+        const dim3 grid(b.groups, b.chunks);
+        out % kVec<float> == 0 ? k_sums<true><<<grid, 256, 0, st>>>(of) : k_sums<false><<<grid, 256, 0, st>>>(of);
         CTP_TRY(hipGetLastError());
         of_b = join_of(sums, a.g_bias, out, 1, b.chunks);
     }
