@@ -1092,11 +1092,13 @@ hipError_t run_few(const Gemm& g, unsigned batches, const Epi& epi, hipStream_t 
 // 4096 -> 4096 bf16 take 17 us cut and 36 us whole.
 unsigned sum_cut(long m, long n, long k, long batches) {
     // a part's terms, and the least of a sum that is cut: 256 x 1024 -> 1024 takes 11 us cut and 8 us whole in bf16, 14
-    // and 25 in floats; of few tiles shorter sums too (108 x 684 -> 29 floats 16 and 23, 1503 x 512 -> 512 17 and 14)
+    // and 25 in floats; of few tiles shorter sums too (108 x 684 -> 29 floats 14 cut and 19 whole, 64 x 512 -> 64 11 and
+    // 14, 1024 x 520 -> 200 13 and 16, 128 x 760 -> 1000 15 and 21, but 1503 x 512 -> 512 17 and 14)
     constexpr long kTerms = kParts == 1 ? 512 : 256;
     const long tiles = div_up(m, 64) * div_up(n, 64) * batches, least = kParts == 1 ? 2048 : tiles <= 64 ? 512 : 768;
     if (k < least) return 1;
-    // a CU holds three workgroups of the float tiles
+    // a CU holds three workgroups of the float tiles (counted as two the gradient of 600 x 1153 -> 1200 takes 42 us for 32,
+    // 200 x 3000 -> 2000 45 for 35, 400 x 900 -> 2000 27 for 26, forward 25 for 25)
     return (unsigned)std::max<long>(1L, std::min<long>((kParts == 1 ? kFill : 3 * kFill / 2) / std::max<long>(1L, tiles), k / kTerms));
 }
 long sum_cut_bytes(long m, long n, long k, long batches) {
