@@ -12,7 +12,7 @@
 // l l) are left out; the other six are summed in fp32, which is a float
 // product's accuracy at 2.7 times the rate of the fp32 matrix instructions
 // (2.5 PFLOP/s over six against 157 TFLOP/s).  What comes out not finite is
-// formed once more of the floats (again_where_beyond).
+// formed once more of the floats (any_beyond).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -369,12 +369,12 @@ __device__ __forceinline__ void by_rows_block(const f32x16 (&acc)[NT][MT], int i
 
 // Products of floats in parts give NaN where an operand is infinite (its parts are infinities of both signs) or where
 // one part's product passes the range and another's does not.  Results that are not finite are formed once more, of the
-// floats themselves, term by term.  (To see that there are none costs the hidden layer of 83325 x 64 -> 64 1% of its 16
-// us.  83325 x 64 -> 4352 with an infinity in every row takes 44 ms, all of it NaN 1.0 ms, 0.33 ms otherwise.)
-// there(m, n): whether row m and column n of the wave's tile belong to the output;
-// term(m, n, k, a, b): the factors of its term k.
-template <int MT, int NT, class There, class Term>
-__device__ __forceinline__ void again_where_beyond(f32x16 (&acc)[NT][MT], float* slab, int lane, int k_end, There&& there, Term&& term) {
+// floats straight from memory.  To see that there are none costs the hidden layer of 83325 x 64 -> 64 1% of its 16 us,
+// its gradients 2% of 29.
+constexpr float kLargestFloat = 3.4028235e38f;
+
+template <int MT, int NT>
+__device__ __forceinline__ bool any_beyond(const f32x16 (&acc)[NT][MT]) {
     float t = 0.0f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -382,8 +382,47 @@ __device__ __forceinline__ void again_where_beyond(f32x16 (&acc)[NT][MT], float*
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) t = __builtin_fmaf(acc[j][i][e], 0.0f, t);
-    if (__ballot(t != t) == 0) [[likely]] return;
+    return __ballot(t != t) != 0;
+}
+
+// By the fp32 matrix instructions, whatever the number of terms (10^6 x 512 -> 512: d_w with an infinite row 24 ms, 5.3
+// without).  read(m, n, k, a, z, b): the factors of term k of the
+// wave's row m and column n, any where the output has none; curve(a, z): makes the first factors of what read gave.
+template <int MT, int NT, class Read, class MakeCurve>
+__device__ __forceinline__ void again_where_beyond(f32x16 (&acc)[NT][MT], int lane, int k_end, Read&& read, MakeCurve&& curve) {
+    if (!any_beyond(acc)) [[likely]] return;
     forget(lane);       // what is derived from it is derived here, not before the products
+    each<MT>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        each<NT>([&](auto j) {
+            constexpr int J = decltype(j)::value, U = 4;
+            f32x16 x = {};
+#pragma unroll 1
+            for (int k0 = 0; k0 < k_end; k0 += 2 * U) {
+                float a[U] = {}, z[U] = {}, b[U] = {};
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    // a lane has row and column lane % 32 and one of two k
+                    const int k = k0 + 2 * u + (lane >> 5);
+                    if (k < k_end) read(32 * I + (lane & 31), 32 * J + (lane & 31), k, a[u], z[u], b[u]);
+                }
+                curve(a, z);
+#pragma unroll
+                for (int u = 0; u < U; ++u) x = __builtin_amdgcn_mfma_f32_32x32x2f32(b[u], a[u], x, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[J][I][e] = fabsf(acc[J][I][e]) <= kLargestFloat ? acc[J][I][e] : x[e];
+        });
+    });
+}
+
+// A lane a result, for kernels that have few terms and no registers left (an infinity in each of 83325 rows of 64 -> 4352:
+// 44 ms, 0.4 without).  slab: the wave's piece of LDS; there(m, n):
+// whether the output has row m and column n; read as above.
+template <int MT, int NT, class There, class Read>
+__device__ __forceinline__ void again_by_lanes(f32x16 (&acc)[NT][MT], float* slab, int lane, int k_end, There&& there, Read&& read) {
+    if (!any_beyond(acc)) [[likely]] return;
+    forget(lane);
     each<MT>([&](auto i) {
         constexpr int I = decltype(i)::value;
         each<NT>([&](auto j) {
@@ -399,12 +438,12 @@ __device__ __forceinline__ void again_where_beyond(f32x16 (&acc)[NT][MT], float*
             for (int id = lane; id < 32 * 32; id += 64) {
                 float* v = slab + id / 32 * kSlab<1> + id % 32;
                 const int m = 32 * I + id / 32, n = 32 * J + id % 32;
-                if (fabsf(*v) <= 3.4028235e38f || !there(m, n)) continue;
+                if (fabsf(*v) <= kLargestFloat || !there(m, n)) continue;
                 float sum = 0.0f;
 #pragma unroll 1
                 for (int k = 0; k < k_end && sum == sum; ++k) {
                     float a, b;
-                    term(m, n, k, a, b);
+                    read(m, n, k, a, b);
                     sum = __builtin_fmaf(a, b, sum);
                 }
                 *v = sum;

@@ -231,20 +231,24 @@ __device__ __forceinline__ void staged_tiles(const Gemm& g, const Epi& epi, cons
         float* slab = reinterpret_cast<float*>(lds) + wave * 32 * kSlab<NT>;
         if constexpr (kParts > 1)
             again_where_beyond(
-                acc, slab, lane, k_end,
-                [&](int m, int n) { return wm + m < m_left && (Pairs ? ((wn + n) >> 6 << 5) + ((wn + n) & 31) : wn + n) < n_left; },
-                [&](int m, int n, int k, float& x, float& y) {
-                    m += wm, n += wn;
-                    x = (float)(AlongA ? a[m * g.a_ld + k] : a[k * g.a_ld + m]);
-                    if constexpr (Curved) {
-                        const float at = (float)(AlongA ? z[m * c.z_ld + k] : z[k * c.z_ld + m]);
+                acc, lane, k_end,
+                [&](int m, int n, int k, float& x, float& at, float& y) {
+                    // rows past the last: the last
+                    const long row = min(wm + m, m_left - 1);
+                    x = (float)(AlongA ? a[row * g.a_ld + k] : a[k * g.a_ld + row]);
+                    if constexpr (Curved) at = (float)(AlongA ? z[row * c.z_ld + k] : z[k * c.z_ld + row]);
+                    y = (float)(AlongB ? b[row_b(wn + n) * g.b_ld + k] : b[k * g.b_ld + row_b(wn + n)]);
+                },
+                [&](auto& x, const auto& at) {
+                    if constexpr (Curved)
                         with_act(c.act, [&](auto is) {
                             float f, d1, d2;
-                            activation<decltype(is)::value>(at, f, d1, d2);
-                            x *= d1;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                activation<decltype(is)::value>(at[u], f, d1, d2);
+                                x[u] *= d1;
+                            }
                         });
-                    }
-                    y = (float)(AlongB ? b[row_b(n) * g.b_ld + k] : b[k * g.b_ld + n]);
                 });
         write_tile<Pairs, MT, NT>(acc, slab, lane, wm, Pairs ? wn / 2 : wn, m_left, n_left, whole_m && whole_n, epi, t.outer, batch, m0, n0);
         lds_barrier();
@@ -631,7 +635,7 @@ __global__ __launch_bounds__(256, Blocks == 2 ? (Pairs ? 1 : 2) : kIsPlain<Epi> 
         }
         const long m0 = (long)t.m * 128 + wave * 32;
         const auto col = [&](int n) { return n0 + (Pairs ? n & 31 : n); };
-        again_where_beyond(
+        again_by_lanes(
             acc, slab, lane, k_end, [&](int m, int n) { return m0 + m < g.m && col(n) < g.n; },
             [&](int m, int n, int k, float& x, float& y) {
                 x = (g.a + batch * g.a_batch)[(m0 + m) * g.a_ld + k];

@@ -272,3 +272,18 @@ def test_orthogonalise_same_bits_in_any_list(ctp, dev, dtype):
     out, = ctp.orthogonalise([wide])
     for k in (0, 17, 39):
         assert torch.equal(out[k], ctp.orthogonalise([wide[k]])[0]), k
+
+
+def test_infinities_in_long_sums(ctp, dev):
+    """One infinity among 200000 rows: its column of d_w, and of d_bias's terms; what has none of it keeps its bits."""
+    g = torch.Generator(dev).manual_seed(11)
+    rows, inner, outer = 200000, 200, 300
+    x, grad = (torch.randn(rows, n, device=dev, generator=g) for n in (inner, outer))
+    w, z = torch.randn(outer, inner, device=dev, generator=g), torch.randn(rows, outer, device=dev, generator=g)
+    clean = ctp.linear_bwd(grad, x, w, z, act="silu")
+    x[123456, 7] = float("inf")
+    d_x, d_w, d_bias = ctp.linear_bwd(grad, x, w, z, act="silu")
+    s = grad[123456].double() * act("silu", z[123456].double())[1]
+    assert torch.equal(d_w[:, 7].double(), s.sign() * float("inf"))
+    keep = torch.arange(inner, device=dev) != 7
+    assert torch.equal(d_x, clean[0]) and torch.equal(d_w[:, keep], clean[1][:, keep]) and torch.equal(d_bias, clean[2])
